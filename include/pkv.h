@@ -66,6 +66,8 @@ typedef enum { PKV_FP16 = 0, PKV_BF16 = 1 } pkv_dtype;
 #define PKV_EFLAG_TIMEOUT       0x8  /* a bounded wait inside a kernel expired */
 #define PKV_EFLAG_GROUP         0x10 /* a shared-prefix group was malformed (its members were
                                         decoded without the shared prefix) */
+#define PKV_EFLAG_POSITION      0x20 /* rotary position outside the cos / sin table */
+#define PKV_EFLAG_TREE          0x40 /* a malformed tree of drafted tokens or accepted path */
 
 #define PKV_MAX_SPLITS 1024           /* upper bound on split-K partitions per sequence */
 
@@ -388,6 +390,158 @@ pkv_status pkv_multi_query_attention(
     int max_context_len, int num_seqs, int q_len, int num_blocks, int block_size,
     int num_q_heads, int num_kv_heads, int head_dim, float scale, void* workspace,
     size_t workspace_bytes, pkv_dtype dtype, int32_t* err_flag, void* stream);
+
+/*
+ * Per-head norms of queries and keys, the position rotation, and the cache
+ * write of the new keys and values, in one launch.  It stands where pkv_append
+ * does in a step, ahead of any of the attention calls, and takes the
+ * projections' outputs as they are ([vllm-06] 2.2 kernel fusion lists the
+ * position rotation and the KV-cache write among the ops to fuse).
+ *
+ * For token i with s = slot_mapping[i] >= 0, query head h and KV head g, in
+ * fp32 with one rounding at the end:
+ *     y = x / sqrt(mean_e x_e^2 + eps) * weight       x = q[i][h] or k[i][g]
+ *         (y = x where the weight is NULL)
+ *     (y_a, y_b) <- (y_a cos_j - y_b sin_j, y_b cos_j + y_a sin_j)
+ *         for the pairs j < rotary_dim / 2 of the first rotary_dim dims:
+ *         (a, b) = (j, j + rotary_dim / 2), or (2j, 2j + 1) when interleaved,
+ *         cos_j = cos_sin[positions[i]][j], sin_j = cos_sin[positions[i]][rotary_dim / 2 + j]
+ *     q_out[i][h] = y (q),  k_cache at slot s = y (k),  v_cache at slot s = v[i]
+ * A token with a negative slot is padding: nothing of it is read or written.
+ *
+ *   q, k, v       token i's heads start q_stride (k_stride, v_stride) elements
+ *                 after token i - 1's and are dense, [num_heads][head_dim], so
+ *                 the three may be parts of one packed projection; strides are
+ *                 multiples of 8 elements, at least a token's heads
+ *   q_out         [num_tokens][num_q_heads][head_dim]; may be q itself when
+ *                 q_stride is a token's heads, must not overlap q, k or v otherwise
+ *   q_weight, k_weight  [head_dim], dtype; NULL: no norm
+ *   eps           finite, >= 0
+ *   cos_sin       float32 [max_position][rotary_dim]: cosines, then sines
+ *   rotary_dim    a multiple of 16, 16 .. head_dim
+ *   positions     int32 [num_tokens]; outside the table: flagged
+ *                 (PKV_EFLAG_POSITION), the token skipped
+ *   slot_mapping  int64 [num_tokens], distinct; beyond the pool: flagged
+ *                 (PKV_EFLAG_SLOT), the token skipped
+ * pkv_norm_rope_append_fp8 writes E4M3 caches: E4M3(y / k_scale) and
+ * E4M3(v / v_scale), the fp32 quotient rounded to the nearest E4M3 value (ties
+ * to even), saturating at +-448 (V's codes are those of pkv_append_fp8).
+ */
+pkv_status pkv_norm_rope_append(void* q_out, const void* q, int64_t q_stride, const void* k,
+                                int64_t k_stride, const void* v, int64_t v_stride,
+                                const void* q_weight, const void* k_weight, float eps,
+                                const float* cos_sin, int max_position, int rotary_dim,
+                                int interleaved, const int32_t* positions, void* k_cache,
+                                void* v_cache, const int64_t* slot_mapping, int num_tokens,
+                                int num_blocks, int block_size, int num_q_heads,
+                                int num_kv_heads, int head_dim, pkv_dtype dtype,
+                                int32_t* err_flag, void* stream);
+
+pkv_status pkv_norm_rope_append_fp8(void* q_out, const void* q, int64_t q_stride, const void* k,
+                                    int64_t k_stride, const void* v, int64_t v_stride,
+                                    const void* q_weight, const void* k_weight, float eps,
+                                    const float* cos_sin, int max_position, int rotary_dim,
+                                    int interleaved, const int32_t* positions, void* k_cache,
+                                    void* v_cache, const int64_t* slot_mapping, int num_tokens,
+                                    int num_blocks, int block_size, int num_q_heads,
+                                    int num_kv_heads, int head_dim, float k_scale, float v_scale,
+                                    pkv_dtype dtype, int32_t* err_flag, void* stream);
+
+/*
+ * A step over a tree of drafted tokens ([inference] "投机采样 (Speculative
+ * Decoding)", with several continuations drafted per sequence and verified in
+ * one pass).  Sequence b holds n_b = context_lens[b] positions: n_b - tree_len
+ * committed ones, then one per tree node, node i at position
+ * n_b - tree_len + i.  The calls of a step:
+ *     pkv_tree_plan, pkv_norm_rope_append (or pkv_append), pkv_tree_attention,
+ *     pkv_tree_commit
+ * A sequence with n_b = 0 is an empty place of the batch: its nodes are
+ * absent, its attention rows are zero and nothing of it is moved.  Any other
+ * n_b below tree_len, negative or beyond the block table or max_context_len is
+ * flagged (PKV_EFLAG_CONTEXT_LEN).
+ */
+#define PKV_TREE_ABSENT (-2)          /* parents entry of a node that is not there */
+#define PKV_MAX_TREE_LEN 1024
+
+/*
+ * The plan of a step: from each node's parent, what the other calls read.
+ *
+ *   parents       int32 [num_seqs][tree_len]: the parent's index, below the
+ *                 node's own; -1 for a child of the committed context (a root);
+ *                 PKV_TREE_ABSENT for a node that is not there.  Any other
+ *                 value, or an absent parent, is flagged (PKV_EFLAG_TREE) and
+ *                 makes the node (and its descendants) absent
+ *   tree_mask     int32 [num_seqs][tree_len][ceil(tree_len / 32)] (written): bit
+ *                 j % 32 of word j / 32 of row i is set when node j is node i or
+ *                 an ancestor of it; the row of an absent node is zero
+ *   positions     int32 [num_seqs][tree_len] (written): n_b - tree_len + the
+ *                 node's depth (0 for an absent node)
+ *   slot_mapping  int64 [num_seqs][tree_len] (written): the cache slot of the
+ *                 node's position, -1 for an absent node, and for all nodes of a
+ *                 sequence whose context length is flagged, or whose block id is
+ *                 (PKV_EFLAG_BLOCK_ID)
+ */
+pkv_status pkv_tree_plan(int32_t* tree_mask, int32_t* positions, int64_t* slot_mapping,
+                         const int32_t* parents, const int32_t* context_lens,
+                         const int32_t* block_tables, int max_blocks_per_seq,
+                         int max_context_len, int num_seqs, int tree_len, int num_blocks,
+                         int block_size, int32_t* err_flag, void* stream);
+
+/*
+ * Attention of a tree's nodes: pkv_multi_query_attention with the chunk's
+ * causal limit replaced by a mask.  The nodes' K/V are appended first.  Query
+ * row i of sequence b attends to position t < n_b when t < n_b - tree_len, or
+ * when bit t - (n_b - tree_len) of tree_mask[b][i] is set.  The mask may hold
+ * any bits (pkv_tree_plan writes the ancestors'); bits past tree_len are
+ * ignored.  A row that attends to nothing becomes zero.  What the cache holds
+ * at a position that a row does not attend to never reaches that row, whatever
+ * its bits (infinities and NaN included).
+ *
+ *   q, out        [num_seqs][tree_len][num_q_heads][head_dim], dtype
+ *   tree_mask     int32 [num_seqs][tree_len][ceil(tree_len / 32)], rows of
+ *                 sequence b mask_stride words after those of b - 1 (0: one
+ *                 mask for all sequences)
+ *   other arguments as for pkv_multi_query_attention; workspace of at least
+ *   pkv_tree_attention_workspace_size(...) bytes (contents on entry do not matter)
+ */
+size_t pkv_tree_attention_workspace_size(int num_seqs, int tree_len, int num_q_heads,
+                                         int num_kv_heads, int head_dim, int block_size,
+                                         int max_context_len);
+
+pkv_status pkv_tree_attention(void* out, const void* q, const void* k_cache, const void* v_cache,
+                              const int32_t* block_tables, int max_blocks_per_seq,
+                              const int32_t* context_lens, int max_context_len,
+                              const int32_t* tree_mask, int64_t mask_stride, int num_seqs,
+                              int tree_len, int num_blocks, int block_size, int num_q_heads,
+                              int num_kv_heads, int head_dim, float scale, void* workspace,
+                              size_t workspace_bytes, pkv_dtype dtype, int32_t* err_flag,
+                              void* stream);
+
+/*
+ * Commit of a step: the cache rows of the accepted path move to the positions
+ * behind the committed context, in place and bit-exact.  For j < accepted_lens[b],
+ * K and V of position n_b - tree_len + accepted[b][j] are copied to position
+ * n_b - tree_len + j, and
+ *     new_context_lens[b] = n_b - tree_len + accepted_lens[b].
+ * The rows of the other nodes, and all others, keep their bytes.
+ *
+ *   accepted       int32 [num_seqs][max_accepted]: a sequence's accepted nodes,
+ *                  strictly increasing (a path down the tree is); entries past
+ *                  accepted_lens[b] are not read
+ *   accepted_lens  int32 [num_seqs], 0 .. min(max_accepted, tree_len)
+ *   new_context_lens  int32 [num_seqs] (written), nullable; must not overlap
+ *                  context_lens
+ * A malformed path or count is flagged (PKV_EFLAG_TREE): nothing of that
+ * sequence moves, and its new length is the committed one.  The same goes for
+ * a flagged context length (new length max(0, min(n_b, longest) - tree_len))
+ * and for a path that meets a bad block id (PKV_EFLAG_BLOCK_ID).
+ */
+pkv_status pkv_tree_commit(void* k_cache, void* v_cache, const int32_t* block_tables,
+                           int max_blocks_per_seq, const int32_t* context_lens, int tree_len,
+                           const int32_t* accepted, const int32_t* accepted_lens,
+                           int max_accepted, int32_t* new_context_lens, int num_seqs,
+                           int num_blocks, int block_size, int num_kv_heads, int head_dim,
+                           pkv_dtype dtype, int32_t* err_flag, void* stream);
 
 /*
  * Log-sum-exp merge of split-K partials ([inference] combine_result and the

@@ -13,10 +13,15 @@ Calls (same names as the C entry points, without the ``pkv_`` prefix):
   decode_attention(q, k_cache, v_cache, block_tables, context_lens, max_context_len)
   merge(partial_o, partial_lse)
   gather(k_cache, v_cache, block_tables, context_lens, max_context_len)
+  norm_rope_append(q, k, v, positions, cos_sin, k_cache, v_cache, slot_mapping)
+  tree_plan(parents, context_lens, block_tables, num_blocks, block_size, max_context_len)
+  tree_attention(q, k_cache, v_cache, block_tables, context_lens, max_context_len, tree_mask)
+  tree_commit(k_cache, v_cache, block_tables, context_lens, tree_len, accepted, accepted_lens)
   check_error(err_flag)
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -33,6 +38,8 @@ STATUS_NAMES = {0: "PKV_OK", 1: "PKV_ERR_INVALID_ARG", 2: "PKV_ERR_UNSUPPORTED",
                 3: "PKV_ERR_WORKSPACE", 4: "PKV_ERR_CUDA", 5: "PKV_ERR_DEVICE_INDEX",
                 6: "PKV_ERR_DEVICE_TIMEOUT"}
 EFLAG_BLOCK_ID, EFLAG_SLOT, EFLAG_CONTEXT_LEN, EFLAG_TIMEOUT, EFLAG_GROUP = 0x1, 0x2, 0x4, 0x8, 0x10
+EFLAG_POSITION, EFLAG_TREE = 0x20, 0x40
+TREE_ABSENT, MAX_TREE_LEN = -2, 1024
 MAX_SPLITS = 1024
 _DTYPES = {torch.float16: 0, torch.bfloat16: 1}
 SIZE_MAX = ctypes.c_size_t(-1).value
@@ -86,6 +93,16 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                                               sz, i, p, p]
     lib.pkv_merge.argtypes = [p, p, p, i, i, i, i, i, p]
     lib.pkv_gather.argtypes = [p, p, p, p, p, i, p, i, i, i, i, i, i, i, p, p]
+    i64 = ctypes.c_int64
+    rope = [p, p, i64, p, i64, p, i64, p, p, f, p, i, i, i, p, p, p, p, i, i, i, i, i, i]
+    lib.pkv_norm_rope_append.argtypes = rope + [i, p, p]
+    lib.pkv_norm_rope_append_fp8.argtypes = rope + [f, f, i, p, p]
+    lib.pkv_tree_plan.argtypes = [p, p, p, p, p, p, i, i, i, i, i, i, p, p]
+    lib.pkv_tree_attention_workspace_size.argtypes = [i, i, i, i, i, i, i]
+    lib.pkv_tree_attention_workspace_size.restype = sz
+    lib.pkv_tree_attention.argtypes = [p, p, p, p, p, i, p, i, p, i64, i, i, i, i, i, i, i, f, p,
+                                       sz, i, p, p]
+    lib.pkv_tree_commit.argtypes = [p, p, p, i, p, i, p, p, i, p, i, i, i, i, i, i, p, p]
     lib.pkv_check_error.argtypes = [p, p, ctypes.POINTER(ctypes.c_int32)]
     lib.pkv_status_string.argtypes = [i]
     lib.pkv_status_string.restype = ctypes.c_char_p
@@ -97,6 +114,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                  "pkv_append_decode_attention", "pkv_append_decode_attention_fp8",
                  "pkv_append_fp8", "pkv_decode_attention_fp8",
                  "pkv_decode_attention_prefix_shared", "pkv_multi_query_attention",
+                 "pkv_norm_rope_append", "pkv_norm_rope_append_fp8", "pkv_tree_plan",
+                 "pkv_tree_attention", "pkv_tree_commit",
                  "pkv_merge", "pkv_gather", "pkv_selftest_wait_timeout",
                  "pkv_check_error", "pkv_max_group_size", "pkv_multi_query_plan"):
         getattr(lib, name).restype = i
@@ -588,6 +607,281 @@ def gather(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Ten
                         _stream(stream, k_cache.device))
     _check(st, "pkv_gather")
     return k_out, v_out
+
+
+def _arg(t: Optional[torch.Tensor], name: str, dtype, device, optional: bool = False,
+         dense: bool = True) -> int:
+    """The address of a tensor argument that must be of ``dtype`` on ``device``."""
+    if t is None and optional:
+        return 0
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device (there is no CPU path)")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if dense and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _call_on(device, stream):
+    """(context that makes ``device`` current, the stream to launch on)."""
+    ctx = contextlib.nullcontext() if torch.cuda.current_device() == device.index \
+        else torch.cuda.device(device)
+    return ctx, (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+
+
+def _keep(t: torch.Tensor, stream) -> torch.Tensor:
+    """A tensor allocated here for a call on ``stream``: when that is another
+    stream than the allocator's current one, its memory must outlast the call."""
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def _head_rows(t: torch.Tensor, name: str, dtype, device, heads: int, d: int):
+    """(address, elements between tokens) of [T, heads, d] rows whose heads are dense."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
+        raise ValueError(f"{name} must be [tokens, {heads}, {d}], got {tuple(t.shape)}")
+    ptr = _arg(t, name, dtype, device, dense=False)
+    s0, s1, s2 = t.stride()
+    if t.numel() and (s2 != 1 or (heads > 1 and s1 != d)):
+        raise ValueError(f"{name}: a token's heads must be dense")
+    return ptr, (s0 if t.shape[0] > 1 else heads * d)
+
+
+def _norm_rope(name, q, k, v, positions, cos_sin, k_cache, v_cache, slot_mapping, q_weight,
+               k_weight, eps, style, q_out, err_flag, stream, layout, scales):
+    lib = load()
+    if not isinstance(q, torch.Tensor) or not q.is_cuda:
+        raise ValueError("q must be on a CUDA device (there is no CPU path)")
+    if q.dim() != 3:
+        raise ValueError("q must be [tokens, heads, head_dim]")
+    if style not in ("half", "interleaved"):
+        raise ValueError(f"style must be 'half' or 'interleaved', got {style!r}")
+    t, h_q, d = q.shape
+    nb, bs, h_kv, d2 = _cache_dims(k_cache, layout)
+    dt, dev = q.dtype, q.device
+    if d2 != d or v_cache.shape != k_cache.shape or k.shape[:1] != (t,) or \
+            v.shape[:1] != (t,) or slot_mapping.shape != (t,) or positions.shape != (t,) or \
+            cos_sin.dim() != 2:
+        raise ValueError("inconsistent norm-rope-append shapes")
+    for w in (q_weight, k_weight):
+        if w is not None and w.shape != (d,):
+            raise ValueError("a norm's weight must be [head_dim]")
+    if q_out is None:
+        q_out = _keep(torch.empty((t, h_q, d), dtype=dt, device=dev), stream)
+    elif q_out.shape != q.shape:
+        raise ValueError("q_out must have the shape of q")
+    code = _kv_code(q, layout)
+    cache_dt = torch.uint8 if scales else dt
+    qp, qs = _head_rows(q, "q", dt, dev, h_q, d)
+    kp, ks = _head_rows(k, "k", dt, dev, h_kv, d)
+    vp, vs = _head_rows(v, "v", dt, dev, h_kv, d)
+    ctx, st = _call_on(dev, stream)
+    with ctx:
+        r = getattr(lib, name)(
+            _arg(q_out, "q_out", dt, dev), qp, qs, kp, ks, vp, vs,
+            _arg(q_weight, "q_weight", dt, dev, True), _arg(k_weight, "k_weight", dt, dev, True),
+            float(eps), _arg(cos_sin, "cos_sin", torch.float32, dev), cos_sin.shape[0],
+            cos_sin.shape[1], int(style == "interleaved"),
+            _arg(positions, "positions", torch.int32, dev),
+            _arg(k_cache, "k_cache", cache_dt, dev), _arg(v_cache, "v_cache", cache_dt, dev),
+            _arg(slot_mapping, "slot_mapping", torch.int64, dev), t, nb, bs, h_q, h_kv, d,
+            *scales, code, _arg(err_flag, "err_flag", torch.int32, dev, True), st)
+    _check(r, name)
+    return q_out
+
+
+def norm_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
+                     cos_sin: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                     slot_mapping: torch.Tensor, q_weight: Optional[torch.Tensor] = None,
+                     k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                     style: str = "half", q_out: Optional[torch.Tensor] = None,
+                     err_flag: Optional[torch.Tensor] = None, stream=None,
+                     layout: str = "nhd") -> torch.Tensor:
+    """Per-head RMS norms of q [T, H_q, d] and k [T, H_kv, d] (none without a
+    weight [d]), the rotation by ``positions`` (int32 [T]) into ``cos_sin``
+    (float32 [max_position, rotary_dim]: cosines, then sines), and the append of
+    the new k and v rows at ``slot_mapping`` (int64 [T], negative: padding, the
+    token is left out).  Returns the new q rows (``q_out``, which may be q itself).
+
+    q, k and v may be parts of one packed projection (a token's heads dense);
+    ``style``: pairs (j, j + rotary_dim/2) ("half") or (2j, 2j + 1) ("interleaved").
+    """
+    return _norm_rope("pkv_norm_rope_append", q, k, v, positions, cos_sin, k_cache, v_cache,
+                      slot_mapping, q_weight, k_weight, eps, style, q_out, err_flag, stream,
+                      layout, ())
+
+
+def norm_rope_append_fp8(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                         positions: torch.Tensor, cos_sin: torch.Tensor, k_cache: torch.Tensor,
+                         v_cache: torch.Tensor, slot_mapping: torch.Tensor, k_scale: float,
+                         v_scale: float, q_weight: Optional[torch.Tensor] = None,
+                         k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                         style: str = "half", q_out: Optional[torch.Tensor] = None,
+                         err_flag: Optional[torch.Tensor] = None, stream=None,
+                         layout: str = "nhd") -> torch.Tensor:
+    """``norm_rope_append`` into uint8 E4M3 caches: E4M3(y / k_scale) of the rotated
+    keys and E4M3(v / v_scale) (nearest, ties to even, saturating at +-448)."""
+    return _norm_rope("pkv_norm_rope_append_fp8", q, k, v, positions, cos_sin, k_cache, v_cache,
+                      slot_mapping, q_weight, k_weight, eps, style, q_out, err_flag, stream,
+                      layout, (float(k_scale), float(v_scale)))
+
+
+def tree_plan(parents: torch.Tensor, context_lens: torch.Tensor, block_tables: torch.Tensor,
+              num_blocks: int, block_size: int, max_context_len: int,
+              tree_mask: Optional[torch.Tensor] = None,
+              positions: Optional[torch.Tensor] = None,
+              slot_mapping: Optional[torch.Tensor] = None,
+              err_flag: Optional[torch.Tensor] = None, stream=None):
+    """(tree_mask, positions, slot_mapping) of a step over trees of drafted tokens.
+
+    parents int32 [B, T]: each node's parent (an earlier node), -1 for a child of
+    the committed context, ``TREE_ABSENT`` for a node that is not there.
+    context_lens counts the T nodes' positions.  tree_mask int32
+    [B, T, ceil(T / 32)]: the bits of a node and its ancestors; positions int32
+    [B, T]: the nodes' rotary positions; slot_mapping int64 [B, T]: their cache
+    slots (-1 for an absent node).
+    """
+    lib = load()
+    if not isinstance(parents, torch.Tensor) or not parents.is_cuda:
+        raise ValueError("parents must be on a CUDA device (there is no CPU path)")
+    if parents.dim() != 2 or block_tables.dim() != 2:
+        raise ValueError("inconsistent tree-plan shapes")
+    b, t = parents.shape
+    dev, i32 = parents.device, torch.int32
+    words = (t + 31) // 32
+    if context_lens.shape != (b,) or block_tables.shape[0] != b:
+        raise ValueError("inconsistent tree-plan shapes")
+    if tree_mask is None:
+        tree_mask = _keep(torch.empty((b, t, words), dtype=i32, device=dev), stream)
+    if positions is None:
+        positions = _keep(torch.empty((b, t), dtype=i32, device=dev), stream)
+    if slot_mapping is None:
+        slot_mapping = _keep(torch.empty((b, t), dtype=torch.int64, device=dev), stream)
+    if tree_mask.shape != (b, t, words) or positions.shape != (b, t) or \
+            slot_mapping.shape != (b, t):
+        raise ValueError("inconsistent tree-plan outputs")
+    ctx, st = _call_on(dev, stream)
+    with ctx:
+        r = lib.pkv_tree_plan(
+            _arg(tree_mask, "tree_mask", i32, dev), _arg(positions, "positions", i32, dev),
+            _arg(slot_mapping, "slot_mapping", torch.int64, dev),
+            _arg(parents, "parents", i32, dev), _arg(context_lens, "context_lens", i32, dev),
+            _arg(block_tables, "block_tables", i32, dev), block_tables.shape[1],
+            int(max_context_len), b, t, int(num_blocks), int(block_size),
+            _arg(err_flag, "err_flag", i32, dev, True), st)
+    _check(r, "pkv_tree_plan")
+    return tree_mask, positions, slot_mapping
+
+
+def tree_attention_workspace_size(num_seqs: int, tree_len: int, num_q_heads: int,
+                                  num_kv_heads: int, head_dim: int, block_size: int,
+                                  max_context_len: int) -> int:
+    """Bytes of workspace ``tree_attention`` needs on the current device."""
+    n = load().pkv_tree_attention_workspace_size(num_seqs, tree_len, num_q_heads, num_kv_heads,
+                                                 head_dim, block_size, max_context_len)
+    if n == SIZE_MAX:
+        raise PkvError(1, "pkv_tree_attention_workspace_size")
+    return int(n)
+
+
+def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                   block_tables: torch.Tensor, context_lens: torch.Tensor, max_context_len: int,
+                   tree_mask: torch.Tensor, scale: Optional[float] = None,
+                   out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                   err_flag: Optional[torch.Tensor] = None, stream=None,
+                   layout: str = "nhd") -> torch.Tensor:
+    """Attention of trees of drafted tokens over the paged cache.
+
+    q [B, T, H_q, d]; context_lens counts the T nodes' positions (appended
+    first); node i of sequence b attends to the committed positions and to the
+    nodes whose bits are set in tree_mask[b, i] (int32 [B, T, ceil(T / 32)], or
+    [1, T, ...] for one mask of all sequences).
+    """
+    lib = load()
+    if not isinstance(q, torch.Tensor) or not q.is_cuda:
+        raise ValueError("q must be on a CUDA device (there is no CPU path)")
+    if q.dim() != 4:
+        raise ValueError("q must be [sequences, nodes, heads, head_dim]")
+    b, t, h_q, d = q.shape
+    nb, bs, h_kv, d2 = _cache_dims(k_cache, layout)
+    words = (t + 31) // 32
+    if d2 != d or v_cache.shape != k_cache.shape or block_tables.dim() != 2 or \
+            block_tables.shape[0] != b or context_lens.shape != (b,) or \
+            tree_mask.dim() != 3 or tree_mask.shape[0] not in (1, b) or \
+            tree_mask.shape[1:] != (t, words):
+        raise ValueError("inconsistent tree attention shapes")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    dt, dev, i32 = q.dtype, q.device, torch.int32
+    if out is None:
+        out = _keep(torch.empty_like(q), stream)
+    elif out.shape != q.shape:
+        raise ValueError("out must have the shape of q")
+    s0, s1, s2 = tree_mask.stride()
+    if tree_mask.numel() and ((words > 1 and s2 != 1) or (t > 1 and s1 != words)):
+        raise ValueError("tree_mask: the rows of a sequence must be dense")
+    mask_stride = s0 if tree_mask.shape[0] > 1 else 0
+    ctx, st = _call_on(dev, stream)
+    with ctx:
+        if workspace is None:  # a given workspace is checked by the library itself
+            need = tree_attention_workspace_size(b, t, h_q, h_kv, d, bs, max_context_len)
+            workspace = _keep(torch.empty(need, dtype=torch.uint8, device=dev), stream)
+        r = lib.pkv_tree_attention(
+            _arg(out, "out", dt, dev), _arg(q, "q", dt, dev), _arg(k_cache, "k_cache", dt, dev),
+            _arg(v_cache, "v_cache", dt, dev), _arg(block_tables, "block_tables", i32, dev),
+            block_tables.shape[1], _arg(context_lens, "context_lens", i32, dev),
+            int(max_context_len), _arg(tree_mask, "tree_mask", i32, dev, dense=False),
+            mask_stride, b, t, nb, bs, h_q, h_kv, d, float(scale),
+            _arg(workspace, "workspace", workspace.dtype, dev),
+            workspace.numel() * workspace.element_size(), _kv_code(q, layout),
+            _arg(err_flag, "err_flag", i32, dev, True), st)
+    _check(r, "pkv_tree_attention")
+    return out
+
+
+def tree_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+                context_lens: torch.Tensor, tree_len: int, accepted: torch.Tensor,
+                accepted_lens: torch.Tensor, new_context_lens: Optional[torch.Tensor] = None,
+                err_flag: Optional[torch.Tensor] = None, stream=None,
+                layout: str = "nhd") -> torch.Tensor:
+    """Moves the accepted path's cache rows behind the committed context, in place.
+
+    accepted int32 [B, A]: each sequence's accepted nodes, strictly increasing,
+    accepted_lens int32 [B] of them.  Returns the new context lengths (int32 [B]):
+    context_lens - tree_len + accepted_lens.
+    """
+    lib = load()
+    if not isinstance(k_cache, torch.Tensor) or not k_cache.is_cuda:
+        raise ValueError("k_cache must be on a CUDA device (there is no CPU path)")
+    nb, bs, h_kv, d = _cache_dims(k_cache, layout)
+    dt, dev, i32 = k_cache.dtype, k_cache.device, torch.int32
+    if block_tables.dim() != 2 or accepted.dim() != 2:
+        raise ValueError("inconsistent tree-commit shapes")
+    b = block_tables.shape[0]
+    if v_cache.shape != k_cache.shape or context_lens.shape != (b,) or \
+            accepted.shape[0] != b or accepted_lens.shape != (b,):
+        raise ValueError("inconsistent tree-commit shapes")
+    if new_context_lens is None:
+        new_context_lens = _keep(torch.empty(b, dtype=i32, device=dev), stream)
+    elif new_context_lens.shape != (b,):
+        raise ValueError("new_context_lens must be [sequences]")
+    ctx, st = _call_on(dev, stream)
+    with ctx:
+        r = lib.pkv_tree_commit(
+            _arg(k_cache, "k_cache", dt, dev), _arg(v_cache, "v_cache", dt, dev),
+            _arg(block_tables, "block_tables", i32, dev), block_tables.shape[1],
+            _arg(context_lens, "context_lens", i32, dev), int(tree_len),
+            _arg(accepted, "accepted", i32, dev), _arg(accepted_lens, "accepted_lens", i32, dev),
+            accepted.shape[1], _arg(new_context_lens, "new_context_lens", i32, dev), b, nb, bs,
+            h_kv, d, _kv_code(k_cache, layout), _arg(err_flag, "err_flag", i32, dev, True), st)
+    _check(r, "pkv_tree_commit")
+    return new_context_lens
 
 
 def check_error(err_flag: torch.Tensor, stream=None) -> int:

@@ -1,6 +1,7 @@
 // Device and host helpers shared by the pkv kernels (CUDA, sm_103a).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -85,5 +86,16 @@ pkv_status decode_workspace_16bit(int num_seqs, int num_q_heads, int num_kv_head
 // reuses an id within a process, so per-context state keyed by it cannot be
 // served to a context that replaced a destroyed one.
 bool current_context_id(unsigned long long* id);
+
+// SMs of the current device, or -1.
+int current_sm_count();
+
+// Validates the shape arguments shared by planning and launching.
+pkv_status check_shapes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                        int block_size, int max_context_len, int num_splits);
+
+// The TMA tensor map of a cache (see its definition), remembered across calls.
+bool make_cache_map(CUtensorMap* map, const void* base, pkv_dtype dtype, int num_blocks,
+                    int block_size, int num_kv_heads, int head_dim, bool hnd, bool f8 = false);
 
 }  // namespace pkv

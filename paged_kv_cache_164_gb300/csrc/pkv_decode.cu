@@ -38,15 +38,14 @@
 #include <cudaTypedefs.h>
 
 #include "pkv_common.cuh"
+#include "pkv_device.cuh"
 #include "pkv_ptx.cuh"
 
 namespace pkv {
 
-constexpr int kStageTokens = 16;      // tokens per pipeline stage
 constexpr int kConsumerWarps = 4;
 constexpr int kThreads = (kConsumerWarps + 1) * 32;
 constexpr int kMaxChunkPages = 128;   // pages per partition (block-table slice in smem)
-constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s per wait before giving up
 
 // Shared-memory geometry of a decode stage: K then V of 16 tokens, as 128-byte
 // swizzled rows per column block (64 dims of a 16-bit cache, 128 of an E4M3 one).
@@ -113,10 +112,6 @@ struct DecodeParams {
     int* unit_left;
 };
 
-// Context length of sequence b as the kernels use it: negative or too long
-// values are clamped (and flagged by the decode kernel).
-__device__ __forceinline__ int clamped_len(int n, int cap) { return n < 0 ? 0 : (n > cap ? cap : n); }
-
 // Partitions of a sequence's suffix of `suffix` tokens (the whole context
 // without a shared prefix): partition j covers tokens [j*C, (j+1)*C) of it, C
 // = chunk_tokens.  Without a shared prefix (slot0 == 0) an empty context still
@@ -126,65 +121,6 @@ __device__ __forceinline__ int suffix_partitions(int suffix, int slot0, int chun
     if (suffix == 0) return slot0 > 0 ? 0 : 1;
     return (suffix + chunk - 1) / chunk;
 }
-
-__device__ __forceinline__ uint32_t pack2(float lo, float hi, __nv_bfloat16) {
-    __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<uint32_t*>(&v);
-}
-__device__ __forceinline__ uint32_t pack2(float lo, float hi, __half) {
-    __half2 v = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<uint32_t*>(&v);
-}
-__device__ __forceinline__ float2 unpack2(uint32_t x, __nv_bfloat16) {
-    return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&x));
-}
-__device__ __forceinline__ float2 unpack2(uint32_t x, __half) {
-    return __half22float2(*reinterpret_cast<__half2*>(&x));
-}
-
-// 16-token box of K or V for KV head g at token offset toff of block blk,
-// 64-dim region starting at dim c0, in either cache layout.
-__device__ __forceinline__ void load_kv_box(uint32_t dst, const CUtensorMap* map, uint32_t bar,
-                                            int c0, int g, int toff, int blk, bool hnd,
-                                            uint64_t policy) {
-    if (hnd)
-        ptx::tma_load_4d(dst, map, bar, c0, toff, g, blk, policy);
-    else
-        ptx::tma_load_4d(dst, map, bar, c0, g, toff, blk, policy);
-}
-
-// Bounded wait on an mbarrier phase.  Returns false (after raising the CTA's
-// abort flag and the device error bit on expiry) if the phase did not complete.
-__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                           int32_t* err_flag,
-                                           uint64_t limit_ns = kWaitLimitNs) {
-    if (ptx::mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = ptx::globaltimer();
-    while (true) {
-        if (ptx::mbar_try_wait(bar, parity)) return true;
-        if (*abort_flag) return false;
-        if (ptx::globaltimer() - t0 > limit_ns) {
-            *abort_flag = 1;
-            flag_error(err_flag, PKV_EFLAG_TIMEOUT);
-            return false;
-        }
-    }
-}
-
-#ifdef PKV_DEBUG
-// Debug builds (-DPKV_DEBUG) fill ring slots with all-ones bytes, a NaN in
-// fp16, bf16 and E4M3 alike, whenever their contents stop being valid: the
-// whole ring at the start, and each slot when its stage is released.  A read
-// of a slot whose copy has not landed, or of a stage already released, then
-// turns the output to NaN instead of passing unnoticed.  `lanes` threads
-// (lane index `lane`) share the fill; each makes its writes visible to the
-// async proxy, which writes the slot next.
-__device__ __forceinline__ void poison_smem(uint8_t* base, int bytes, int lane, int lanes) {
-    for (int i = lane; i < bytes / 16; i += lanes)
-        reinterpret_cast<uint4*>(base)[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
-    ptx::fence_proxy_async_smem();
-}
-#endif
 
 // Two E4M3 codes (the first in the low byte) as a pair of T, exactly: every
 // E4M3 value is an fp16 (and a bf16) value.
@@ -1198,16 +1134,6 @@ struct PrefixTile {
     static_assert(!ONE_ACC || kColQ + D / 2 <= kColOa, "Q fits between S and O");
 };
 
-// Instruction descriptor of tcgen05.mma kind::f16: fp32 accumulator, A and B
-// of one 16-bit type (0 = fp16, 1 = bf16), A K-major, B K-major or MN-major.
-__host__ __device__ constexpr uint32_t mma_idesc(uint32_t fmt, int m, int n, bool b_mn_major) {
-    return (1u << 4) | (fmt << 7) | (fmt << 10) | ((b_mn_major ? 1u : 0u) << 16) |
-           ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
-}
-template <typename T> struct F16Format;
-template <> struct F16Format<__half> { static constexpr uint32_t value = 0; };
-template <> struct F16Format<__nv_bfloat16> { static constexpr uint32_t value = 1; };
-
 // A group is used only when its bounds and prefix length are sane; otherwise
 // its members are decoded in full by the decode kernel (and the error flagged).
 __device__ __forceinline__ bool group_valid(const int32_t* group_start,
@@ -1227,32 +1153,6 @@ __device__ __forceinline__ bool prefix_group_valid(const PrefixParams& p, int gr
                                                    int& last, int& plen) {
     return group_valid(p.group_start, p.group_prefix_len, grp, p.num_seqs, p.max_group_size,
                        p.max_prefix_len, p.block_size, p.max_blocks_per_seq, first, last, plen);
-}
-
-// A bounded wait whose outcome is the same for the whole warp (a lane that
-// gives up raises the CTA's abort flag; the warp then leaves together, so
-// warp-collective tensor-memory instructions never run on part of a warp).
-__device__ __forceinline__ bool warp_wait_phase(uint32_t bar, uint32_t parity,
-                                                volatile int* abort_flag, int32_t* err_flag) {
-    const bool ok = wait_phase(bar, parity, abort_flag, err_flag);
-    return __all_sync(0xffffffffu, ok);
-}
-
-// Two fp32 weights as hi + lo 16-bit terms packed in pairs (element 0 in the
-// low half).  bf16: both terms by truncation (a bit mask; hi + lo keeps p to
-// 2^-14 relative); fp16: both terms rounded to nearest.
-__device__ __forceinline__ void split_hi_lo(float p0, float p1, uint32_t& hi, uint32_t& lo,
-                                            __nv_bfloat16) {
-    const uint32_t b0 = __float_as_uint(p0), b1 = __float_as_uint(p1);
-    hi = __byte_perm(b0, b1, 0x7632);
-    const float r0 = p0 - __uint_as_float(b0 & 0xffff0000u);
-    const float r1 = p1 - __uint_as_float(b1 & 0xffff0000u);
-    lo = __byte_perm(__float_as_uint(r0), __float_as_uint(r1), 0x7632);
-}
-__device__ __forceinline__ void split_hi_lo(float p0, float p1, uint32_t& hi, uint32_t& lo, __half) {
-    hi = pack2(p0, p1, __half());
-    const float2 back = unpack2(hi, __half());
-    lo = pack2(p0 - back.x, p1 - back.y, __half());
 }
 
 // The plan of a shared-prefix call, one CTA.  Every
@@ -2027,7 +1927,7 @@ __global__ void __launch_bounds__(32) wait_timeout_selftest_kernel(int32_t* err_
 // Host side: split planning, tensor maps, launches
 // ---------------------------------------------------------------------------
 
-static int current_sm_count() {
+int current_sm_count() {
     static std::atomic<int> cache[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) {
@@ -2097,8 +1997,8 @@ struct Plan {
 };
 
 // Validates the shape arguments shared by planning and launching.
-static pkv_status check_shapes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
-                               int block_size, int max_context_len, int num_splits) {
+pkv_status check_shapes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                        int block_size, int max_context_len, int num_splits) {
     if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
         block_size <= 0 || max_context_len < 0 || num_splits < 0 || num_splits > PKV_MAX_SPLITS)
         return PKV_ERR_INVALID_ARG;
@@ -2233,9 +2133,8 @@ static int g_map_count = 0, g_map_next = 0;
 static bool encode_cache_map(CUtensorMap* map, const void* base, pkv_dtype dtype, int num_blocks,
                              int block_size, int num_kv_heads, int head_dim, bool hnd, bool f8);
 
-static bool make_cache_map(CUtensorMap* map, const void* base, pkv_dtype dtype, int num_blocks,
-                           int block_size, int num_kv_heads, int head_dim, bool hnd,
-                           bool f8 = false) {
+bool make_cache_map(CUtensorMap* map, const void* base, pkv_dtype dtype, int num_blocks,
+                    int block_size, int num_kv_heads, int head_dim, bool hnd, bool f8) {
     const CacheMapKey key{base, (int)dtype, num_blocks, block_size, num_kv_heads, head_dim, hnd, f8};
     {
         std::lock_guard<std::mutex> lock(g_map_mutex);

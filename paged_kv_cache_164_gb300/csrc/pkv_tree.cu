@@ -1,0 +1,307 @@
+// A step over trees of drafted tokens: the plan (ancestor masks, rotary
+// positions, cache slots) and the commit of an accepted path.  The attention of
+// the nodes is in pkv_tree_attention.cu.
+#include <algorithm>
+#include <climits>
+#include <cmath>
+
+#include "pkv_common.cuh"
+#include "pkv_device.cuh"
+
+namespace pkv {
+
+// ---------------------------------------------------------------------------
+// The plan
+// ---------------------------------------------------------------------------
+// One CTA per sequence, one thread per node.  A node's ancestors are its parent
+// chain, whose indices fall, so a thread walks the chain once (parents in
+// shared memory), gathering the 32 bits of a mask word in a register before it
+// goes on to the next lower word.  Latency is all it costs: a few dependent
+// loads and a walk as long as the tree is deep.
+
+struct TreePlanParams {
+    int32_t* tree_mask;
+    int32_t* positions;
+    int64_t* slot_mapping;
+    const int32_t* parents;
+    const int32_t* context_lens;
+    const int32_t* block_tables;
+    int32_t* err_flag;
+    int max_blocks_per_seq;
+    int cap;
+    int tree_len;
+    int num_blocks;
+    int block_size;
+};
+
+__global__ void __launch_bounds__(PKV_MAX_TREE_LEN) tree_plan_kernel(const TreePlanParams p) {
+    __shared__ int32_t s_parent[PKV_MAX_TREE_LEN];
+    ptx::launch_dependents();
+    ptx::grid_dependency_wait();
+    const int b = blockIdx.x;
+    const int t = p.tree_len;
+    const int i = threadIdx.x;
+    const int64_t at = (int64_t)b * t + i;
+    const int n_raw = __ldg(p.context_lens + b);
+    const int par = i < t ? __ldg(p.parents + at) : PKV_TREE_ABSENT;
+    const bool n_ok = n_raw >= t && n_raw <= p.cap;
+    if (i < t) s_parent[i] = par;
+    if (i == 0 && !n_ok && n_raw != 0) flag_error(p.err_flag, PKV_EFLAG_CONTEXT_LEN);
+    const int base = clamped_len(n_raw, p.cap) - t;
+    // the slot's block id, read while the parents settle
+    const int pos = base + i;
+    int blk = -1;
+    if (i < t && n_ok)
+        blk = __ldg(p.block_tables + (int64_t)b * p.max_blocks_per_seq + pos / p.block_size);
+    __syncthreads();
+    if (i >= t) return;
+
+    // is every link of the chain sound (an earlier, present node, or the context)?
+    int depth = 0;
+    bool there = n_raw != 0;
+    for (int cur = i;;) {
+        const int up = s_parent[cur];
+        if (up == -1) break;
+        if (up < -1 || up >= cur) {
+            there = false;
+            break;
+        }
+        ++depth;
+        cur = up;
+    }
+    if (n_raw != 0 && !there && par != PKV_TREE_ABSENT) flag_error(p.err_flag, PKV_EFLAG_TREE);
+    const int words = (t + 31) / 32;
+    int32_t* mask = p.tree_mask + at * words;
+    int cur = there ? i : -1;
+    for (int w = words - 1; w >= 0; --w) {
+        uint32_t bits = 0;
+        while (cur >= 0 && (cur >> 5) == w) {
+            bits |= 1u << (cur & 31);
+            cur = s_parent[cur];
+        }
+        mask[w] = (int32_t)bits;
+    }
+    p.positions[at] = there ? max(0, base + depth) : 0;
+    int64_t slot = -1;
+    if (there && n_ok) {
+        if (blk < 0 || blk >= p.num_blocks)
+            flag_error(p.err_flag, PKV_EFLAG_BLOCK_ID);
+        else
+            slot = (int64_t)blk * p.block_size + pos % p.block_size;
+    }
+    p.slot_mapping[at] = slot;
+}
+
+// ---------------------------------------------------------------------------
+// The commit
+// ---------------------------------------------------------------------------
+// Each accepted row is read once and written once.  In place and without a
+// buffer: the path is strictly increasing, so path[j] >= j, and a thread that
+// moves its own 16-byte column of the rows in increasing j never overwrites a
+// row it still has to read (a later source path[j'] >= j' > j).  Threads share
+// no bytes, so there is nothing to wait for; kMoveBatch loads are in flight
+// before the first store.
+
+struct TreeCommitParams {
+    uint4* k_cache;
+    uint4* v_cache;
+    const int32_t* block_tables;
+    const int32_t* context_lens;
+    const int32_t* accepted;
+    const int32_t* accepted_lens;
+    int32_t* new_context_lens;  // nullable
+    int32_t* err_flag;
+    int max_blocks_per_seq;
+    int tree_len;
+    int max_accepted;
+    int num_blocks;
+    int block_size;
+    int num_kv_heads;
+    int head_vecs;              // 16-byte vectors of a head row
+    int cap;
+    bool hnd;
+};
+
+constexpr int kCommitThreads = 128;
+constexpr int kMoveBatch = 8;
+
+__global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const TreeCommitParams p) {
+    // cache rows (slots) of the path's sources and destinations
+    __shared__ int64_t s_src[PKV_MAX_TREE_LEN];
+    __shared__ int64_t s_dst[PKV_MAX_TREE_LEN];
+    __shared__ int s_bad;
+    ptx::launch_dependents();
+    ptx::grid_dependency_wait();
+    const int b = blockIdx.y;
+    const int tid = threadIdx.x;
+    if (tid == 0) s_bad = 0;
+    const int n_raw = __ldg(p.context_lens + b);
+    const int a_raw = __ldg(p.accepted_lens + b);
+    const int base = max(0, clamped_len(n_raw, p.cap) - p.tree_len);
+    const bool n_ok = n_raw >= p.tree_len && n_raw <= p.cap;
+    const bool a_ok = a_raw >= 0 && a_raw <= min(p.max_accepted, p.tree_len);
+    const int a = n_ok && a_ok ? a_raw : 0;
+    __syncthreads();
+    int bad = 0;
+    if (!n_ok && n_raw != 0) bad |= PKV_EFLAG_CONTEXT_LEN;
+    if (n_raw != 0 && !a_ok) bad |= PKV_EFLAG_TREE;
+    const int32_t* path = p.accepted + (int64_t)b * p.max_accepted;
+    const int32_t* table = p.block_tables + (int64_t)b * p.max_blocks_per_seq;
+    for (int j = tid; j < a; j += kCommitThreads) {
+        const int node = __ldg(path + j);
+        const int before = j > 0 ? __ldg(path + j - 1) : -1;
+        if (node <= before || node < 0 || node >= p.tree_len) {
+            bad |= PKV_EFLAG_TREE;
+            continue;
+        }
+        const int from = base + node, to = base + j;
+        const int sb = __ldg(table + from / p.block_size), db = __ldg(table + to / p.block_size);
+        if (sb < 0 || sb >= p.num_blocks || db < 0 || db >= p.num_blocks) {
+            bad |= PKV_EFLAG_BLOCK_ID;
+            continue;
+        }
+        s_src[j] = (int64_t)sb * p.block_size + from % p.block_size;
+        s_dst[j] = (int64_t)db * p.block_size + to % p.block_size;
+    }
+    if (bad) atomicOr(&s_bad, bad);
+    __syncthreads();
+    const int fault = s_bad;
+    if (blockIdx.x == 0 && tid == 0) {
+        if (fault) flag_error(p.err_flag, fault);
+        if (p.new_context_lens != nullptr) p.new_context_lens[b] = base + (fault ? 0 : a);
+    }
+    if (fault) return;
+
+    const int row_vecs = p.num_kv_heads * p.head_vecs;
+    const int c = blockIdx.x * kCommitThreads + tid;  // column of K, then of V
+    if (c >= 2 * row_vecs) return;
+    uint4* cache = c < row_vecs ? p.k_cache : p.v_cache;
+    const int col = c < row_vecs ? c : c - row_vecs;
+    const int head = col / p.head_vecs;
+    auto vec = [&](int64_t slot) -> uint4* {
+        if (!p.hnd) return cache + slot * row_vecs + col;
+        const int64_t blk = slot / p.block_size;
+        return cache + ((blk * p.num_kv_heads + head) * p.block_size + slot - blk * p.block_size) *
+                           p.head_vecs + (col - head * p.head_vecs);
+    };
+    for (int j0 = 0; j0 < a; j0 += kMoveBatch) {
+        uint4 x[kMoveBatch];
+#pragma unroll
+        for (int u = 0; u < kMoveBatch; ++u)
+            if (j0 + u < a && s_src[j0 + u] != s_dst[j0 + u]) x[u] = *vec(s_src[j0 + u]);
+#pragma unroll
+        for (int u = 0; u < kMoveBatch; ++u)
+            if (j0 + u < a && s_src[j0 + u] != s_dst[j0 + u]) *vec(s_dst[j0 + u]) = x[u];
+    }
+}
+
+template <typename P>
+static pkv_status launch_pdl(void (*kern)(const P), const P& p, dim3 grid, int threads,
+                             void* stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = (cudaStream_t)stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) {
+        cudaGetLastError();
+        return PKV_ERR_CUDA;
+    }
+    return PKV_OK;
+}
+
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" pkv_status pkv_tree_plan(int32_t* tree_mask, int32_t* positions, int64_t* slot_mapping,
+                                    const int32_t* parents, const int32_t* context_lens,
+                                    const int32_t* block_tables, int max_blocks_per_seq,
+                                    int max_context_len, int num_seqs, int tree_len,
+                                    int num_blocks, int block_size, int32_t* err_flag,
+                                    void* stream) {
+    if (num_seqs < 0 || tree_len <= 0 || max_blocks_per_seq <= 0 || max_context_len < 0 ||
+        num_blocks <= 0 || block_size <= 0)
+        return PKV_ERR_INVALID_ARG;
+    if (tree_len > PKV_MAX_TREE_LEN || !supported_block_size(block_size) ||
+        (int64_t)max_blocks_per_seq * block_size > INT_MAX)
+        return PKV_ERR_UNSUPPORTED;
+    if (num_seqs == 0) return PKV_OK;
+    if (!tree_mask || !positions || !slot_mapping || !parents || !context_lens || !block_tables)
+        return PKV_ERR_INVALID_ARG;
+    if (((reinterpret_cast<uintptr_t>(tree_mask) | reinterpret_cast<uintptr_t>(positions) |
+          reinterpret_cast<uintptr_t>(parents) | reinterpret_cast<uintptr_t>(context_lens) |
+          reinterpret_cast<uintptr_t>(block_tables)) & 3u) ||
+        (reinterpret_cast<uintptr_t>(slot_mapping) & 7u))
+        return PKV_ERR_INVALID_ARG;
+    TreePlanParams p = {};
+    p.tree_mask = tree_mask;
+    p.positions = positions;
+    p.slot_mapping = slot_mapping;
+    p.parents = parents;
+    p.context_lens = context_lens;
+    p.block_tables = block_tables;
+    p.err_flag = err_flag;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    p.cap = std::min(max_blocks_per_seq * block_size, max_context_len);
+    p.tree_len = tree_len;
+    p.num_blocks = num_blocks;
+    p.block_size = block_size;
+    return launch_pdl(tree_plan_kernel, p, dim3(num_seqs), (tree_len + 31) / 32 * 32, stream);
+}
+
+extern "C" pkv_status pkv_tree_commit(void* k_cache, void* v_cache, const int32_t* block_tables,
+                                      int max_blocks_per_seq, const int32_t* context_lens,
+                                      int tree_len, const int32_t* accepted,
+                                      const int32_t* accepted_lens, int max_accepted,
+                                      int32_t* new_context_lens, int num_seqs, int num_blocks,
+                                      int block_size, int num_kv_heads, int head_dim,
+                                      pkv_dtype dtype, int32_t* err_flag, void* stream) {
+    const bool hnd = take_layout(dtype);
+    if (num_seqs < 0 || tree_len <= 0 || max_accepted <= 0 || max_blocks_per_seq <= 0 ||
+        num_blocks <= 0 || block_size <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
+        (dtype != PKV_FP16 && dtype != PKV_BF16))
+        return PKV_ERR_INVALID_ARG;
+    if (tree_len > PKV_MAX_TREE_LEN || !supported_block_size(block_size) ||
+        !supported_head_dim(head_dim) || num_seqs > 65535 || num_kv_heads > 65535 ||
+        (int64_t)max_blocks_per_seq * block_size > INT_MAX)
+        return PKV_ERR_UNSUPPORTED;
+    if (num_seqs == 0) return PKV_OK;
+    if (!k_cache || !v_cache || !block_tables || !context_lens || !accepted || !accepted_lens)
+        return PKV_ERR_INVALID_ARG;
+    if (!aligned16(k_cache) || !aligned16(v_cache) ||
+        ((reinterpret_cast<uintptr_t>(block_tables) | reinterpret_cast<uintptr_t>(context_lens) |
+          reinterpret_cast<uintptr_t>(accepted) | reinterpret_cast<uintptr_t>(accepted_lens) |
+          reinterpret_cast<uintptr_t>(new_context_lens)) & 3u))
+        return PKV_ERR_INVALID_ARG;
+    // every CTA of a sequence reads its length: the new one goes elsewhere
+    if (new_context_lens != nullptr && new_context_lens < context_lens + num_seqs &&
+        context_lens < new_context_lens + num_seqs)
+        return PKV_ERR_INVALID_ARG;
+    TreeCommitParams p = {};
+    p.k_cache = static_cast<uint4*>(k_cache);
+    p.v_cache = static_cast<uint4*>(v_cache);
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.accepted = accepted;
+    p.accepted_lens = accepted_lens;
+    p.new_context_lens = new_context_lens;
+    p.err_flag = err_flag;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    p.tree_len = tree_len;
+    p.max_accepted = max_accepted;
+    p.num_blocks = num_blocks;
+    p.block_size = block_size;
+    p.num_kv_heads = num_kv_heads;
+    p.head_vecs = head_dim / 8;
+    p.cap = max_blocks_per_seq * block_size;
+    p.hnd = hnd;
+    const int cols = 2 * num_kv_heads * p.head_vecs;
+    return launch_pdl(tree_commit_kernel, p,
+                      dim3((cols + kCommitThreads - 1) / kCommitThreads, num_seqs), kCommitThreads,
+                      stream);
+}
