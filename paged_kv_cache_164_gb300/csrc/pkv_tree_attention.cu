@@ -1,13 +1,40 @@
-// Attention of a tree's drafted nodes over a paged KV cache.
+// Attention of a tree's drafted nodes over a paged KV cache (tcgen05).
 //
 // The math: node i of sequence b attends to the committed positions
 // t < base = n - tree_len and to the nodes j (position base + j) of its mask:
 //     s_t = scale * <q_i, K_t>,  out_i = softmax(s) V      over those t
-// with the online softmax (running maximum m, sum l, accumulator O; one
-// division at the end).
+// The (node, query head) rows of one KV head form a dense matrix that meets
+// every cached token once, so the two products run on the tensor cores
+// (tcgen05, fp32 accumulators in tensor memory), with the online softmax
+// between them: running reference m, sum l and accumulator O per row, one
+// division at the end.
+//
+// Tiles: 128 rows x 128 tokens.  Two softmax warpgroups, one thread per row,
+// each with its own S and O in tensor memory (all 512 columns):
+//   S_w = Q K^T     tcgen05.mma 128 x 128 x D, Q and K from shared memory
+//   softmax         a thread reads its row of S, writes P over it
+//   O_w += P V      P from tensor memory, as hi + lo 16-bit terms (a single
+//                   16-bit P would cost the outputs of short contexts half
+//                   their precision), V from shared memory
+// While one warpgroup is at its softmax, the tensor cores work for the other.
+// ROWS (more than 128 rows per KV head): the warpgroups take 128 rows each of
+// the same tokens, so 256 rows meet a K/V tile that was read once.  Otherwise
+// they take the same rows and every other tile, and meet at the end.
+// Warp 8 streams K and V tiles by TMA through the block table into a ring of
+// tile slots; one thread of warp 9 issues all the products.
+//
+// Work: the (sequence, KV head, row block) units' tiles lie on one line, and
+// each of the persistent CTAs (one an SM) takes an equal stretch of it, so
+// ragged contexts and few long ones fill the SMs alike.  A unit inside one
+// stretch is written to the output at once; one that is cut leaves a partial
+// (normalised O and its log-sum-exp) per CTA, at most two a CTA, and
+// tree_merge_kernel joins them.
+//
+// Every wait is bounded, as in the decode kernels.
 #include <algorithm>
 #include <climits>
 #include <cmath>
+#include <mutex>
 
 #include "pkv_common.cuh"
 #include "pkv_device.cuh"
@@ -24,104 +51,880 @@ struct TreeParams {
     const int32_t* tree_mask;
     int64_t mask_stride;
     int32_t* err_flag;
+    int2* unit_ctas;     // per unit: the first and last CTA of its tiles; null: no unit is cut
+    float* partial_o;    // [2 * CTAs][rows per unit][D]
+    float* partial_lse;  // [2 * CTAs][rows per unit], base 2
     int max_blocks_per_seq;
     int num_blocks;
     int block_size;
+    int num_seqs;
     int num_q_heads;
     int num_kv_heads;
+    int group;           // query heads per KV head
     int tree_len;
     int cap;
+    int row_blocks;      // units per (sequence, KV head)
     bool hnd;
-    float scale_log2;
+    float scale_log2;    // |scale| * log2(e) (of 1 where scale is 0)
+    float scale_sign;    // 1, -1 or 0
 };
 
-constexpr int kTreeWarps = 4;
+constexpr int kTreeTile = 128;                     // rows (MMA M) and tokens of a tile
+constexpr int kTreeSoftmaxWarps = 8;               // two warpgroups
+constexpr int kTreeTmaWarp = kTreeSoftmaxWarps;
+constexpr int kTreeMmaWarp = kTreeSoftmaxWarps + 1;
+constexpr int kTreeThreads = (kTreeSoftmaxWarps + 4) * 32;  // two warps fill the third warpgroup
+// Registers: a softmax thread holds a row of S (128 values), which does not fit
+// the 168 a thread that 384 threads get at launch; the third warpgroup hands
+// over what it does not need (2 x 216 + 72 = 3 x 168).
+constexpr int kTreeLaunchRegs = 168, kTreeSoftmaxRegs = 216, kTreeOtherRegs = 72;
+static_assert(2 * kTreeSoftmaxRegs + kTreeOtherRegs <= 3 * kTreeLaunchRegs, "register shares");
+// Scores may exceed a row's reference by this much (base 2) before it moves: P
+// stays below 2^8, and O / l and the log-sum-exp come out the same.
+constexpr float kTreeLazyLog2 = 8.f;
+constexpr int kTreeBoxes = kTreeTile / kStageTokens;  // TMA boxes along a tile's tokens
 
-// One CTA per (query head, node, sequence): its warps take every fourth
-// token, D / 32 dims a lane, and meet at the end.
-template <typename T, int D>
-__global__ void __launch_bounds__(kTreeWarps * 32) tree_attention_kernel(const TreeParams p) {
-    constexpr int E = D / 32;
-    __shared__ float s_o[kTreeWarps][D];
-    __shared__ float s_m[kTreeWarps], s_l[kTreeWarps];
-    ptx::launch_dependents();
-    ptx::grid_dependency_wait();
-    const int h = blockIdx.x, i = blockIdx.y, b = blockIdx.z;
-    const int g = h / (p.num_q_heads / p.num_kv_heads);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int n_raw = __ldg(p.context_lens + b);
-    if (h == 0 && i == 0 && threadIdx.x == 0 &&
-        (n_raw < 0 || n_raw > p.cap || (n_raw != 0 && n_raw < p.tree_len)))
-        flag_error(p.err_flag, PKV_EFLAG_CONTEXT_LEN);
-    const int n = clamped_len(n_raw, p.cap);
-    const int base = n - p.tree_len;
-    const int64_t row = ((int64_t)b * p.tree_len + i) * p.num_q_heads + h;
-    float q[E], o[E];
-    load_as_float<T, E>(static_cast<const T*>(p.q) + row * D + lane * E, q);
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = 0.f;
-    float m = -INFINITY, l = 0.f;
-    const int32_t* mask = p.tree_mask + b * p.mask_stride + (int64_t)i * ((p.tree_len + 31) / 32);
-    for (int t = warp; t < n; t += kTreeWarps) {
-        const int j = t - base;
-        if (j >= 0 && !((__ldg(mask + (j >> 5)) >> (j & 31)) & 1)) continue;
-        const int blk = __ldg(p.block_tables + (int64_t)b * p.max_blocks_per_seq + t / p.block_size);
-        if (blk < 0 || blk >= p.num_blocks) {
-            if (lane == 0) flag_error(p.err_flag, PKV_EFLAG_BLOCK_ID);
-            continue;
-        }
-        const int off = t % p.block_size;
-        const int64_t at =
-            (p.hnd ? ((int64_t)blk * p.num_kv_heads + g) * p.block_size + off
-                   : ((int64_t)blk * p.block_size + off) * p.num_kv_heads + g) * D + lane * E;
-        float k[E], v[E];
-        load_as_float<T, E>(static_cast<const T*>(p.k_cache) + at, k);
-        load_as_float<T, E>(static_cast<const T*>(p.v_cache) + at, v);
-        float s = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) s = fmaf(q[e], k[e], s);
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-        s *= p.scale_log2;
-        const float mn = fmaxf(m, s);
-        const float alpha = exp2f(m - mn), w = exp2f(s - mn);
-        m = mn;
-        l = l * alpha + w;
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf(w, v[e], o[e] * alpha);
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = o[e];
-    if (lane == 0) {
-        s_m[warp] = m;
-        s_l[warp] = l;
-    }
-    __syncthreads();
-    float mx = -INFINITY;
-    for (int w = 0; w < kTreeWarps; ++w) mx = fmaxf(mx, s_m[w]);
-    for (int d = threadIdx.x; d < D; d += kTreeWarps * 32) {
-        float num = 0.f, den = 0.f;
-        for (int w = 0; w < kTreeWarps; ++w) {
-            const float f = s_m[w] == -INFINITY ? 0.f : exp2f(s_m[w] - mx);
-            if (f != 0.f) {
-                num = fmaf(f, s_o[w][d], num);
-                den = fmaf(f, s_l[w], den);
+template <int D>
+struct TreeTileCfg {
+    static constexpr int kRegions = D / 64;                    // 128-byte column blocks
+    static constexpr int kRegionBytes = kTreeTile * 128;
+    static constexpr int kSlotBytes = kRegions * kRegionBytes;  // K or V of a tile; Q of 128 rows
+    static constexpr int kSlots = D == 128 ? 5 : 8;
+    static constexpr int kQBytes = 2 * kSlotBytes;
+    static constexpr int kXchBytes = 2 * kTreeTile * 8;         // (m, l) of each half and row
+    // full[slots], empty[slots], s_full[2], p_ready[2], o_done[2], q_ready, met, o_free, drain
+    static constexpr int kBarriers = 2 * kSlots + 10;
+    static constexpr int kSmemBytes =
+        kQBytes + kSlots * kSlotBytes + kXchBytes + kBarriers * 8 + 256;
+    static constexpr uint32_t kColO = 2 * kTreeTile;  // S_0, S_1, then O_0, O_1
+    static_assert(kColO + 2 * D <= 512, "tensor memory layout");
+    static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
+};
+
+__host__ __device__ inline int tree_tiles(int n) {
+    return n <= 0 ? 1 : (n + kTreeTile - 1) / kTreeTile;  // an empty context has a tile of nothing
+}
+
+// A stretch of one unit's tiles.
+struct TreeSeg {
+    int b, g, rb;        // sequence, KV head, row block
+    int n;               // context length
+    int tile0, tiles;    // first tile and tiles of the stretch
+    int unit_tiles;
+};
+
+// Walks a CTA's stretch of the line of tiles (sequence, KV head, row block,
+// tile; the last fastest).  Every thread that takes part walks it by itself.
+struct TreeWalk {
+    int64_t at, end;
+    int b, unit, tile, n;
+
+    __device__ __forceinline__ bool next(const TreeParams& p, TreeSeg& s) {
+        if (at >= end) return false;
+        s.b = b;
+        s.g = unit / p.row_blocks;
+        s.rb = unit - s.g * p.row_blocks;
+        s.n = n;
+        s.unit_tiles = tree_tiles(n);
+        s.tile0 = tile;
+        s.tiles = (int)min((int64_t)(s.unit_tiles - tile), end - at);
+        at += s.tiles;
+        tile += s.tiles;
+        if (tile == s.unit_tiles) {
+            tile = 0;
+            if (++unit == p.num_kv_heads * p.row_blocks) {
+                unit = 0;
+                ++b;
+                if (at < end) n = clamped_len(__ldg(p.context_lens + b), p.cap);
             }
         }
-        static_cast<T*>(p.out)[row * D + d] = from_float(den == 0.f ? 0.f : num / den, T());
+        return true;
+    }
+};
+
+// K and V tiles of a stretch of nt tiles lie in the ring in the order in which
+// the products take them.  ROWS: K0 V0 K1 V1 ...; else both warpgroups' first
+// K tiles come first: K0 K1 V0 K2 V1 ... V(nt-1).
+template <bool ROWS>
+__device__ __forceinline__ int k_place(int j) { return ROWS ? 2 * j : (j == 0 ? 0 : 2 * j - 1); }
+template <bool ROWS>
+__device__ __forceinline__ int v_place(int j, int nt) {
+    return ROWS ? 2 * j + 1 : (j < nt - 1 ? 2 * j + 2 : 2 * nt - 1);
+}
+
+// Whether one of the two 16-bit values is an infinity or a NaN.
+__device__ __forceinline__ bool not_finite(uint16_t x, __nv_bfloat16) {
+    return (x & 0x7f80u) == 0x7f80u;
+}
+__device__ __forceinline__ bool not_finite(uint16_t x, __half) { return (x & 0x7c00u) == 0x7c00u; }
+
+template <typename T, int D, bool ROWS>
+__global__ void __launch_bounds__(kTreeThreads, 1)
+tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v, const TreeParams p) {
+    using Cfg = TreeTileCfg<D>;
+    constexpr int R = Cfg::kRegions;
+    constexpr int NS = Cfg::kSlots;
+    constexpr int TT = kTreeTile;
+    constexpr int kUnitRows = ROWS ? 2 * TT : TT;
+
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t* sq = smem;  // two Q tiles [region][128 rows][128 B], swizzled
+    uint8_t* ring = sq + Cfg::kQBytes;
+    float2* xch = reinterpret_cast<float2*>(ring + NS * Cfg::kSlotBytes);
+    uint64_t* full_bar = reinterpret_cast<uint64_t*>(ring + NS * Cfg::kSlotBytes + Cfg::kXchBytes);
+    uint64_t* empty_bar = full_bar + NS;
+    uint64_t* s_full = empty_bar + NS;  // [2]
+    uint64_t* p_ready = s_full + 2;     // [2]
+    uint64_t* o_done = p_ready + 2;     // [2]: a stretch's last O_w += P V is done
+    uint64_t* q_ready = o_done + 2;
+    uint64_t* met = q_ready + 1;        // both warpgroups are through the stretch (not ROWS)
+    uint64_t* o_free = met + 1;         // both have read O_0 and O_1 (not ROWS)
+    uint64_t* drain = o_free + 1;
+    int* words = reinterpret_cast<int*>(full_bar + Cfg::kBarriers);
+    volatile int* abort_flag = words;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(words + 1);
+    int* s_start = words + 2;            // sequence and (two words) its first tile on the line
+    volatile int* s_bad = words + 6;     // [4]: 1 + the stretch (mod 4 its place) with a bad V value
+    int* s_scan = words + 10;            // [12]
+
+    const int tid = threadIdx.x;
+    const int warp = tid >> 5;
+    const int lane = tid & 31;
+    const int bs = p.block_size;
+    const int bs_shift = __ffs(bs) - 1;
+    const int rows = p.tree_len * p.group;
+
+    ptx::launch_dependents();
+    if (tid == 0) {
+        for (int i = 0; i < NS; ++i) {
+            ptx::mbar_init(ptx::smem_addr(&full_bar[i]), 1);
+            ptx::mbar_init(ptx::smem_addr(&empty_bar[i]), 1);
+        }
+        for (int w = 0; w < 2; ++w) {
+            ptx::mbar_init(ptx::smem_addr(&s_full[w]), 1);
+            ptx::mbar_init(ptx::smem_addr(&p_ready[w]), TT);
+            ptx::mbar_init(ptx::smem_addr(&o_done[w]), 1);
+        }
+        ptx::mbar_init(ptx::smem_addr(q_ready), 2 * TT);
+        ptx::mbar_init(ptx::smem_addr(met), 2 * TT);
+        ptx::mbar_init(ptx::smem_addr(o_free), 2 * TT);
+        ptx::mbar_init(ptx::smem_addr(drain), 1);
+        *abort_flag = 0;
+        for (int i = 0; i < 4; ++i) s_bad[i] = 0;
+        ptx::fence_barrier_init();
+        ptx::prefetch_tensormap(&tm_k);
+        ptx::prefetch_tensormap(&tm_v);
+    }
+    if (warp == kTreeMmaWarp) {
+        ptx::tmem_alloc(ptx::smem_addr(tmem_slot), 512);
+        ptx::tmem_relinquish_alloc_permit();
+    }
+#ifdef PKV_DEBUG
+    poison_smem(ring, NS * Cfg::kSlotBytes, tid, kTreeThreads);
+#endif
+    ptx::grid_dependency_wait();
+
+    // The line of tiles: a thread sums the tiles of a run of sequences, a scan
+    // places the runs, and the thread whose run holds this CTA's first tile
+    // finds its sequence.
+    const int per = (p.num_seqs + kTreeThreads - 1) / kTreeThreads;
+    const int b_lo = min(p.num_seqs, tid * per), b_hi = min(p.num_seqs, b_lo + per);
+    int mine = 0;  // at most INT_MAX / 128 tiles a sequence, 65535 sequences: the host checks
+    for (int b = b_lo; b < b_hi; ++b)
+        mine += tree_tiles(clamped_len(__ldg(p.context_lens + b), p.cap));
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) s_scan[warp] = incl;
+    ptx::tc_fence_before_sync();
+    __syncthreads();
+    ptx::tc_fence_after_sync();
+    int total = 0, before = incl - mine;
+    for (int w = 0; w < kTreeThreads / 32; ++w) {
+        if (w < warp) before += s_scan[w];
+        total += s_scan[w];
+    }
+    const int units = p.num_kv_heads * p.row_blocks;
+    const int64_t line = (int64_t)total * units;
+    const int64_t ctas = min((int64_t)gridDim.x, line);  // with a tile at least; the rest idle
+    const int64_t start = min((int64_t)blockIdx.x, ctas) * line / ctas;
+    const int64_t stop = min((int64_t)blockIdx.x + 1, ctas) * line / ctas;
+    if (start >= (int64_t)before * units && start < (int64_t)(before + mine) * units) {
+        int b = b_lo;
+        int64_t first = (int64_t)before * units;
+        while (true) {
+            const int64_t next =
+                first + (int64_t)units * tree_tiles(clamped_len(__ldg(p.context_lens + b), p.cap));
+            if (start < next) break;
+            first = next;
+            ++b;
+        }
+        s_start[0] = b;
+        s_start[1] = (int)(start - first);  // tiles into the sequence's part of the line
+    }
+    __syncthreads();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t ring_addr = ptx::smem_addr(ring);
+    const uint32_t q_addr = ptx::smem_addr(sq);
+
+    TreeWalk walk;
+    walk.at = start;
+    walk.end = stop;
+    if (start < stop) {
+        walk.b = s_start[0];
+        walk.n = clamped_len(__ldg(p.context_lens + walk.b), p.cap);
+        const int tiles = tree_tiles(walk.n);
+        walk.unit = s_start[1] / tiles;
+        walk.tile = s_start[1] - walk.unit * tiles;
+    }
+    TreeSeg seg;
+
+    if (warp >= kTreeSoftmaxWarps) {
+        ptx::reg_dec<kTreeOtherRegs>();
+        if (warp == kTreeTmaWarp) {
+            // ------------------------------------------------------------ producer
+            // A lane issues one box (16 tokens x 64 dims) of the tile's K, then of V.
+            const uint64_t policy =
+                p.row_blocks > 1 ? ptx::l2_policy_evict_last() : ptx::l2_policy_evict_first();
+            const int bx = lane / R, rr = lane % R;
+            const bool loads = lane < kTreeBoxes * R;
+            int place0 = 0;  // places of the stretches before this one
+            int issued = 0;
+            bool ok = true;
+            while (ok && walk.next(p, seg)) {
+                const int32_t* table = p.block_tables + (int64_t)seg.b * p.max_blocks_per_seq;
+                auto box_block = [&](int j) {
+                    const int tok = (seg.tile0 + j) * TT + bx * kStageTokens;
+                    if (!loads || j >= seg.tiles || tok >= seg.n) return -1;
+                    const int blk = __ldg(table + (tok >> bs_shift));
+                    if (blk < 0 || blk >= p.num_blocks) {
+                        flag_error(p.err_flag, PKV_EFLAG_BLOCK_ID);
+                        return -1;
+                    }
+                    return blk;
+                };
+                auto load = [&](const CUtensorMap* map, int place, int j, int blk) {
+                    const int at = place0 + place;
+                    const int slot = at % NS;
+                    if (at >= NS && !warp_wait_phase(ptx::smem_addr(&empty_bar[slot]),
+                                                     ((at / NS) - 1) & 1, abort_flag, p.err_flag))
+                        return false;
+#ifdef PKV_DEBUG
+                    if (at >= NS) {
+                        ptx::tc_fence_after_sync();
+                        poison_smem(ring + slot * Cfg::kSlotBytes, Cfg::kSlotBytes, lane, 32);
+                        __syncwarp();
+                    }
+#endif
+                    const uint32_t fb = ptx::smem_addr(&full_bar[slot]);
+                    const uint32_t boxes = __ballot_sync(0xffffffffu, blk >= 0);
+                    if (lane == 0) {
+                        if (boxes == 0)
+                            ptx::mbar_arrive(fb);  // every token of the tile is masked
+                        else
+                            ptx::mbar_arrive_expect_tx(fb, __popc(boxes) * kStageTokens * 128);
+                    }
+                    __syncwarp();
+                    if (blk >= 0) {
+                        const int tok = (seg.tile0 + j) * TT + bx * kStageTokens;
+                        load_kv_box(ring_addr + slot * Cfg::kSlotBytes + rr * Cfg::kRegionBytes +
+                                        bx * kStageTokens * 128,
+                                    map, fb, rr * 64, seg.g, tok & (bs - 1), blk, p.hnd, policy);
+                    }
+                    issued = max(issued, at + 1);
+                    return true;
+                };
+                int blk = box_block(0), blk_next = box_block(1);
+                ok = load(&tm_k, k_place<ROWS>(0), 0, blk);
+                for (int j = 0; j < seg.tiles && ok; ++j) {
+                    const int blk_after = box_block(j + 2);
+                    const bool more = j + 1 < seg.tiles;
+                    if (!ROWS && more) ok = load(&tm_k, k_place<ROWS>(j + 1), j + 1, blk_next);
+                    if (ok) ok = load(&tm_v, v_place<ROWS>(j, seg.tiles), j, blk);
+                    if (ROWS && more && ok) ok = load(&tm_k, k_place<ROWS>(j + 1), j + 1, blk_next);
+                    blk = blk_next;
+                    blk_next = blk_after;
+                }
+                place0 += 2 * seg.tiles;
+            }
+            if (lane == 0 && *abort_flag) {
+                // wait (bounded) for the copies in flight before leaving
+                for (int at = max(0, issued - NS); at < issued; ++at) {
+                    const uint32_t fb = ptx::smem_addr(&full_bar[at % NS]);
+                    const uint64_t t0 = ptx::globaltimer();
+                    while (!ptx::mbar_try_wait(fb, (at / NS) & 1) &&
+                           ptx::globaltimer() - t0 < kWaitLimitNs) {
+                    }
+                }
+            }
+        } else if (warp == kTreeMmaWarp) {
+            // ------------------------------------------------------------ MMA issuer
+            if (lane == 0) {
+                constexpr uint32_t fmt = F16Format<T>::value;
+                constexpr uint32_t idesc_s = mma_idesc(fmt, TT, TT, false);
+                constexpr uint32_t idesc_o = mma_idesc(fmt, TT, D, true);
+                int place0 = 0, nseg = 0;
+                int p_count[2] = {0, 0};
+                bool ok = true;
+                while (ok && walk.next(p, seg)) {
+                    const int nt = seg.tiles;
+                    // step x: ROWS: warpgroup x % 2 at tile x / 2; else at tile x
+                    const int steps = ROWS ? 2 * nt : nt;
+                    auto wait = [&](uint64_t* bar, int parity) {
+                        return wait_phase(ptx::smem_addr(bar), parity & 1, abort_flag, p.err_flag);
+                    };
+                    auto issue_s = [&](int x) {
+                        const int w = x & 1, j = ROWS ? x >> 1 : x;
+                        const int at = place0 + k_place<ROWS>(j);
+                        const int slot = at % NS;
+                        if (!wait(&full_bar[slot], at / NS)) return false;
+                        ptx::tc_fence_after_sync();
+                        const uint32_t kb = ring_addr + slot * Cfg::kSlotBytes;
+                        const uint32_t qb = q_addr + (ROWS ? w : nseg & 1) * Cfg::kSlotBytes;
+#pragma unroll
+                        for (int ks = 0; ks < D / 16; ++ks) {
+                            const uint32_t off = (ks / 4) * Cfg::kRegionBytes + (ks % 4) * 32;
+                            ptx::tc_mma_f16(tmem + w * TT, ptx::smem_desc_sw128(qb + off, 16, 1024),
+                                            ptx::smem_desc_sw128(kb + off, 16, 1024), idesc_s,
+                                            ks > 0 ? 1u : 0u);
+                        }
+                        ptx::tc_commit(ptx::smem_addr(&s_full[w]));
+                        if (!ROWS || w == 1) ptx::tc_commit(ptx::smem_addr(&empty_bar[slot]));
+                        return true;
+                    };
+                    auto issue_pv = [&](int x) {
+                        const int w = x & 1, j = ROWS ? x >> 1 : x;
+                        const int at = place0 + v_place<ROWS>(j, nt);
+                        const int slot = at % NS;
+                        if (!wait(&full_bar[slot], at / NS) || !wait(&p_ready[w], p_count[w]++))
+                            return false;
+                        ptx::tc_fence_after_sync();
+                        const uint32_t vb = ring_addr + slot * Cfg::kSlotBytes;
+                        const uint32_t acc = tmem + Cfg::kColO + w * D;
+#pragma unroll
+                        for (int kt = 0; kt < TT / 16; ++kt) {
+                            // tokens 16 kt ..: of each 32 tokens of P, 16 columns of hi
+                            // pairs, then 16 of lo pairs
+                            const uint32_t a = tmem + w * TT + (kt / 2) * 32 + (kt % 2) * 8;
+                            const uint64_t v = ptx::smem_desc_sw128(vb + kt * 16 * 128,
+                                                                    Cfg::kRegionBytes, 1024);
+                            ptx::tc_mma_f16_ts(acc, a, v, idesc_o, (x >= 2 || kt > 0) ? 1u : 0u);
+                            ptx::tc_mma_f16_ts(acc, a + 16, v, idesc_o, 1u);
+                        }
+                        if (!ROWS || w == 1) ptx::tc_commit(ptx::smem_addr(&empty_bar[slot]));
+                        if (x + 2 >= steps) ptx::tc_commit(ptx::smem_addr(&o_done[w]));
+                        return true;
+                    };
+                    // The tensor core runs the products in the order of their issue:
+                    // S_w(next) over P_w comes after the O_w += P_w V that reads it.
+                    ok = wait(q_ready, nseg) && issue_s(0) && (steps < 2 || issue_s(1));
+                    for (int x = 0; x < steps && ok; ++x)
+                        ok = issue_pv(x) && (x + 2 >= steps || issue_s(x + 2));
+                    place0 += 2 * nt;
+                    ++nseg;
+                }
+                // every product has completed before the tensor memory is released
+                ptx::tc_commit(ptx::smem_addr(drain));
+                const uint64_t t0 = ptx::globaltimer();
+                while (!ptx::mbar_try_wait(ptx::smem_addr(drain), 0) &&
+                       ptx::globaltimer() - t0 < kWaitLimitNs) {
+                }
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ softmax rows
+        ptx::reg_inc<kTreeSoftmaxRegs>();
+        const int wg = warp / 4;                  // warpgroup
+        const int srow = 32 * (warp % 4) + lane;  // row of the tile = tensor-memory lane
+        const uint32_t lane_base = (uint32_t)(32 * (warp % 4)) << 16;
+        const uint32_t s_col = tmem + lane_base + wg * TT;
+        const int urow = ROWS ? wg * TT + srow : srow;  // row of the unit
+        int place0 = 0, nseg = 0, steps_done = 0, o_count = 0;
+        bool ok = true;
+
+        // Query row r of the unit: node r / group, head g * group + r % group.
+        auto row_of = [&](const TreeSeg& s, int& node, int64_t& orow) {
+            const int r = s.rb * kUnitRows + urow;
+            const bool live = r < rows;
+            node = live ? r / p.group : 0;
+            orow = ((int64_t)s.b * p.tree_len + node) * p.num_q_heads + s.g * p.group +
+                   (live ? r - node * p.group : 0);
+            return live;
+        };
+        // This thread's part of its row of Q (not ROWS: half of it) into the Q
+        // tile of stretch `which`, 16-byte chunk c of a 128-byte row at c ^ (row % 8).
+        auto load_q = [&](const TreeSeg& s, int which) {
+            constexpr int QV = ROWS ? D / 8 : D / 16;
+            int node;
+            int64_t orow;
+            const bool live = row_of(s, node, orow);
+            const int c0 = ROWS ? 0 : wg * QV;
+            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + orow * D);
+            uint8_t* dst = sq + (ROWS ? wg : which & 1) * Cfg::kSlotBytes + srow * 128;
+            uint4 x[QV];
+#pragma unroll
+            for (int k = 0; k < QV; ++k)
+                x[k] = live ? __ldg(src + c0 + k) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int k = 0; k < QV; ++k) {
+                const int c = c0 + k;
+                *reinterpret_cast<uint4*>(dst + (c / 8) * Cfg::kRegionBytes +
+                                          (((c % 8) ^ (srow & 7)) << 4)) = x[k];
+            }
+            ptx::fence_proxy_async_smem();
+            ptx::mbar_arrive(ptx::smem_addr(q_ready));
+        };
+
+        bool have = walk.next(p, seg);
+        if (have) load_q(seg, 0);
+        int64_t seg_at = start;  // the stretch's first tile on the line
+        while (have && ok) {
+            const TreeSeg s = seg;
+            const int base = s.n - p.tree_len;
+            int node;
+            int64_t orow;
+            const bool live = row_of(s, node, orow);
+            const bool warp_live = __any_sync(0xffffffffu, live);
+            if (s.tile0 == 0 && s.g == 0 && s.rb == 0 && tid == 0) {
+                const int n_raw = __ldg(p.context_lens + s.b);
+                if (n_raw < 0 || n_raw > p.cap || (n_raw != 0 && n_raw < p.tree_len))
+                    flag_error(p.err_flag, PKV_EFLAG_CONTEXT_LEN);
+            }
+            const int mask_words = (p.tree_len + 31) / 32;
+            const int32_t* mask = p.tree_mask + s.b * p.mask_stride + (int64_t)node * mask_words;
+            // bits of nodes jb .. jb + 31 (below 0: committed positions)
+            auto tree_bits = [&](int jb) -> uint32_t {
+                if (jb <= -32) return ~0u;
+                const int w = jb >> 5;
+                const uint32_t lo = w < 0 ? ~0u : w < mask_words ? (uint32_t)__ldg(mask + w) : 0u;
+                const uint32_t hi = w + 1 < 0 ? ~0u
+                                    : w + 1 < mask_words ? (uint32_t)__ldg(mask + w + 1)
+                                                         : 0u;
+                return __funnelshift_r(lo, hi, jb & 31);
+            };
+            const int32_t* table = p.block_tables + (int64_t)s.b * p.max_blocks_per_seq;
+            // lanes 0-7: whether box `lane` of tile j is there
+            auto box_there = [&](int j) {
+                const int tok = (s.tile0 + j) * TT + lane * kStageTokens;
+                if (lane >= kTreeBoxes || j >= s.tiles || tok >= s.n) return false;
+                const int blk = __ldg(table + (tok >> bs_shift));
+                return blk >= 0 && blk < p.num_blocks;
+            };
+
+            float m_ref = -INFINITY, l = 0.f;
+            constexpr int kStep = ROWS ? 1 : 2;
+            bool there = box_there(ROWS ? 0 : wg);
+            bool worked = false;
+            // not ROWS: both warpgroups read O_0, O_1 and the exchanged (m, l) of the
+            // stretch before; neither is written anew until both have
+            auto others_read = [&] {
+                return ROWS || nseg == 0 ||
+                       warp_wait_phase(ptx::smem_addr(o_free), (nseg - 1) & 1, abort_flag,
+                                       p.err_flag);
+            };
+            for (int j = ROWS ? 0 : wg; j < s.tiles; j += kStep) {
+                const uint32_t boxes = __ballot_sync(0xffffffffu, there);
+                there = box_there(j + kStep);
+                if (!warp_wait_phase(ptx::smem_addr(&s_full[wg]), steps_done & 1, abort_flag,
+                                     p.err_flag)) {
+                    ok = false;
+                    break;
+                }
+                ++steps_done;
+                ptx::tc_fence_after_sync();
+                const int t0 = (s.tile0 + j) * TT;
+                const bool whole = boxes == 0xffu && t0 + TT <= s.n;
+                const bool tree = t0 + TT > base;
+                if (warp_live) {
+                    uint32_t sv[TT];
+#pragma unroll
+                    for (int c = 0; c < TT / 32; ++c)
+                        ptx::tmem_ld32_async(s_col + c * 32,
+                                             *reinterpret_cast<uint32_t(*)[32]>(sv + c * 32));
+                    ptx::tmem_wait_ld();
+#pragma unroll
+                    for (int c = 0; c < TT / 32; ++c)
+                        ptx::tmem_loaded(*reinterpret_cast<uint32_t(*)[32]>(sv + c * 32));
+                    float sc[TT];
+#pragma unroll
+                    for (int i = 0; i < TT; ++i) sc[i] = __uint_as_float(sv[i]);
+                    if (p.scale_sign != 1.f) {
+#pragma unroll
+                        for (int i = 0; i < TT; ++i) sc[i] *= p.scale_sign;
+                    }
+                    if (!whole || tree) {
+#pragma unroll
+                        for (int c = 0; c < TT / 32; ++c) {
+                            const int tc = t0 + c * 32;
+                            const int left = s.n - tc;
+                            uint32_t allow = left >= 32 ? ~0u : left <= 0 ? 0u : (1u << left) - 1u;
+                            const uint32_t bb = boxes >> (2 * c);
+                            allow &= ((bb & 1u) ? 0x0000ffffu : 0u) | ((bb & 2u) ? 0xffff0000u : 0u);
+                            if (tree) allow &= tree_bits(tc - base);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (!((allow >> i) & 1u)) sc[c * 32 + i] = -INFINITY;
+                        }
+                    }
+                    float mx[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) mx[c] = sc[c];
+#pragma unroll
+                    for (int i = 4; i < TT; ++i) mx[i % 4] = fmaxf(mx[i % 4], sc[i]);
+                    const float top =
+                        fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+                    float alpha = 1.f;
+                    if (m_ref == -INFINITY) {
+                        m_ref = top;  // O and l are still zero for this row
+                    } else if (top > m_ref + kTreeLazyLog2) {
+                        alpha = ptx::ex2_approx(m_ref - top);
+                        m_ref = top;
+                    }
+                    const float ref = m_ref == -INFINITY ? 0.f : m_ref;
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int i = 0; i < TT; ++i) {
+                        sc[i] = ptx::ex2_approx(fmaf(sc[i], p.scale_log2, -ref));
+                        sum[i % 4] += sc[i];
+                    }
+                    l = fmaf(l, alpha, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+                    __syncwarp();
+                    // O_w is rescaled when a reference moved: S_w(j) complete implies
+                    // that O_w += P V of the tile before is
+                    if (__any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t ov[32];
+                            const uint32_t ta = tmem + lane_base + Cfg::kColO + wg * D + c * 32;
+                            ptx::tmem_ld32(ta, ov);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+                            ptx::tmem_st32(ta, ov);
+                        }
+                    }
+#pragma unroll
+                    for (int c = 0; c < TT / 32; ++c) {
+                        uint32_t pv[32];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            split_hi_lo(sc[c * 32 + 2 * e], sc[c * 32 + 2 * e + 1], pv[e],
+                                        pv[16 + e], T());
+                        ptx::tmem_st32_async(s_col + c * 32, pv);
+                    }
+                    ptx::tmem_wait_st();
+                }
+                __syncwarp();
+                if (!whole || tree) {
+                    // V rows of absent tokens hold stale bytes, and a node's V may hold
+                    // infinities or NaN that only some rows attend to: zeroed in
+                    // shared memory, so that 0 * V is 0; the rows that do attend to
+                    // such a value get it back at the end.
+                    const int at = place0 + v_place<ROWS>(j, s.tiles);
+                    if (!warp_wait_phase(ptx::smem_addr(&full_bar[at % NS]), (at / NS) & 1,
+                                         abort_flag, p.err_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* vst = ring + (at % NS) * Cfg::kSlotBytes;
+                    for (int idx = srow; idx < TT * R * 8; idx += TT) {
+                        const int row = idx / (R * 8), rem = idx - row * (R * 8);
+                        uint4* cell = reinterpret_cast<uint4*>(
+                            vst + (rem / 8) * Cfg::kRegionBytes + row * 128 + (rem % 8) * 16);
+                        if (t0 + row >= s.n || !((boxes >> (row / kStageTokens)) & 1u)) {
+                            *cell = make_uint4(0u, 0u, 0u, 0u);
+                        } else if (t0 + row >= base) {
+                            uint4 x = *cell;
+                            uint16_t* e = reinterpret_cast<uint16_t*>(&x);
+                            bool bad = false;
+#pragma unroll
+                            for (int u = 0; u < 8; ++u)
+                                if (not_finite(e[u], T())) {
+                                    e[u] = 0;
+                                    bad = true;
+                                }
+                            if (bad) {
+                                s_bad[nseg & 3] = nseg + 1;
+                                __threadfence_block();  // before the value is gone
+                                *cell = x;
+                            }
+                        }
+                    }
+                    ptx::fence_proxy_async_smem();
+                }
+                if (!worked && !others_read()) {
+                    ok = false;
+                    break;
+                }
+                worked = true;
+                ptx::tc_fence_before_sync();
+                ptx::mbar_arrive(ptx::smem_addr(&p_ready[wg]));
+            }
+            if (!ok) break;
+            place0 += 2 * s.tiles;
+
+            // the next stretch's Q, while the last products run (ROWS: S_w of this
+            // stretch is complete; else that Q tile belongs to the stretch before)
+            have = walk.next(p, seg);
+            if (have) load_q(seg, nseg + 1);
+
+            if (worked) {
+                if (!warp_wait_phase(ptx::smem_addr(&o_done[wg]), o_count & 1, abort_flag,
+                                     p.err_flag))
+                    break;
+                ++o_count;
+            }
+            float fa = 0.f, fb = 0.f, lse;  // out = O_0 fa + O_1 fb (ROWS: O_w fa)
+            bool worked_b = false;
+            if constexpr (ROWS) {
+                fa = l == 0.f ? 0.f : 1.f / l;
+                lse = l == 0.f ? -INFINITY : m_ref + log2f(l);
+            } else {
+                // both warpgroups are through: their halves of the softmax meet
+                if (!worked && !others_read()) break;
+                xch[wg * TT + srow] = make_float2(m_ref, l);
+                ptx::mbar_arrive(ptx::smem_addr(met));
+                if (!warp_wait_phase(ptx::smem_addr(met), nseg & 1, abort_flag, p.err_flag)) break;
+                const float2 ha = xch[srow], hb = xch[TT + srow];
+                const float mm = fmaxf(ha.x, hb.x);
+                worked_b = s.tiles > 1;
+                fa = ha.x == -INFINITY ? 0.f : ptx::ex2_approx(ha.x - mm);
+                fb = hb.x == -INFINITY ? 0.f : ptx::ex2_approx(hb.x - mm);
+                const float sum = ha.y * fa + hb.y * fb;
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                fa *= inv;
+                fb *= inv;
+                lse = sum == 0.f ? -INFINITY : mm + log2f(sum);
+            }
+            ptx::tc_fence_after_sync();
+            const bool direct = s.tiles == s.unit_tiles;
+            const int slot = 2 * blockIdx.x + (s.tile0 == 0 ? 1 : 0);
+            const bool bad_v = s_bad[nseg & 3] == nseg + 1;
+            if (p.unit_ctas != nullptr && s.tile0 == 0 && tid == 0) {
+                // the line's tile u belongs to CTA c when c * line < (u + 1) * CTAs
+                const int64_t unit =
+                    ((int64_t)s.b * p.num_kv_heads + s.g) * p.row_blocks + s.rb;
+                p.unit_ctas[unit] = make_int2(
+                    blockIdx.x, (int)(((seg_at + s.unit_tiles) * ctas - 1) / line));
+            }
+            // columns: ROWS: the whole row; else this warpgroup's half
+            constexpr int kCols = ROWS ? D : D / 2;
+            const int col0 = ROWS ? 0 : wg * kCols;
+#pragma unroll 1
+            for (int c = 0; c < kCols; c += 32) {
+                float v[32];
+                uint32_t ov[32];
+                __syncwarp();
+                if constexpr (ROWS) {
+                    ptx::tmem_ld32(tmem + lane_base + Cfg::kColO + wg * D + c, ov);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(ov[i]) * fa;
+                } else {
+                    ptx::tmem_ld32(tmem + lane_base + Cfg::kColO + col0 + c, ov);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(ov[i]) * fa;
+                    if (worked_b) {
+                        ptx::tmem_ld32(tmem + lane_base + Cfg::kColO + D + col0 + c, ov);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = fmaf(__uint_as_float(ov[i]), fb, v[i]);
+                    }
+                }
+                if (live && bad_v) {
+                    // infinities and NaN in the V of nodes that this row attends to
+                    const int t_hi = min(s.n, (s.tile0 + s.tiles) * TT);
+                    for (int t = max(max(0, base), s.tile0 * TT); t < t_hi; ++t) {
+                        const int j = t - base;
+                        if (!((__ldg(mask + (j >> 5)) >> (j & 31)) & 1)) continue;
+                        const int blk = __ldg(table + (t >> bs_shift));
+                        if (blk < 0 || blk >= p.num_blocks) continue;
+                        const int off = t & (bs - 1);
+                        const uint16_t* vr =
+                            static_cast<const uint16_t*>(p.v_cache) +
+                            (p.hnd ? ((int64_t)blk * p.num_kv_heads + s.g) * bs + off
+                                   : ((int64_t)blk * bs + off) * p.num_kv_heads + s.g) * D +
+                            col0 + c;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const uint16_t e = __ldg(vr + i);
+                            if (not_finite(e, T())) v[i] += unpack2(e, T()).x;
+                        }
+                    }
+                }
+                if (live && direct) {
+                    uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + orow * D +
+                                                          col0 + c);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        dst[i] = make_uint4(pack2(v[8 * i], v[8 * i + 1], T()),
+                                            pack2(v[8 * i + 2], v[8 * i + 3], T()),
+                                            pack2(v[8 * i + 4], v[8 * i + 5], T()),
+                                            pack2(v[8 * i + 6], v[8 * i + 7], T()));
+                } else if (live) {
+                    float4* dst = reinterpret_cast<float4*>(
+                        p.partial_o + ((int64_t)slot * kUnitRows + urow) * D + col0 + c);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                }
+            }
+            if (live && !direct && (ROWS || wg == 0))
+                p.partial_lse[(int64_t)slot * kUnitRows + urow] = lse;
+            if constexpr (!ROWS) {
+                ptx::tc_fence_before_sync();
+                ptx::mbar_arrive(ptx::smem_addr(o_free));
+            }
+            seg_at += s.tiles;
+            ++nseg;
+        }
+    }
+
+    ptx::tc_fence_before_sync();
+    __syncthreads();
+    if (warp == kTreeMmaWarp) {
+        __syncwarp();
+        ptx::tc_fence_after_sync();
+        ptx::tmem_dealloc(tmem, 512);
     }
 }
 
-// Arguments that the workspace size and the launch share.
-static pkv_status check_tree(int num_seqs, int tree_len, int num_q_heads, int num_kv_heads,
-                             int head_dim, int block_size, int max_context_len) {
+// Joins the partials of the units that were cut: one warp per row of the
+// output, w_c = 2^(lse_c - max), out = sum_c w_c O_c / sum_c w_c over the CTAs
+// of the unit.
+constexpr int kTreeMergeWarps = 4;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kTreeMergeWarps * 32)
+tree_merge_kernel(const TreeParams p, int unit_rows) {
+    constexpr int E = D / 32;
+    ptx::launch_dependents();
+    ptx::grid_dependency_wait();
+    const int lane = threadIdx.x & 31;
+    const int64_t row = (int64_t)blockIdx.x * kTreeMergeWarps + (threadIdx.x >> 5);
+    if (row >= (int64_t)p.num_seqs * p.tree_len * p.num_q_heads) return;
+    const int h = (int)(row % p.num_q_heads);
+    const int64_t bi = row / p.num_q_heads;
+    const int b = (int)(bi / p.tree_len), node = (int)(bi - (int64_t)b * p.tree_len);
+    const int g = h / p.group;
+    const int r = node * p.group + h - g * p.group;
+    const int rb = r / unit_rows;
+    const int2 ctas = __ldg(p.unit_ctas + ((int64_t)b * p.num_kv_heads + g) * p.row_blocks + rb);
+    if (ctas.x == ctas.y) return;  // written whole
+    const int urow = r - rb * unit_rows;
+    auto place = [&](int c) {
+        return (int64_t)(2 * c + (c == ctas.x ? 1 : 0)) * unit_rows + urow;
+    };
+    float mx = -INFINITY;
+    for (int c = ctas.x + lane; c <= ctas.y; c += 32) mx = fmaxf(mx, __ldg(p.partial_lse + place(c)));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const float ref = mx == -INFINITY ? 0.f : mx;
+    float acc[E], den = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    for (int c = ctas.x; c <= ctas.y; ++c) {
+        const float wgt = exp2f(__ldg(p.partial_lse + place(c)) - ref);
+        if (wgt == 0.f) continue;
+        den += wgt;
+        const float* o = p.partial_o + place(c) * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(wgt, __ldg(o + e), acc[e]);
+    }
+    const float inv = den == 0.f ? 0.f : 1.f / den;
+    uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + row * D + lane * E);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) out[e / 2] = pack2(acc[e] * inv, acc[e + 1] * inv, T());
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+
+// Arguments that the workspace size and the launch share, and the plan of a
+// call: the rows' split, the CTAs and the workspace.
+struct TreeCallPlan {
+    bool two_row_tiles;  // ROWS
+    int row_blocks;
+    int unit_rows;
+    int ctas;
+    bool cut;            // a unit may be cut: partials and a merge
+    size_t units_bytes;
+    size_t workspace_bytes;
+};
+
+static pkv_status plan_tree(int num_seqs, int tree_len, int num_q_heads, int num_kv_heads,
+                            int head_dim, int block_size, int max_context_len,
+                            TreeCallPlan* plan) {
     const pkv_status st = check_shapes(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
                                        max_context_len, 0);
     if (st != PKV_OK) return st;
     if (tree_len <= 0) return PKV_ERR_INVALID_ARG;
     if (tree_len > PKV_MAX_TREE_LEN || (int64_t)num_seqs * num_kv_heads > 65535)
         return PKV_ERR_UNSUPPORTED;
+    const int tiles = tree_tiles(max_context_len);
+    if ((int64_t)num_seqs * tiles > INT_MAX) return PKV_ERR_UNSUPPORTED;
+    const int sms = current_sm_count();
+    if (sms <= 0) return PKV_ERR_CUDA;
+    const int rows = tree_len * (num_q_heads / num_kv_heads);
+    plan->two_row_tiles = rows > kTreeTile;
+    plan->unit_rows = plan->two_row_tiles ? 2 * kTreeTile : kTreeTile;
+    plan->row_blocks = (rows + plan->unit_rows - 1) / plan->unit_rows;
+    const int64_t units = (int64_t)num_seqs * num_kv_heads * plan->row_blocks;
+    if ((int64_t)num_kv_heads * plan->row_blocks * tiles > INT_MAX) return PKV_ERR_UNSUPPORTED;
+    plan->ctas = (int)std::max<int64_t>(1, std::min<int64_t>(sms, units * tiles));
+    plan->cut = tiles > 1;
+    plan->units_bytes = ((size_t)units * sizeof(int2) + 255) & ~size_t(255);
+    plan->workspace_bytes =
+        256 + (plan->cut ? plan->units_bytes + (size_t)2 * plan->ctas * plan->unit_rows *
+                                                   (head_dim + 1) * sizeof(float)
+                         : 0);
     return PKV_OK;
+}
+
+template <typename T, int D, bool ROWS>
+static cudaError_t launch_tree_t(const CUtensorMap& mk, const CUtensorMap& mv, const TreeParams& p,
+                                 const TreeCallPlan& plan, cudaStream_t stream) {
+    using Cfg = TreeTileCfg<D>;
+    auto kern = tree_attention_kernel<T, D, ROWS>;
+    static std::once_flag once;
+    static cudaError_t attr_err = cudaSuccess;
+    std::call_once(once, [&] {
+        attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        Cfg::kSmemBytes);
+    });
+    if (attr_err != cudaSuccess) return attr_err;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(plan.ctas);
+    cfg.blockDim = dim3(kTreeThreads);
+    cfg.dynamicSmemBytes = Cfg::kSmemBytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, mk, mv, p);
+    if (e != cudaSuccess || !plan.cut) return e;
+    const int64_t rows = (int64_t)p.num_seqs * p.tree_len * p.num_q_heads;
+    const int64_t ctas = (rows + kTreeMergeWarps - 1) / kTreeMergeWarps;
+    if (ctas > INT_MAX) return cudaErrorInvalidValue;
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(kTreeMergeWarps * 32);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, tree_merge_kernel<T, D>, p, plan.unit_rows);
+}
+
+template <typename T>
+static cudaError_t launch_tree(const CUtensorMap& mk, const CUtensorMap& mv, const TreeParams& p,
+                               const TreeCallPlan& plan, int head_dim, cudaStream_t stream) {
+    if (head_dim == 64)
+        return plan.two_row_tiles ? launch_tree_t<T, 64, true>(mk, mv, p, plan, stream)
+                                  : launch_tree_t<T, 64, false>(mk, mv, p, plan, stream);
+    return plan.two_row_tiles ? launch_tree_t<T, 128, true>(mk, mv, p, plan, stream)
+                              : launch_tree_t<T, 128, false>(mk, mv, p, plan, stream);
 }
 
 }  // namespace pkv
@@ -131,10 +934,11 @@ using namespace pkv;
 extern "C" size_t pkv_tree_attention_workspace_size(int num_seqs, int tree_len, int num_q_heads,
                                                     int num_kv_heads, int head_dim,
                                                     int block_size, int max_context_len) {
-    if (check_tree(num_seqs, tree_len, num_q_heads, num_kv_heads, head_dim, block_size,
-                   max_context_len) != PKV_OK)
+    TreeCallPlan plan;
+    if (plan_tree(num_seqs, tree_len, num_q_heads, num_kv_heads, head_dim, block_size,
+                  max_context_len, &plan) != PKV_OK)
         return SIZE_MAX;
-    return 256;
+    return plan.workspace_bytes;
 }
 
 extern "C" pkv_status pkv_tree_attention(
@@ -145,13 +949,15 @@ extern "C" pkv_status pkv_tree_attention(
     void* workspace, size_t workspace_bytes, pkv_dtype dtype, int32_t* err_flag, void* stream) {
     const bool hnd = take_layout(dtype);
     if ((dtype != PKV_FP16 && dtype != PKV_BF16) || max_blocks_per_seq <= 0 || num_blocks <= 0 ||
-        !std::isfinite(scale))
+        !std::isfinite(scale) || tree_len <= 0)
         return PKV_ERR_INVALID_ARG;
-    const pkv_status st = check_tree(num_seqs, tree_len, num_q_heads, num_kv_heads, head_dim,
-                                     block_size, max_context_len);
-    if (st != PKV_OK) return st;
-    const int64_t mask_words = (int64_t)tree_len * ((tree_len + 31) / 32);
+    const int64_t mask_words = (int64_t)tree_len * (((int64_t)tree_len + 31) / 32);
     if (mask_stride != 0 && mask_stride < mask_words) return PKV_ERR_INVALID_ARG;
+    pkv_status st = check_shapes(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
+                                 max_context_len, 0);
+    if (st != PKV_OK) return st;
+    if (tree_len > PKV_MAX_TREE_LEN || (int64_t)num_seqs * num_kv_heads > 65535)
+        return PKV_ERR_UNSUPPORTED;
     if (num_seqs == 0) return PKV_OK;
     if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || !tree_mask ||
         !workspace)
@@ -162,8 +968,16 @@ extern "C" pkv_status pkv_tree_attention(
           reinterpret_cast<uintptr_t>(tree_mask)) & 3u))
         return PKV_ERR_INVALID_ARG;
     if ((int64_t)max_blocks_per_seq * block_size > INT_MAX) return PKV_ERR_UNSUPPORTED;
-    if (workspace_bytes < 256) return PKV_ERR_WORKSPACE;
+    TreeCallPlan plan;
+    st = plan_tree(num_seqs, tree_len, num_q_heads, num_kv_heads, head_dim, block_size,
+                   max_context_len, &plan);
+    if (st != PKV_OK) return st;
+    if (workspace_bytes < plan.workspace_bytes) return PKV_ERR_WORKSPACE;
 
+    CUtensorMap mk, mv;
+    if (!make_cache_map(&mk, k_cache, dtype, num_blocks, block_size, num_kv_heads, head_dim, hnd) ||
+        !make_cache_map(&mv, v_cache, dtype, num_blocks, block_size, num_kv_heads, head_dim, hnd))
+        return PKV_ERR_CUDA;
     TreeParams p = {};
     p.out = out;
     p.q = q;
@@ -174,27 +988,31 @@ extern "C" pkv_status pkv_tree_attention(
     p.tree_mask = tree_mask;
     p.mask_stride = mask_stride;
     p.err_flag = err_flag;
+    if (plan.cut) {
+        p.unit_ctas = static_cast<int2*>(workspace);
+        p.partial_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.units_bytes);
+        p.partial_lse = p.partial_o + (size_t)2 * plan.ctas * plan.unit_rows * head_dim;
+    }
     p.max_blocks_per_seq = max_blocks_per_seq;
     p.num_blocks = num_blocks;
     p.block_size = block_size;
+    p.num_seqs = num_seqs;
     p.num_q_heads = num_q_heads;
     p.num_kv_heads = num_kv_heads;
+    p.group = num_q_heads / num_kv_heads;
     p.tree_len = tree_len;
     p.cap = std::min(max_blocks_per_seq * block_size, max_context_len);
+    p.row_blocks = plan.row_blocks;
     p.hnd = hnd;
-    p.scale_log2 = scale * kLog2e;
+    p.scale_log2 = (scale == 0.f ? 1.f : std::fabs(scale)) * kLog2e;
+    p.scale_sign = scale > 0.f ? 1.f : scale < 0.f ? -1.f : 0.f;
     cudaStream_t s = (cudaStream_t)stream;
-    const dim3 grid(num_q_heads, tree_len, num_seqs);
-    if (head_dim == 64) {
-        if (dtype == PKV_FP16)
-            tree_attention_kernel<__half, 64><<<grid, kTreeWarps * 32, 0, s>>>(p);
-        else
-            tree_attention_kernel<__nv_bfloat16, 64><<<grid, kTreeWarps * 32, 0, s>>>(p);
-    } else {
-        if (dtype == PKV_FP16)
-            tree_attention_kernel<__half, 128><<<grid, kTreeWarps * 32, 0, s>>>(p);
-        else
-            tree_attention_kernel<__nv_bfloat16, 128><<<grid, kTreeWarps * 32, 0, s>>>(p);
+    const cudaError_t e = dtype == PKV_FP16
+                              ? launch_tree<__half>(mk, mv, p, plan, head_dim, s)
+                              : launch_tree<__nv_bfloat16>(mk, mv, p, plan, head_dim, s);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return PKV_ERR_CUDA;
     }
-    return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+    return PKV_OK;
 }
