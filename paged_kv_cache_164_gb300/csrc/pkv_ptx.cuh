@@ -277,6 +277,15 @@ __device__ __forceinline__ float ex2_approx(float x) {
     return y;
 }
 
+// True in one lane of a converged warp, the same one each time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t is;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(is));
+    return is != 0;
+}
+
 // ---- programmatic dependent launch ------------------------------------------------
 
 __device__ __forceinline__ void grid_dependency_wait() {

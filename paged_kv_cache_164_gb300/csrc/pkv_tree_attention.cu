@@ -71,9 +71,10 @@ struct TreeParams {
 
 constexpr int kTreeTile = 128;                     // rows (MMA M) and tokens of a tile
 constexpr int kTreeSoftmaxWarps = 8;               // two warpgroups
-constexpr int kTreeTmaWarp = kTreeSoftmaxWarps;
-constexpr int kTreeMmaWarp = kTreeSoftmaxWarps + 1;
-constexpr int kTreeThreads = (kTreeSoftmaxWarps + 4) * 32;  // two warps fill the third warpgroup
+constexpr int kTreeTmaWarpK = kTreeSoftmaxWarps;
+constexpr int kTreeTmaWarpV = kTreeSoftmaxWarps + 1;
+constexpr int kTreeMmaWarp = kTreeSoftmaxWarps + 2;
+constexpr int kTreeThreads = (kTreeSoftmaxWarps + 4) * 32;  // one warp fills the third warpgroup
 // Registers: a softmax thread holds a row of S (128 values), which does not fit
 // the 168 a thread that 384 threads get at launch; the third warpgroup hands
 // over what it does not need (2 x 216 + 72 = 3 x 168).
@@ -285,15 +286,19 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
 
     if (warp >= kTreeSoftmaxWarps) {
         ptx::reg_dec<kTreeOtherRegs>();
-        if (warp == kTreeTmaWarp) {
+        if (warp == kTreeTmaWarpK || warp == kTreeTmaWarpV) {
             // ------------------------------------------------------------ producer
-            // A lane issues one box (16 tokens x 64 dims) of the tile's K, then of V.
+            // One warp loads the K tiles, one the V tiles; a lane issues one box (16
+            // tokens x 64 dims).
             const uint64_t policy =
                 p.row_blocks > 1 ? ptx::l2_policy_evict_last() : ptx::l2_policy_evict_first();
             const int bx = lane / R, rr = lane % R;
             const bool loads = lane < kTreeBoxes * R;
+            const bool is_v = warp == kTreeTmaWarpV;
+            const CUtensorMap* map = is_v ? &tm_v : &tm_k;
             int place0 = 0;  // places of the stretches before this one
-            int issued = 0;
+            int issued = 0;     // one past this warp's last place filled
+            uint32_t own = 0u;  // bit i: place issued - 1 - i is this warp's
             bool ok = true;
             while (ok && walk.next(p, seg)) {
                 const int32_t* table = p.block_tables + (int64_t)seg.b * p.max_blocks_per_seq;
@@ -302,13 +307,14 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                     if (!loads || j >= seg.tiles || tok >= seg.n) return -1;
                     const int blk = __ldg(table + (tok >> bs_shift));
                     if (blk < 0 || blk >= p.num_blocks) {
-                        flag_error(p.err_flag, PKV_EFLAG_BLOCK_ID);
+                        if (!is_v) flag_error(p.err_flag, PKV_EFLAG_BLOCK_ID);
                         return -1;
                     }
                     return blk;
                 };
-                auto load = [&](const CUtensorMap* map, int place, int j, int blk) {
-                    const int at = place0 + place;
+                auto load = [&](int j, int blk) {
+                    const int at =
+                        place0 + (is_v ? v_place<ROWS>(j, seg.tiles) : k_place<ROWS>(j));
                     const int slot = at % NS;
                     if (at >= NS && !warp_wait_phase(ptx::smem_addr(&empty_bar[slot]),
                                                      ((at / NS) - 1) & 1, abort_flag, p.err_flag))
@@ -335,25 +341,22 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                                         bx * kStageTokens * 128,
                                     map, fb, rr * 64, seg.g, tok & (bs - 1), blk, p.hnd, policy);
                     }
-                    issued = max(issued, at + 1);
+                    own = (at + 1 - issued < 32 ? own << (at + 1 - issued) : 0u) | 1u;
+                    issued = at + 1;
                     return true;
                 };
-                int blk = box_block(0), blk_next = box_block(1);
-                ok = load(&tm_k, k_place<ROWS>(0), 0, blk);
+                int blk = box_block(0);
                 for (int j = 0; j < seg.tiles && ok; ++j) {
-                    const int blk_after = box_block(j + 2);
-                    const bool more = j + 1 < seg.tiles;
-                    if (!ROWS && more) ok = load(&tm_k, k_place<ROWS>(j + 1), j + 1, blk_next);
-                    if (ok) ok = load(&tm_v, v_place<ROWS>(j, seg.tiles), j, blk);
-                    if (ROWS && more && ok) ok = load(&tm_k, k_place<ROWS>(j + 1), j + 1, blk_next);
+                    const int blk_next = box_block(j + 1);
+                    ok = load(j, blk);
                     blk = blk_next;
-                    blk_next = blk_after;
                 }
                 place0 += 2 * seg.tiles;
             }
             if (lane == 0 && *abort_flag) {
-                // wait (bounded) for the copies in flight before leaving
+                // wait (bounded) for this warp's copies in flight before leaving
                 for (int at = max(0, issued - NS); at < issued; ++at) {
+                    if (!((own >> (issued - 1 - at)) & 1u)) continue;
                     const uint32_t fb = ptx::smem_addr(&full_bar[at % NS]);
                     const uint64_t t0 = ptx::globaltimer();
                     while (!ptx::mbar_try_wait(fb, (at / NS) & 1) &&
@@ -363,76 +366,92 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             }
         } else if (warp == kTreeMmaWarp) {
             // ------------------------------------------------------------ MMA issuer
-            if (lane == 0) {
-                constexpr uint32_t fmt = F16Format<T>::value;
-                constexpr uint32_t idesc_s = mma_idesc(fmt, TT, TT, false);
-                constexpr uint32_t idesc_o = mma_idesc(fmt, TT, D, true);
-                int place0 = 0, nseg = 0;
-                int p_count[2] = {0, 0};
-                bool ok = true;
-                while (ok && walk.next(p, seg)) {
-                    const int nt = seg.tiles;
-                    // step x: ROWS: warpgroup x % 2 at tile x / 2; else at tile x
-                    const int steps = ROWS ? 2 * nt : nt;
-                    auto wait = [&](uint64_t* bar, int parity) {
-                        return wait_phase(ptx::smem_addr(bar), parity & 1, abort_flag, p.err_flag);
-                    };
-                    auto issue_s = [&](int x) {
-                        const int w = x & 1, j = ROWS ? x >> 1 : x;
-                        const int at = place0 + k_place<ROWS>(j);
-                        const int slot = at % NS;
-                        if (!wait(&full_bar[slot], at / NS)) return false;
-                        ptx::tc_fence_after_sync();
-                        const uint32_t kb = ring_addr + slot * Cfg::kSlotBytes;
-                        const uint32_t qb = q_addr + (ROWS ? w : nseg & 1) * Cfg::kSlotBytes;
+            // The whole warp walks the steps, so that addresses and descriptors are
+            // uniform values; one elected lane issues.  (One lane alone walking
+            // them took 110 cycles a product to issue, of the 64 that it runs.)
+            constexpr uint32_t fmt = F16Format<T>::value;
+            constexpr uint32_t idesc_s = mma_idesc(fmt, TT, TT, false);
+            constexpr uint32_t idesc_o = mma_idesc(fmt, TT, D, true);
+            // descriptors of the first slots: a byte offset adds its sixteenth (the
+            // address field stays within its 14 bits: shared memory is 228 KB)
+            const uint64_t qdesc = ptx::smem_desc_sw128(q_addr, 16, 1024);
+            const uint64_t kdesc = ptx::smem_desc_sw128(ring_addr, 16, 1024);
+            const uint64_t vdesc = ptx::smem_desc_sw128(ring_addr, Cfg::kRegionBytes, 1024);
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            int place0 = 0, nseg = 0;
+            int p_count[2] = {0, 0};
+            bool ok = true;
+            while (ok && walk.next(p, seg)) {
+                const int nt = __shfl_sync(0xffffffffu, seg.tiles, 0);
+                // step x: ROWS: warpgroup x % 2 at tile x / 2; else at tile x
+                const int steps = ROWS ? 2 * nt : nt;
+                auto wait = [&](uint64_t* bar, int parity) {
+                    return warp_wait_phase(ptx::smem_addr(bar), parity & 1, abort_flag,
+                                           p.err_flag);
+                };
+                auto issue_s = [&](int x) {
+                    const int w = x & 1, j = ROWS ? x >> 1 : x;
+                    const int at = place0 + k_place<ROWS>(j);
+                    const int slot = at % NS;
+                    if (!wait(&full_bar[slot], at / NS)) return false;
+                    ptx::tc_fence_after_sync();
+                    const uint64_t kd = kdesc + (uint32_t)(slot * (Cfg::kSlotBytes / 16));
+                    const uint64_t qd =
+                        qdesc + (uint32_t)((ROWS ? w : nseg & 1) * (Cfg::kSlotBytes / 16));
+                    const uint32_t acc = tm + w * TT;
+                    if (ptx::elect_one()) {
 #pragma unroll
                         for (int ks = 0; ks < D / 16; ++ks) {
-                            const uint32_t off = (ks / 4) * Cfg::kRegionBytes + (ks % 4) * 32;
-                            ptx::tc_mma_f16(tmem + w * TT, ptx::smem_desc_sw128(qb + off, 16, 1024),
-                                            ptx::smem_desc_sw128(kb + off, 16, 1024), idesc_s,
-                                            ks > 0 ? 1u : 0u);
+                            const uint32_t off =
+                                (ks / 4) * (Cfg::kRegionBytes / 16) + (ks % 4) * (32 / 16);
+                            ptx::tc_mma_f16(acc, qd + off, kd + off, idesc_s, ks > 0 ? 1u : 0u);
                         }
                         ptx::tc_commit(ptx::smem_addr(&s_full[w]));
                         if (!ROWS || w == 1) ptx::tc_commit(ptx::smem_addr(&empty_bar[slot]));
-                        return true;
-                    };
-                    auto issue_pv = [&](int x) {
-                        const int w = x & 1, j = ROWS ? x >> 1 : x;
-                        const int at = place0 + v_place<ROWS>(j, nt);
-                        const int slot = at % NS;
-                        if (!wait(&full_bar[slot], at / NS) || !wait(&p_ready[w], p_count[w]++))
-                            return false;
-                        ptx::tc_fence_after_sync();
-                        const uint32_t vb = ring_addr + slot * Cfg::kSlotBytes;
-                        const uint32_t acc = tmem + Cfg::kColO + w * D;
+                    }
+                    __syncwarp();
+                    return true;
+                };
+                auto issue_pv = [&](int x) {
+                    const int w = x & 1, j = ROWS ? x >> 1 : x;
+                    const int at = place0 + v_place<ROWS>(j, nt);
+                    const int slot = at % NS;
+                    if (!wait(&full_bar[slot], at / NS) || !wait(&p_ready[w], p_count[w]++))
+                        return false;
+                    ptx::tc_fence_after_sync();
+                    const uint64_t vd = vdesc + (uint32_t)(slot * (Cfg::kSlotBytes / 16));
+                    const uint32_t acc = tm + Cfg::kColO + w * D;
+                    const uint32_t pt = tm + w * TT;
+                    if (ptx::elect_one()) {
 #pragma unroll
                         for (int kt = 0; kt < TT / 16; ++kt) {
                             // tokens 16 kt ..: of each 32 tokens of P, 16 columns of hi
                             // pairs, then 16 of lo pairs
-                            const uint32_t a = tmem + w * TT + (kt / 2) * 32 + (kt % 2) * 8;
-                            const uint64_t v = ptx::smem_desc_sw128(vb + kt * 16 * 128,
-                                                                    Cfg::kRegionBytes, 1024);
+                            const uint32_t a = pt + (kt / 2) * 32 + (kt % 2) * 8;
+                            const uint64_t v = vd + (uint32_t)(kt * 16 * 128 / 16);
                             ptx::tc_mma_f16_ts(acc, a, v, idesc_o, (x >= 2 || kt > 0) ? 1u : 0u);
                             ptx::tc_mma_f16_ts(acc, a + 16, v, idesc_o, 1u);
                         }
                         if (!ROWS || w == 1) ptx::tc_commit(ptx::smem_addr(&empty_bar[slot]));
                         if (x + 2 >= steps) ptx::tc_commit(ptx::smem_addr(&o_done[w]));
-                        return true;
-                    };
-                    // The tensor core runs the products in the order of their issue:
-                    // S_w(next) over P_w comes after the O_w += P_w V that reads it.
-                    ok = wait(q_ready, nseg) && issue_s(0) && (steps < 2 || issue_s(1));
-                    for (int x = 0; x < steps && ok; ++x)
-                        ok = issue_pv(x) && (x + 2 >= steps || issue_s(x + 2));
-                    place0 += 2 * nt;
-                    ++nseg;
-                }
-                // every product has completed before the tensor memory is released
-                ptx::tc_commit(ptx::smem_addr(drain));
-                const uint64_t t0 = ptx::globaltimer();
-                while (!ptx::mbar_try_wait(ptx::smem_addr(drain), 0) &&
-                       ptx::globaltimer() - t0 < kWaitLimitNs) {
-                }
+                    }
+                    __syncwarp();
+                    return true;
+                };
+                // The tensor core runs the products in the order of their issue:
+                // S_w(next) over P_w comes after the O_w += P_w V that reads it.
+                ok = wait(q_ready, nseg) && issue_s(0) && (steps < 2 || issue_s(1));
+                for (int x = 0; x < steps && ok; ++x)
+                    ok = issue_pv(x) && (x + 2 >= steps || issue_s(x + 2));
+                place0 += 2 * nt;
+                ++nseg;
+            }
+            // every product has completed before the tensor memory is released
+            if (ptx::elect_one()) ptx::tc_commit(ptx::smem_addr(drain));
+            __syncwarp();
+            const uint64_t t0 = ptx::globaltimer();
+            while (!ptx::mbar_try_wait(ptx::smem_addr(drain), 0) &&
+                   ptx::globaltimer() - t0 < kWaitLimitNs) {
             }
         }
     } else {
