@@ -93,8 +93,8 @@ struct TreeTileCfg {
     static constexpr int kSlots = D == 128 ? 5 : 8;
     static constexpr int kQBytes = 2 * kSlotBytes;
     static constexpr int kXchBytes = 2 * kTreeTile * 8;         // (m, l) of each half and row
-    // full[slots], empty[slots], s_full[2], p_ready[2], o_done[2], q_ready, met, o_free, drain
-    static constexpr int kBarriers = 2 * kSlots + 10;
+    // full[slots], empty[slots], s_full[2], p_ready[2][2], o_done[2], q_ready, met, o_free, drain
+    static constexpr int kBarriers = 2 * kSlots + 12;
     static constexpr int kSmemBytes =
         kQBytes + kSlots * kSlotBytes + kXchBytes + kBarriers * 8 + 256;
     static constexpr uint32_t kColO = 2 * kTreeTile;  // S_0, S_1, then O_0, O_1
@@ -153,7 +153,32 @@ __device__ __forceinline__ int v_place(int j, int nt) {
     return ROWS ? 2 * j + 1 : (j < nt - 1 ? 2 * j + 2 : 2 * nt - 1);
 }
 
-// Whether one of the two 16-bit values is an infinity or a NaN.
+// A row's weights are 2^(score - reference + bias).  fp16 has few exponents:
+// with the bias its largest weight is 2^(8 + 7), and what subnormals lose of
+// one is below 2^-32 of the row's largest.
+template <typename T> struct WeightBias { static constexpr float value = 0.f; };
+template <> struct WeightBias<__half> { static constexpr float value = 7.f; };
+
+// Two softmax weights as hi + lo 16-bit pairs: hi the weight cut to the type's
+// fraction bits, lo the rest (cut again for bf16: 2^-14 of the weight is lost;
+// rounded for fp16).
+__device__ __forceinline__ void split_pair(float2 x, uint32_t& hi, uint32_t& lo, __nv_bfloat16) {
+    const uint32_t a = __float_as_uint(x.x), b = __float_as_uint(x.y);
+    hi = __byte_perm(a, b, 0x7632);
+    const float2 r = ptx::fma2(make_float2(__uint_as_float(a & 0xffff0000u),
+                                           __uint_as_float(b & 0xffff0000u)),
+                               make_float2(-1.f, -1.f), x);
+    lo = __byte_perm(__float_as_uint(r.x), __float_as_uint(r.y), 0x7632);
+}
+__device__ __forceinline__ void split_pair(float2 x, uint32_t& hi, uint32_t& lo, __half) {
+    const float2 h = make_float2(__uint_as_float(__float_as_uint(x.x) & 0xffffe000u),
+                                 __uint_as_float(__float_as_uint(x.y) & 0xffffe000u));
+    hi = pack2(h.x, h.y, __half());
+    const float2 r = ptx::fma2(h, make_float2(-1.f, -1.f), x);
+    lo = pack2(r.x, r.y, __half());
+}
+
+// Whether a 16-bit value is an infinity or a NaN.
 __device__ __forceinline__ bool not_finite(uint16_t x, __nv_bfloat16) {
     return (x & 0x7f80u) == 0x7f80u;
 }
@@ -176,8 +201,8 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
     uint64_t* full_bar = reinterpret_cast<uint64_t*>(ring + NS * Cfg::kSlotBytes + Cfg::kXchBytes);
     uint64_t* empty_bar = full_bar + NS;
     uint64_t* s_full = empty_bar + NS;  // [2]
-    uint64_t* p_ready = s_full + 2;     // [2]
-    uint64_t* o_done = p_ready + 2;     // [2]: a stretch's last O_w += P V is done
+    uint64_t* p_ready = s_full + 2;     // [warpgroup][half of the tile's tokens]
+    uint64_t* o_done = p_ready + 4;     // [2]: a stretch's last O_w += P V is done
     uint64_t* q_ready = o_done + 2;
     uint64_t* met = q_ready + 1;        // both warpgroups are through the stretch (not ROWS)
     uint64_t* o_free = met + 1;         // both have read O_0 and O_1 (not ROWS)
@@ -204,7 +229,8 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
         }
         for (int w = 0; w < 2; ++w) {
             ptx::mbar_init(ptx::smem_addr(&s_full[w]), 1);
-            ptx::mbar_init(ptx::smem_addr(&p_ready[w]), TT);
+            ptx::mbar_init(ptx::smem_addr(&p_ready[2 * w]), TT);
+            ptx::mbar_init(ptx::smem_addr(&p_ready[2 * w + 1]), TT);
             ptx::mbar_init(ptx::smem_addr(&o_done[w]), 1);
         }
         ptx::mbar_init(ptx::smem_addr(q_ready), 2 * TT);
@@ -282,10 +308,10 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
         walk.unit = s_start[1] / tiles;
         walk.tile = s_start[1] - walk.unit * tiles;
     }
-    TreeSeg seg;
 
     if (warp >= kTreeSoftmaxWarps) {
         ptx::reg_dec<kTreeOtherRegs>();
+        TreeSeg seg;
         if (warp == kTreeTmaWarpK || warp == kTreeTmaWarpV) {
             // ------------------------------------------------------------ producer
             // One warp loads the K tiles, one the V tiles; a lane issues one box (16
@@ -416,26 +442,34 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                     const int w = x & 1, j = ROWS ? x >> 1 : x;
                     const int at = place0 + v_place<ROWS>(j, nt);
                     const int slot = at % NS;
-                    if (!wait(&full_bar[slot], at / NS) || !wait(&p_ready[w], p_count[w]++))
-                        return false;
-                    ptx::tc_fence_after_sync();
+                    const int phase = p_count[w]++;
+                    if (!wait(&full_bar[slot], at / NS)) return false;
                     const uint64_t vd = vdesc + (uint32_t)(slot * (Cfg::kSlotBytes / 16));
                     const uint32_t acc = tm + Cfg::kColO + w * D;
                     const uint32_t pt = tm + w * TT;
-                    if (ptx::elect_one()) {
+                    // the tokens' upper half is written first
 #pragma unroll
-                        for (int kt = 0; kt < TT / 16; ++kt) {
-                            // tokens 16 kt ..: of each 32 tokens of P, 16 columns of hi
-                            // pairs, then 16 of lo pairs
-                            const uint32_t a = pt + (kt / 2) * 32 + (kt % 2) * 8;
-                            const uint64_t v = vd + (uint32_t)(kt * 16 * 128 / 16);
-                            ptx::tc_mma_f16_ts(acc, a, v, idesc_o, (x >= 2 || kt > 0) ? 1u : 0u);
-                            ptx::tc_mma_f16_ts(acc, a + 16, v, idesc_o, 1u);
+                    for (int half = 1; half >= 0; --half) {
+                        if (!wait(&p_ready[2 * w + half], phase)) return false;
+                        ptx::tc_fence_after_sync();
+                        if (ptx::elect_one()) {
+#pragma unroll
+                            for (int kt = half * 4; kt < half * 4 + 4; ++kt) {
+                                // tokens 16 kt ..: of each 32 tokens of P, 16 columns of
+                                // hi pairs, then 16 of lo pairs
+                                const uint32_t a = pt + (kt / 2) * 32 + (kt % 2) * 8;
+                                const uint64_t v = vd + (uint32_t)(kt * 16 * 128 / 16);
+                                ptx::tc_mma_f16_ts(acc, a, v, idesc_o,
+                                                   (x >= 2 || kt != 4) ? 1u : 0u);
+                                ptx::tc_mma_f16_ts(acc, a + 16, v, idesc_o, 1u);
+                            }
+                            if (half == 0) {
+                                if (!ROWS || w == 1) ptx::tc_commit(ptx::smem_addr(&empty_bar[slot]));
+                                if (x + 2 >= steps) ptx::tc_commit(ptx::smem_addr(&o_done[w]));
+                            }
                         }
-                        if (!ROWS || w == 1) ptx::tc_commit(ptx::smem_addr(&empty_bar[slot]));
-                        if (x + 2 >= steps) ptx::tc_commit(ptx::smem_addr(&o_done[w]));
+                        __syncwarp();
                     }
-                    __syncwarp();
                     return true;
                 };
                 // The tensor core runs the products in the order of their issue:
@@ -475,7 +509,8 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             return live;
         };
         // This thread's part of its row of Q (not ROWS: half of it) into the Q
-        // tile of stretch `which`, 16-byte chunk c of a 128-byte row at c ^ (row % 8).
+        // tile of stretch `which`, 16-byte chunk c of a 128-byte row at
+        // c ^ (row % 8); zeros past the rows in use.
         auto load_q = [&](const TreeSeg& s, int which) {
             constexpr int QV = ROWS ? D / 8 : D / 16;
             int node;
@@ -483,26 +518,28 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             const bool live = row_of(s, node, orow);
             const int c0 = ROWS ? 0 : wg * QV;
             const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + orow * D);
-            uint8_t* dst = sq + (ROWS ? wg : which & 1) * Cfg::kSlotBytes + srow * 128;
-            uint4 x[QV];
-#pragma unroll
-            for (int k = 0; k < QV; ++k)
-                x[k] = live ? __ldg(src + c0 + k) : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t dst = q_addr + (ROWS ? wg : which & 1) * Cfg::kSlotBytes + srow * 128;
 #pragma unroll
             for (int k = 0; k < QV; ++k) {
                 const int c = c0 + k;
-                *reinterpret_cast<uint4*>(dst + (c / 8) * Cfg::kRegionBytes +
-                                          (((c % 8) ^ (srow & 7)) << 4)) = x[k];
+                ptx::cp_async_16(dst + (c / 8) * Cfg::kRegionBytes + (((c % 8) ^ (srow & 7)) << 4),
+                                 src + c, live);
             }
+        };
+        auto q_loaded = [&] {
+            ptx::cp_async_wait_all();
             ptx::fence_proxy_async_smem();
             ptx::mbar_arrive(ptx::smem_addr(q_ready));
         };
 
-        bool have = walk.next(p, seg);
-        if (have) load_q(seg, 0);
+        TreeSeg s, next;
+        bool have = walk.next(p, s);
+        if (have) {
+            load_q(s, 0);
+            q_loaded();
+        }
         int64_t seg_at = start;  // the stretch's first tile on the line
         while (have && ok) {
-            const TreeSeg s = seg;
             const int base = s.n - p.tree_len;
             int node;
             int64_t orow;
@@ -513,6 +550,11 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 if (n_raw < 0 || n_raw > p.cap || (n_raw != 0 && n_raw < p.tree_len))
                     flag_error(p.err_flag, PKV_EFLAG_CONTEXT_LEN);
             }
+            // The next stretch's Q is on its way long before it is needed: from the
+            // start of this one (its Q tile belonged to the stretch before; ROWS:
+            // from the last S_w of this one, which reads the same Q tile).
+            const bool have_next = walk.next(p, next);
+            if (!ROWS && have_next) load_q(next, nseg + 1);
             const int mask_words = (p.tree_len + 31) / 32;
             const int32_t* mask = p.tree_mask + s.b * p.mask_stride + (int64_t)node * mask_words;
             // bits of nodes jb .. jb + 31 (below 0: committed positions)
@@ -555,90 +597,10 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 }
                 ++steps_done;
                 ptx::tc_fence_after_sync();
+                if (ROWS && have_next && j + 1 == s.tiles) load_q(next, nseg + 1);
                 const int t0 = (s.tile0 + j) * TT;
-                const bool whole = boxes == 0xffu && t0 + TT <= s.n;
-                const bool tree = t0 + TT > base;
-                if (warp_live) {
-                    uint32_t sv[TT];
-#pragma unroll
-                    for (int c = 0; c < TT / 32; ++c)
-                        ptx::tmem_ld32_async(s_col + c * 32,
-                                             *reinterpret_cast<uint32_t(*)[32]>(sv + c * 32));
-                    ptx::tmem_wait_ld();
-#pragma unroll
-                    for (int c = 0; c < TT / 32; ++c)
-                        ptx::tmem_loaded(*reinterpret_cast<uint32_t(*)[32]>(sv + c * 32));
-                    float sc[TT];
-#pragma unroll
-                    for (int i = 0; i < TT; ++i) sc[i] = __uint_as_float(sv[i]);
-                    if (p.scale_sign != 1.f) {
-#pragma unroll
-                        for (int i = 0; i < TT; ++i) sc[i] *= p.scale_sign;
-                    }
-                    if (!whole || tree) {
-#pragma unroll
-                        for (int c = 0; c < TT / 32; ++c) {
-                            const int tc = t0 + c * 32;
-                            const int left = s.n - tc;
-                            uint32_t allow = left >= 32 ? ~0u : left <= 0 ? 0u : (1u << left) - 1u;
-                            const uint32_t bb = boxes >> (2 * c);
-                            allow &= ((bb & 1u) ? 0x0000ffffu : 0u) | ((bb & 2u) ? 0xffff0000u : 0u);
-                            if (tree) allow &= tree_bits(tc - base);
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (!((allow >> i) & 1u)) sc[c * 32 + i] = -INFINITY;
-                        }
-                    }
-                    float mx[4];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) mx[c] = sc[c];
-#pragma unroll
-                    for (int i = 4; i < TT; ++i) mx[i % 4] = fmaxf(mx[i % 4], sc[i]);
-                    const float top =
-                        fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
-                    float alpha = 1.f;
-                    if (m_ref == -INFINITY) {
-                        m_ref = top;  // O and l are still zero for this row
-                    } else if (top > m_ref + kTreeLazyLog2) {
-                        alpha = ptx::ex2_approx(m_ref - top);
-                        m_ref = top;
-                    }
-                    const float ref = m_ref == -INFINITY ? 0.f : m_ref;
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int i = 0; i < TT; ++i) {
-                        sc[i] = ptx::ex2_approx(fmaf(sc[i], p.scale_log2, -ref));
-                        sum[i % 4] += sc[i];
-                    }
-                    l = fmaf(l, alpha, (sum[0] + sum[1]) + (sum[2] + sum[3]));
-                    __syncwarp();
-                    // O_w is rescaled when a reference moved: S_w(j) complete implies
-                    // that O_w += P V of the tile before is
-                    if (__any_sync(0xffffffffu, alpha != 1.f)) {
-#pragma unroll
-                        for (int c = 0; c < D / 32; ++c) {
-                            uint32_t ov[32];
-                            const uint32_t ta = tmem + lane_base + Cfg::kColO + wg * D + c * 32;
-                            ptx::tmem_ld32(ta, ov);
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
-                            ptx::tmem_st32(ta, ov);
-                        }
-                    }
-#pragma unroll
-                    for (int c = 0; c < TT / 32; ++c) {
-                        uint32_t pv[32];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            split_hi_lo(sc[c * 32 + 2 * e], sc[c * 32 + 2 * e + 1], pv[e],
-                                        pv[16 + e], T());
-                        ptx::tmem_st32_async(s_col + c * 32, pv);
-                    }
-                    ptx::tmem_wait_st();
-                }
-                __syncwarp();
-                if (!whole || tree) {
+                const bool plain = boxes == 0xffu && t0 + TT <= s.n && t0 + TT <= base;
+                if (!plain) {
                     // V rows of absent tokens hold stale bytes, and a node's V may hold
                     // infinities or NaN that only some rows attend to: zeroed in
                     // shared memory, so that 0 * V is 0; the rows that do attend to
@@ -650,7 +612,8 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                         break;
                     }
                     uint8_t* vst = ring + (at % NS) * Cfg::kSlotBytes;
-                    for (int idx = srow; idx < TT * R * 8; idx += TT) {
+                    const int row0 = boxes == 0xffu ? max(0, min(base, s.n) - t0) : 0;
+                    for (int idx = row0 * R * 8 + srow; idx < TT * R * 8; idx += TT) {
                         const int row = idx / (R * 8), rem = idx - row * (R * 8);
                         uint4* cell = reinterpret_cast<uint4*>(
                             vst + (rem / 8) * Cfg::kRegionBytes + row * 128 + (rem % 8) * 16);
@@ -680,16 +643,120 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                     break;
                 }
                 worked = true;
+
+                // The row's scores come from tensor memory a half (64 tokens) at a
+                // time: both for the maximum, then the upper half's weights while its
+                // scores are still in registers, then the lower half's anew.  The
+                // products take the upper half's while the lower's are made.
+                uint32_t allow[TT / 32];  // tokens that the row attends to
+                if (!plain && warp_live) {
+#pragma unroll
+                    for (int c = 0; c < TT / 32; ++c) {
+                        const int tc = t0 + c * 32;
+                        const int left = s.n - tc;
+                        uint32_t a = left >= 32 ? ~0u : left <= 0 ? 0u : (1u << left) - 1u;
+                        const uint32_t bb = boxes >> (2 * c);
+                        a &= ((bb & 1u) ? 0x0000ffffu : 0u) | ((bb & 2u) ? 0xffff0000u : 0u);
+                        allow[c] = a & tree_bits(tc - base);
+                    }
+                }
+                float sc[TT / 2];
+                auto load_half = [&](int half) {
+                    uint32_t(&r0)[32] = *reinterpret_cast<uint32_t(*)[32]>(sc);
+                    uint32_t(&r1)[32] = *reinterpret_cast<uint32_t(*)[32]>(sc + 32);
+                    __syncwarp();
+                    ptx::tmem_ld32_async(s_col + half * 64, r0);
+                    ptx::tmem_ld32_async(s_col + half * 64 + 32, r1);
+                    ptx::tmem_wait_ld();
+                    ptx::tmem_loaded(r0);
+                    ptx::tmem_loaded(r1);
+                    if (p.scale_sign != 1.f) {
+#pragma unroll
+                        for (int i = 0; i < TT / 2; ++i) sc[i] *= p.scale_sign;
+                    }
+                    if (!plain) {
+#pragma unroll
+                        for (int i = 0; i < TT / 2; ++i)
+                            if (!((allow[half * 2 + i / 32] >> (i % 32)) & 1u)) sc[i] = -INFINITY;
+                    }
+                };
+                auto max_half = [&] {
+                    float mx[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) mx[c] = fmaxf(sc[2 * c], sc[2 * c + 1]);
+#pragma unroll
+                    for (int i = 8; i < TT / 2; i += 2)
+                        mx[(i / 2) % 4] = fmaxf(fmaxf(mx[(i / 2) % 4], sc[i]), sc[i + 1]);
+                    return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                };
+                float2 ref2, sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                // weights of the half in registers, summed and written over its scores
+                auto weigh_half = [&](int half) {
+                    const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
+#pragma unroll
+                    for (int i = 0; i < TT / 2; i += 2) {
+                        const float2 y = ptx::fma2(make_float2(sc[i], sc[i + 1]), scale2, ref2);
+                        sc[i] = ptx::ex2_approx(y.x);
+                        sc[i + 1] = ptx::ex2_approx(y.y);
+                        sum[(i / 2) % 2] =
+                            ptx::add2(sum[(i / 2) % 2], make_float2(sc[i], sc[i + 1]));
+                    }
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t pv[32];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            split_pair(make_float2(sc[c * 32 + 2 * e], sc[c * 32 + 2 * e + 1]),
+                                       pv[e], pv[16 + e], T());
+                        ptx::tmem_st32_async(s_col + half * 64 + c * 32, pv);
+                    }
+                    ptx::tmem_wait_st();
+                };
+                if (warp_live) {
+                    load_half(0);
+                    float top = max_half();
+                    load_half(1);
+                    top = fmaxf(top, max_half()) * p.scale_log2;
+                    float alpha = 1.f;
+                    if (m_ref == -INFINITY) {
+                        m_ref = top;  // O and l are still zero for this row
+                    } else if (top > m_ref + kTreeLazyLog2) {
+                        alpha = ptx::ex2_approx(m_ref - top);
+                        m_ref = top;
+                    }
+                    const float ref = (m_ref == -INFINITY ? 0.f : m_ref) - WeightBias<T>::value;
+                    ref2 = make_float2(-ref, -ref);
+                    l *= alpha;
+                    // O_w is rescaled when a reference moved: S_w(j) complete implies
+                    // that O_w += P V of the tile before is
+                    if (__any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t ov[32];
+                            const uint32_t ta = tmem + lane_base + Cfg::kColO + wg * D + c * 32;
+                            __syncwarp();
+                            ptx::tmem_ld32(ta, ov);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+                            ptx::tmem_st32(ta, ov);
+                        }
+                    }
+                    weigh_half(1);
+                }
                 ptx::tc_fence_before_sync();
-                ptx::mbar_arrive(ptx::smem_addr(&p_ready[wg]));
+                ptx::mbar_arrive(ptx::smem_addr(&p_ready[2 * wg + 1]));
+                if (warp_live) {
+                    load_half(0);
+                    weigh_half(0);
+                    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                }
+                ptx::tc_fence_before_sync();
+                ptx::mbar_arrive(ptx::smem_addr(&p_ready[2 * wg]));
             }
             if (!ok) break;
             place0 += 2 * s.tiles;
-
-            // the next stretch's Q, while the last products run (ROWS: S_w of this
-            // stretch is complete; else that Q tile belongs to the stretch before)
-            have = walk.next(p, seg);
-            if (have) load_q(seg, nseg + 1);
+            if (have_next) q_loaded();
 
             if (worked) {
                 if (!warp_wait_phase(ptx::smem_addr(&o_done[wg]), o_count & 1, abort_flag,
@@ -701,7 +768,7 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             bool worked_b = false;
             if constexpr (ROWS) {
                 fa = l == 0.f ? 0.f : 1.f / l;
-                lse = l == 0.f ? -INFINITY : m_ref + log2f(l);
+                lse = l == 0.f ? -INFINITY : m_ref - WeightBias<T>::value + log2f(l);
             } else {
                 // both warpgroups are through: their halves of the softmax meet
                 if (!worked && !others_read()) break;
@@ -717,7 +784,7 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 const float inv = sum == 0.f ? 0.f : 1.f / sum;
                 fa *= inv;
                 fb *= inv;
-                lse = sum == 0.f ? -INFINITY : mm + log2f(sum);
+                lse = sum == 0.f ? -INFINITY : mm - WeightBias<T>::value + log2f(sum);
             }
             ptx::tc_fence_after_sync();
             const bool direct = s.tiles == s.unit_tiles;
@@ -798,6 +865,8 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             }
             seg_at += s.tiles;
             ++nseg;
+            s = next;
+            have = have_next;
         }
     }
 
