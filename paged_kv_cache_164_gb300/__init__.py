@@ -21,7 +21,6 @@ Calls (same names as the C entry points, without the ``pkv_`` prefix):
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
@@ -609,29 +608,56 @@ def gather(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Ten
     return k_out, v_out
 
 
-def _arg(t: Optional[torch.Tensor], name: str, dtype, device, optional: bool = False,
-         dense: bool = True) -> int:
-    """The address of a tensor argument that must be of ``dtype`` on ``device``."""
-    if t is None and optional:
-        return 0
+# The calls below are made several times a layer with a dozen tensors each, on
+# batches whose kernels take a few microseconds, so their checks are one pass of
+# cheap tests; what fails one is told apart afterwards.
+
+def _refuse(t, name: str, dtype, device: int):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device (there is no CPU path)")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, the other tensors on cuda:{device}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if dense and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _call_on(device, stream):
-    """(context that makes ``device`` current, the stream to launch on)."""
-    ctx = contextlib.nullcontext() if torch.cuda.current_device() == device.index \
-        else torch.cuda.device(device)
-    return ctx, (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+def _arg(t: torch.Tensor, name: str, dtype, device: int) -> int:
+    """The address of a dense tensor argument of ``dtype`` on CUDA device ``device``."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device and \
+            t.is_contiguous():
+        return t.data_ptr()
+    return _refuse(t, name, dtype, device)
+
+
+def _cuda_index(t: torch.Tensor, name: str, dims: int) -> int:
+    """The CUDA device index of a call's first tensor."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device (there is no CPU path)")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions")
+    return t.get_device()
+
+
+# The current stream's handle without a Stream object around it (1 us a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+def _stream_on(device: int, stream) -> int:
+    return _raw_stream(device) if stream is None else stream.cuda_stream
+
+
+def _run(fn, device: int, args) -> int:
+    """fn(*args) with CUDA device ``device`` current."""
+    if torch.cuda.current_device() == device:
+        return fn(*args)
+    with torch.cuda.device(device):
+        return fn(*args)
 
 
 def _keep(t: torch.Tensor, stream) -> torch.Tensor:
@@ -642,57 +668,58 @@ def _keep(t: torch.Tensor, stream) -> torch.Tensor:
     return t
 
 
-def _head_rows(t: torch.Tensor, name: str, dtype, device, heads: int, d: int):
-    """(address, elements between tokens) of [T, heads, d] rows whose heads are dense."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
-        raise ValueError(f"{name} must be [tokens, {heads}, {d}], got {tuple(t.shape)}")
-    ptr = _arg(t, name, dtype, device, dense=False)
+def _head_rows(t: torch.Tensor, name: str, dtype, device: int, shape):
+    """(address, elements between tokens) of [tokens, heads, d] rows whose heads are dense."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != device:
+        _refuse(t, name, dtype, device)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
     s0, s1, s2 = t.stride()
-    if t.numel() and (s2 != 1 or (heads > 1 and s1 != d)):
+    n, heads, d = shape
+    if n and (s2 != 1 or (heads > 1 and s1 != d)):
         raise ValueError(f"{name}: a token's heads must be dense")
-    return ptr, (s0 if t.shape[0] > 1 else heads * d)
+    return t.data_ptr(), (s0 if n > 1 else heads * d)
 
 
 def _norm_rope(name, q, k, v, positions, cos_sin, k_cache, v_cache, slot_mapping, q_weight,
                k_weight, eps, style, q_out, err_flag, stream, layout, scales):
     lib = load()
-    if not isinstance(q, torch.Tensor) or not q.is_cuda:
-        raise ValueError("q must be on a CUDA device (there is no CPU path)")
-    if q.dim() != 3:
-        raise ValueError("q must be [tokens, heads, head_dim]")
-    if style not in ("half", "interleaved"):
+    dev = _cuda_index(q, "q", 3)
+    if style != "half" and style != "interleaved":
         raise ValueError(f"style must be 'half' or 'interleaved', got {style!r}")
     t, h_q, d = q.shape
     nb, bs, h_kv, d2 = _cache_dims(k_cache, layout)
-    dt, dev = q.dtype, q.device
-    if d2 != d or v_cache.shape != k_cache.shape or k.shape[:1] != (t,) or \
-            v.shape[:1] != (t,) or slot_mapping.shape != (t,) or positions.shape != (t,) or \
-            cos_sin.dim() != 2:
+    dt, i32 = q.dtype, torch.int32
+    if d2 != d or v_cache.shape != k_cache.shape or slot_mapping.shape != (t,) or \
+            positions.shape != (t,) or cos_sin.dim() != 2:
         raise ValueError("inconsistent norm-rope-append shapes")
-    for w in (q_weight, k_weight):
-        if w is not None and w.shape != (d,):
-            raise ValueError("a norm's weight must be [head_dim]")
+    qw = kw = 0
+    if q_weight is not None:
+        qw = _arg(q_weight, "q_weight", dt, dev)
+    if k_weight is not None:
+        kw = _arg(k_weight, "k_weight", dt, dev)
+    if (qw and q_weight.shape != (d,)) or (kw and k_weight.shape != (d,)):
+        raise ValueError("a norm's weight must be [head_dim]")
     if q_out is None:
-        q_out = _keep(torch.empty((t, h_q, d), dtype=dt, device=dev), stream)
+        q_out = _keep(torch.empty((t, h_q, d), dtype=dt, device=q.device), stream)
     elif q_out.shape != q.shape:
         raise ValueError("q_out must have the shape of q")
     code = _kv_code(q, layout)
     cache_dt = torch.uint8 if scales else dt
-    qp, qs = _head_rows(q, "q", dt, dev, h_q, d)
-    kp, ks = _head_rows(k, "k", dt, dev, h_kv, d)
-    vp, vs = _head_rows(v, "v", dt, dev, h_kv, d)
-    ctx, st = _call_on(dev, stream)
-    with ctx:
-        r = getattr(lib, name)(
-            _arg(q_out, "q_out", dt, dev), qp, qs, kp, ks, vp, vs,
-            _arg(q_weight, "q_weight", dt, dev, True), _arg(k_weight, "k_weight", dt, dev, True),
-            float(eps), _arg(cos_sin, "cos_sin", torch.float32, dev), cos_sin.shape[0],
-            cos_sin.shape[1], int(style == "interleaved"),
-            _arg(positions, "positions", torch.int32, dev),
-            _arg(k_cache, "k_cache", cache_dt, dev), _arg(v_cache, "v_cache", cache_dt, dev),
-            _arg(slot_mapping, "slot_mapping", torch.int64, dev), t, nb, bs, h_q, h_kv, d,
-            *scales, code, _arg(err_flag, "err_flag", torch.int32, dev, True), st)
-    _check(r, name)
+    qp, qs = _head_rows(q, "q", dt, dev, (t, h_q, d))
+    kp, ks = _head_rows(k, "k", dt, dev, (t, h_kv, d))
+    vp, vs = _head_rows(v, "v", dt, dev, (t, h_kv, d))
+    npos, rd = cos_sin.shape
+    r = _run(getattr(lib, name), dev, (
+        _arg(q_out, "q_out", dt, dev), qp, qs, kp, ks, vp, vs, qw, kw, float(eps),
+        _arg(cos_sin, "cos_sin", torch.float32, dev), npos, rd,
+        style == "interleaved", _arg(positions, "positions", i32, dev),
+        _arg(k_cache, "k_cache", cache_dt, dev), _arg(v_cache, "v_cache", cache_dt, dev),
+        _arg(slot_mapping, "slot_mapping", torch.int64, dev), t, nb, bs, h_q, h_kv, d,
+        *scales, code, 0 if err_flag is None else _arg(err_flag, "err_flag", i32, dev),
+        _stream_on(dev, stream)))
+    if r:
+        _check(r, name)
     return q_out
 
 
@@ -748,34 +775,32 @@ def tree_plan(parents: torch.Tensor, context_lens: torch.Tensor, block_tables: t
     slots (-1 for an absent node).
     """
     lib = load()
-    if not isinstance(parents, torch.Tensor) or not parents.is_cuda:
-        raise ValueError("parents must be on a CUDA device (there is no CPU path)")
-    if parents.dim() != 2 or block_tables.dim() != 2:
-        raise ValueError("inconsistent tree-plan shapes")
+    dev = _cuda_index(parents, "parents", 2)
     b, t = parents.shape
-    dev, i32 = parents.device, torch.int32
+    i32 = torch.int32
     words = (t + 31) // 32
-    if context_lens.shape != (b,) or block_tables.shape[0] != b:
+    if block_tables.dim() != 2 or context_lens.shape != (b,) or block_tables.shape[0] != b:
         raise ValueError("inconsistent tree-plan shapes")
     if tree_mask is None:
-        tree_mask = _keep(torch.empty((b, t, words), dtype=i32, device=dev), stream)
+        tree_mask = _keep(torch.empty((b, t, words), dtype=i32, device=parents.device), stream)
     if positions is None:
-        positions = _keep(torch.empty((b, t), dtype=i32, device=dev), stream)
+        positions = _keep(torch.empty((b, t), dtype=i32, device=parents.device), stream)
     if slot_mapping is None:
-        slot_mapping = _keep(torch.empty((b, t), dtype=torch.int64, device=dev), stream)
+        slot_mapping = _keep(torch.empty((b, t), dtype=torch.int64, device=parents.device),
+                             stream)
     if tree_mask.shape != (b, t, words) or positions.shape != (b, t) or \
             slot_mapping.shape != (b, t):
         raise ValueError("inconsistent tree-plan outputs")
-    ctx, st = _call_on(dev, stream)
-    with ctx:
-        r = lib.pkv_tree_plan(
-            _arg(tree_mask, "tree_mask", i32, dev), _arg(positions, "positions", i32, dev),
-            _arg(slot_mapping, "slot_mapping", torch.int64, dev),
-            _arg(parents, "parents", i32, dev), _arg(context_lens, "context_lens", i32, dev),
-            _arg(block_tables, "block_tables", i32, dev), block_tables.shape[1],
-            int(max_context_len), b, t, int(num_blocks), int(block_size),
-            _arg(err_flag, "err_flag", i32, dev, True), st)
-    _check(r, "pkv_tree_plan")
+    r = _run(lib.pkv_tree_plan, dev, (
+        _arg(tree_mask, "tree_mask", i32, dev), _arg(positions, "positions", i32, dev),
+        _arg(slot_mapping, "slot_mapping", torch.int64, dev),
+        _arg(parents, "parents", i32, dev), _arg(context_lens, "context_lens", i32, dev),
+        _arg(block_tables, "block_tables", i32, dev), block_tables.shape[1],
+        int(max_context_len), b, t, int(num_blocks), int(block_size),
+        0 if err_flag is None else _arg(err_flag, "err_flag", i32, dev),
+        _stream_on(dev, stream)))
+    if r:
+        _check(r, "pkv_tree_plan")
     return tree_mask, positions, slot_mapping
 
 
@@ -804,44 +829,43 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     [1, T, ...] for one mask of all sequences).
     """
     lib = load()
-    if not isinstance(q, torch.Tensor) or not q.is_cuda:
-        raise ValueError("q must be on a CUDA device (there is no CPU path)")
-    if q.dim() != 4:
-        raise ValueError("q must be [sequences, nodes, heads, head_dim]")
+    dev = _cuda_index(q, "q", 4)
     b, t, h_q, d = q.shape
     nb, bs, h_kv, d2 = _cache_dims(k_cache, layout)
     words = (t + 31) // 32
     if d2 != d or v_cache.shape != k_cache.shape or block_tables.dim() != 2 or \
-            block_tables.shape[0] != b or context_lens.shape != (b,) or \
-            tree_mask.dim() != 3 or tree_mask.shape[0] not in (1, b) or \
-            tree_mask.shape[1:] != (t, words):
+            block_tables.shape[0] != b or context_lens.shape != (b,) or tree_mask.dim() != 3:
         raise ValueError("inconsistent tree attention shapes")
+    m0, m1, m2 = tree_mask.shape
+    s0, s1, s2 = tree_mask.stride()
+    if (m0 != b and m0 != 1) or m1 != t or m2 != words:
+        raise ValueError("inconsistent tree attention shapes")
+    dt, i32 = q.dtype, torch.int32
+    if tree_mask.dtype is not i32 or tree_mask.get_device() != dev:
+        _refuse(tree_mask, "tree_mask", i32, dev)
+    if m0 and ((words > 1 and s2 != 1) or (t > 1 and s1 != words)):
+        raise ValueError("tree_mask: the rows of a sequence must be dense")
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    dt, dev, i32 = q.dtype, q.device, torch.int32
     if out is None:
         out = _keep(torch.empty_like(q), stream)
     elif out.shape != q.shape:
         raise ValueError("out must have the shape of q")
-    s0, s1, s2 = tree_mask.stride()
-    if tree_mask.numel() and ((words > 1 and s2 != 1) or (t > 1 and s1 != words)):
-        raise ValueError("tree_mask: the rows of a sequence must be dense")
-    mask_stride = s0 if tree_mask.shape[0] > 1 else 0
-    ctx, st = _call_on(dev, stream)
-    with ctx:
-        if workspace is None:  # a given workspace is checked by the library itself
+    if workspace is None:  # a given workspace is checked by the library itself
+        with torch.cuda.device(dev):
             need = tree_attention_workspace_size(b, t, h_q, h_kv, d, bs, max_context_len)
-            workspace = _keep(torch.empty(need, dtype=torch.uint8, device=dev), stream)
-        r = lib.pkv_tree_attention(
-            _arg(out, "out", dt, dev), _arg(q, "q", dt, dev), _arg(k_cache, "k_cache", dt, dev),
-            _arg(v_cache, "v_cache", dt, dev), _arg(block_tables, "block_tables", i32, dev),
-            block_tables.shape[1], _arg(context_lens, "context_lens", i32, dev),
-            int(max_context_len), _arg(tree_mask, "tree_mask", i32, dev, dense=False),
-            mask_stride, b, t, nb, bs, h_q, h_kv, d, float(scale),
-            _arg(workspace, "workspace", workspace.dtype, dev),
-            workspace.numel() * workspace.element_size(), _kv_code(q, layout),
-            _arg(err_flag, "err_flag", i32, dev, True), st)
-    _check(r, "pkv_tree_attention")
+        workspace = _keep(torch.empty(need, dtype=torch.uint8, device=q.device), stream)
+    r = _run(lib.pkv_tree_attention, dev, (
+        _arg(out, "out", dt, dev), _arg(q, "q", dt, dev),
+        _arg(k_cache, "k_cache", dt, dev), _arg(v_cache, "v_cache", dt, dev),
+        _arg(block_tables, "block_tables", i32, dev), block_tables.shape[1],
+        _arg(context_lens, "context_lens", i32, dev), int(max_context_len),
+        tree_mask.data_ptr(), s0 if m0 > 1 else 0, b, t, nb, bs, h_q, h_kv, d, float(scale),
+        _arg(workspace, "workspace", workspace.dtype, dev), workspace.nbytes,
+        _kv_code(q, layout), 0 if err_flag is None else _arg(err_flag, "err_flag", i32, dev),
+        _stream_on(dev, stream)))
+    if r:
+        _check(r, "pkv_tree_attention")
     return out
 
 
@@ -857,10 +881,9 @@ def tree_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torc
     context_lens - tree_len + accepted_lens.
     """
     lib = load()
-    if not isinstance(k_cache, torch.Tensor) or not k_cache.is_cuda:
-        raise ValueError("k_cache must be on a CUDA device (there is no CPU path)")
+    dev = _cuda_index(k_cache, "k_cache", 4)
     nb, bs, h_kv, d = _cache_dims(k_cache, layout)
-    dt, dev, i32 = k_cache.dtype, k_cache.device, torch.int32
+    dt, i32 = k_cache.dtype, torch.int32
     if block_tables.dim() != 2 or accepted.dim() != 2:
         raise ValueError("inconsistent tree-commit shapes")
     b = block_tables.shape[0]
@@ -868,19 +891,20 @@ def tree_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torc
             accepted.shape[0] != b or accepted_lens.shape != (b,):
         raise ValueError("inconsistent tree-commit shapes")
     if new_context_lens is None:
-        new_context_lens = _keep(torch.empty(b, dtype=i32, device=dev), stream)
+        new_context_lens = _keep(torch.empty(b, dtype=i32, device=k_cache.device), stream)
     elif new_context_lens.shape != (b,):
         raise ValueError("new_context_lens must be [sequences]")
-    ctx, st = _call_on(dev, stream)
-    with ctx:
-        r = lib.pkv_tree_commit(
-            _arg(k_cache, "k_cache", dt, dev), _arg(v_cache, "v_cache", dt, dev),
-            _arg(block_tables, "block_tables", i32, dev), block_tables.shape[1],
-            _arg(context_lens, "context_lens", i32, dev), int(tree_len),
-            _arg(accepted, "accepted", i32, dev), _arg(accepted_lens, "accepted_lens", i32, dev),
-            accepted.shape[1], _arg(new_context_lens, "new_context_lens", i32, dev), b, nb, bs,
-            h_kv, d, _kv_code(k_cache, layout), _arg(err_flag, "err_flag", i32, dev, True), st)
-    _check(r, "pkv_tree_commit")
+    r = _run(lib.pkv_tree_commit, dev, (
+        _arg(k_cache, "k_cache", dt, dev), _arg(v_cache, "v_cache", dt, dev),
+        _arg(block_tables, "block_tables", i32, dev), block_tables.shape[1],
+        _arg(context_lens, "context_lens", i32, dev), int(tree_len),
+        _arg(accepted, "accepted", i32, dev), _arg(accepted_lens, "accepted_lens", i32, dev),
+        accepted.shape[1], _arg(new_context_lens, "new_context_lens", i32, dev), b, nb, bs,
+        h_kv, d, _kv_code(k_cache, layout),
+        0 if err_flag is None else _arg(err_flag, "err_flag", i32, dev),
+        _stream_on(dev, stream)))
+    if r:
+        _check(r, "pkv_tree_commit")
     return new_context_lens
 
 

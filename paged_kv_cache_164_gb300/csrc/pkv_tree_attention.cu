@@ -9,24 +9,29 @@
 // between them: running reference m, sum l and accumulator O per row, one
 // division at the end.
 //
-// Tiles: 128 rows x 128 tokens.  Two softmax warpgroups, one thread per row,
-// each with its own S and O in tensor memory (all 512 columns):
-//   S_w = Q K^T     tcgen05.mma 128 x 128 x D, Q and K from shared memory
+// Tiles: 128 rows x 64 tokens.  Two softmax warpgroups, one thread per row, each
+// with two S tiles and an O of its own in tensor memory (all 512 columns):
+//   S_w = Q K^T     tcgen05.mma 128 x 64 x D, Q and K from shared memory
 //   softmax         a thread reads its row of S, writes P over it
 //   O_w += P V      P from tensor memory, as hi + lo 16-bit terms (a single
 //                   16-bit P would cost the outputs of short contexts half
 //                   their precision), V from shared memory
-// While one warpgroup is at its softmax, the tensor cores work for the other.
+// A warpgroup's next S is made while it is at its softmax, and the other's
+// products run meanwhile: with one S of 128 tokens a warpgroup, which its P
+// frees only for the step after, the step was a chain of S, softmax and P V
+// (32 nodes on long contexts of the Llama-70B layer: LONG_BEFORE us; so LONG_AFTER us).
 // ROWS (more than 128 rows per KV head): the warpgroups take 128 rows each of
 // the same tokens, so 256 rows meet a K/V tile that was read once.  Otherwise
 // they take the same rows and every other tile, and meet at the end.
-// Warp 8 streams K and V tiles by TMA through the block table into a ring of
-// tile slots; one thread of warp 9 issues all the products.
+// Four warps stream the K and V tiles by TMA through the block table into a ring
+// of tile slots (a warp takes about 95 cycles to issue a box, and the HBM rate
+// leaves 88 for the 2 KB boxes of 16-token pages), and one warp each issues a
+// warpgroup's products.
 //
-// Work: the (sequence, KV head, row block) units' tiles lie on one line, and
-// each of the persistent CTAs (one an SM) takes an equal stretch of it, so
-// ragged contexts and few long ones fill the SMs alike.  A unit inside one
-// stretch is written to the output at once; one that is cut leaves a partial
+// Work: the (sequence, KV head, row block) units' stretches of 128 tokens lie on
+// one line, and each of the persistent CTAs (one an SM) takes an equal part of
+// it, so ragged contexts and few long ones fill the SMs alike.  A unit inside
+// one part is written to the output at once; one that is cut leaves a partial
 // (normalised O and its log-sum-exp) per CTA, at most two a CTA, and
 // tree_merge_kernel joins them.
 //
@@ -69,53 +74,60 @@ struct TreeParams {
     float scale_sign;    // 1, -1 or 0
 };
 
-constexpr int kTreeTile = 128;                     // rows (MMA M) and tokens of a tile
+constexpr int kTreeRows = 128;                     // rows of a tile (MMA M)
+constexpr int kTreeTokens = 64;                    // tokens of a tile
+constexpr int kTreePair = 2 * kTreeTokens;         // tokens of a place on the line of work
 constexpr int kTreeSoftmaxWarps = 8;               // two warpgroups
-constexpr int kTreeTmaWarpK = kTreeSoftmaxWarps;
-constexpr int kTreeTmaWarpV = kTreeSoftmaxWarps + 1;
-constexpr int kTreeMmaWarp = kTreeSoftmaxWarps + 2;
-constexpr int kTreeThreads = (kTreeSoftmaxWarps + 4) * 32;  // one warp fills the third warpgroup
-// Registers: a softmax thread holds a row of S (128 values), which does not fit
-// the 168 a thread that 384 threads get at launch; the third warpgroup hands
-// over what it does not need (2 x 216 + 72 = 3 x 168).
-constexpr int kTreeLaunchRegs = 168, kTreeSoftmaxRegs = 216, kTreeOtherRegs = 72;
-static_assert(2 * kTreeSoftmaxRegs + kTreeOtherRegs <= 3 * kTreeLaunchRegs, "register shares");
+constexpr int kTreeTmaWarp = kTreeSoftmaxWarps;    // four producers: K and V of even and odd tiles
+constexpr int kTreeMmaWarp = kTreeTmaWarp + 4;     // an issuer for each softmax warpgroup
+constexpr int kTreeThreads = (kTreeSoftmaxWarps + 8) * 32;  // the last two warps only fill up
+// Registers: the other warpgroups hand over what they do not need, so that a
+// softmax thread's row of S and its copies stay in registers (the shares add up
+// to the 128 a thread of the launch).
+constexpr int kTreeLaunchRegs = 128, kTreeSoftmaxRegs = 184, kTreeOtherRegs = 72;
+static_assert(2 * kTreeSoftmaxRegs + 2 * kTreeOtherRegs <= 4 * kTreeLaunchRegs, "register shares");
 // Scores may exceed a row's reference by this much (base 2) before it moves: P
 // stays below 2^8, and O / l and the log-sum-exp come out the same.
 constexpr float kTreeLazyLog2 = 8.f;
-constexpr int kTreeBoxes = kTreeTile / kStageTokens;  // TMA boxes along a tile's tokens
+constexpr int kTreeBoxes = kTreeTokens / kStageTokens;  // TMA boxes along a tile's tokens
 
 template <int D>
 struct TreeTileCfg {
-    static constexpr int kRegions = D / 64;                    // 128-byte column blocks
-    static constexpr int kRegionBytes = kTreeTile * 128;
-    static constexpr int kSlotBytes = kRegions * kRegionBytes;  // K or V of a tile; Q of 128 rows
-    static constexpr int kSlots = D == 128 ? 5 : 8;
-    static constexpr int kQBytes = 2 * kSlotBytes;
-    static constexpr int kXchBytes = 2 * kTreeTile * 8;         // (m, l) of each half and row
-    // full[slots], empty[slots], s_full[2], p_ready[2][2], o_done[2], q_ready, met, o_free, drain
-    static constexpr int kBarriers = 2 * kSlots + 12;
-    static constexpr int kSmemBytes =
-        kQBytes + kSlots * kSlotBytes + kXchBytes + kBarriers * 8 + 256;
-    static constexpr uint32_t kColO = 2 * kTreeTile;  // S_0, S_1, then O_0, O_1
+    static constexpr int kRegions = D / 64;                     // 128-byte column blocks
+    static constexpr int kQRegionBytes = kTreeRows * 128;
+    static constexpr int kQTileBytes = kRegions * kQRegionBytes;
+    static constexpr int kRegionBytes = kTreeTokens * 128;
+    static constexpr int kSlotBytes = kRegions * kRegionBytes;  // K or V of a tile
+    static constexpr int kSlots = D == 128 ? 10 : 16;
+    // The output's way through shared memory, 32 rows x 32 columns a warp.  D =
+    // 128 leaves no room for it: it takes the Q tile that the stretch is done with.
+    static constexpr int kStageBytes = D == 128 ? 0 : kTreeSoftmaxWarps * 4096;
+    static constexpr int kXchBytes = 2 * kTreeRows * 8;         // (m, l) of each half and row
+    // full[slots], empty[slots], s_full[2][2], p_ready[2][2], pv_done[2][2], drain[2],
+    // q_ready, met, o_free
+    static constexpr int kBarriers = 2 * kSlots + 17;
+    static constexpr int kSmemBytes = 2 * kQTileBytes + kSlots * kSlotBytes + kStageBytes +
+                                      kXchBytes + kBarriers * 8 + 256;
+    static constexpr uint32_t kColO = 4 * kTreeTokens;  // S of (warpgroup, buffer), then O
     static_assert(kColO + 2 * D <= 512, "tensor memory layout");
     static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
 };
 
 __host__ __device__ inline int tree_tiles(int n) {
-    return n <= 0 ? 1 : (n + kTreeTile - 1) / kTreeTile;  // an empty context has a tile of nothing
+    // places on the line (pairs of tiles); an empty context has one of nothing
+    return n <= 0 ? 1 : (n + kTreePair - 1) / kTreePair;
 }
 
-// A stretch of one unit's tiles.
+// A stretch of one unit's places.
 struct TreeSeg {
     int b, g, rb;        // sequence, KV head, row block
     int n;               // context length
-    int tile0, tiles;    // first tile and tiles of the stretch
-    int unit_tiles;
+    int tile0, tiles;    // first place and places of the stretch
+    int unit_tiles;      // the unit's places
 };
 
-// Walks a CTA's stretch of the line of tiles (sequence, KV head, row block,
-// tile; the last fastest).  Every thread that takes part walks it by itself.
+// Walks a CTA's part of the line of places (sequence, KV head, row block,
+// place; the last fastest).  Every thread that takes part walks it by itself.
 struct TreeWalk {
     int64_t at, end;
     int b, unit, tile, n;
@@ -143,15 +155,26 @@ struct TreeWalk {
     }
 };
 
-// K and V tiles of a stretch of nt tiles lie in the ring in the order in which
-// the products take them.  ROWS: K0 V0 K1 V1 ...; else both warpgroups' first
-// K tiles come first: K0 K1 V0 K2 V1 ... V(nt-1).
-template <bool ROWS>
-__device__ __forceinline__ int k_place(int j) { return ROWS ? 2 * j : (j == 0 ? 0 : 2 * j - 1); }
-template <bool ROWS>
-__device__ __forceinline__ int v_place(int j, int nt) {
-    return ROWS ? 2 * j + 1 : (j < nt - 1 ? 2 * j + 2 : 2 * nt - 1);
+// Where tile j of a stretch of nt tiles lies in the ring of slots.  ROWS: one
+// ring, which both warpgroups' issuers walk; else a ring for each warpgroup,
+// half of the slots (tile j belongs to warpgroup j % 2).  A ring's places are in
+// the order in which its issuer takes them, S two steps ahead: K0 K1 V0 K2 V1
+// ....  An issuer that took every other place of one ring could meet a slot
+// whose fill before the one it waits for is still to come, and a wait by the
+// phase's parity would not tell the two apart.
+struct TreePlace {
+    int slot, phase;
+};
+template <bool ROWS, int NS>
+__device__ __forceinline__ TreePlace tree_place(bool is_v, int place0, int j, int nt) {
+    constexpr int kRing = ROWS ? NS : NS / 2;
+    const int k = ROWS ? j : j >> 1, n = ROWS ? nt : nt >> 1;  // tile k of the ring's n
+    const int at = place0 + (is_v ? min(k + 2, n) + k : (k < 2 ? k : 2 * k - 1));
+    return {at % kRing + (ROWS ? 0 : (j & 1) * kRing), at / kRing};
 }
+// A ring's places in a stretch (a K and a V for each of its tiles).
+template <bool ROWS>
+__device__ __forceinline__ int tree_places(int nt) { return ROWS ? 2 * nt : nt; }
 
 // A row's weights are 2^(score - reference + bias).  fp16 has few exponents:
 // with the bias its largest weight is 2^(8 + 7), and what subnormals lose of
@@ -191,28 +214,30 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
     using Cfg = TreeTileCfg<D>;
     constexpr int R = Cfg::kRegions;
     constexpr int NS = Cfg::kSlots;
-    constexpr int TT = kTreeTile;
-    constexpr int kUnitRows = ROWS ? 2 * TT : TT;
+    constexpr int TR = kTreeRows;
+    constexpr int TT = kTreeTokens;
+    constexpr int kUnitRows = ROWS ? 2 * TR : TR;
 
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* sq = smem;  // two Q tiles [region][128 rows][128 B], swizzled
-    uint8_t* ring = sq + Cfg::kQBytes;
-    float2* xch = reinterpret_cast<float2*>(ring + NS * Cfg::kSlotBytes);
-    uint64_t* full_bar = reinterpret_cast<uint64_t*>(ring + NS * Cfg::kSlotBytes + Cfg::kXchBytes);
+    uint8_t* ring = sq + 2 * Cfg::kQTileBytes;
+    uint8_t* stage = ring + NS * Cfg::kSlotBytes;
+    float2* xch = reinterpret_cast<float2*>(stage + Cfg::kStageBytes);
+    uint64_t* full_bar = reinterpret_cast<uint64_t*>(stage + Cfg::kStageBytes + Cfg::kXchBytes);
     uint64_t* empty_bar = full_bar + NS;
-    uint64_t* s_full = empty_bar + NS;  // [2]
-    uint64_t* p_ready = s_full + 2;     // [warpgroup][half of the tile's tokens]
-    uint64_t* o_done = p_ready + 4;     // [2]: a stretch's last O_w += P V is done
-    uint64_t* q_ready = o_done + 2;
+    uint64_t* s_full = empty_bar + NS;  // [warpgroup][buffer]
+    uint64_t* p_ready = s_full + 4;     // [warpgroup][buffer]
+    uint64_t* pv_done = p_ready + 4;    // [warpgroup][buffer]
+    uint64_t* drain = pv_done + 4;      // [warpgroup]
+    uint64_t* q_ready = drain + 2;
     uint64_t* met = q_ready + 1;        // both warpgroups are through the stretch (not ROWS)
     uint64_t* o_free = met + 1;         // both have read O_0 and O_1 (not ROWS)
-    uint64_t* drain = o_free + 1;
     int* words = reinterpret_cast<int*>(full_bar + Cfg::kBarriers);
     volatile int* abort_flag = words;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(words + 1);
-    int* s_start = words + 2;            // sequence and (two words) its first tile on the line
-    volatile int* s_bad = words + 6;     // [4]: 1 + the stretch (mod 4 its place) with a bad V value
-    int* s_scan = words + 10;            // [12]
+    int* s_start = words + 2;           // first sequence, and the first place in its part
+    volatile int* s_bad = words + 6;    // [4]: 1 + the stretch (its place: mod 4) with a bad V
+    int* s_scan = words + 10;           // [16]
 
     const int tid = threadIdx.x;
     const int warp = tid >> 5;
@@ -225,18 +250,18 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) {
             ptx::mbar_init(ptx::smem_addr(&full_bar[i]), 1);
-            ptx::mbar_init(ptx::smem_addr(&empty_bar[i]), 1);
+            ptx::mbar_init(ptx::smem_addr(&empty_bar[i]), ROWS ? 2 : 1);  // readers of a tile
         }
-        for (int w = 0; w < 2; ++w) {
-            ptx::mbar_init(ptx::smem_addr(&s_full[w]), 1);
-            ptx::mbar_init(ptx::smem_addr(&p_ready[2 * w]), TT);
-            ptx::mbar_init(ptx::smem_addr(&p_ready[2 * w + 1]), TT);
-            ptx::mbar_init(ptx::smem_addr(&o_done[w]), 1);
+        for (int i = 0; i < 4; ++i) {
+            ptx::mbar_init(ptx::smem_addr(&s_full[i]), 1);
+            ptx::mbar_init(ptx::smem_addr(&p_ready[i]), TR);
+            ptx::mbar_init(ptx::smem_addr(&pv_done[i]), 1);
         }
-        ptx::mbar_init(ptx::smem_addr(q_ready), 2 * TT);
-        ptx::mbar_init(ptx::smem_addr(met), 2 * TT);
-        ptx::mbar_init(ptx::smem_addr(o_free), 2 * TT);
-        ptx::mbar_init(ptx::smem_addr(drain), 1);
+        ptx::mbar_init(ptx::smem_addr(&drain[0]), 1);
+        ptx::mbar_init(ptx::smem_addr(&drain[1]), 1);
+        ptx::mbar_init(ptx::smem_addr(q_ready), 2 * TR);
+        ptx::mbar_init(ptx::smem_addr(met), 2 * TR);
+        ptx::mbar_init(ptx::smem_addr(o_free), 2 * TR);
         *abort_flag = 0;
         for (int i = 0; i < 4; ++i) s_bad[i] = 0;
         ptx::fence_barrier_init();
@@ -252,12 +277,12 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
 #endif
     ptx::grid_dependency_wait();
 
-    // The line of tiles: a thread sums the tiles of a run of sequences, a scan
-    // places the runs, and the thread whose run holds this CTA's first tile
+    // The line of places: a thread sums those of a run of sequences, a scan
+    // places the runs, and the thread whose run holds this CTA's first place
     // finds its sequence.
     const int per = (p.num_seqs + kTreeThreads - 1) / kTreeThreads;
     const int b_lo = min(p.num_seqs, tid * per), b_hi = min(p.num_seqs, b_lo + per);
-    int mine = 0;  // at most INT_MAX / 128 tiles a sequence, 65535 sequences: the host checks
+    int mine = 0;  // the host checks that all sequences' places fit an int
     for (int b = b_lo; b < b_hi; ++b)
         mine += tree_tiles(clamped_len(__ldg(p.context_lens + b), p.cap));
     int incl = mine;
@@ -277,7 +302,7 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
     }
     const int units = p.num_kv_heads * p.row_blocks;
     const int64_t line = (int64_t)total * units;
-    const int64_t ctas = min((int64_t)gridDim.x, line);  // with a tile at least; the rest idle
+    const int64_t ctas = min((int64_t)gridDim.x, line);  // with a place at least; the rest idle
     const int64_t start = min((int64_t)blockIdx.x, ctas) * line / ctas;
     const int64_t stop = min((int64_t)blockIdx.x + 1, ctas) * line / ctas;
     if (start >= (int64_t)before * units && start < (int64_t)(before + mine) * units) {
@@ -291,7 +316,7 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             ++b;
         }
         s_start[0] = b;
-        s_start[1] = (int)(start - first);  // tiles into the sequence's part of the line
+        s_start[1] = (int)(start - first);
     }
     __syncthreads();
     const uint32_t tmem = *tmem_slot;
@@ -312,41 +337,42 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
     if (warp >= kTreeSoftmaxWarps) {
         ptx::reg_dec<kTreeOtherRegs>();
         TreeSeg seg;
-        if (warp == kTreeTmaWarpK || warp == kTreeTmaWarpV) {
-            // ------------------------------------------------------------ producer
-            // One warp loads the K tiles, one the V tiles; a lane issues one box (16
-            // tokens x 64 dims).
+        if (warp < kTreeMmaWarp) {
+            // ------------------------------------------------------------ producers
+            // A warp loads the K or the V of every other tile; a lane issues one box
+            // (16 tokens x 64 dims).
+            const bool is_v = warp & 1;
+            const int odd = (warp - kTreeTmaWarp) >> 1;
+            const CUtensorMap* map = is_v ? &tm_v : &tm_k;
             const uint64_t policy =
                 p.row_blocks > 1 ? ptx::l2_policy_evict_last() : ptx::l2_policy_evict_first();
             const int bx = lane / R, rr = lane % R;
             const bool loads = lane < kTreeBoxes * R;
-            const bool is_v = warp == kTreeTmaWarpV;
-            const CUtensorMap* map = is_v ? &tm_v : &tm_k;
-            int place0 = 0;  // places of the stretches before this one
-            int issued = 0;     // one past this warp's last place filled
-            uint32_t own = 0u;  // bit i: place issued - 1 - i is this warp's
+            int place0 = 0;      // a ring's places of the stretches before this one
+            uint64_t filled = 0; // slots with a copy of this warp's that may be in flight,
+            uint64_t parity = 0; // and its phase's parity
             bool ok = true;
             while (ok && walk.next(p, seg)) {
+                const int nt = 2 * seg.tiles;
                 const int32_t* table = p.block_tables + (int64_t)seg.b * p.max_blocks_per_seq;
+                // the block of this lane's box of tile j, as the table has it (-1: none)
                 auto box_block = [&](int j) {
-                    const int tok = (seg.tile0 + j) * TT + bx * kStageTokens;
-                    if (!loads || j >= seg.tiles || tok >= seg.n) return -1;
-                    const int blk = __ldg(table + (tok >> bs_shift));
-                    if (blk < 0 || blk >= p.num_blocks) {
-                        if (!is_v) flag_error(p.err_flag, PKV_EFLAG_BLOCK_ID);
-                        return -1;
-                    }
-                    return blk;
+                    const int tok = seg.tile0 * kTreePair + j * TT + bx * kStageTokens;
+                    return loads && j < nt && tok < seg.n ? __ldg(table + (tok >> bs_shift)) : -1;
                 };
                 auto load = [&](int j, int blk) {
-                    const int at =
-                        place0 + (is_v ? v_place<ROWS>(j, seg.tiles) : k_place<ROWS>(j));
-                    const int slot = at % NS;
-                    if (at >= NS && !warp_wait_phase(ptx::smem_addr(&empty_bar[slot]),
-                                                     ((at / NS) - 1) & 1, abort_flag, p.err_flag))
+                    const int tok = seg.tile0 * kTreePair + j * TT + bx * kStageTokens;
+                    if (blk < 0 || blk >= p.num_blocks) {
+                        if (!is_v && loads && tok < seg.n)
+                            flag_error(p.err_flag, PKV_EFLAG_BLOCK_ID);
+                        blk = -1;
+                    }
+                    const auto [slot, phase] = tree_place<ROWS, NS>(is_v, place0, j, nt);
+                    if (phase > 0 && !warp_wait_phase(ptx::smem_addr(&empty_bar[slot]),
+                                                      (phase - 1) & 1, abort_flag, p.err_flag))
                         return false;
 #ifdef PKV_DEBUG
-                    if (at >= NS) {
+                    if (phase > 0) {
                         ptx::tc_fence_after_sync();
                         poison_smem(ring + slot * Cfg::kSlotBytes, Cfg::kSlotBytes, lane, 32);
                         __syncwarp();
@@ -362,129 +388,125 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                     }
                     __syncwarp();
                     if (blk >= 0) {
-                        const int tok = (seg.tile0 + j) * TT + bx * kStageTokens;
                         load_kv_box(ring_addr + slot * Cfg::kSlotBytes + rr * Cfg::kRegionBytes +
                                         bx * kStageTokens * 128,
                                     map, fb, rr * 64, seg.g, tok & (bs - 1), blk, p.hnd, policy);
                     }
-                    own = (at + 1 - issued < 32 ? own << (at + 1 - issued) : 0u) | 1u;
-                    issued = at + 1;
+                    filled |= 1ull << slot;
+                    parity = (parity & ~(1ull << slot)) | ((uint64_t)(phase & 1) << slot);
                     return true;
                 };
-                int blk = box_block(0);
-                for (int j = 0; j < seg.tiles && ok; ++j) {
-                    const int blk_next = box_block(j + 1);
+                // read a turn ahead: a table entry takes about as long as a tile's turn
+                int blk = box_block(odd), blk_next = box_block(odd + 2);
+                for (int j = odd; j < nt && ok; j += 2) {
+                    const int far = box_block(j + 4);
                     ok = load(j, blk);
                     blk = blk_next;
+                    blk_next = far;
                 }
-                place0 += 2 * seg.tiles;
+                place0 += tree_places<ROWS>(nt);
             }
             if (lane == 0 && *abort_flag) {
                 // wait (bounded) for this warp's copies in flight before leaving
-                for (int at = max(0, issued - NS); at < issued; ++at) {
-                    if (!((own >> (issued - 1 - at)) & 1u)) continue;
-                    const uint32_t fb = ptx::smem_addr(&full_bar[at % NS]);
-                    const uint64_t t0 = ptx::globaltimer();
-                    while (!ptx::mbar_try_wait(fb, (at / NS) & 1) &&
+                const uint64_t t0 = ptx::globaltimer();
+                for (int i = 0; i < NS; ++i) {
+                    if (!((filled >> i) & 1)) continue;
+                    while (!ptx::mbar_try_wait(ptx::smem_addr(&full_bar[i]),
+                                               (uint32_t)(parity >> i) & 1u) &&
                            ptx::globaltimer() - t0 < kWaitLimitNs) {
                     }
                 }
             }
-        } else if (warp == kTreeMmaWarp) {
-            // ------------------------------------------------------------ MMA issuer
-            // The whole warp walks the steps, so that addresses and descriptors are
-            // uniform values; one elected lane issues.  (One lane alone walking
-            // them took 110 cycles a product to issue, of the 64 that it runs.)
+        } else if (warp < kTreeMmaWarp + 2) {
+            // ------------------------------------------------------------ MMA issuers
+            // One warp per softmax warpgroup.  The whole warp walks the steps, so
+            // that addresses and descriptors are uniform values; one elected lane
+            // issues.  (One lane alone walking them took 110 cycles a product to
+            // issue, of the 64 that it runs.)
             constexpr uint32_t fmt = F16Format<T>::value;
-            constexpr uint32_t idesc_s = mma_idesc(fmt, TT, TT, false);
-            constexpr uint32_t idesc_o = mma_idesc(fmt, TT, D, true);
+            constexpr uint32_t idesc_s = mma_idesc(fmt, TR, TT, false);
+            constexpr uint32_t idesc_o = mma_idesc(fmt, TR, D, true);
+            const int w = __shfl_sync(0xffffffffu, warp - kTreeMmaWarp, 0);
             // descriptors of the first slots: a byte offset adds its sixteenth (the
             // address field stays within its 14 bits: shared memory is 228 KB)
             const uint64_t qdesc = ptx::smem_desc_sw128(q_addr, 16, 1024);
             const uint64_t kdesc = ptx::smem_desc_sw128(ring_addr, 16, 1024);
             const uint64_t vdesc = ptx::smem_desc_sw128(ring_addr, Cfg::kRegionBytes, 1024);
             const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            const uint32_t acc_o = tm + Cfg::kColO + w * D;
             int place0 = 0, nseg = 0;
-            int p_count[2] = {0, 0};
+            int step0 = 0;  // this warpgroup's steps before the stretch
             bool ok = true;
             while (ok && walk.next(p, seg)) {
-                const int nt = __shfl_sync(0xffffffffu, seg.tiles, 0);
-                // step x: ROWS: warpgroup x % 2 at tile x / 2; else at tile x
-                const int steps = ROWS ? 2 * nt : nt;
+                const int nt = __shfl_sync(0xffffffffu, 2 * seg.tiles, 0);
+                const int steps = ROWS ? nt : nt / 2;  // step k: tile k, or tile 2k + w
                 auto wait = [&](uint64_t* bar, int parity) {
                     return warp_wait_phase(ptx::smem_addr(bar), parity & 1, abort_flag,
                                            p.err_flag);
                 };
-                auto issue_s = [&](int x) {
-                    const int w = x & 1, j = ROWS ? x >> 1 : x;
-                    const int at = place0 + k_place<ROWS>(j);
-                    const int slot = at % NS;
-                    if (!wait(&full_bar[slot], at / NS)) return false;
+                auto issue_s = [&](int k) {
+                    const auto [slot, phase] =
+                        tree_place<ROWS, NS>(false, place0, ROWS ? k : 2 * k + w, nt);
+                    const int buf = (step0 + k) & 1;
+                    if (!wait(&full_bar[slot], phase)) return false;
                     ptx::tc_fence_after_sync();
                     const uint64_t kd = kdesc + (uint32_t)(slot * (Cfg::kSlotBytes / 16));
                     const uint64_t qd =
-                        qdesc + (uint32_t)((ROWS ? w : nseg & 1) * (Cfg::kSlotBytes / 16));
-                    const uint32_t acc = tm + w * TT;
+                        qdesc + (uint32_t)((ROWS ? w : nseg & 1) * (Cfg::kQTileBytes / 16));
+                    const uint32_t acc = tm + (2 * w + buf) * TT;
                     if (ptx::elect_one()) {
 #pragma unroll
-                        for (int ks = 0; ks < D / 16; ++ks) {
-                            const uint32_t off =
-                                (ks / 4) * (Cfg::kRegionBytes / 16) + (ks % 4) * (32 / 16);
-                            ptx::tc_mma_f16(acc, qd + off, kd + off, idesc_s, ks > 0 ? 1u : 0u);
-                        }
-                        ptx::tc_commit(ptx::smem_addr(&s_full[w]));
-                        if (!ROWS || w == 1) ptx::tc_commit(ptx::smem_addr(&empty_bar[slot]));
+                        for (int ks = 0; ks < D / 16; ++ks)
+                            ptx::tc_mma_f16(
+                                acc, qd + (ks / 4) * (Cfg::kQRegionBytes / 16) + (ks % 4) * 2,
+                                kd + (ks / 4) * (Cfg::kRegionBytes / 16) + (ks % 4) * 2, idesc_s,
+                                ks > 0 ? 1u : 0u);
+                        ptx::tc_commit(ptx::smem_addr(&s_full[2 * w + buf]));
+                        ptx::tc_commit(ptx::smem_addr(&empty_bar[slot]));
                     }
                     __syncwarp();
                     return true;
                 };
-                auto issue_pv = [&](int x) {
-                    const int w = x & 1, j = ROWS ? x >> 1 : x;
-                    const int at = place0 + v_place<ROWS>(j, nt);
-                    const int slot = at % NS;
-                    const int phase = p_count[w]++;
-                    if (!wait(&full_bar[slot], at / NS)) return false;
+                auto issue_pv = [&](int k) {
+                    const auto [slot, phase] =
+                        tree_place<ROWS, NS>(true, place0, ROWS ? k : 2 * k + w, nt);
+                    const int buf = (step0 + k) & 1;
+                    if (!wait(&full_bar[slot], phase) ||
+                        !wait(&p_ready[2 * w + buf], (step0 + k) >> 1))
+                        return false;
+                    ptx::tc_fence_after_sync();
                     const uint64_t vd = vdesc + (uint32_t)(slot * (Cfg::kSlotBytes / 16));
-                    const uint32_t acc = tm + Cfg::kColO + w * D;
-                    const uint32_t pt = tm + w * TT;
-                    // the tokens' upper half is written first
+                    const uint32_t pt = tm + (2 * w + buf) * TT;
+                    if (ptx::elect_one()) {
 #pragma unroll
-                    for (int half = 1; half >= 0; --half) {
-                        if (!wait(&p_ready[2 * w + half], phase)) return false;
-                        ptx::tc_fence_after_sync();
-                        if (ptx::elect_one()) {
-#pragma unroll
-                            for (int kt = half * 4; kt < half * 4 + 4; ++kt) {
-                                // tokens 16 kt ..: of each 32 tokens of P, 16 columns of
-                                // hi pairs, then 16 of lo pairs
-                                const uint32_t a = pt + (kt / 2) * 32 + (kt % 2) * 8;
-                                const uint64_t v = vd + (uint32_t)(kt * 16 * 128 / 16);
-                                ptx::tc_mma_f16_ts(acc, a, v, idesc_o,
-                                                   (x >= 2 || kt != 4) ? 1u : 0u);
-                                ptx::tc_mma_f16_ts(acc, a + 16, v, idesc_o, 1u);
-                            }
-                            if (half == 0) {
-                                if (!ROWS || w == 1) ptx::tc_commit(ptx::smem_addr(&empty_bar[slot]));
-                                if (x + 2 >= steps) ptx::tc_commit(ptx::smem_addr(&o_done[w]));
-                            }
+                        for (int kt = 0; kt < TT / 16; ++kt) {
+                            // tokens 16 kt ..: of each 32 tokens of P, 16 columns of hi
+                            // pairs, then 16 of lo pairs
+                            const uint32_t a = pt + (kt / 2) * 32 + (kt % 2) * 8;
+                            const uint64_t v = vd + (uint32_t)(kt * 16 * 128 / 16);
+                            ptx::tc_mma_f16_ts(acc_o, a, v, idesc_o, (k > 0 || kt > 0) ? 1u : 0u);
+                            ptx::tc_mma_f16_ts(acc_o, a + 16, v, idesc_o, 1u);
                         }
-                        __syncwarp();
+                        ptx::tc_commit(ptx::smem_addr(&pv_done[2 * w + buf]));
+                        ptx::tc_commit(ptx::smem_addr(&empty_bar[slot]));
                     }
+                    __syncwarp();
                     return true;
                 };
-                // The tensor core runs the products in the order of their issue:
-                // S_w(next) over P_w comes after the O_w += P_w V that reads it.
+                // The tensor core runs a warp's products in the order of their issue:
+                // S over a buffer's P comes after the O += P V that reads it.
                 ok = wait(q_ready, nseg) && issue_s(0) && (steps < 2 || issue_s(1));
-                for (int x = 0; x < steps && ok; ++x)
-                    ok = issue_pv(x) && (x + 2 >= steps || issue_s(x + 2));
-                place0 += 2 * nt;
+                for (int k = 0; k < steps && ok; ++k)
+                    ok = issue_pv(k) && (k + 2 >= steps || issue_s(k + 2));
+                place0 += tree_places<ROWS>(nt);
+                step0 += steps;
                 ++nseg;
             }
             // every product has completed before the tensor memory is released
-            if (ptx::elect_one()) ptx::tc_commit(ptx::smem_addr(drain));
+            if (ptx::elect_one()) ptx::tc_commit(ptx::smem_addr(&drain[w]));
             __syncwarp();
             const uint64_t t0 = ptx::globaltimer();
-            while (!ptx::mbar_try_wait(ptx::smem_addr(drain), 0) &&
+            while (!ptx::mbar_try_wait(ptx::smem_addr(&drain[w]), 0) &&
                    ptx::globaltimer() - t0 < kWaitLimitNs) {
             }
         }
@@ -494,39 +516,67 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
         const int wg = warp / 4;                  // warpgroup
         const int srow = 32 * (warp % 4) + lane;  // row of the tile = tensor-memory lane
         const uint32_t lane_base = (uint32_t)(32 * (warp % 4)) << 16;
-        const uint32_t s_col = tmem + lane_base + wg * TT;
-        const int urow = ROWS ? wg * TT + srow : srow;  // row of the unit
-        int place0 = 0, nseg = 0, steps_done = 0, o_count = 0;
+        const uint32_t o_col = tmem + lane_base + Cfg::kColO;
+        const int urow = ROWS ? wg * TR + srow : srow;  // row of the unit
+        int place0 = 0, nseg = 0;
+        int step = 0;  // this warpgroup's steps so far
         bool ok = true;
 
-        // Query row r of the unit: node r / group, head g * group + r % group.
-        auto row_of = [&](const TreeSeg& s, int& node, int64_t& orow) {
+        // Query row r of the unit: node r / group, head g * group + r % group; its
+        // place in the (node, query head) rows of the sequence, or -1 past them.
+        auto row_of = [&](const TreeSeg& s, int& node) {
             const int r = s.rb * kUnitRows + urow;
-            const bool live = r < rows;
-            node = live ? r / p.group : 0;
-            orow = ((int64_t)s.b * p.tree_len + node) * p.num_q_heads + s.g * p.group +
-                   (live ? r - node * p.group : 0);
-            return live;
+            if (r >= rows) {
+                node = 0;
+                return -1;
+            }
+            node = r / p.group;
+            return node * p.num_q_heads + s.g * p.group + r - node * p.group;
         };
-        // This thread's part of its row of Q (not ROWS: half of it) into the Q
-        // tile of stretch `which`, 16-byte chunk c of a 128-byte row at
-        // c ^ (row % 8); zeros past the rows in use.
-        auto load_q = [&](const TreeSeg& s, int which) {
-            constexpr int QV = ROWS ? D / 8 : D / 16;
+        auto q_row = [&](const TreeSeg& s, int rel) {
+            return reinterpret_cast<const uint4*>(
+                static_cast<const T*>(p.q) +
+                ((int64_t)s.b * p.tree_len * p.num_q_heads + max(rel, 0)) * D);
+        };
+        // where 16-byte chunk c of this thread's row lies in a Q tile
+        auto q_chunk = [&](int c) {
+            return (c / 8) * Cfg::kQRegionBytes + srow * 128 + (((c % 8) ^ (srow & 7)) << 4);
+        };
+        // not ROWS: this thread's half of its row of Q into the Q tile of stretch `which`
+        auto load_q_half = [&](const TreeSeg& s, int which) {
             int node;
-            int64_t orow;
-            const bool live = row_of(s, node, orow);
-            const int c0 = ROWS ? 0 : wg * QV;
-            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + orow * D);
-            const uint32_t dst = q_addr + (ROWS ? wg : which & 1) * Cfg::kSlotBytes + srow * 128;
+            const int rel = row_of(s, node);
+            const uint4* src = q_row(s, rel);
+            const uint32_t dst = q_addr + (which & 1) * Cfg::kQTileBytes;
 #pragma unroll
-            for (int k = 0; k < QV; ++k) {
-                const int c = c0 + k;
-                ptx::cp_async_16(dst + (c / 8) * Cfg::kRegionBytes + (((c % 8) ^ (srow & 7)) << 4),
-                                 src + c, live);
+            for (int k = 0; k < D / 16; ++k) {
+                const int c = wg * (D / 16) + k;
+                ptx::cp_async_16(dst + q_chunk(c), src + c, rel >= 0);
+            }
+        };
+        // ROWS: its row of Q into Q tile wg.  Where the output leaves by way of the Q
+        // tile's first region, that region's part waits in registers until it has.
+        constexpr int QH = ROWS && D == 128 ? 8 : 1;
+        uint4 held[QH];
+        auto load_q_row = [&](const TreeSeg& s) {
+            int node;
+            const int rel = row_of(s, node);
+            const uint4* src = q_row(s, rel);
+#pragma unroll
+            for (int c = D == 128 ? 8 : 0; c < D / 8; ++c)
+                ptx::cp_async_16(q_addr + wg * Cfg::kQTileBytes + q_chunk(c), src + c, rel >= 0);
+            if constexpr (QH > 1) {
+#pragma unroll
+                for (int c = 0; c < QH; ++c)
+                    held[c] = rel >= 0 ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
             }
         };
         auto q_loaded = [&] {
+            if constexpr (QH > 1) {
+#pragma unroll
+                for (int c = 0; c < QH; ++c)
+                    *reinterpret_cast<uint4*>(sq + wg * Cfg::kQTileBytes + q_chunk(c)) = held[c];
+            }
             ptx::cp_async_wait_all();
             ptx::fence_proxy_async_smem();
             ptx::mbar_arrive(ptx::smem_addr(q_ready));
@@ -535,26 +585,28 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
         TreeSeg s, next;
         bool have = walk.next(p, s);
         if (have) {
-            load_q(s, 0);
+            if constexpr (ROWS)
+                load_q_row(s);
+            else
+                load_q_half(s, 0);
             q_loaded();
         }
-        int64_t seg_at = start;  // the stretch's first tile on the line
+        int64_t seg_at = start;  // the stretch's first place on the line
         while (have && ok) {
             const int base = s.n - p.tree_len;
             int node;
-            int64_t orow;
-            const bool live = row_of(s, node, orow);
+            const int rel = row_of(s, node);
+            const bool live = rel >= 0;
             const bool warp_live = __any_sync(0xffffffffu, live);
             if (s.tile0 == 0 && s.g == 0 && s.rb == 0 && tid == 0) {
                 const int n_raw = __ldg(p.context_lens + s.b);
                 if (n_raw < 0 || n_raw > p.cap || (n_raw != 0 && n_raw < p.tree_len))
                     flag_error(p.err_flag, PKV_EFLAG_CONTEXT_LEN);
             }
-            // The next stretch's Q is on its way long before it is needed: from the
-            // start of this one (its Q tile belonged to the stretch before; ROWS:
-            // from the last S_w of this one, which reads the same Q tile).
+            // the next stretch's Q is on its way long before it is needed (its tile
+            // belonged to the stretch before this one)
             const bool have_next = walk.next(p, next);
-            if (!ROWS && have_next) load_q(next, nseg + 1);
+            if (!ROWS && have_next) load_q_half(next, nseg + 1);
             const int mask_words = (p.tree_len + 31) / 32;
             const int32_t* mask = p.tree_mask + s.b * p.mask_stride + (int64_t)node * mask_words;
             // bits of nodes jb .. jb + 31 (below 0: committed positions)
@@ -567,53 +619,51 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                                                          : 0u;
                 return __funnelshift_r(lo, hi, jb & 31);
             };
+            const int nt = 2 * s.tiles;
+            const int tok0 = s.tile0 * kTreePair;
             const int32_t* table = p.block_tables + (int64_t)s.b * p.max_blocks_per_seq;
-            // lanes 0-7: whether box `lane` of tile j is there
-            auto box_there = [&](int j) {
-                const int tok = (s.tile0 + j) * TT + lane * kStageTokens;
-                if (lane >= kTreeBoxes || j >= s.tiles || tok >= s.n) return false;
-                const int blk = __ldg(table + (tok >> bs_shift));
-                return blk >= 0 && blk < p.num_blocks;
+            // lanes 0-3: the block of box `lane` of tile j, as the table has it (-1: none)
+            auto box_block = [&](int j) {
+                const int tok = tok0 + j * TT + lane * kStageTokens;
+                return lane < kTreeBoxes && j < nt && tok < s.n ? __ldg(table + (tok >> bs_shift))
+                                                                : -1;
             };
 
             float m_ref = -INFINITY, l = 0.f;
             constexpr int kStep = ROWS ? 1 : 2;
-            bool there = box_there(ROWS ? 0 : wg);
-            bool worked = false;
-            // not ROWS: both warpgroups read O_0, O_1 and the exchanged (m, l) of the
-            // stretch before; neither is written anew until both have
-            auto others_read = [&] {
-                return ROWS || nseg == 0 ||
-                       warp_wait_phase(ptx::smem_addr(o_free), (nseg - 1) & 1, abort_flag,
-                                       p.err_flag);
-            };
-            for (int j = ROWS ? 0 : wg; j < s.tiles; j += kStep) {
-                const uint32_t boxes = __ballot_sync(0xffffffffu, there);
-                there = box_there(j + kStep);
-                if (!warp_wait_phase(ptx::smem_addr(&s_full[wg]), steps_done & 1, abort_flag,
-                                     p.err_flag)) {
+            const int j0 = ROWS ? 0 : wg;
+            int blk = box_block(j0), blk_next = box_block(j0 + kStep);  // two steps ahead
+            for (int j = j0; j < nt; j += kStep, ++step) {
+                const uint32_t boxes = __ballot_sync(0xffffffffu, blk >= 0 && blk < p.num_blocks);
+                blk = blk_next;
+                blk_next = box_block(j + 2 * kStep);
+                const int buf = step & 1;
+                const uint32_t s_col = tmem + lane_base + (2 * wg + buf) * TT;
+                const int t0 = tok0 + j * TT;
+                const bool plain = boxes == (1u << kTreeBoxes) - 1u && t0 + TT <= s.n &&
+                                   t0 + TT <= base;
+                if (!warp_wait_phase(ptx::smem_addr(&s_full[2 * wg + buf]), (step >> 1) & 1,
+                                     abort_flag, p.err_flag)) {
                     ok = false;
                     break;
                 }
-                ++steps_done;
                 ptx::tc_fence_after_sync();
-                if (ROWS && have_next && j + 1 == s.tiles) load_q(next, nseg + 1);
-                const int t0 = (s.tile0 + j) * TT;
-                const bool plain = boxes == 0xffu && t0 + TT <= s.n && t0 + TT <= base;
                 if (!plain) {
                     // V rows of absent tokens hold stale bytes, and a node's V may hold
                     // infinities or NaN that only some rows attend to: zeroed in
                     // shared memory, so that 0 * V is 0; the rows that do attend to
                     // such a value get it back at the end.
-                    const int at = place0 + v_place<ROWS>(j, s.tiles);
-                    if (!warp_wait_phase(ptx::smem_addr(&full_bar[at % NS]), (at / NS) & 1,
-                                         abort_flag, p.err_flag)) {
+                    const auto [slot, phase] = tree_place<ROWS, NS>(true, place0, j, nt);
+                    if (!warp_wait_phase(ptx::smem_addr(&full_bar[slot]), phase & 1, abort_flag,
+                                         p.err_flag)) {
                         ok = false;
                         break;
                     }
-                    uint8_t* vst = ring + (at % NS) * Cfg::kSlotBytes;
-                    const int row0 = boxes == 0xffu ? max(0, min(base, s.n) - t0) : 0;
-                    for (int idx = row0 * R * 8 + srow; idx < TT * R * 8; idx += TT) {
+                    uint8_t* vst = ring + slot * Cfg::kSlotBytes;
+                    const int row0 = boxes == (1u << kTreeBoxes) - 1u
+                                         ? min(max(0, min(base, s.n) - t0), TT)
+                                         : 0;
+                    for (int idx = row0 * R * 8 + srow; idx < TT * R * 8; idx += TR) {
                         const int row = idx / (R * 8), rem = idx - row * (R * 8);
                         uint4* cell = reinterpret_cast<uint4*>(
                             vst + (rem / 8) * Cfg::kRegionBytes + row * 128 + (rem % 8) * 16);
@@ -638,85 +688,53 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                     }
                     ptx::fence_proxy_async_smem();
                 }
-                if (!worked && !others_read()) {
+                if (!ROWS && j == j0 && nseg > 0 &&
+                    !warp_wait_phase(ptx::smem_addr(o_free), (nseg - 1) & 1, abort_flag,
+                                     p.err_flag)) {
+                    // both warpgroups read O_0, O_1 and the exchanged (m, l) of the
+                    // stretch before; neither is written anew until both have
                     ok = false;
                     break;
                 }
-                worked = true;
-
-                // The row's scores come from tensor memory a half (64 tokens) at a
-                // time: both for the maximum, then the upper half's weights while its
-                // scores are still in registers, then the lower half's anew.  The
-                // products take the upper half's while the lower's are made.
-                uint32_t allow[TT / 32];  // tokens that the row attends to
-                if (!plain && warp_live) {
-#pragma unroll
-                    for (int c = 0; c < TT / 32; ++c) {
-                        const int tc = t0 + c * 32;
-                        const int left = s.n - tc;
-                        uint32_t a = left >= 32 ? ~0u : left <= 0 ? 0u : (1u << left) - 1u;
-                        const uint32_t bb = boxes >> (2 * c);
-                        a &= ((bb & 1u) ? 0x0000ffffu : 0u) | ((bb & 2u) ? 0xffff0000u : 0u);
-                        allow[c] = a & tree_bits(tc - base);
+                if (warp_live) {
+                    float sc[TT];
+                    {
+                        uint32_t(&r0)[32] = *reinterpret_cast<uint32_t(*)[32]>(sc);
+                        uint32_t(&r1)[32] = *reinterpret_cast<uint32_t(*)[32]>(sc + 32);
+                        __syncwarp();
+                        ptx::tmem_ld32_async(s_col, r0);
+                        ptx::tmem_ld32_async(s_col + 32, r1);
+                        ptx::tmem_wait_ld();
+                        ptx::tmem_loaded(r0);
+                        ptx::tmem_loaded(r1);
                     }
-                }
-                float sc[TT / 2];
-                auto load_half = [&](int half) {
-                    uint32_t(&r0)[32] = *reinterpret_cast<uint32_t(*)[32]>(sc);
-                    uint32_t(&r1)[32] = *reinterpret_cast<uint32_t(*)[32]>(sc + 32);
-                    __syncwarp();
-                    ptx::tmem_ld32_async(s_col + half * 64, r0);
-                    ptx::tmem_ld32_async(s_col + half * 64 + 32, r1);
-                    ptx::tmem_wait_ld();
-                    ptx::tmem_loaded(r0);
-                    ptx::tmem_loaded(r1);
                     if (p.scale_sign != 1.f) {
 #pragma unroll
-                        for (int i = 0; i < TT / 2; ++i) sc[i] *= p.scale_sign;
+                        for (int i = 0; i < TT; ++i) sc[i] *= p.scale_sign;
                     }
                     if (!plain) {
 #pragma unroll
-                        for (int i = 0; i < TT / 2; ++i)
-                            if (!((allow[half * 2 + i / 32] >> (i % 32)) & 1u)) sc[i] = -INFINITY;
+                        for (int c = 0; c < TT / 32; ++c) {
+                            const int tc = t0 + c * 32;
+                            const int left = s.n - tc;
+                            uint32_t allow = left >= 32 ? ~0u : left <= 0 ? 0u : (1u << left) - 1u;
+                            const uint32_t bb = boxes >> (2 * c);
+                            allow &= ((bb & 1u) ? 0x0000ffffu : 0u) |
+                                     ((bb & 2u) ? 0xffff0000u : 0u);
+                            allow &= tree_bits(tc - base);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (!((allow >> i) & 1u)) sc[c * 32 + i] = -INFINITY;
+                        }
                     }
-                };
-                auto max_half = [&] {
                     float mx[4];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) mx[c] = fmaxf(sc[2 * c], sc[2 * c + 1]);
 #pragma unroll
-                    for (int i = 8; i < TT / 2; i += 2)
+                    for (int i = 8; i < TT; i += 2)
                         mx[(i / 2) % 4] = fmaxf(fmaxf(mx[(i / 2) % 4], sc[i]), sc[i + 1]);
-                    return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                };
-                float2 ref2, sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                // weights of the half in registers, summed and written over its scores
-                auto weigh_half = [&](int half) {
-                    const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
-#pragma unroll
-                    for (int i = 0; i < TT / 2; i += 2) {
-                        const float2 y = ptx::fma2(make_float2(sc[i], sc[i + 1]), scale2, ref2);
-                        sc[i] = ptx::ex2_approx(y.x);
-                        sc[i + 1] = ptx::ex2_approx(y.y);
-                        sum[(i / 2) % 2] =
-                            ptx::add2(sum[(i / 2) % 2], make_float2(sc[i], sc[i + 1]));
-                    }
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        uint32_t pv[32];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            split_pair(make_float2(sc[c * 32 + 2 * e], sc[c * 32 + 2 * e + 1]),
-                                       pv[e], pv[16 + e], T());
-                        ptx::tmem_st32_async(s_col + half * 64 + c * 32, pv);
-                    }
-                    ptx::tmem_wait_st();
-                };
-                if (warp_live) {
-                    load_half(0);
-                    float top = max_half();
-                    load_half(1);
-                    top = fmaxf(top, max_half()) * p.scale_log2;
+                    const float top =
+                        fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
                     float alpha = 1.f;
                     if (m_ref == -INFINITY) {
                         m_ref = top;  // O and l are still zero for this row
@@ -725,59 +743,75 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                         m_ref = top;
                     }
                     const float ref = (m_ref == -INFINITY ? 0.f : m_ref) - WeightBias<T>::value;
-                    ref2 = make_float2(-ref, -ref);
-                    l *= alpha;
-                    // O_w is rescaled when a reference moved: S_w(j) complete implies
-                    // that O_w += P V of the tile before is
+                    // O is rescaled when a reference moved, once the last O += P V has
+                    // completed (that of the step before it has: S of this step is
+                    // complete, and was issued behind it)
                     if (__any_sync(0xffffffffu, alpha != 1.f)) {
+                        if (!warp_wait_phase(ptx::smem_addr(&pv_done[2 * wg + (buf ^ 1)]),
+                                             ((step - 1) >> 1) & 1, abort_flag, p.err_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        ptx::tc_fence_after_sync();
 #pragma unroll 1
                         for (int c = 0; c < D / 32; ++c) {
                             uint32_t ov[32];
-                            const uint32_t ta = tmem + lane_base + Cfg::kColO + wg * D + c * 32;
                             __syncwarp();
-                            ptx::tmem_ld32(ta, ov);
+                            ptx::tmem_ld32(o_col + wg * D + c * 32, ov);
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
                                 ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
-                            ptx::tmem_st32(ta, ov);
+                            ptx::tmem_st32(o_col + wg * D + c * 32, ov);
                         }
+                        l *= alpha;
                     }
-                    weigh_half(1);
-                }
-                ptx::tc_fence_before_sync();
-                ptx::mbar_arrive(ptx::smem_addr(&p_ready[2 * wg + 1]));
-                if (warp_live) {
-                    load_half(0);
-                    weigh_half(0);
+                    const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
+                    const float2 ref2 = make_float2(-ref, -ref);
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                    for (int c = 0; c < TT / 32; ++c) {
+                        uint32_t pv[32];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const int i = c * 32 + 2 * e;
+                            float2 y = ptx::fma2(make_float2(sc[i], sc[i + 1]), scale2, ref2);
+                            y.x = ptx::ex2_approx(y.x);
+                            y.y = ptx::ex2_approx(y.y);
+                            sum[e % 2] = ptx::add2(sum[e % 2], y);
+                            split_pair(y, pv[e], pv[16 + e], T());
+                        }
+                        ptx::tmem_st32_async(s_col + c * 32, pv);
+                    }
                     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                    ptx::tmem_wait_st();
                 }
                 ptx::tc_fence_before_sync();
-                ptx::mbar_arrive(ptx::smem_addr(&p_ready[2 * wg]));
+                ptx::mbar_arrive(ptx::smem_addr(&p_ready[2 * wg + buf]));
             }
             if (!ok) break;
-            place0 += 2 * s.tiles;
-            if (have_next) q_loaded();
-
-            if (worked) {
-                if (!warp_wait_phase(ptx::smem_addr(&o_done[wg]), o_count & 1, abort_flag,
-                                     p.err_flag))
-                    break;
-                ++o_count;
+            place0 += tree_places<ROWS>(nt);
+            if (have_next) {
+                if constexpr (ROWS)
+                    load_q_row(next);
+                else
+                    q_loaded();
             }
-            float fa = 0.f, fb = 0.f, lse;  // out = O_0 fa + O_1 fb (ROWS: O_w fa)
-            bool worked_b = false;
+
+            // the stretch's last O += P V
+            if (!warp_wait_phase(ptx::smem_addr(&pv_done[2 * wg + ((step - 1) & 1)]),
+                                 ((step - 1) >> 1) & 1, abort_flag, p.err_flag))
+                break;
+            float fa, fb = 0.f, lse;  // out = O_0 fa + O_1 fb (ROWS: O_w fa)
             if constexpr (ROWS) {
                 fa = l == 0.f ? 0.f : 1.f / l;
                 lse = l == 0.f ? -INFINITY : m_ref - WeightBias<T>::value + log2f(l);
             } else {
                 // both warpgroups are through: their halves of the softmax meet
-                if (!worked && !others_read()) break;
-                xch[wg * TT + srow] = make_float2(m_ref, l);
+                xch[wg * TR + srow] = make_float2(m_ref, l);
                 ptx::mbar_arrive(ptx::smem_addr(met));
                 if (!warp_wait_phase(ptx::smem_addr(met), nseg & 1, abort_flag, p.err_flag)) break;
-                const float2 ha = xch[srow], hb = xch[TT + srow];
+                const float2 ha = xch[srow], hb = xch[TR + srow];
                 const float mm = fmaxf(ha.x, hb.x);
-                worked_b = s.tiles > 1;
                 fa = ha.x == -INFINITY ? 0.f : ptx::ex2_approx(ha.x - mm);
                 fb = hb.x == -INFINITY ? 0.f : ptx::ex2_approx(hb.x - mm);
                 const float sum = ha.y * fa + hb.y * fb;
@@ -791,38 +825,39 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             const int slot = 2 * blockIdx.x + (s.tile0 == 0 ? 1 : 0);
             const bool bad_v = s_bad[nseg & 3] == nseg + 1;
             if (p.unit_ctas != nullptr && s.tile0 == 0 && tid == 0) {
-                // the line's tile u belongs to CTA c when c * line < (u + 1) * CTAs
+                // the line's place u belongs to the last CTA c with c * line < (u + 1) * CTAs
                 const int64_t unit =
                     ((int64_t)s.b * p.num_kv_heads + s.g) * p.row_blocks + s.rb;
                 p.unit_ctas[unit] = make_int2(
                     blockIdx.x, (int)(((seg_at + s.unit_tiles) * ctas - 1) / line));
             }
-            // columns: ROWS: the whole row; else this warpgroup's half
+            // Columns: ROWS: the whole row; else this warpgroup's half.  They leave
+            // through shared memory, 32 at a time, so that a warp writes whole lines
+            // (a row a thread: 4 cycles of the load/store unit for every one).
             constexpr int kCols = ROWS ? D : D / 2;
             const int col0 = ROWS ? 0 : wg * kCols;
+            uint8_t* tray = D == 128
+                                ? sq + (ROWS ? wg : nseg & 1) * Cfg::kQTileBytes +
+                                      (ROWS ? 0 : wg) * Cfg::kQRegionBytes + (warp % 4) * 4096
+                                : stage + warp * 4096;
 #pragma unroll 1
             for (int c = 0; c < kCols; c += 32) {
+                if (!warp_live) break;
                 float v[32];
                 uint32_t ov[32];
                 __syncwarp();
-                if constexpr (ROWS) {
-                    ptx::tmem_ld32(tmem + lane_base + Cfg::kColO + wg * D + c, ov);
+                ptx::tmem_ld32(o_col + (ROWS ? wg * D : 0) + col0 + c, ov);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(ov[i]) * fa;
-                } else {
-                    ptx::tmem_ld32(tmem + lane_base + Cfg::kColO + col0 + c, ov);
+                for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(ov[i]) * fa;
+                if constexpr (!ROWS) {
+                    ptx::tmem_ld32(o_col + D + col0 + c, ov);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(ov[i]) * fa;
-                    if (worked_b) {
-                        ptx::tmem_ld32(tmem + lane_base + Cfg::kColO + D + col0 + c, ov);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = fmaf(__uint_as_float(ov[i]), fb, v[i]);
-                    }
+                    for (int i = 0; i < 32; ++i) v[i] = fmaf(__uint_as_float(ov[i]), fb, v[i]);
                 }
                 if (live && bad_v) {
                     // infinities and NaN in the V of nodes that this row attends to
-                    const int t_hi = min(s.n, (s.tile0 + s.tiles) * TT);
-                    for (int t = max(max(0, base), s.tile0 * TT); t < t_hi; ++t) {
+                    const int t_hi = min(s.n, tok0 + nt * TT);
+                    for (int t = max(max(0, base), tok0); t < t_hi; ++t) {
                         const int j = t - base;
                         if (!((__ldg(mask + (j >> 5)) >> (j & 31)) & 1)) continue;
                         const int blk = __ldg(table + (t >> bs_shift));
@@ -840,26 +875,48 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                         }
                     }
                 }
-                if (live && direct) {
-                    uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + orow * D +
-                                                          col0 + c);
+                // row `lane` of the tray, 16-byte chunk i at i ^ (row % 8)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        dst[i] = make_uint4(pack2(v[8 * i], v[8 * i + 1], T()),
-                                            pack2(v[8 * i + 2], v[8 * i + 3], T()),
-                                            pack2(v[8 * i + 4], v[8 * i + 5], T()),
-                                            pack2(v[8 * i + 6], v[8 * i + 7], T()));
-                } else if (live) {
-                    float4* dst = reinterpret_cast<float4*>(
-                        p.partial_o + ((int64_t)slot * kUnitRows + urow) * D + col0 + c);
+                for (int i = 0; i < 8; ++i)
+                    *reinterpret_cast<float4*>(tray + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+                        make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                __syncwarp();
+                auto chunk = [&](int row, int i) {
+                    return *reinterpret_cast<const float4*>(tray + row * 128 +
+                                                            ((i ^ (row & 7)) << 4));
+                };
+                if (direct) {
+                    const int64_t first = (int64_t)s.b * p.tree_len * p.num_q_heads;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                    for (int i = 0; i < 4; ++i) {  // 8 rows of 32 columns at a time
+                        const int row = i * 8 + lane / 4, q4 = lane % 4;
+                        const int rr = __shfl_sync(0xffffffffu, rel, row);
+                        const float4 x = chunk(row, 2 * q4), y = chunk(row, 2 * q4 + 1);
+                        if (rr >= 0)
+                            reinterpret_cast<uint4*>(static_cast<T*>(p.out) + (first + rr) * D +
+                                                     col0 + c)[q4] =
+                                make_uint4(pack2(x.x, x.y, T()), pack2(x.z, x.w, T()),
+                                           pack2(y.x, y.y, T()), pack2(y.z, y.w, T()));
+                    }
+                } else {
+                    float* part = p.partial_o +
+                                  ((int64_t)slot * kUnitRows + urow - lane) * D + col0 + c;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {  // 4 rows
+                        const int row = i * 4 + lane / 8;
+                        const int rr = __shfl_sync(0xffffffffu, rel, row);
+                        if (rr >= 0)
+                            reinterpret_cast<float4*>(part + row * D)[lane % 8] =
+                                chunk(row, lane % 8);
+                    }
                 }
             }
             if (live && !direct && (ROWS || wg == 0))
                 p.partial_lse[(int64_t)slot * kUnitRows + urow] = lse;
-            if constexpr (!ROWS) {
+            if constexpr (ROWS) {
+                __syncwarp();
+                if (have_next) q_loaded();
+            } else {
                 ptx::tc_fence_before_sync();
                 ptx::mbar_arrive(ptx::smem_addr(o_free));
             }
@@ -879,19 +936,22 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
     }
 }
 
-// Joins the partials of the units that were cut: one warp per row of the
-// output, w_c = 2^(lse_c - max), out = sum_c w_c O_c / sum_c w_c over the CTAs
-// of the unit.
-constexpr int kTreeMergeWarps = 4;
+// Joins the partials of the units that were cut: w_c = 2^(lse_c - max),
+// out = sum_c w_c O_c / sum_c w_c over the CTAs of the unit, two partials at a
+// time with a running maximum.  Eight lanes take a row of the output, all of
+// a partial's loads in flight at once (a warp a row, one partial after another,
+// took 20 us for the 65536 rows of 32 nodes on the Llama-70B layer).
+constexpr int kTreeMergeThreads = 128;
+constexpr int kTreeMergeRows = kTreeMergeThreads / 8;
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kTreeMergeWarps * 32)
+__global__ void __launch_bounds__(kTreeMergeThreads)
 tree_merge_kernel(const TreeParams p, int unit_rows) {
-    constexpr int E = D / 32;
+    constexpr int E = D / 32;  // float4 columns of a lane: 8 k + lane % 8
     ptx::launch_dependents();
     ptx::grid_dependency_wait();
-    const int lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * kTreeMergeWarps + (threadIdx.x >> 5);
+    const int q8 = threadIdx.x & 7;
+    const int64_t row = (int64_t)blockIdx.x * kTreeMergeRows + (threadIdx.x >> 3);
     if (row >= (int64_t)p.num_seqs * p.tree_len * p.num_q_heads) return;
     const int h = (int)(row % p.num_q_heads);
     const int64_t bi = row / p.num_q_heads;
@@ -902,29 +962,54 @@ tree_merge_kernel(const TreeParams p, int unit_rows) {
     const int2 ctas = __ldg(p.unit_ctas + ((int64_t)b * p.num_kv_heads + g) * p.row_blocks + rb);
     if (ctas.x == ctas.y) return;  // written whole
     const int urow = r - rb * unit_rows;
-    auto place = [&](int c) {
-        return (int64_t)(2 * c + (c == ctas.x ? 1 : 0)) * unit_rows + urow;
-    };
-    float mx = -INFINITY;
-    for (int c = ctas.x + lane; c <= ctas.y; c += 32) mx = fmaxf(mx, __ldg(p.partial_lse + place(c)));
+    float m = -INFINITY, den = 0.f;
+    float4 acc[E];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    const float ref = mx == -INFINITY ? 0.f : mx;
-    float acc[E], den = 0.f;
+    for (int e = 0; e < E; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = ctas.x; c <= ctas.y; c += 2) {
+        // a unit's first CTA leaves its last partial, the others their first
+        const bool two = c < ctas.y;
+        const int64_t at0 = (int64_t)(2 * c + (c == ctas.x ? 1 : 0)) * unit_rows + urow;
+        const int64_t at1 = two ? (int64_t)(2 * c + 2) * unit_rows + urow : at0;
+        const float lse0 = __ldg(p.partial_lse + at0);
+        const float lse1 = two ? __ldg(p.partial_lse + at1) : -INFINITY;
+        const float4* o0 = reinterpret_cast<const float4*>(p.partial_o + at0 * D) + q8;
+        const float4* o1 = reinterpret_cast<const float4*>(p.partial_o + at1 * D) + q8;
+        float4 x[E], y[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    for (int c = ctas.x; c <= ctas.y; ++c) {
-        const float wgt = exp2f(__ldg(p.partial_lse + place(c)) - ref);
-        if (wgt == 0.f) continue;
-        den += wgt;
-        const float* o = p.partial_o + place(c) * D + lane * E;
+        for (int e = 0; e < E; ++e) {
+            x[e] = __ldg(o0 + 8 * e);
+            y[e] = __ldg(o1 + 8 * e);
+        }
+        const float mn = fmaxf(m, fmaxf(lse0, lse1));
+        const float ref = mn == -INFINITY ? 0.f : mn;
+        const float f = exp2f(m - ref), w0 = exp2f(lse0 - ref), w1 = exp2f(lse1 - ref);
+        m = mn;
+        den = den * f + w0 + w1;
+        // a zero weight adds nothing, whatever its partial holds
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = fmaf(wgt, __ldg(o + e), acc[e]);
+        for (int e = 0; e < E; ++e) {
+            acc[e] = make_float4(acc[e].x * f, acc[e].y * f, acc[e].z * f, acc[e].w * f);
+            if (w0 != 0.f) {
+                acc[e].x = fmaf(w0, x[e].x, acc[e].x);
+                acc[e].y = fmaf(w0, x[e].y, acc[e].y);
+                acc[e].z = fmaf(w0, x[e].z, acc[e].z);
+                acc[e].w = fmaf(w0, x[e].w, acc[e].w);
+            }
+            if (w1 != 0.f) {
+                acc[e].x = fmaf(w1, y[e].x, acc[e].x);
+                acc[e].y = fmaf(w1, y[e].y, acc[e].y);
+                acc[e].z = fmaf(w1, y[e].z, acc[e].z);
+                acc[e].w = fmaf(w1, y[e].w, acc[e].w);
+            }
+        }
     }
     const float inv = den == 0.f ? 0.f : 1.f / den;
-    uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + row * D + lane * E);
+    uint2* out = reinterpret_cast<uint2*>(static_cast<T*>(p.out) + row * D) + q8;
 #pragma unroll
-    for (int e = 0; e < E; e += 2) out[e / 2] = pack2(acc[e] * inv, acc[e + 1] * inv, T());
+    for (int e = 0; e < E; ++e)
+        out[8 * e] = make_uint2(pack2(acc[e].x * inv, acc[e].y * inv, T()),
+                                pack2(acc[e].z * inv, acc[e].w * inv, T()));
 }
 
 // ---------------------------------------------------------------------------
@@ -957,8 +1042,8 @@ static pkv_status plan_tree(int num_seqs, int tree_len, int num_q_heads, int num
     const int sms = current_sm_count();
     if (sms <= 0) return PKV_ERR_CUDA;
     const int rows = tree_len * (num_q_heads / num_kv_heads);
-    plan->two_row_tiles = rows > kTreeTile;
-    plan->unit_rows = plan->two_row_tiles ? 2 * kTreeTile : kTreeTile;
+    plan->two_row_tiles = rows > kTreeRows;
+    plan->unit_rows = plan->two_row_tiles ? 2 * kTreeRows : kTreeRows;
     plan->row_blocks = (rows + plan->unit_rows - 1) / plan->unit_rows;
     const int64_t units = (int64_t)num_seqs * num_kv_heads * plan->row_blocks;
     if ((int64_t)num_kv_heads * plan->row_blocks * tiles > INT_MAX) return PKV_ERR_UNSUPPORTED;
@@ -997,10 +1082,10 @@ static cudaError_t launch_tree_t(const CUtensorMap& mk, const CUtensorMap& mv, c
     cudaError_t e = cudaLaunchKernelEx(&cfg, kern, mk, mv, p);
     if (e != cudaSuccess || !plan.cut) return e;
     const int64_t rows = (int64_t)p.num_seqs * p.tree_len * p.num_q_heads;
-    const int64_t ctas = (rows + kTreeMergeWarps - 1) / kTreeMergeWarps;
+    const int64_t ctas = (rows + kTreeMergeRows - 1) / kTreeMergeRows;
     if (ctas > INT_MAX) return cudaErrorInvalidValue;
     cfg.gridDim = dim3((unsigned)ctas);
-    cfg.blockDim = dim3(kTreeMergeWarps * 32);
+    cfg.blockDim = dim3(kTreeMergeThreads);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, tree_merge_kernel<T, D>, p, plan.unit_rows);
 }
