@@ -104,8 +104,8 @@ struct TreeTileCfg {
     static constexpr int kStageBytes = D == 128 ? 0 : kTreeSoftmaxWarps * 4096;
     static constexpr int kXchBytes = 2 * kTreeRows * 8;         // (m, l) of each half and row
     // full[slots], empty[slots], s_full[2][2], p_ready[2][2], pv_done[2][2], drain[2],
-    // q_ready, met, o_free
-    static constexpr int kBarriers = 2 * kSlots + 17;
+    // q_ready[2], met, o_free
+    static constexpr int kBarriers = 2 * kSlots + 18;
     static constexpr int kSmemBytes = 2 * kQTileBytes + kSlots * kSlotBytes + kStageBytes +
                                       kXchBytes + kBarriers * 8 + 256;
     static constexpr uint32_t kColO = 4 * kTreeTokens;  // S of (warpgroup, buffer), then O
@@ -229,8 +229,8 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
     uint64_t* p_ready = s_full + 4;     // [warpgroup][buffer]
     uint64_t* pv_done = p_ready + 4;    // [warpgroup][buffer]
     uint64_t* drain = pv_done + 4;      // [warpgroup]
-    uint64_t* q_ready = drain + 2;
-    uint64_t* met = q_ready + 1;        // both warpgroups are through the stretch (not ROWS)
+    uint64_t* q_ready = drain + 2;      // Q is in place (ROWS: [warpgroup], its rows)
+    uint64_t* met = q_ready + 2;        // both warpgroups are through the stretch (not ROWS)
     uint64_t* o_free = met + 1;         // both have read O_0 and O_1 (not ROWS)
     int* words = reinterpret_cast<int*>(full_bar + Cfg::kBarriers);
     volatile int* abort_flag = words;
@@ -259,7 +259,8 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
         }
         ptx::mbar_init(ptx::smem_addr(&drain[0]), 1);
         ptx::mbar_init(ptx::smem_addr(&drain[1]), 1);
-        ptx::mbar_init(ptx::smem_addr(q_ready), 2 * TR);
+        ptx::mbar_init(ptx::smem_addr(&q_ready[0]), ROWS ? TR : 2 * TR);
+        ptx::mbar_init(ptx::smem_addr(&q_ready[1]), TR);
         ptx::mbar_init(ptx::smem_addr(met), 2 * TR);
         ptx::mbar_init(ptx::smem_addr(o_free), 2 * TR);
         *abort_flag = 0;
@@ -495,7 +496,8 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 };
                 // The tensor core runs a warp's products in the order of their issue:
                 // S over a buffer's P comes after the O += P V that reads it.
-                ok = wait(q_ready, nseg) && issue_s(0) && (steps < 2 || issue_s(1));
+                // ROWS: a warpgroup's rows of Q are its own, and it need not wait for the other's
+                ok = wait(&q_ready[ROWS ? w : 0], nseg) && issue_s(0) && (steps < 2 || issue_s(1));
                 for (int k = 0; k < steps && ok; ++k)
                     ok = issue_pv(k) && (k + 2 >= steps || issue_s(k + 2));
                 place0 += tree_places<ROWS>(nt);
@@ -579,7 +581,7 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             }
             ptx::cp_async_wait_all();
             ptx::fence_proxy_async_smem();
-            ptx::mbar_arrive(ptx::smem_addr(q_ready));
+            ptx::mbar_arrive(ptx::smem_addr(&q_ready[ROWS ? wg : 0]));
         };
 
         TreeSeg s, next;
