@@ -40,6 +40,7 @@
 #include <climits>
 #include <cmath>
 #include <mutex>
+#include <type_traits>
 
 #include "pkv_common.cuh"
 #include "pkv_device.cuh"
@@ -118,6 +119,12 @@ __host__ __device__ inline int tree_tiles(int n) {
     return n <= 0 ? 1 : (n + kTreePair - 1) / kTreePair;
 }
 
+// A unit costs more than its places: its queries, the first products with
+// nothing to run beside, the masked tiles of its nodes, its output.  It counts
+// this many places ahead of its own on the line (COST0).
+constexpr int kTreeUnitCost = 3;
+__host__ __device__ inline int tree_cost(int n) { return kTreeUnitCost + tree_tiles(n); }
+
 // A stretch of one unit's places.
 struct TreeSeg {
     int b, g, rb;        // sequence, KV head, row block
@@ -130,28 +137,34 @@ struct TreeSeg {
 // place; the last fastest).  Every thread that takes part walks it by itself.
 struct TreeWalk {
     int64_t at, end;
-    int b, unit, tile, n;
+    int b, unit, pos, n;  // pos: in the unit's cost, its places from kTreeUnitCost on
 
     __device__ __forceinline__ bool next(const TreeParams& p, TreeSeg& s) {
-        if (at >= end) return false;
-        s.b = b;
-        s.g = unit / p.row_blocks;
-        s.rb = unit - s.g * p.row_blocks;
-        s.n = n;
-        s.unit_tiles = tree_tiles(n);
-        s.tile0 = tile;
-        s.tiles = (int)min((int64_t)(s.unit_tiles - tile), end - at);
-        at += s.tiles;
-        tile += s.tiles;
-        if (tile == s.unit_tiles) {
-            tile = 0;
-            if (++unit == p.num_kv_heads * p.row_blocks) {
-                unit = 0;
-                ++b;
-                if (at < end) n = clamped_len(__ldg(p.context_lens + b), p.cap);
+        while (at < end) {
+            s.b = b;
+            s.n = n;
+            s.unit_tiles = tree_tiles(n);
+            const int u = unit;
+            const int take = (int)min((int64_t)(kTreeUnitCost + s.unit_tiles - pos), end - at);
+            s.tile0 = max(0, pos - kTreeUnitCost);
+            s.tiles = max(0, pos + take - kTreeUnitCost) - s.tile0;
+            at += take;
+            pos += take;
+            if (pos == kTreeUnitCost + s.unit_tiles) {
+                pos = 0;
+                if (++unit == p.num_kv_heads * p.row_blocks) {
+                    unit = 0;
+                    ++b;
+                    if (at < end) n = clamped_len(__ldg(p.context_lens + b), p.cap);
+                }
+            }
+            if (s.tiles > 0) {
+                s.g = u / p.row_blocks;
+                s.rb = u - s.g * p.row_blocks;
+                return true;
             }
         }
-        return true;
+        return false;
     }
 };
 
@@ -206,6 +219,15 @@ __device__ __forceinline__ bool not_finite(uint16_t x, __nv_bfloat16) {
     return (x & 0x7f80u) == 0x7f80u;
 }
 __device__ __forceinline__ bool not_finite(uint16_t x, __half) { return (x & 0x7c00u) == 0x7c00u; }
+
+// Zeroes what is not finite in a pair of 16-bit values; not 0 if something was.
+template <typename T>
+__device__ __forceinline__ uint32_t drop_not_finite(uint32_t& x, T) {
+    constexpr uint32_t k = std::is_same<T, __half>::value ? 0x7c007c00u : 0x7f807f80u;
+    const uint32_t bad = __vcmpeq2(x & k, k);
+    x &= ~bad;
+    return bad;
+}
 
 template <typename T, int D, bool ROWS>
 __global__ void __launch_bounds__(kTreeThreads, 1)
@@ -283,9 +305,9 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
     // finds its sequence.
     const int per = (p.num_seqs + kTreeThreads - 1) / kTreeThreads;
     const int b_lo = min(p.num_seqs, tid * per), b_hi = min(p.num_seqs, b_lo + per);
-    int mine = 0;  // the host checks that all sequences' places fit an int
+    int mine = 0;  // the host checks that all sequences' costs fit an int
     for (int b = b_lo; b < b_hi; ++b)
-        mine += tree_tiles(clamped_len(__ldg(p.context_lens + b), p.cap));
+        mine += tree_cost(clamped_len(__ldg(p.context_lens + b), p.cap));
     int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -311,7 +333,7 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
         int64_t first = (int64_t)before * units;
         while (true) {
             const int64_t next =
-                first + (int64_t)units * tree_tiles(clamped_len(__ldg(p.context_lens + b), p.cap));
+                first + (int64_t)units * tree_cost(clamped_len(__ldg(p.context_lens + b), p.cap));
             if (start < next) break;
             first = next;
             ++b;
@@ -330,9 +352,9 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
     if (start < stop) {
         walk.b = s_start[0];
         walk.n = clamped_len(__ldg(p.context_lens + walk.b), p.cap);
-        const int tiles = tree_tiles(walk.n);
-        walk.unit = s_start[1] / tiles;
-        walk.tile = s_start[1] - walk.unit * tiles;
+        const int cost = tree_cost(walk.n);
+        walk.unit = s_start[1] / cost;
+        walk.pos = s_start[1] - walk.unit * cost;
     }
 
     if (warp >= kTreeSoftmaxWarps) {
@@ -356,6 +378,22 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             while (ok && walk.next(p, seg)) {
                 const int nt = 2 * seg.tiles;
                 const int32_t* table = p.block_tables + (int64_t)seg.b * p.max_blocks_per_seq;
+                if (p.unit_ctas != nullptr && warp == kTreeTmaWarp && lane == 0 &&
+                    seg.tile0 == 0) {
+                    // the unit's first and last CTA: cost position u of the line belongs to
+                    // the last CTA c with c * line < (u + 1) * CTAs.  The unit's first
+                    // place may lie behind this CTA's first position in it.
+                    const int64_t last = walk.at + (seg.unit_tiles - seg.tiles);  // one past it
+                    p.unit_ctas[((int64_t)seg.b * p.num_kv_heads + seg.g) * p.row_blocks +
+                                seg.rb] =
+                        make_int2(blockIdx.x, (int)((last * ctas - 1) / line));
+                }
+                if (warp == kTreeTmaWarp + 1 && lane == 0 && seg.tile0 == 0 && seg.g == 0 &&
+                    seg.rb == 0) {
+                    const int n_raw = __ldg(p.context_lens + seg.b);
+                    if (n_raw < 0 || n_raw > p.cap || (n_raw != 0 && n_raw < p.tree_len))
+                        flag_error(p.err_flag, PKV_EFLAG_CONTEXT_LEN);
+                }
                 // the block of this lane's box of tile j, as the table has it (-1: none)
                 auto box_block = [&](int j) {
                     const int tok = seg.tile0 * kTreePair + j * TT + bx * kStageTokens;
@@ -593,18 +631,12 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 load_q_half(s, 0);
             q_loaded();
         }
-        int64_t seg_at = start;  // the stretch's first place on the line
         while (have && ok) {
             const int base = s.n - p.tree_len;
             int node;
             const int rel = row_of(s, node);
             const bool live = rel >= 0;
             const bool warp_live = __any_sync(0xffffffffu, live);
-            if (s.tile0 == 0 && s.g == 0 && s.rb == 0 && tid == 0) {
-                const int n_raw = __ldg(p.context_lens + s.b);
-                if (n_raw < 0 || n_raw > p.cap || (n_raw != 0 && n_raw < p.tree_len))
-                    flag_error(p.err_flag, PKV_EFLAG_CONTEXT_LEN);
-            }
             // the next stretch's Q is on its way long before it is needed (its tile
             // belonged to the stretch before this one)
             const bool have_next = walk.next(p, next);
@@ -673,14 +705,10 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                             *cell = make_uint4(0u, 0u, 0u, 0u);
                         } else if (t0 + row >= base) {
                             uint4 x = *cell;
-                            uint16_t* e = reinterpret_cast<uint16_t*>(&x);
-                            bool bad = false;
-#pragma unroll
-                            for (int u = 0; u < 8; ++u)
-                                if (not_finite(e[u], T())) {
-                                    e[u] = 0;
-                                    bad = true;
-                                }
+                            const uint32_t bad = drop_not_finite(x.x, T()) |
+                                                 drop_not_finite(x.y, T()) |
+                                                 drop_not_finite(x.z, T()) |
+                                                 drop_not_finite(x.w, T());
                             if (bad) {
                                 s_bad[nseg & 3] = nseg + 1;
                                 __threadfence_block();  // before the value is gone
@@ -826,13 +854,6 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             const bool direct = s.tiles == s.unit_tiles;
             const int slot = 2 * blockIdx.x + (s.tile0 == 0 ? 1 : 0);
             const bool bad_v = s_bad[nseg & 3] == nseg + 1;
-            if (p.unit_ctas != nullptr && s.tile0 == 0 && tid == 0) {
-                // the line's place u belongs to the last CTA c with c * line < (u + 1) * CTAs
-                const int64_t unit =
-                    ((int64_t)s.b * p.num_kv_heads + s.g) * p.row_blocks + s.rb;
-                p.unit_ctas[unit] = make_int2(
-                    blockIdx.x, (int)(((seg_at + s.unit_tiles) * ctas - 1) / line));
-            }
             // Columns: ROWS: the whole row; else this warpgroup's half.  They leave
             // through shared memory, 32 at a time, so that a warp writes whole lines
             // (a row a thread: 4 cycles of the load/store unit for every one).
@@ -922,7 +943,6 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 ptx::tc_fence_before_sync();
                 ptx::mbar_arrive(ptx::smem_addr(o_free));
             }
-            seg_at += s.tiles;
             ++nseg;
             s = next;
             have = have_next;
@@ -1040,7 +1060,7 @@ static pkv_status plan_tree(int num_seqs, int tree_len, int num_q_heads, int num
     if (tree_len > PKV_MAX_TREE_LEN || (int64_t)num_seqs * num_kv_heads > 65535)
         return PKV_ERR_UNSUPPORTED;
     const int tiles = tree_tiles(max_context_len);
-    if ((int64_t)num_seqs * tiles > INT_MAX) return PKV_ERR_UNSUPPORTED;
+    if ((int64_t)num_seqs * tree_cost(max_context_len) > INT_MAX) return PKV_ERR_UNSUPPORTED;
     const int sms = current_sm_count();
     if (sms <= 0) return PKV_ERR_CUDA;
     const int rows = tree_len * (num_q_heads / num_kv_heads);
@@ -1048,7 +1068,8 @@ static pkv_status plan_tree(int num_seqs, int tree_len, int num_q_heads, int num
     plan->unit_rows = plan->two_row_tiles ? 2 * kTreeRows : kTreeRows;
     plan->row_blocks = (rows + plan->unit_rows - 1) / plan->unit_rows;
     const int64_t units = (int64_t)num_seqs * num_kv_heads * plan->row_blocks;
-    if ((int64_t)num_kv_heads * plan->row_blocks * tiles > INT_MAX) return PKV_ERR_UNSUPPORTED;
+    if ((int64_t)num_kv_heads * plan->row_blocks * tree_cost(max_context_len) > INT_MAX)
+        return PKV_ERR_UNSUPPORTED;
     plan->ctas = (int)std::max<int64_t>(1, std::min<int64_t>(sms, units * tiles));
     plan->cut = tiles > 1;
     plan->units_bytes = ((size_t)units * sizeof(int2) + 255) & ~size_t(255);
