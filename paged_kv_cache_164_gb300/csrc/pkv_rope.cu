@@ -7,11 +7,12 @@
 // It is bound by memory: every row is read once and written once (q to q_out,
 // k and v into the cache), a few operations an element.
 //
-// A group of head_dim / 8 lanes holds a row in registers, 8 consecutive dims
-// (one 16-byte load and store) a lane: the mean is a few shuffles inside the
-// group, and a pair's other half is in the same lane (interleaved pairs) or in
-// a fixed partner lane (halves).  A CTA takes rows of one token, so a lane
-// reads its cosines and sines once for all of its rows.
+// A group of head_dim / 8 lanes holds a row in registers, two blocks of 4 dims a
+// lane, chosen so that a lane has both halves of its pairs (halves: 4 l and
+// rotary_dim / 2 + 4 l; interleaved pairs and dims that are not rotated: 8 l
+// and 8 l + 4): the rotation needs no exchange between lanes, and the mean is
+// the group's only one.  A CTA takes rows of one token, of q or of k and v, so a
+// lane reads its cosines, sines and weights once for all of its rows.
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -44,159 +45,181 @@ struct RopeParams {
     int rotary_dim;
     int num_q_heads, num_kv_heads;
     int block_size;
-    int rows_per_cta;                      // head rows (q, then k, then v) of a token per CTA
+    int block_shift;                       // log2 of the block size
+    int rows_per_cta;                      // head rows of a token per CTA
+    int q_blocks;                          // CTAs of a token with q rows; then k and v rows
     bool interleaved;
     bool hnd;
 };
 
 constexpr int kRopeThreads = 128;
+constexpr int kRopeBatch = 4;    // a group's rows, all in flight at once
+constexpr int kRopeMinCtas = 8;
 
-template <typename T, int D, bool F8>
+template <typename T>
+__device__ __forceinline__ void widen4(uint2 w, float2 (&x)[2], T) {
+    x[0] = pair_to_float2(w.x, T());
+    x[1] = pair_to_float2(w.y, T());
+}
+
+template <typename T, int D, bool F8, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads) norm_rope_append_kernel(const RopeParams p) {
     constexpr int LPR = D / 8;                    // lanes per row
     constexpr int kGroups = kRopeThreads / LPR;   // rows a CTA holds at a time
     ptx::launch_dependents();
     ptx::grid_dependency_wait();
     const int64_t i = blockIdx.x;
+    const int lane = threadIdx.x % LPR;
+    const int group = threadIdx.x / LPR;
+    const int half = p.rotary_dim / 2;
+    const bool turns = lane * 8 < p.rotary_dim;
+    // the lane's two blocks of 4 dims
+    const int d0 = !INTER && turns ? 4 * lane : 8 * lane;
+    const int d1 = !INTER && turns ? half + 4 * lane : 8 * lane + 4;
+    const bool kv = (int)blockIdx.y >= p.q_blocks;  // k, then v rows; else q rows
+    const int first = (kv ? blockIdx.y - p.q_blocks : blockIdx.y) * p.rows_per_cta;
+    const int r_end = min(kv ? 2 * p.num_kv_heads : p.num_q_heads, first + p.rows_per_cta);
+    const int r0 = first + group;
+
+    // every load that depends on no other first: the slot, the position, the
+    // group's rows
     const int64_t slot = __ldg(p.slot_mapping + i);
-    if (slot < 0) return;  // padding
     const int pos = __ldg(p.positions + i);
+    const T* qk = static_cast<const T*>(kv ? p.k : p.q) + i * (kv ? p.k_stride : p.q_stride);
+    const T* vv = static_cast<const T*>(p.v) + i * p.v_stride - (int64_t)p.num_kv_heads * D;
+    uint2 lo[kRopeBatch], hi[kRopeBatch];
+#pragma unroll
+    for (int u = 0; u < kRopeBatch; ++u) {
+        const int r = r0 + u * kGroups;
+        lo[u] = hi[u] = make_uint2(0u, 0u);
+        if (r < r_end) {
+            const T* src = (kv && r >= p.num_kv_heads ? vv : qk) + r * D;
+            if constexpr (INTER) {
+                const uint4 x = *reinterpret_cast<const uint4*>(src + d0);
+                lo[u] = make_uint2(x.x, x.y);
+                hi[u] = make_uint2(x.z, x.w);
+            } else {
+                lo[u] = *reinterpret_cast<const uint2*>(src + d0);
+                hi[u] = *reinterpret_cast<const uint2*>(src + d1);
+            }
+        }
+    }
+    const T* weight = static_cast<const T*>(kv ? p.k_weight : p.q_weight);
+    float2 wl[2], wh[2];
+    wl[0] = wl[1] = wh[0] = wh[1] = make_float2(1.f, 1.f);
+    if (weight != nullptr) {
+        widen4(__ldg(reinterpret_cast<const uint2*>(weight + d0)), wl, T());
+        widen4(__ldg(reinterpret_cast<const uint2*>(weight + d1)), wh, T());
+    }
+    if (slot < 0) return;  // padding
     if (slot >= p.num_slots || pos < 0 || pos >= p.max_position) {
         if (threadIdx.x == 0 && blockIdx.y == 0)
             flag_error(p.err_flag, (slot >= p.num_slots ? PKV_EFLAG_SLOT : 0) |
                                        (pos < 0 || pos >= p.max_position ? PKV_EFLAG_POSITION : 0));
         return;
     }
-    const int lane = threadIdx.x % LPR;
-    const int group = threadIdx.x / LPR;
-    const int half = p.rotary_dim / 2;
-    const int e0 = lane * 8;                      // this lane's first dim
-    const bool turns = e0 < p.rotary_dim;
-
-    // this lane's cosines and sines: of dims e0.. (halves: 8 of each, the same
-    // for both halves), or of the 4 pairs that start at e0
-    float cs[8], sn[8];
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-        cs[u] = 1.f;
-        sn[u] = 0.f;
+    // the lane's 4 pairs' cosines and sines
+    float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (turns && !(kv && first >= p.num_kv_heads)) {
+        const float* row = p.cos_sin + (int64_t)pos * p.rotary_dim + 4 * lane;
+        c = __ldg(reinterpret_cast<const float4*>(row));
+        s = __ldg(reinterpret_cast<const float4*>(row + half));
     }
-    if (turns) {
-        const float* row = p.cos_sin + (int64_t)pos * p.rotary_dim;
-        const int j0 = p.interleaved ? e0 / 2 : (e0 < half ? e0 : e0 - half);
+    const int64_t blk = slot >> p.block_shift;
+    const int off = (int)(slot & ((1 << p.block_shift) - 1));
+    // elements from a head's row to the next head's in the cache, and the first
+    const int64_t head_step = (p.hnd ? (int64_t)1 << p.block_shift : 1) * D;
+    const int64_t cell0 =
+        p.hnd ? (((blk * p.num_kv_heads) << p.block_shift) + off) * D : slot * p.num_kv_heads * D;
 #pragma unroll
-        for (int u = 0; u < 8; u += 4) {
-            if (u >= 4 && p.interleaved) break;
-            const float4 c = __ldg(reinterpret_cast<const float4*>(row + j0 + u));
-            const float4 s = __ldg(reinterpret_cast<const float4*>(row + half + j0 + u));
-            cs[u] = c.x; cs[u + 1] = c.y; cs[u + 2] = c.z; cs[u + 3] = c.w;
-            sn[u] = s.x; sn[u + 1] = s.y; sn[u + 2] = s.z; sn[u + 3] = s.w;
-        }
-    }
-    const int partner = e0 < half ? lane + half / 8 : lane - half / 8;
-
-    const int rows = p.num_q_heads + 2 * p.num_kv_heads;
-    const int r_end = min(rows, (int)(blockIdx.y + 1) * p.rows_per_cta);
-    const int r_begin = blockIdx.y * p.rows_per_cta;
-    const int64_t blk = slot / p.block_size;
-    const int off = (int)(slot - blk * p.block_size);
-    // whole warps stay in the loop (the shuffles name all lanes)
-    for (int base = r_begin; base < r_end; base += kGroups) {
-        const int r = base + group;
-        const bool live = r < r_end;
-        const bool is_q = r < p.num_q_heads;
-        const bool is_v = r >= p.num_q_heads + p.num_kv_heads;
-        const int head = is_q ? r : is_v ? r - p.num_q_heads - p.num_kv_heads : r - p.num_q_heads;
-        const T* src = static_cast<const T*>(is_q ? p.q : is_v ? p.v : p.k) +
-                       i * (is_q ? p.q_stride : is_v ? p.v_stride : p.k_stride) + head * D + e0;
-        uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-        if (live) raw = *reinterpret_cast<const uint4*>(src);
-        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-        float x[8];
+    for (int u = 0; u < kRopeBatch; ++u) {
+        const int r = r0 + u * kGroups;
+        if (r - group >= r_end) break;  // the same for the whole CTA
+        const bool is_v = kv && r >= p.num_kv_heads;
+        float2 x[2], y[2];  // the blocks at d0 and d1
+        widen4(lo[u], x, T());
+        widen4(hi[u], y, T());
+        if (weight != nullptr && !(kv && r - group >= p.num_kv_heads)) {
+            // (whole warps take part in the shuffles)
+            float2 q = ptx::mul2(x[0], x[0]);
+            q = ptx::fma2(x[1], x[1], q);
+            q = ptx::fma2(y[0], y[0], q);
+            q = ptx::fma2(y[1], y[1], q);
+            float sq = q.x + q.y;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const float2 f = pair_to_float2(w[u], T());
-            x[2 * u] = f.x;
-            x[2 * u + 1] = f.y;
-        }
-        float sq = 0.f;
-#pragma unroll
-        for (int u = 0; u < 8; ++u) sq = fmaf(x[u], x[u], sq);
-#pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o, LPR);
-        const void* weight = is_q ? p.q_weight : is_v ? nullptr : p.k_weight;
-        if (weight != nullptr) {
-            const float inv = rsqrtf(sq * (1.f / D) + p.eps);
-            const uint4 wr = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(weight) + e0));
-            const uint32_t ww[4] = {wr.x, wr.y, wr.z, wr.w};
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const float2 f = pair_to_float2(ww[u], T());
-                x[2 * u] = x[2 * u] * inv * f.x;
-                x[2 * u + 1] = x[2 * u + 1] * inv * f.y;
-            }
-        }
-        if (p.interleaved) {
+            for (int o = LPR / 2; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o, LPR);
             if (!is_v) {
+                const float inv = rsqrtf(sq * (1.f / D) + p.eps);
+                const float2 inv2 = make_float2(inv, inv);
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const float a = x[2 * u], b = x[2 * u + 1];
-                    x[2 * u] = a * cs[u] - b * sn[u];
-                    x[2 * u + 1] = b * cs[u] + a * sn[u];
+                for (int e = 0; e < 2; ++e) {
+                    x[e] = ptx::mul2(ptx::mul2(x[e], inv2), wl[e]);
+                    y[e] = ptx::mul2(ptx::mul2(y[e], inv2), wh[e]);
                 }
             }
-        } else {
+        }
+        if (turns && !is_v) {
+            if constexpr (INTER) {
+                // pairs (x, y) of each float2: a cos - b sin, b cos + a sin
+                auto turn = [](float2 v, float cc, float ss) {
+                    return make_float2(v.x * cc - v.y * ss, v.y * cc + v.x * ss);
+                };
+                x[0] = turn(x[0], c.x, s.x);
+                x[1] = turn(x[1], c.y, s.y);
+                y[0] = turn(y[0], c.z, s.z);
+                y[1] = turn(y[1], c.w, s.w);
+            } else {
+                // pairs (x element, y element)
+                const float2 cc[2] = {make_float2(c.x, c.y), make_float2(c.z, c.w)};
+                const float2 ss[2] = {make_float2(s.x, s.y), make_float2(s.z, s.w)};
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const float other = __shfl_sync(0xffffffffu, x[u], partner, LPR);
-                if (turns && !is_v)
-                    x[u] = e0 < half ? x[u] * cs[u] - other * sn[u] : x[u] * cs[u] + other * sn[u];
+                for (int e = 0; e < 2; ++e) {
+                    const float2 a = x[e], b = y[e];
+                    x[e] = ptx::fma2(make_float2(-b.x, -b.y), ss[e], ptx::mul2(a, cc[e]));
+                    y[e] = ptx::fma2(a, ss[e], ptx::mul2(b, cc[e]));
+                }
             }
         }
-        if (!live) continue;
-        if (is_q || !F8) {
-            uint4 y;
-            y.x = pack2(x[0], x[1], T());
-            y.y = pack2(x[2], x[3], T());
-            y.z = pack2(x[4], x[5], T());
-            y.w = pack2(x[6], x[7], T());
-            if (is_v) y = raw;  // bit-exact, NaN payloads included
-            T* dst;
-            if (is_q)
-                dst = static_cast<T*>(p.q_out) + (i * p.num_q_heads + head) * D + e0;
-            else
-                dst = static_cast<T*>(is_v ? p.v_cache : p.k_cache) +
-                      (p.hnd ? (blk * p.num_kv_heads + head) * p.block_size + off
-                             : slot * p.num_kv_heads + head) * D + e0;
-            *reinterpret_cast<uint4*>(dst) = y;
+        if (r >= r_end) continue;
+        if (!kv || !F8) {
+            uint2 out0 = lo[u], out1 = hi[u];  // v: bit-exact, NaN payloads included
+            if (!is_v) {
+                out0 = make_uint2(pack2(x[0].x, x[0].y, T()), pack2(x[1].x, x[1].y, T()));
+                out1 = make_uint2(pack2(y[0].x, y[0].y, T()), pack2(y[1].x, y[1].y, T()));
+            }
+            T* dst = !kv ? static_cast<T*>(p.q_out) + (i * p.num_q_heads + r) * D
+                   : is_v ? static_cast<T*>(p.v_cache) + cell0 + (r - p.num_kv_heads) * head_step
+                          : static_cast<T*>(p.k_cache) + cell0 + r * head_step;
+            if constexpr (INTER) {
+                *reinterpret_cast<uint4*>(dst + d0) = make_uint4(out0.x, out0.y, out1.x, out1.y);
+            } else {
+                *reinterpret_cast<uint2*>(dst + d0) = out0;
+                *reinterpret_cast<uint2*>(dst + d1) = out1;
+            }
         } else {
             const float sc = is_v ? p.v_scale : p.k_scale;
-            uint32_t codes[2] = {0u, 0u};
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const float2 f = make_float2(__fdiv_rn(x[2 * u], sc), __fdiv_rn(x[2 * u + 1], sc));
-                const uint32_t two = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
-                codes[u / 2] |= two << (16 * (u % 2));
-            }
-            uint8_t* dst = static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) +
-                           (p.hnd ? (blk * p.num_kv_heads + head) * p.block_size + off
-                                  : slot * p.num_kv_heads + head) * D + e0;
-            *reinterpret_cast<uint2*>(dst) = make_uint2(codes[0], codes[1]);
+            auto code4 = [sc](const float2 (&v)[2]) {
+                const uint32_t a = __nv_cvt_float2_to_fp8x2(
+                    make_float2(__fdiv_rn(v[0].x, sc), __fdiv_rn(v[0].y, sc)), __NV_SATFINITE,
+                    __NV_E4M3);
+                const uint32_t b = __nv_cvt_float2_to_fp8x2(
+                    make_float2(__fdiv_rn(v[1].x, sc), __fdiv_rn(v[1].y, sc)), __NV_SATFINITE,
+                    __NV_E4M3);
+                return a | (b << 16);
+            };
+            uint8_t* dst =
+                is_v ? static_cast<uint8_t*>(p.v_cache) + cell0 + (r - p.num_kv_heads) * head_step
+                     : static_cast<uint8_t*>(p.k_cache) + cell0 + r * head_step;
+            *reinterpret_cast<uint32_t*>(dst + d0) = code4(x);
+            *reinterpret_cast<uint32_t*>(dst + d1) = code4(y);
         }
     }
 }
 
-template <typename T, int D, bool F8>
-static cudaError_t launch_rope(RopeParams p, int num_tokens, int sms, cudaStream_t stream) {
-    constexpr int kGroups = kRopeThreads / (D / 8);
-    const int rows = p.num_q_heads + 2 * p.num_kv_heads;
-    // Enough CTAs for about eight an SM; then each takes more of a token's rows.
-    const int passes = (rows + kGroups - 1) / kGroups;  // CTAs of one row a group
-    const int64_t want = std::max<int64_t>(1, (int64_t)sms * 8 / num_tokens);
-    const int splits = (int)std::min<int64_t>(passes, want);
-    p.rows_per_cta = (passes + splits - 1) / splits * kGroups;
+template <typename T, int D, bool F8, bool INTER>
+static cudaError_t launch_rope_t(const RopeParams& p, dim3 grid, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(num_tokens, (rows + p.rows_per_cta - 1) / p.rows_per_cta);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(kRopeThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -204,7 +227,25 @@ static cudaError_t launch_rope(RopeParams p, int num_tokens, int sms, cudaStream
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, norm_rope_append_kernel<T, D, F8>, p);
+    return cudaLaunchKernelEx(&cfg, norm_rope_append_kernel<T, D, F8, INTER>, p);
+}
+
+template <typename T, int D, bool F8>
+static cudaError_t launch_rope(RopeParams p, int num_tokens, int sms, cudaStream_t stream) {
+    constexpr int kGroups = kRopeThreads / (D / 8);
+    // As many rows a group as leave kRopeMinCtas CTAs an SM: few tokens spread over
+    // the SMs, many share a token's cosines among more rows.
+    auto blocks = [&](int batch, int rows) { return (rows + batch * kGroups - 1) / (batch * kGroups); };
+    int batch = kRopeBatch;
+    while (batch > 1 &&
+           (int64_t)num_tokens * (blocks(batch, p.num_q_heads) + blocks(batch, 2 * p.num_kv_heads)) <
+               (int64_t)sms * kRopeMinCtas)
+        batch /= 2;
+    p.rows_per_cta = batch * kGroups;
+    p.q_blocks = blocks(batch, p.num_q_heads);
+    const dim3 grid(num_tokens, p.q_blocks + blocks(batch, 2 * p.num_kv_heads));
+    return p.interleaved ? launch_rope_t<T, D, F8, true>(p, grid, stream)
+                         : launch_rope_t<T, D, F8, false>(p, grid, stream);
 }
 
 // Whether [a, a + an) and [b, b + bn) share a byte.
@@ -254,6 +295,8 @@ static pkv_status norm_rope_impl(RopeParams p, int num_tokens, int num_blocks, i
     const int sms = current_sm_count();
     if (sms <= 0) return PKV_ERR_CUDA;
     p.num_slots = (int64_t)num_blocks * bs;
+    p.block_shift = 0;
+    while ((1 << p.block_shift) < bs) ++p.block_shift;
     cudaStream_t s = (cudaStream_t)stream;
     cudaError_t e;
     const bool half = dtype == PKV_FP16;
