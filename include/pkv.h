@@ -407,7 +407,8 @@ pkv_status pkv_multi_query_attention(
  *         (a, b) = (j, j + rotary_dim / 2), or (2j, 2j + 1) when interleaved,
  *         cos_j = cos_sin[positions[i]][j], sin_j = cos_sin[positions[i]][rotary_dim / 2 + j]
  *     q_out[i][h] = y (q),  k_cache at slot s = y (k),  v_cache at slot s = v[i]
- * A token with a negative slot is padding: nothing of it is read or written.
+ * A token with a negative slot is padding: nothing of it is written, and what its
+ * rows and its position hold does not matter.
  *
  *   q, k, v       token i's heads start q_stride (k_stride, v_stride) elements
  *                 after token i - 1's and are dense, [num_heads][head_dim], so
@@ -523,7 +524,8 @@ pkv_status pkv_tree_attention(void* out, const void* q, const void* k_cache, con
  * K and V of position n_b - tree_len + accepted[b][j] are copied to position
  * n_b - tree_len + j, and
  *     new_context_lens[b] = n_b - tree_len + accepted_lens[b].
- * The rows of the other nodes, and all others, keep their bytes.
+ * The rows of the other nodes, and all others, keep their bytes.  The pages that
+ * hold the nodes are the sequence's own (as for any append).
  *
  *   accepted       int32 [num_seqs][max_accepted]: a sequence's accepted nodes,
  *                  strictly increasing (a path down the tree is); entries past

@@ -116,7 +116,7 @@ struct TreeTileCfg {
 
 __host__ __device__ inline int tree_tiles(int n) {
     // places on the line (pairs of tiles); an empty context has one of nothing
-    return n <= 0 ? 1 : (n + kTreePair - 1) / kTreePair;
+    return n <= 0 ? 1 : (n - 1) / kTreePair + 1;
 }
 
 // A unit costs more than its places: its queries, the first products with
@@ -1040,6 +1040,7 @@ tree_merge_kernel(const TreeParams p, int unit_rows) {
 
 // Arguments that the workspace size and the launch share, and the plan of a
 // call: the rows' split, the CTAs and the workspace.
+constexpr int kTreeMaxContext = INT_MAX - 1024;  // positions of the last tile fit an int
 struct TreeCallPlan {
     bool two_row_tiles;  // ROWS
     int row_blocks;
@@ -1059,6 +1060,7 @@ static pkv_status plan_tree(int num_seqs, int tree_len, int num_q_heads, int num
     if (tree_len <= 0) return PKV_ERR_INVALID_ARG;
     if (tree_len > PKV_MAX_TREE_LEN || (int64_t)num_seqs * num_kv_heads > 65535)
         return PKV_ERR_UNSUPPORTED;
+    if (max_context_len > kTreeMaxContext) return PKV_ERR_UNSUPPORTED;
     const int tiles = tree_tiles(max_context_len);
     if ((int64_t)num_seqs * tree_cost(max_context_len) > INT_MAX) return PKV_ERR_UNSUPPORTED;
     const int sms = current_sm_count();
@@ -1163,7 +1165,7 @@ extern "C" pkv_status pkv_tree_attention(
         ((reinterpret_cast<uintptr_t>(block_tables) | reinterpret_cast<uintptr_t>(context_lens) |
           reinterpret_cast<uintptr_t>(tree_mask)) & 3u))
         return PKV_ERR_INVALID_ARG;
-    if ((int64_t)max_blocks_per_seq * block_size > INT_MAX) return PKV_ERR_UNSUPPORTED;
+    if ((int64_t)max_blocks_per_seq * block_size > kTreeMaxContext) return PKV_ERR_UNSUPPORTED;
     TreeCallPlan plan;
     st = plan_tree(num_seqs, tree_len, num_q_heads, num_kv_heads, head_dim, block_size,
                    max_context_len, &plan);

@@ -95,12 +95,14 @@ def test_tree_attention_refuses(lib):
     assert _attention(lib, ms=4) == 1 and _attention(lib, ms=-5) == 1
     assert _attention(lib, d=80) == 2 and _attention(lib, bs=8) == 2 and _attention(lib, hq=34) == 2
     assert _attention(lib, t=1025, ms=0) == 2 and _attention(lib, b=40000) == 2
-    assert _attention(lib, mb=2 ** 28) == 2
+    assert _attention(lib, mb=2 ** 28) == 2 and _attention(lib, mb=2 ** 27) == 2
+    assert _attention(lib, mcl=2 ** 31 - 1) == 2
     assert _attention(lib, b=0, q=NULL) == 0
     size = lib.pkv_tree_attention_workspace_size
     assert size(2, 0, 8, 2, 64, 16, 64) == pkv.SIZE_MAX
     assert size(2, 5, 8, 2, 96, 16, 64) == pkv.SIZE_MAX
     assert size(2, 1025, 8, 2, 64, 16, 64) == pkv.SIZE_MAX
+    assert size(2, 5, 8, 2, 64, 16, 2 ** 31 - 1) == pkv.SIZE_MAX
 
 
 def _commit(lib, **kw):
