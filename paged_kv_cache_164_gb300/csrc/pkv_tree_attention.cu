@@ -37,9 +37,9 @@
 //
 // Every wait is bounded, as in the decode kernels.
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <cmath>
-#include <mutex>
 #include <type_traits>
 
 #include "pkv_common.cuh"
@@ -1087,13 +1087,17 @@ static cudaError_t launch_tree_t(const CUtensorMap& mk, const CUtensorMap& mv, c
                                  const TreeCallPlan& plan, cudaStream_t stream) {
     using Cfg = TreeTileCfg<D>;
     auto kern = tree_attention_kernel<T, D, ROWS>;
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [&] {
-        attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        Cfg::kSmemBytes);
-    });
-    if (attr_err != cudaSuccess) return attr_err;
+    // the attribute belongs to a device's copy of the kernel
+    static std::atomic<bool> set[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !set[dev].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 Cfg::kSmemBytes);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) set[dev].store(true, std::memory_order_release);
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(plan.ctas);
     cfg.blockDim = dim3(kTreeThreads);
@@ -1104,7 +1108,7 @@ static cudaError_t launch_tree_t(const CUtensorMap& mk, const CUtensorMap& mv, c
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, mk, mv, p);
+    e = cudaLaunchKernelEx(&cfg, kern, mk, mv, p);
     if (e != cudaSuccess || !plan.cut) return e;
     const int64_t rows = (int64_t)p.num_seqs * p.tree_len * p.num_q_heads;
     const int64_t ctas = (rows + kTreeMergeRows - 1) / kTreeMergeRows;
