@@ -5,7 +5,11 @@
 //     y = x * rsqrt(mean(x^2) + eps) * weight             (no weight: y = x)
 //     y_a' = y_a cos - y_b sin,  y_b' = y_b cos + y_a sin  for each rotated pair
 // It is bound by memory: every row is read once and written once (q to q_out,
-// k and v into the cache), a few operations an element.
+// k and v into the cache), a few operations an element.  16411 packed tokens of
+// the Llama-7B layer (815 MB) take 130 us, 6.25 TB/s (92 % of the copy rate);
+// 2043 tokens of the Llama-70B layer (80 MB) 20.6 us into E4M3 pages, 19 us into
+// 16-bit ones, where starting and draining the SMs shows; 32 tokens 2 us, a
+// launch's least.
 //
 // A group of head_dim / 8 lanes holds a row in registers, two blocks of 4 dims a
 // lane, chosen so that a lane has both halves of its pairs (halves: 4 l and
@@ -53,7 +57,12 @@ struct RopeParams {
 };
 
 constexpr int kRopeThreads = 128;
-constexpr int kRopeBatch = 4;    // a group's rows, all in flight at once
+// A group's rows, all in flight at once.  16411 packed tokens of the Llama-7B
+// layer with 2, 4 and 8: 157, 130 and 136 us; 2043 tokens of the Llama-70B layer
+// into E4M3 pages 20.4, 20.6 and 34 us.
+constexpr int kRopeBatch = 4;
+// CTAs an SM below which a group takes fewer rows: 32 tokens of the Llama-70B
+// layer 2.0 us, with four rows a group all the same 2.3 us.
 constexpr int kRopeMinCtas = 8;
 
 template <typename T>
@@ -235,15 +244,18 @@ static cudaError_t launch_rope(RopeParams p, int num_tokens, int sms, cudaStream
     constexpr int kGroups = kRopeThreads / (D / 8);
     // As many rows a group as leave kRopeMinCtas CTAs an SM: few tokens spread over
     // the SMs, many share a token's cosines among more rows.
-    auto blocks = [&](int batch, int rows) { return (rows + batch * kGroups - 1) / (batch * kGroups); };
+    auto blocks = [](int batch, int rows) {
+        return (rows + batch * kGroups - 1) / (batch * kGroups);
+    };
+    const int kv_rows = 2 * p.num_kv_heads;
     int batch = kRopeBatch;
     while (batch > 1 &&
-           (int64_t)num_tokens * (blocks(batch, p.num_q_heads) + blocks(batch, 2 * p.num_kv_heads)) <
+           (int64_t)num_tokens * (blocks(batch, p.num_q_heads) + blocks(batch, kv_rows)) <
                (int64_t)sms * kRopeMinCtas)
         batch /= 2;
     p.rows_per_cta = batch * kGroups;
     p.q_blocks = blocks(batch, p.num_q_heads);
-    const dim3 grid(num_tokens, p.q_blocks + blocks(batch, 2 * p.num_kv_heads));
+    const dim3 grid(num_tokens, p.q_blocks + blocks(batch, kv_rows));
     return p.interleaved ? launch_rope_t<T, D, F8, true>(p, grid, stream)
                          : launch_rope_t<T, D, F8, false>(p, grid, stream);
 }

@@ -19,10 +19,10 @@
 // A warpgroup's next S is made while it is at its softmax, and the other's
 // products run meanwhile: with one S of 128 tokens a warpgroup, which its P
 // frees only for the step after, the step was a chain of S, softmax and P V
-// (32 nodes on long contexts of the Llama-70B layer: LONG_BEFORE us; so LONG_AFTER us).
-// ROWS (more than 128 rows per KV head): the warpgroups take 128 rows each of
-// the same tokens, so 256 rows meet a K/V tile that was read once.  Otherwise
-// they take the same rows and every other tile, and meet at the end.
+// (32 nodes over 8 contexts of 82000 tokens, Llama-70B layer: 702 us; so 621 us).
+// ROWS: the warpgroups take 128 rows each of the same tokens, so 256 rows meet a
+// K/V tile that was read once.  Otherwise they take the same rows and every
+// other tile, and meet at the end.  (The rule and both sides' times: plan_tree.)
 // Four warps stream the K and V tiles by TMA through the block table into a ring
 // of tile slots (a warp takes about 95 cycles to issue a box, and the HBM rate
 // leaves 88 for the 2 KB boxes of 16-token pages), and one warp each issues a
@@ -34,6 +34,15 @@
 // one part is written to the output at once; one that is cut leaves a partial
 // (normalised O and its log-sum-exp) per CTA, at most two a CTA, and
 // tree_merge_kernel joins them.
+//
+// What bounds it: up to 128 rows per KV head, memory: 16 nodes on the Llama-70B
+// layer over 8 ragged contexts of 33000 to 131000 tokens take 390 to 404 us for
+// 2.69 GB (6.7 to 6.9 TB/s, 98 to 102 % of the copy rate), 8 nodes on the
+// Llama-7B layer (16 contexts of 520 to 4096) 97 to 100 us for 607 MB (90 to
+// 92 %).  With 256 rows, the tensor cores and the softmax beside them: 32 nodes
+// on the Llama-70B layer (32 x 4096 tokens) 149 us, of which the products alone,
+// with P twice, would take 109 at the dense rate (tensor pipe 65 % active); a
+// single 16-bit P would take 129.  Head dim 64 is bound by the softmax threads.
 //
 // Every wait is bounded, as in the decode kernels.
 #include <algorithm>
@@ -50,7 +59,6 @@ namespace pkv {
 struct TreeParams {
     void* out;
     const void* q;
-    const void* k_cache;
     const void* v_cache;
     const int32_t* block_tables;
     const int32_t* context_lens;
@@ -121,7 +129,10 @@ __host__ __device__ inline int tree_tiles(int n) {
 
 // A unit costs more than its places: its queries, the first products with
 // nothing to run beside, the masked tiles of its nodes, its output.  It counts
-// this many places ahead of its own on the line (COST0).
+// this many places ahead of its own on the line.  Measured for 0, 2, 3 and 4:
+// 8 nodes on the Llama-7B layer with ragged contexts 131, 116, 102 and 109 us,
+// 63 nodes on a ragged mix of 48 contexts (300 to 9000 tokens) 303, 262, 250 and
+// 253 us, 32 nodes on the Llama-70B layer 155, 150, 149 and 152 us.
 constexpr int kTreeUnitCost = 3;
 __host__ __device__ inline int tree_cost(int n) { return kTreeUnitCost + tree_tiles(n); }
 
@@ -1066,7 +1077,12 @@ static pkv_status plan_tree(int num_seqs, int tree_len, int num_q_heads, int num
     const int sms = current_sm_count();
     if (sms <= 0) return PKV_ERR_CUDA;
     const int rows = tree_len * (num_q_heads / num_kv_heads);
-    plan->two_row_tiles = rows > kTreeRows;
+    // ROWS or 128-row units (each reading the K/V again, mostly from L2).  32 x 4096
+    // tokens on the Llama-70B layer, ROWS against 128-row units: 136 rows per KV
+    // head 143 / 180 us, 256 rows 151 / 187, 512 rows 299 / 359; of three blocks of
+    // 128 rows ROWS would compute four: 320 rows 280 / 268 us, 384 rows 285 / 274.
+    const int blocks = (rows + kTreeRows - 1) / kTreeRows;
+    plan->two_row_tiles = blocks > 1 && blocks != 3;
     plan->unit_rows = plan->two_row_tiles ? 2 * kTreeRows : kTreeRows;
     plan->row_blocks = (rows + plan->unit_rows - 1) / plan->unit_rows;
     const int64_t units = (int64_t)num_seqs * num_kv_heads * plan->row_blocks;
@@ -1183,7 +1199,6 @@ extern "C" pkv_status pkv_tree_attention(
     TreeParams p = {};
     p.out = out;
     p.q = q;
-    p.k_cache = k_cache;
     p.v_cache = v_cache;
     p.block_tables = block_tables;
     p.context_lens = context_lens;
