@@ -626,9 +626,11 @@ def _refuse(t, name: str, dtype, device: int):
 
 def _arg(t: torch.Tensor, name: str, dtype, device: int) -> int:
     """The address of a dense tensor argument of ``dtype`` on CUDA device ``device``."""
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device and \
-            t.is_contiguous():
-        return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.get_device() == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass  # not a tensor
     return _refuse(t, name, dtype, device)
 
 
@@ -643,21 +645,36 @@ def _cuda_index(t: torch.Tensor, name: str, dims: int) -> int:
     return t.get_device()
 
 
-# The current stream's handle without a Stream object around it (1 us a call).
+# The current device and the current stream's handle, the latter without a Stream
+# object around it (1 us a call).
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
-def _stream_on(device: int, stream) -> int:
-    return _raw_stream(device) if stream is None else stream.cuda_stream
-
-
 def _run(fn, device: int, args) -> int:
     """fn(*args) with CUDA device ``device`` current."""
-    if torch.cuda.current_device() == device:
+    if _current_device() == device:
         return fn(*args)
     with torch.cuda.device(device):
         return fn(*args)
+
+
+def _caches(k_cache: torch.Tensor, v_cache: torch.Tensor, layout: str, dtype):
+    """(num_blocks, block_size, num_kv_heads, head_dim, dtype argument) of a call's
+    caches; ``dtype`` is the 16-bit type of its activations."""
+    shape = k_cache.shape
+    if v_cache.shape != shape or len(shape) != 4:
+        raise ValueError("the caches must be 4-D and of one shape")
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise TypeError(f"KV dtype must be float16 or bfloat16, got {dtype}")
+    nb, a, c, d = shape
+    if layout == "nhd":
+        return nb, a, c, d, code
+    if layout == "hnd":
+        return nb, c, a, d, code | LAYOUT_HND
+    raise ValueError(f"layout must be one of {_LAYOUTS}, got {layout!r}")
 
 
 def _keep(t: torch.Tensor, stream) -> torch.Tensor:
@@ -687,11 +704,12 @@ def _norm_rope(name, q, k, v, positions, cos_sin, k_cache, v_cache, slot_mapping
     dev = _cuda_index(q, "q", 3)
     if style != "half" and style != "interleaved":
         raise ValueError(f"style must be 'half' or 'interleaved', got {style!r}")
-    t, h_q, d = q.shape
-    nb, bs, h_kv, d2 = _cache_dims(k_cache, layout)
+    t, h_q, d = qshape = q.shape
     dt, i32 = q.dtype, torch.int32
-    if d2 != d or v_cache.shape != k_cache.shape or slot_mapping.shape != (t,) or \
-            positions.shape != (t,) or cos_sin.dim() != 2:
+    nb, bs, h_kv, d2, code = _caches(k_cache, v_cache, layout, dt)
+    tokens, kv_shape = (t,), (t, h_kv, d)
+    if d2 != d or slot_mapping.shape != tokens or positions.shape != tokens or \
+            cos_sin.dim() != 2:
         raise ValueError("inconsistent norm-rope-append shapes")
     qw = kw = 0
     if q_weight is not None:
@@ -702,13 +720,12 @@ def _norm_rope(name, q, k, v, positions, cos_sin, k_cache, v_cache, slot_mapping
         raise ValueError("a norm's weight must be [head_dim]")
     if q_out is None:
         q_out = _keep(torch.empty((t, h_q, d), dtype=dt, device=q.device), stream)
-    elif q_out.shape != q.shape:
+    elif q_out.shape != qshape:
         raise ValueError("q_out must have the shape of q")
-    code = _kv_code(q, layout)
     cache_dt = torch.uint8 if scales else dt
     qp, qs = _head_rows(q, "q", dt, dev, (t, h_q, d))
-    kp, ks = _head_rows(k, "k", dt, dev, (t, h_kv, d))
-    vp, vs = _head_rows(v, "v", dt, dev, (t, h_kv, d))
+    kp, ks = _head_rows(k, "k", dt, dev, kv_shape)
+    vp, vs = _head_rows(v, "v", dt, dev, kv_shape)
     npos, rd = cos_sin.shape
     r = _run(getattr(lib, name), dev, (
         _arg(q_out, "q_out", dt, dev), qp, qs, kp, ks, vp, vs, qw, kw, float(eps),
@@ -717,7 +734,7 @@ def _norm_rope(name, q, k, v, positions, cos_sin, k_cache, v_cache, slot_mapping
         _arg(k_cache, "k_cache", cache_dt, dev), _arg(v_cache, "v_cache", cache_dt, dev),
         _arg(slot_mapping, "slot_mapping", torch.int64, dev), t, nb, bs, h_q, h_kv, d,
         *scales, code, 0 if err_flag is None else _arg(err_flag, "err_flag", i32, dev),
-        _stream_on(dev, stream)))
+        _raw_stream(dev) if stream is None else stream.cuda_stream))
     if r:
         _check(r, name)
     return q_out
@@ -776,10 +793,13 @@ def tree_plan(parents: torch.Tensor, context_lens: torch.Tensor, block_tables: t
     """
     lib = load()
     dev = _cuda_index(parents, "parents", 2)
-    b, t = parents.shape
+    b, t = shape = parents.shape
     i32 = torch.int32
     words = (t + 31) // 32
-    if block_tables.dim() != 2 or context_lens.shape != (b,) or block_tables.shape[0] != b:
+    if block_tables.dim() != 2 or context_lens.shape != (b,):
+        raise ValueError("inconsistent tree-plan shapes")
+    tables, width = block_tables.shape
+    if tables != b:
         raise ValueError("inconsistent tree-plan shapes")
     if tree_mask is None:
         tree_mask = _keep(torch.empty((b, t, words), dtype=i32, device=parents.device), stream)
@@ -788,17 +808,17 @@ def tree_plan(parents: torch.Tensor, context_lens: torch.Tensor, block_tables: t
     if slot_mapping is None:
         slot_mapping = _keep(torch.empty((b, t), dtype=torch.int64, device=parents.device),
                              stream)
-    if tree_mask.shape != (b, t, words) or positions.shape != (b, t) or \
-            slot_mapping.shape != (b, t):
+    if tree_mask.shape != (b, t, words) or positions.shape != shape or \
+            slot_mapping.shape != shape:
         raise ValueError("inconsistent tree-plan outputs")
     r = _run(lib.pkv_tree_plan, dev, (
         _arg(tree_mask, "tree_mask", i32, dev), _arg(positions, "positions", i32, dev),
         _arg(slot_mapping, "slot_mapping", torch.int64, dev),
         _arg(parents, "parents", i32, dev), _arg(context_lens, "context_lens", i32, dev),
-        _arg(block_tables, "block_tables", i32, dev), block_tables.shape[1],
+        _arg(block_tables, "block_tables", i32, dev), width,
         int(max_context_len), b, t, int(num_blocks), int(block_size),
         0 if err_flag is None else _arg(err_flag, "err_flag", i32, dev),
-        _stream_on(dev, stream)))
+        _raw_stream(dev) if stream is None else stream.cuda_stream))
     if r:
         _check(r, "pkv_tree_plan")
     return tree_mask, positions, slot_mapping
@@ -830,17 +850,17 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     """
     lib = load()
     dev = _cuda_index(q, "q", 4)
-    b, t, h_q, d = q.shape
-    nb, bs, h_kv, d2 = _cache_dims(k_cache, layout)
+    b, t, h_q, d = qshape = q.shape
+    dt, i32 = q.dtype, torch.int32
+    nb, bs, h_kv, d2, code = _caches(k_cache, v_cache, layout, dt)
     words = (t + 31) // 32
-    if d2 != d or v_cache.shape != k_cache.shape or block_tables.dim() != 2 or \
-            block_tables.shape[0] != b or context_lens.shape != (b,) or tree_mask.dim() != 3:
+    if d2 != d or block_tables.dim() != 2 or context_lens.shape != (b,) or tree_mask.dim() != 3:
         raise ValueError("inconsistent tree attention shapes")
+    tables, width = block_tables.shape
     m0, m1, m2 = tree_mask.shape
     s0, s1, s2 = tree_mask.stride()
-    if (m0 != b and m0 != 1) or m1 != t or m2 != words:
+    if tables != b or (m0 != b and m0 != 1) or m1 != t or m2 != words:
         raise ValueError("inconsistent tree attention shapes")
-    dt, i32 = q.dtype, torch.int32
     if tree_mask.dtype is not i32 or tree_mask.get_device() != dev:
         _refuse(tree_mask, "tree_mask", i32, dev)
     if m0 and ((words > 1 and s2 != 1) or (t > 1 and s1 != words)):
@@ -849,7 +869,7 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
         scale = 1.0 / math.sqrt(d)
     if out is None:
         out = _keep(torch.empty_like(q), stream)
-    elif out.shape != q.shape:
+    elif out.shape != qshape:
         raise ValueError("out must have the shape of q")
     if workspace is None:  # a given workspace is checked by the library itself
         with torch.cuda.device(dev):
@@ -858,12 +878,12 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     r = _run(lib.pkv_tree_attention, dev, (
         _arg(out, "out", dt, dev), _arg(q, "q", dt, dev),
         _arg(k_cache, "k_cache", dt, dev), _arg(v_cache, "v_cache", dt, dev),
-        _arg(block_tables, "block_tables", i32, dev), block_tables.shape[1],
+        _arg(block_tables, "block_tables", i32, dev), width,
         _arg(context_lens, "context_lens", i32, dev), int(max_context_len),
         tree_mask.data_ptr(), s0 if m0 > 1 else 0, b, t, nb, bs, h_q, h_kv, d, float(scale),
         _arg(workspace, "workspace", workspace.dtype, dev), workspace.nbytes,
-        _kv_code(q, layout), 0 if err_flag is None else _arg(err_flag, "err_flag", i32, dev),
-        _stream_on(dev, stream)))
+        code, 0 if err_flag is None else _arg(err_flag, "err_flag", i32, dev),
+        _raw_stream(dev) if stream is None else stream.cuda_stream))
     if r:
         _check(r, "pkv_tree_attention")
     return out
@@ -882,27 +902,28 @@ def tree_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torc
     """
     lib = load()
     dev = _cuda_index(k_cache, "k_cache", 4)
-    nb, bs, h_kv, d = _cache_dims(k_cache, layout)
     dt, i32 = k_cache.dtype, torch.int32
+    nb, bs, h_kv, d, code = _caches(k_cache, v_cache, layout, dt)
     if block_tables.dim() != 2 or accepted.dim() != 2:
         raise ValueError("inconsistent tree-commit shapes")
-    b = block_tables.shape[0]
-    if v_cache.shape != k_cache.shape or context_lens.shape != (b,) or \
-            accepted.shape[0] != b or accepted_lens.shape != (b,):
+    b, width = block_tables.shape
+    paths, most = accepted.shape
+    seqs = (b,)
+    if context_lens.shape != seqs or paths != b or accepted_lens.shape != seqs:
         raise ValueError("inconsistent tree-commit shapes")
     if new_context_lens is None:
         new_context_lens = _keep(torch.empty(b, dtype=i32, device=k_cache.device), stream)
-    elif new_context_lens.shape != (b,):
+    elif new_context_lens.shape != seqs:
         raise ValueError("new_context_lens must be [sequences]")
     r = _run(lib.pkv_tree_commit, dev, (
         _arg(k_cache, "k_cache", dt, dev), _arg(v_cache, "v_cache", dt, dev),
-        _arg(block_tables, "block_tables", i32, dev), block_tables.shape[1],
+        _arg(block_tables, "block_tables", i32, dev), width,
         _arg(context_lens, "context_lens", i32, dev), int(tree_len),
         _arg(accepted, "accepted", i32, dev), _arg(accepted_lens, "accepted_lens", i32, dev),
-        accepted.shape[1], _arg(new_context_lens, "new_context_lens", i32, dev), b, nb, bs,
-        h_kv, d, _kv_code(k_cache, layout),
+        most, _arg(new_context_lens, "new_context_lens", i32, dev), b, nb, bs,
+        h_kv, d, code,
         0 if err_flag is None else _arg(err_flag, "err_flag", i32, dev),
-        _stream_on(dev, stream)))
+        _raw_stream(dev) if stream is None else stream.cuda_stream))
     if r:
         _check(r, "pkv_tree_commit")
     return new_context_lens

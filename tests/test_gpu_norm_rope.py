@@ -27,6 +27,7 @@ CASES = {
     "packed": dict(t=61, h_q=10, h_kv=2, d=128, packed=True),
     "one_head": dict(t=5, h_q=1, h_kv=1, d=64, packed=True, bs=128),
     "wide": dict(t=300, h_q=64, h_kv=8, d=128, pads=17),
+    "more_tokens_than_65535": dict(t=65600, h_q=1, h_kv=1, d=64, bs=128),
     "mha": dict(t=260, h_q=32, h_kv=32, d=128, dtype="fp16", packed=True, style="interleaved"),
 }
 
@@ -212,6 +213,22 @@ def test_strided_and_empty_calls_are_refused_or_do_nothing():
         pkv.norm_rope_append(args[0], args[1].half(), *args[2:], **kw)
     with pytest.raises(TypeError, match="int32"):
         pkv.norm_rope_append(*args[:3], args[3].long(), *args[4:], **kw)
+
+
+def test_on_another_stream():
+    c = _make(t=50, h_q=8, h_kv=2, d=128, packed=True)
+    args, kw = _gpu(c)
+    slots = torch.full_like(args[7], -1)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(2_000_000)
+        slots.copy_(args[7])
+    q_out = pkv.norm_rope_append(*args[:7], slots, stream=side, **kw)
+    junk = torch.full_like(q_out, 7.0)  # the allocator must not hand out the call's output
+    side.synchronize()
+    _check(c, q_out, args[5], args[6])
+    assert (junk == 7).all()
 
 
 def test_captured_in_a_graph_with_the_append_and_decode_it_replaces():

@@ -52,6 +52,20 @@ def test_plan_of_a_chain_and_a_star():
     assert bits[0].sum() == t * (t + 1) // 2 and bits[1].sum() == 2 * t - 1 and bits[2].sum() == t
 
 
+def test_plan_of_more_sequences_than_a_grid_dimension_of_65535():
+    b, t = 66001, 2
+    parents = torch.tensor([[-1, 0]], dtype=torch.int32).repeat(b, 1)
+    parents[-1, 1] = -1
+    tables = torch.arange(b, dtype=torch.int32)[:, None].contiguous()
+    lens = torch.full((b,), 5, dtype=torch.int32)
+    mask, pos, slot = pkv.tree_plan(parents.cuda(), lens.cuda(), tables.cuda(), b, 16, 16)
+    assert mask[:-1, 0, 0].eq(1).all() and mask[:-1, 1, 0].eq(3).all()
+    assert mask[-1, :, 0].tolist() == [1, 2] and pos[-1].tolist() == [3, 3]
+    assert pos[:-1].eq(torch.tensor([3, 4], device="cuda")).all()
+    want = torch.arange(b)[:, None] * 16 + torch.tensor([3, 4])
+    assert torch.equal(slot.cpu(), want)
+
+
 @pytest.mark.parametrize("what", ["forward", "self", "below", "orphan", "block", "short", "long",
                                   "negative"])
 def test_plan_flags_and_leaves_out_what_is_malformed(what):
@@ -113,6 +127,8 @@ ATTENTION = {
     "many_ragged": dict(lens=[8 + 37 * i % 900 for i in range(70)], t=8, h_q=4, h_kv=2, d=64,
                         bs=16, dtype="fp16"),
     "split_over_many": dict(lens=[20000], t=5, h_q=4, h_kv=1, d=64, bs=16, dtype="bf16"),
+    "many_sequences": dict(lens=[1 + 7 * i % 40 for i in range(1400)], t=1, h_q=2, h_kv=2, d=64,
+                           bs=16, dtype="bf16"),
     "peaked": dict(lens=[40, 900], t=16, h_q=8, h_kv=1, d=128, bs=16, dtype="bf16", q_scale=6.0),
 }
 
@@ -410,6 +426,31 @@ def test_commit_flags_and_moves_nothing_of_a_malformed_path(what):
     assert pkv.check_error(flag) == want
     assert torch.equal(got.cpu(), new)
     assert _same_bits(g["k"], k) and _same_bits(g["v"], v)
+
+
+def test_plan_and_commit_on_another_stream():
+    t = 16
+    c = ref.make_case(61, [40, 200], t, 4, 2, 64, 16, "bf16")
+    accepted = torch.tensor([[0, 3, 15], [2, 3, 9]], dtype=torch.int32)
+    counts = torch.tensor([3, 2], dtype=torch.int32)
+    nb = c["k"].shape[0]
+    bits, positions, slots, _ = ref.plan(c["parents"], c["lens"], c["tables"], 16, 200, nb)
+    k, v, new = ref.commit(c, t, accepted, counts)
+    g = ref.on_gpu(c)
+    acc, cnt = accepted.cuda(), counts.cuda()
+    lens = torch.zeros_like(g["lens"])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(2_000_000)
+        lens.copy_(g["lens"])
+    mask, pos, slot = pkv.tree_plan(g["parents"], lens, g["tables"], nb, 16, 200, stream=side)
+    got = pkv.tree_commit(g["k"], g["v"], g["tables"], lens, t, acc, cnt, stream=side)
+    junk = [torch.full_like(x, 7) for x in (mask, pos, slot, got)]  # not the calls' outputs
+    side.synchronize()
+    assert torch.equal(mask.cpu(), ref.pack(bits)) and torch.equal(pos.cpu(), positions)
+    assert torch.equal(slot.cpu(), slots) and torch.equal(got.cpu(), new)
+    assert _same_bits(g["k"], k) and _same_bits(g["v"], v) and all((x == 7).all() for x in junk)
 
 
 # ---------------------------------------------------------------------------
