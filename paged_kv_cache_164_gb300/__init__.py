@@ -4,7 +4,9 @@ A thin ctypes binding over the C ABI in ``include/pkv.h`` (``libpkv.so``).
 Every step of the path runs in the library's CUDA kernels; this module only
 checks tensor types, passes device pointers, sizes and the current CUDA stream,
 and turns status codes into exceptions.  PyTorch provides device memory and
-streams.  There is no CPU fallback: if the library is not built, or a tensor is
+streams.  The calls of the tree step, whose kernels take 2 us at small batches,
+have a quick form of the same checks in C++ (``pkv_binding.so``); what it does
+not take is checked here.  There is no CPU fallback: if the library is not built, or a tensor is
 not on a CUDA device, the call raises.
 
 Calls (same names as the C entry points, without the ``pkv_`` prefix):
@@ -22,6 +24,8 @@ Calls (same names as the C entry points, without the ``pkv_`` prefix):
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import math
 import os
 from typing import Optional
@@ -51,6 +55,10 @@ class PkvError(RuntimeError):
 
 
 _lib: Optional[ctypes.CDLL] = None
+# The quick form of the tree step's calls (csrc/pkv_binding.cpp): for arguments of
+# the usual form a call's status, None for all others; None itself where it was not
+# built, or for another torch than this one.
+_quick = None
 
 
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
@@ -119,7 +127,26 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                  "pkv_check_error", "pkv_max_group_size", "pkv_multi_query_plan"):
         getattr(lib, name).restype = i
     _lib = lib
+    _load_quick(lib)
     return lib
+
+
+def _load_quick(lib: ctypes.CDLL) -> None:
+    global _quick
+    path = os.path.join(_HERE, "_build", "pkv_binding.so")
+    if not os.path.exists(path):
+        return
+    loader = importlib.machinery.ExtensionFileLoader("pkv_binding", path)
+    try:
+        module = importlib.util.module_from_spec(
+            importlib.util.spec_from_loader("pkv_binding", loader))
+    except ImportError:  # built for another Python or torch
+        return
+    if module.torch_version == torch.__version__:
+        module.bind(*(ctypes.cast(getattr(lib, "pkv_" + name), ctypes.c_void_p).value
+                      for name in ("norm_rope_append", "norm_rope_append_fp8", "tree_plan",
+                                   "tree_attention", "tree_commit")))
+        _quick = module
 
 
 def _check(status: int, what: str) -> None:
@@ -645,6 +672,13 @@ def _cuda_index(t: torch.Tensor, name: str, dims: int) -> int:
     return t.get_device()
 
 
+def _c_int(v, name: str) -> int:
+    v = int(v)
+    if not -2 ** 31 <= v < 2 ** 31:
+        raise ValueError(f"{name} does not fit in 32 bits")
+    return v
+
+
 # The current device and the current stream's handle, the latter without a Stream
 # object around it (1 us a call).
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
@@ -700,6 +734,14 @@ def _head_rows(t: torch.Tensor, name: str, dtype, device: int, shape):
 
 def _norm_rope(name, q, k, v, positions, cos_sin, k_cache, v_cache, slot_mapping, q_weight,
                k_weight, eps, style, q_out, err_flag, stream, layout, scales):
+    if _quick is not None and stream is None:
+        r = _quick.norm_rope_append(q, k, v, positions, cos_sin, k_cache, v_cache, slot_mapping,
+                                    q_weight, k_weight, eps, style, q_out, err_flag, layout,
+                                    *scales)
+        if r is not None:
+            if r:
+                _check(r, name)
+            return q_out
     lib = load()
     dev = _cuda_index(q, "q", 3)
     if style != "half" and style != "interleaved":
@@ -791,6 +833,13 @@ def tree_plan(parents: torch.Tensor, context_lens: torch.Tensor, block_tables: t
     [B, T]: the nodes' rotary positions; slot_mapping int64 [B, T]: their cache
     slots (-1 for an absent node).
     """
+    if _quick is not None and stream is None:
+        r = _quick.tree_plan(parents, context_lens, block_tables, num_blocks, block_size,
+                             max_context_len, tree_mask, positions, slot_mapping, err_flag)
+        if r is not None:
+            if r:
+                _check(r, "pkv_tree_plan")
+            return tree_mask, positions, slot_mapping
     lib = load()
     dev = _cuda_index(parents, "parents", 2)
     b, t = shape = parents.shape
@@ -816,7 +865,8 @@ def tree_plan(parents: torch.Tensor, context_lens: torch.Tensor, block_tables: t
         _arg(slot_mapping, "slot_mapping", torch.int64, dev),
         _arg(parents, "parents", i32, dev), _arg(context_lens, "context_lens", i32, dev),
         _arg(block_tables, "block_tables", i32, dev), width,
-        int(max_context_len), b, t, int(num_blocks), int(block_size),
+        _c_int(max_context_len, "max_context_len"), b, t, _c_int(num_blocks, "num_blocks"),
+        _c_int(block_size, "block_size"),
         0 if err_flag is None else _arg(err_flag, "err_flag", i32, dev),
         _raw_stream(dev) if stream is None else stream.cuda_stream))
     if r:
@@ -848,6 +898,14 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     nodes whose bits are set in tree_mask[b, i] (int32 [B, T, ceil(T / 32)], or
     [1, T, ...] for one mask of all sequences).
     """
+    if _quick is not None and stream is None:
+        r = _quick.tree_attention(q, k_cache, v_cache, block_tables, context_lens,
+                                  max_context_len, tree_mask, scale, out, workspace, err_flag,
+                                  layout)
+        if r is not None:
+            if r:
+                _check(r, "pkv_tree_attention")
+            return out
     lib = load()
     dev = _cuda_index(q, "q", 4)
     b, t, h_q, d = qshape = q.shape
@@ -879,7 +937,8 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
         _arg(out, "out", dt, dev), _arg(q, "q", dt, dev),
         _arg(k_cache, "k_cache", dt, dev), _arg(v_cache, "v_cache", dt, dev),
         _arg(block_tables, "block_tables", i32, dev), width,
-        _arg(context_lens, "context_lens", i32, dev), int(max_context_len),
+        _arg(context_lens, "context_lens", i32, dev),
+        _c_int(max_context_len, "max_context_len"),
         tree_mask.data_ptr(), s0 if m0 > 1 else 0, b, t, nb, bs, h_q, h_kv, d, float(scale),
         _arg(workspace, "workspace", workspace.dtype, dev), workspace.nbytes,
         code, 0 if err_flag is None else _arg(err_flag, "err_flag", i32, dev),
@@ -900,6 +959,13 @@ def tree_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torc
     accepted_lens int32 [B] of them.  Returns the new context lengths (int32 [B]):
     context_lens - tree_len + accepted_lens.
     """
+    if _quick is not None and stream is None:
+        r = _quick.tree_commit(k_cache, v_cache, block_tables, context_lens, tree_len, accepted,
+                               accepted_lens, new_context_lens, err_flag, layout)
+        if r is not None:
+            if r:
+                _check(r, "pkv_tree_commit")
+            return new_context_lens
     lib = load()
     dev = _cuda_index(k_cache, "k_cache", 4)
     dt, i32 = k_cache.dtype, torch.int32
@@ -918,7 +984,7 @@ def tree_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torc
     r = _run(lib.pkv_tree_commit, dev, (
         _arg(k_cache, "k_cache", dt, dev), _arg(v_cache, "v_cache", dt, dev),
         _arg(block_tables, "block_tables", i32, dev), width,
-        _arg(context_lens, "context_lens", i32, dev), int(tree_len),
+        _arg(context_lens, "context_lens", i32, dev), _c_int(tree_len, "tree_len"),
         _arg(accepted, "accepted", i32, dev), _arg(accepted_lens, "accepted_lens", i32, dev),
         most, _arg(new_context_lens, "new_context_lens", i32, dev), b, nb, bs,
         h_kv, d, code,

@@ -3,6 +3,11 @@
 Each ``csrc/*.cu`` file is compiled to an object in parallel, then linked into
 one shared object with the CUDA runtime linked statically, so the library
 depends on nothing but the driver at run time.
+
+``csrc/pkv_binding.cpp`` becomes ``_build/pkv_binding.so``, the quick form of
+some Python calls, which needs the headers of Python and torch.  Where they are
+missing it is left out with a warning: those calls are then checked and passed
+on in Python.
 """
 from __future__ import annotations
 
@@ -13,6 +18,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -20,6 +26,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libpkv.so")
+BINDING_SOURCE = os.path.join(CSRC, "pkv_binding.cpp")
+BINDING = os.path.join(OUT_DIR, "pkv_binding.so")
 # The NaN-sentinel debug build (-DPKV_DEBUG), kept apart from the normal one.
 DEBUG_DIR = os.path.join(HERE, "_build_debug")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -50,8 +58,55 @@ def _inputs_digest(flags) -> str:
     return h.hexdigest()
 
 
+def _binding_command():
+    import torch
+    from torch.utils.cpp_extension import include_paths, library_paths
+    flags = ["-O2", "-std=c++17", "-fPIC", "-shared", "-I", INCLUDE,
+             "-I", sysconfig.get_paths()["include"],
+             "-I", os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include"),
+             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+             f'-DPKV_TORCH_VERSION="{torch.__version__}"']
+    for d in include_paths():
+        flags += ["-isystem", d]
+    for d in library_paths():
+        flags += ["-L", d]
+    libs = ["-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    return ["g++", *flags, BINDING_SOURCE, *libs]
+
+
+def build_binding(force: bool = False) -> bool:
+    """Compiles the binding module unless an up-to-date build exists; False: it
+    cannot be built here."""
+    tmp = BINDING + f".tmp{os.getpid()}"
+    try:
+        cmd = _binding_command()
+        h = hashlib.sha256(" ".join([sys.version, *cmd]).encode())
+        for f in (BINDING_SOURCE, os.path.join(INCLUDE, "pkv.h"), os.path.abspath(__file__)):
+            with open(f, "rb") as fh:
+                h.update(fh.read())
+        stamp = BINDING + ".stamp"
+        if not force and os.path.exists(BINDING) and os.path.exists(stamp):
+            with open(stamp) as f:
+                if f.read().strip() == h.hexdigest():
+                    return True
+        os.makedirs(OUT_DIR, exist_ok=True)
+        if os.path.exists(BINDING):  # never one of other headers than these
+            os.remove(BINDING)
+        r = subprocess.run([*cmd, "-o", tmp], capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(r.stderr[-2000:])
+        os.replace(tmp, BINDING)
+        with open(stamp, "w") as f:
+            f.write(h.hexdigest())
+        return True
+    except (ImportError, AttributeError, OSError, RuntimeError) as e:
+        print(f"pkv: the quick binding is left out: {e}", file=sys.stderr)
+        return False
+
+
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
-    """Compiles and links the library unless an up-to-date build exists.
+    """Compiles and links the library, and the binding module, unless up-to-date
+    builds exist.
 
     ``debug``: the -DPKV_DEBUG build (NaN-filled ring slots), in its own
     directory.  PKV_NVCC_EXTRA adds flags to either build.
@@ -64,6 +119,7 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
     if not force and os.path.exists(lib) and os.path.exists(stamp):
         with open(stamp) as f:
             if f.read().strip() == digest:
+                build_binding()
                 return lib
     os.makedirs(out_dir, exist_ok=True)
     nvcc = _nvcc()
@@ -79,7 +135,9 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
         return obj
 
     with concurrent.futures.ThreadPoolExecutor(max_workers=os.cpu_count() or 4) as ex:
+        binding = ex.submit(build_binding, force)
         objs = list(ex.map(compile_one, _sources()))
+        binding.result()
     tmp = lib + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

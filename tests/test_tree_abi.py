@@ -137,3 +137,20 @@ def test_bindings_refuse_cpu_tensors(lib):
         pkv.tree_commit(k, k, i, i[0], 1, i, i[0])
     with pytest.raises(ValueError, match="CUDA"):
         pkv.norm_rope_append(k[0], k[0], k[0], i[0], k[0], k, k, i[0])
+
+
+def test_quick_binding_leaves_what_it_does_not_know_to_python(lib):
+    if pkv._quick is None:
+        pytest.skip("built without the headers of Python and torch")
+    i = torch.zeros((1, 1), dtype=torch.int32)
+    k = torch.zeros((4, 16, 2, 64), dtype=torch.float16)
+    quick = pkv._quick
+    for call, n in ((quick.norm_rope_append, 15), (quick.norm_rope_append, 17),
+                    (quick.tree_plan, 10), (quick.tree_attention, 12), (quick.tree_commit, 10)):
+        for args in ((), (i,) * n, (k,) * n, (k[0],) * n, (None,) * n, (1,) * n, ("nhd",) * n,
+                     (object(),) * (n + 1), (i.to_sparse(),) * n, (k.to("meta"),) * n):
+            assert call(*args) is None
+    with pytest.raises(TypeError):
+        quick.bind(1, 2)
+    with pytest.raises(ValueError):
+        quick.bind(0, 0, 0, 0, 0)
