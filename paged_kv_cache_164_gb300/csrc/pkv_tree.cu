@@ -13,13 +13,16 @@ namespace pkv {
 // ---------------------------------------------------------------------------
 // The plan
 // ---------------------------------------------------------------------------
-// One CTA per sequence, one thread per node.  A node's ancestors are its parent
-// chain, whose indices fall, so a thread walks the chain once (parents in
-// shared memory), gathering the 32 bits of a mask word in a register before it
-// goes on to the next lower word.  Latency is all it costs: a few dependent
-// loads and a walk as long as the tree is deep (one sequence's 64 nodes: 2.3 us,
-// a launch's least; 256 sequences of 250 nodes, some 55 deep: 7.7 us).  Soundness
-// and bits take a walk each: one walk that does both measured 13.3 us.
+// A thread per node, a CTA per kPlanRows nodes of a sequence.  A node's
+// ancestors are its parent chain, whose indices fall.  The nodes of one mask word
+// belong to one warp, which finds their ancestors among themselves by doubling
+// (five rounds of shuffles: the bits, and the first ancestor before the word, if
+// the chain is sound); then a thread hops from word to word instead of from node
+// to node, and the bits it gathers count its depth.  The rows go through shared
+// memory, so that their stores are dense: a row is 4 to 128 bytes.
+// Latency is all it costs.  One sequence's 64 nodes: 1.7 us, a launch's least;
+// 256 sequences of 250 nodes, some 55 deep: 5.1 us (8.7 with a walk of the whole
+// chain for its soundness and another for its bits, and each thread storing its row).
 
 struct TreePlanParams {
     int32_t* tree_mask;
@@ -36,62 +39,98 @@ struct TreePlanParams {
     int block_size;
 };
 
-__global__ void __launch_bounds__(PKV_MAX_TREE_LEN) tree_plan_kernel(const TreePlanParams p) {
-    __shared__ int32_t s_parent[PKV_MAX_TREE_LEN];
+constexpr int kPlanRows = 256;
+
+// Shared memory: {next ancestor before the node's word, bits in its word} of each
+// node, then the CTA's rows of the mask, an odd number of words apart.
+static int plan_smem_bytes(int tree_len) {
+    const int words = (tree_len + 31) / 32;
+    return words * 32 * (int)sizeof(int2) + std::min(tree_len, kPlanRows) * (words | 1) * 4;
+}
+
+__global__ void __launch_bounds__(kPlanRows) tree_plan_kernel(const TreePlanParams p) {
+    extern __shared__ int2 s_link[];
     ptx::launch_dependents();
     ptx::grid_dependency_wait();
-    const int b = blockIdx.x;
     const int t = p.tree_len;
-    const int i = threadIdx.x;
-    const int64_t at = (int64_t)b * t + i;
-    const int n_raw = __ldg(p.context_lens + b);
-    const int par = i < t ? __ldg(p.parents + at) : PKV_TREE_ABSENT;
-    const bool n_ok = n_raw >= t && n_raw <= p.cap;
-    if (i < t) s_parent[i] = par;
-    if (i == 0 && !n_ok && n_raw != 0) flag_error(p.err_flag, PKV_EFLAG_CONTEXT_LEN);
-    const int base = clamped_len(n_raw, p.cap) - t;
-    // the slot's block id, read while the parents settle
-    const int pos = base + i;
-    int blk = -1;
-    if (i < t && n_ok)
-        blk = __ldg(p.block_tables + (int64_t)b * p.max_blocks_per_seq + pos / p.block_size);
-    __syncthreads();
-    if (i >= t) return;
-
-    // is every link of the chain sound (an earlier, present node, or the context)?
-    int depth = 0;
-    bool there = n_raw != 0;
-    for (int cur = i;;) {
-        const int up = s_parent[cur];
-        if (up == -1) break;
-        if (up < -1 || up >= cur) {
-            there = false;
-            break;
-        }
-        ++depth;
-        cur = up;
-    }
-    if (n_raw != 0 && !there && par != PKV_TREE_ABSENT) flag_error(p.err_flag, PKV_EFLAG_TREE);
     const int words = (t + 31) / 32;
-    int32_t* mask = p.tree_mask + at * words;
-    int cur = there ? i : -1;
-    for (int w = words - 1; w >= 0; --w) {
-        uint32_t bits = 0;
-        while (cur >= 0 && (cur >> 5) == w) {
-            bits |= 1u << (cur & 31);
-            cur = s_parent[cur];
+    const int parts = (t + kPlanRows - 1) / kPlanRows;
+    const int b = blockIdx.x / parts;
+    const int r0 = (blockIdx.x - b * parts) * kPlanRows;
+    const int nrows = min(kPlanRows, t - r0);
+    const int lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int i = r0 + threadIdx.x;  // this thread's node
+    const int n_raw = __ldg(p.context_lens + b);
+    const bool n_ok = n_raw >= t && n_raw <= p.cap;
+    const int base = clamped_len(n_raw, p.cap) - t;
+    const int pos = base + i;
+    const int bs_shift = __ffs(p.block_size) - 1;
+
+    // The links of the words up to the CTA's last one; a warp's last word is its
+    // own (words of rows are kPlanRows / 32 apart, which is the warps of a CTA
+    // where a sequence has several).
+    int par = PKV_TREE_ABSENT, up = PKV_TREE_ABSENT, blk = -1;
+    uint32_t bits = 0;
+    for (int w = warp; w * 32 < r0 + nrows; w += warps) {
+        const int node = w * 32 + lane;
+        par = node < t ? __ldg(p.parents + (int64_t)b * t + node) : PKV_TREE_ABSENT;
+        if (node == i && i < t && n_ok)  // (read while the links settle)
+            blk = __ldg(p.block_tables + (int64_t)b * p.max_blocks_per_seq + (pos >> bs_shift));
+        up = par < -1 || par >= node ? PKV_TREE_ABSENT : par;
+        bits = 1u << lane;
+#pragma unroll
+        for (int round = 0; round < 5; ++round) {
+            const uint32_t more = __shfl_sync(0xffffffffu, bits, up & 31);
+            const int next = __shfl_sync(0xffffffffu, up, up & 31);
+            if (up >= w * 32) {
+                bits |= more;
+                up = next;
+            }
         }
-        mask[w] = (int32_t)bits;
+        s_link[node] = make_int2(up, (int)bits);
     }
-    p.positions[at] = there ? max(0, base + depth) : 0;
-    int64_t slot = -1;
-    if (there && n_ok) {
-        if (blk < 0 || blk >= p.num_blocks)
-            flag_error(p.err_flag, PKV_EFLAG_BLOCK_ID);
-        else
-            slot = (int64_t)blk * p.block_size + pos % p.block_size;
+    __syncthreads();
+
+    uint32_t* s_mask = reinterpret_cast<uint32_t*>(s_link + words * 32);
+    if (i < t) {
+        uint32_t* row = s_mask + threadIdx.x * (words | 1);
+        int depth = __popc(bits) - 1;
+        int w = words - 1;
+        for (; w > i >> 5; --w) row[w] = 0;
+        row[w--] = bits;
+        while (up >= 0) {
+            const int2 link = s_link[up];
+            for (; w > up >> 5; --w) row[w] = 0;
+            row[w--] = (uint32_t)link.y;
+            depth += __popc(link.y);
+            up = link.x;
+        }
+        for (; w >= 0; --w) row[w] = 0;
+        // every link of the chain is sound: an earlier, present node, or the context
+        const bool there = n_raw != 0 && up == -1;
+        if (!there)
+            for (w = 0; w < words; ++w) row[w] = 0;
+        if (n_raw != 0 && !there && par != PKV_TREE_ABSENT)
+            flag_error(p.err_flag, PKV_EFLAG_TREE);
+        if (i == 0 && !n_ok && n_raw != 0) flag_error(p.err_flag, PKV_EFLAG_CONTEXT_LEN);
+        const int64_t at = (int64_t)b * t + i;
+        p.positions[at] = there ? max(0, base + depth) : 0;
+        int64_t slot = -1;
+        if (there && n_ok) {
+            if (blk < 0 || blk >= p.num_blocks)
+                flag_error(p.err_flag, PKV_EFLAG_BLOCK_ID);
+            else
+                slot = ((int64_t)blk << bs_shift) + (pos & (p.block_size - 1));
+        }
+        p.slot_mapping[at] = slot;
     }
-    p.slot_mapping[at] = slot;
+    __syncthreads();
+    int32_t* mask = p.tree_mask + ((int64_t)b * t + r0) * words;
+    for (int k = threadIdx.x; k < nrows * words; k += blockDim.x) {
+        const int r = k / words;
+        mask[k] = (int32_t)s_mask[r * (words | 1) + k - r * words];
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -204,10 +243,11 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const TreeC
 
 template <typename P>
 static pkv_status launch_pdl(void (*kern)(const P), const P& p, dim3 grid, int threads,
-                             void* stream) {
+                             void* stream, int smem_bytes = 0) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem_bytes;
     cfg.stream = (cudaStream_t)stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -258,7 +298,11 @@ extern "C" pkv_status pkv_tree_plan(int32_t* tree_mask, int32_t* positions, int6
     p.tree_len = tree_len;
     p.num_blocks = num_blocks;
     p.block_size = block_size;
-    return launch_pdl(tree_plan_kernel, p, dim3(num_seqs), (tree_len + 31) / 32 * 32, stream);
+    const int parts = (tree_len + kPlanRows - 1) / kPlanRows;
+    if (num_seqs > INT_MAX / parts) return PKV_ERR_UNSUPPORTED;
+    return launch_pdl(tree_plan_kernel, p, dim3(num_seqs * parts),
+                      std::min((tree_len + 31) / 32 * 32, kPlanRows), stream,
+                      plan_smem_bytes(tree_len));
 }
 
 extern "C" pkv_status pkv_tree_commit(void* k_cache, void* v_cache, const int32_t* block_tables,

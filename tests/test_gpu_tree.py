@@ -66,6 +66,36 @@ def test_plan_of_more_sequences_than_a_grid_dimension_of_65535():
     assert torch.equal(slot.cpu(), want)
 
 
+@pytest.mark.parametrize("t", [31, 64, 100, 257, 513, 1000])
+def test_plan_of_random_chains_with_unsound_links(t):
+    """Links to the parent just before, to nodes far before, to nothing, to the node itself,
+    behind it and out of range."""
+    gen = torch.Generator().manual_seed(t)
+    b = 9
+    i = torch.arange(t)
+    parents = torch.empty(b, t, dtype=torch.int32)
+    for s in range(b):
+        near = i - 1 - (torch.rand(t, generator=gen) * (1, 3, 40)[s % 3]).to(torch.int64)
+        far = (torch.rand(t, generator=gen) * i).to(torch.int64)
+        parents[s] = torch.where(torch.rand(t, generator=gen) < 0.1, far, near).clamp(min=-1)
+    odd = torch.rand(b, t, generator=gen) < torch.linspace(0, 0.02, b)[:, None]
+    kind = torch.randint(0, 6, (b, t), generator=gen)
+    bad = torch.stack([i, i + 1, torch.full((t,), 2 ** 31 - 1), torch.full((t,), -3),
+                       torch.full((t,), ref.ABSENT), torch.full((t,), -2 ** 31)])
+    parents = torch.where(odd, bad[kind, i.expand(b, t)], parents.long()).to(torch.int32)
+    lens = torch.randint(t, t + 200, (b,), generator=gen, dtype=torch.int32)
+    width = (t + 200 + 15) // 16
+    tables = torch.randperm(b * width, generator=gen).to(torch.int32).view(b, width)
+    bits, positions, slots, flags = ref.plan(parents, lens, tables, 16, t + 200, b * width)
+    flag = pkv.new_error_flag("cuda")
+    mask, pos, slot = pkv.tree_plan(parents.cuda(), lens.cuda(), tables.cuda(), b * width, 16,
+                                    t + 200, err_flag=flag)
+    torch.cuda.synchronize()
+    assert int(flag.item()) == flags
+    assert torch.equal(mask.cpu(), ref.pack(bits))
+    assert torch.equal(pos.cpu(), positions) and torch.equal(slot.cpu(), slots)
+
+
 @pytest.mark.parametrize("what", ["forward", "self", "below", "orphan", "block", "short", "long",
                                   "negative"])
 def test_plan_flags_and_leaves_out_what_is_malformed(what):
