@@ -141,9 +141,11 @@ __global__ void __launch_bounds__(kPlanRows) tree_plan_kernel(const TreePlanPara
 // moves its own 16-byte column of the rows in increasing j never overwrites a
 // row it still has to read (a later source path[j'] >= j' > j).  Threads share
 // no bytes, so there is nothing to wait for; kMoveBatch loads are in flight
-// before the first store.  Bound by memory where there is much to move (256
-// sequences' 5.5 rows of 16 KB on average: 10.3 us, 45.6 MB), else by the
-// chain of length, path, table and row.
+// before the first store.  Bound by memory where there is much to move, else by
+// the chain of length, path, table and row.  256 sequences' 5.5 rows of 16 KB on
+// average, 45.6 MB: 9.7 us, with 32 registers a thread, so that the 2048 CTAs are
+// all there at once; 10.4 with 8 loads in flight and nine CTAs an SM, 11.3 and
+// 13.5 where a thread moves two or four columns after one reading of the path.
 
 struct TreeCommitParams {
     uint4* k_cache;
@@ -166,12 +168,14 @@ struct TreeCommitParams {
 };
 
 constexpr int kCommitThreads = 128;
-constexpr int kMoveBatch = 8;
+constexpr int kMoveBatch = 4;
+constexpr int kCommitCtas = 14;  // an SM
 
-__global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const TreeCommitParams p) {
+__global__ void __launch_bounds__(kCommitThreads, kCommitCtas)
+tree_commit_kernel(const TreeCommitParams p) {
     // cache rows (slots) of the path's sources and destinations
-    __shared__ int64_t s_src[PKV_MAX_TREE_LEN];
-    __shared__ int64_t s_dst[PKV_MAX_TREE_LEN];
+    extern __shared__ int64_t s_src[];
+    int64_t* s_dst = s_src + min(p.max_accepted, p.tree_len);
     __shared__ int s_bad;
     ptx::launch_dependents();
     ptx::grid_dependency_wait();
@@ -354,5 +358,6 @@ extern "C" pkv_status pkv_tree_commit(void* k_cache, void* v_cache, const int32_
     const int cols = 2 * num_kv_heads * p.head_vecs;
     return launch_pdl(tree_commit_kernel, p,
                       dim3((cols + kCommitThreads - 1) / kCommitThreads, num_seqs), kCommitThreads,
-                      stream);
+                      stream,
+                      2 * std::min(max_accepted, tree_len) * (int)sizeof(int64_t));
 }
