@@ -6,12 +6,12 @@
 //     y_a' = y_a cos - y_b sin,  y_b' = y_b cos + y_a sin  for each rotated pair
 // It is bound by memory: every row is read once and written once (q to q_out,
 // k and v into the cache), a few operations an element.  16411 packed tokens of
-// the Llama-7B layer (815 MB) take 130 us, 6.25 TB/s (92 % of the copy rate);
-// 2043 tokens of the Llama-70B layer (80 MB) 20.6 us into E4M3 pages, 19 us into
+// the Llama-7B layer (815 MB) take 124 us, 6.57 TB/s (97 % of the copy rate);
+// 2043 tokens of the Llama-70B layer (80 MB) 18.3 us into E4M3 pages, 17.7 us into
 // 16-bit ones, where starting and draining the SMs shows; 32 tokens 2 us, a
 // launch's least.
 //
-// A group of head_dim / 8 lanes holds a row in registers, two blocks of 4 dims a
+// A group of head_dim / 8 lanes takes a row, two blocks of 4 dims a
 // lane, chosen so that a lane has both halves of its pairs (halves: 4 l and
 // rotary_dim / 2 + 4 l; interleaved pairs and dims that are not rotated: 8 l
 // and 8 l + 4): the rotation needs no exchange between lanes, and the mean is
@@ -57,10 +57,14 @@ struct RopeParams {
 };
 
 constexpr int kRopeThreads = 128;
-// A group's rows, all in flight at once.  16411 packed tokens of the Llama-7B
-// layer with 2, 4 and 8: 157, 130 and 136 us; 2043 tokens of the Llama-70B layer
-// into E4M3 pages 20.4, 20.6 and 34 us.
+// A group's rows, all in flight at once, and the CTAs an SM that the registers
+// leave room for.  The rows come by cp.async: held in registers as plain loads
+// they leave seven or eight CTAs an SM.  16411 packed tokens of the Llama-7B layer
+// and 2043 tokens of the Llama-70B layer into E4M3 pages: 124 and 18.3 us (plain
+// loads: 130 and 20.6); for 8, 10 and 12 CTAs 124 and 18.7, 128 and 17.8, 122 and
+// 19.2; with 2 and 8 rows 139 and 19.1, 131 and 19.6.
 constexpr int kRopeBatch = 4;
+constexpr int kRopeCtas = 9;
 // CTAs an SM below which a group takes fewer rows: 32 tokens of the Llama-70B
 // layer 2.0 us, with four rows a group all the same 2.3 us.
 constexpr int kRopeMinCtas = 8;
@@ -72,9 +76,11 @@ __device__ __forceinline__ void widen4(uint2 w, float2 (&x)[2], T) {
 }
 
 template <typename T, int D, bool F8, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads) norm_rope_append_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
+norm_rope_append_kernel(const RopeParams p) {
     constexpr int LPR = D / 8;                    // lanes per row
     constexpr int kGroups = kRopeThreads / LPR;   // rows a CTA holds at a time
+    __shared__ uint4 s_rows[kRopeBatch][kGroups][LPR];
     ptx::launch_dependents();
     ptx::grid_dependency_wait();
     const int64_t i = blockIdx.x;
@@ -96,22 +102,12 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_append_kernel(const Ro
     const int pos = __ldg(p.positions + i);
     const T* qk = static_cast<const T*>(kv ? p.k : p.q) + i * (kv ? p.k_stride : p.q_stride);
     const T* vv = static_cast<const T*>(p.v) + i * p.v_stride - (int64_t)p.num_kv_heads * D;
-    uint2 lo[kRopeBatch], hi[kRopeBatch];
 #pragma unroll
     for (int u = 0; u < kRopeBatch; ++u) {
         const int r = r0 + u * kGroups;
-        lo[u] = hi[u] = make_uint2(0u, 0u);
-        if (r < r_end) {
-            const T* src = (kv && r >= p.num_kv_heads ? vv : qk) + r * D;
-            if constexpr (INTER) {
-                const uint4 x = *reinterpret_cast<const uint4*>(src + d0);
-                lo[u] = make_uint2(x.x, x.y);
-                hi[u] = make_uint2(x.z, x.w);
-            } else {
-                lo[u] = *reinterpret_cast<const uint2*>(src + d0);
-                hi[u] = *reinterpret_cast<const uint2*>(src + d1);
-            }
-        }
+        if (r < r_end)
+            ptx::cp_async_16(ptx::smem_addr(&s_rows[u][group][lane]),
+                             (kv && r >= p.num_kv_heads ? vv : qk) + r * D + 8 * lane, true);
     }
     const T* weight = static_cast<const T*>(kv ? p.k_weight : p.q_weight);
     float2 wl[2], wh[2];
@@ -120,8 +116,12 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_append_kernel(const Ro
         widen4(__ldg(reinterpret_cast<const uint2*>(weight + d0)), wl, T());
         widen4(__ldg(reinterpret_cast<const uint2*>(weight + d1)), wh, T());
     }
-    if (slot < 0) return;  // padding
+    if (slot < 0) {  // padding
+        ptx::cp_async_wait_all();
+        return;
+    }
     if (slot >= p.num_slots || pos < 0 || pos >= p.max_position) {
+        ptx::cp_async_wait_all();
         if (threadIdx.x == 0 && blockIdx.y == 0)
             flag_error(p.err_flag, (slot >= p.num_slots ? PKV_EFLAG_SLOT : 0) |
                                        (pos < 0 || pos >= p.max_position ? PKV_EFLAG_POSITION : 0));
@@ -140,14 +140,19 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_append_kernel(const Ro
     const int64_t head_step = (p.hnd ? (int64_t)1 << p.block_shift : 1) * D;
     const int64_t cell0 =
         p.hnd ? (((blk * p.num_kv_heads) << p.block_shift) + off) * D : slot * p.num_kv_heads * D;
-#pragma unroll
+    ptx::cp_async_wait_all();
+    __syncwarp();
+#pragma unroll 1
     for (int u = 0; u < kRopeBatch; ++u) {
         const int r = r0 + u * kGroups;
         if (r - group >= r_end) break;  // the same for the whole CTA
+        const T* row_in = reinterpret_cast<const T*>(s_rows[u][group]);
+        const uint2 lo = *reinterpret_cast<const uint2*>(row_in + d0);
+        const uint2 hi = *reinterpret_cast<const uint2*>(row_in + d1);
         const bool is_v = kv && r >= p.num_kv_heads;
         float2 x[2], y[2];  // the blocks at d0 and d1
-        widen4(lo[u], x, T());
-        widen4(hi[u], y, T());
+        widen4(lo, x, T());
+        widen4(hi, y, T());
         if (weight != nullptr && !(kv && r - group >= p.num_kv_heads)) {
             // (whole warps take part in the shuffles)
             float2 q = ptx::mul2(x[0], x[0]);
@@ -191,7 +196,7 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_append_kernel(const Ro
         }
         if (r >= r_end) continue;
         if (!kv || !F8) {
-            uint2 out0 = lo[u], out1 = hi[u];  // v: bit-exact, NaN payloads included
+            uint2 out0 = lo, out1 = hi;  // v: bit-exact, NaN payloads included
             if (!is_v) {
                 out0 = make_uint2(pack2(x[0].x, x[0].y, T()), pack2(x[1].x, x[1].y, T()));
                 out1 = make_uint2(pack2(y[0].x, y[0].y, T()), pack2(y[1].x, y[1].y, T()));
