@@ -136,6 +136,15 @@ __host__ __device__ inline int tree_tiles(int n) {
 constexpr int kTreeUnitCost = 3;
 __host__ __device__ inline int tree_cost(int n) { return kTreeUnitCost + tree_tiles(n); }
 
+__device__ __forceinline__ int warp_scan(int x) {  // inclusive
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, x, o);
+        if ((threadIdx.x & 31) >= o) x += v;
+    }
+    return x;
+}
+
 // A stretch of one unit's places.
 struct TreeSeg {
     int b, g, rb;        // sequence, KV head, row block
@@ -311,61 +320,89 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
 #endif
     ptx::grid_dependency_wait();
 
-    // The line of places: a thread sums those of a run of sequences, a scan
-    // places the runs, and the thread whose run holds this CTA's first place
-    // finds its sequence.
-    const int per = (p.num_seqs + kTreeThreads - 1) / kTreeThreads;
-    const int b_lo = min(p.num_seqs, tid * per), b_hi = min(p.num_seqs, b_lo + per);
-    int mine = 0;  // the host checks that all sequences' costs fit an int
-    for (int b = b_lo; b < b_hi; ++b)
-        mine += tree_cost(clamped_len(__ldg(p.context_lens + b), p.cap));
-    int incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-    }
-    if (lane == 31) s_scan[warp] = incl;
-    ptx::tc_fence_before_sync();
-    __syncthreads();
-    ptx::tc_fence_after_sync();
-    int total = 0, before = incl - mine;
-    for (int w = 0; w < kTreeThreads / 32; ++w) {
-        if (w < warp) before += s_scan[w];
-        total += s_scan[w];
-    }
+    // The line of places, and the sequence and the place in it where this CTA's part
+    // starts.  Up to 32 sequences a warp scans by itself, a lane a sequence: without
+    // the exchange of the block-wide scan a call of two sequences of 50 tokens takes
+    // 5.6 us instead of 6.1.
     const int units = p.num_kv_heads * p.row_blocks;
-    const int64_t line = (int64_t)total * units;
-    const int64_t ctas = min((int64_t)gridDim.x, line);  // with a place at least; the rest idle
-    const int64_t start = min((int64_t)blockIdx.x, ctas) * line / ctas;
-    const int64_t stop = min((int64_t)blockIdx.x + 1, ctas) * line / ctas;
-    if (start >= (int64_t)before * units && start < (int64_t)(before + mine) * units) {
-        int b = b_lo;
-        int64_t first = (int64_t)before * units;
-        while (true) {
-            const int64_t next =
-                first + (int64_t)units * tree_cost(clamped_len(__ldg(p.context_lens + b), p.cap));
-            if (start < next) break;
-            first = next;
-            ++b;
+    int64_t line, ctas, start, stop;
+    auto parts = [&](int total) {
+        line = (int64_t)total * units;
+        ctas = min((int64_t)gridDim.x, line);  // with a place at least; the rest idle
+        const int64_t x = min((int64_t)blockIdx.x, ctas), y = min((int64_t)blockIdx.x + 1, ctas);
+        if (y * line <= UINT_MAX) {  // (a 64-bit division takes several times as long)
+            start = (uint32_t)(x * line) / (uint32_t)ctas;
+            stop = (uint32_t)(y * line) / (uint32_t)ctas;
+        } else {
+            start = x * line / ctas;
+            stop = y * line / ctas;
         }
-        s_start[0] = b;
-        s_start[1] = (int)(start - first);
+    };
+    TreeWalk walk;
+    int in_seq = 0;  // the first place in its sequence's part of the line
+    if (p.num_seqs <= 32) {
+        const int n = lane < p.num_seqs ? clamped_len(__ldg(p.context_lens + lane), p.cap) : 0;
+        const int mine = lane < p.num_seqs ? tree_cost(n) : 0;
+        const int incl = warp_scan(mine);
+        parts(__shfl_sync(0xffffffffu, incl, 31));
+        // the sequences that end at or before the start (a later CTA than the last has none)
+        const uint32_t over =
+            __ballot_sync(0xffffffffu, lane < p.num_seqs && (int64_t)incl * units <= start);
+        walk.b = min(__popc(over), p.num_seqs - 1);
+        walk.n = __shfl_sync(0xffffffffu, n, walk.b);
+        in_seq = (int)(start - (int64_t)__shfl_sync(0xffffffffu, incl - mine, walk.b) * units);
+        ptx::tc_fence_before_sync();
+        __syncthreads();
+        ptx::tc_fence_after_sync();
+    } else {
+        // a thread sums those of a run of sequences, a scan places the runs, and the
+        // thread whose run holds this CTA's first place finds its sequence
+        const int per = (p.num_seqs + kTreeThreads - 1) / kTreeThreads;
+        const int b_lo = min(p.num_seqs, tid * per), b_hi = min(p.num_seqs, b_lo + per);
+        int mine = 0;  // the host checks that all sequences' costs fit an int
+        for (int b = b_lo; b < b_hi; ++b)
+            mine += tree_cost(clamped_len(__ldg(p.context_lens + b), p.cap));
+        const int incl = warp_scan(mine);
+        if (lane == 31) s_scan[warp] = incl;
+        ptx::tc_fence_before_sync();
+        __syncthreads();
+        ptx::tc_fence_after_sync();
+        int total = 0, before = incl - mine;
+        for (int w = 0; w < kTreeThreads / 32; ++w) {
+            if (w < warp) before += s_scan[w];
+            total += s_scan[w];
+        }
+        parts(total);
+        if (start >= (int64_t)before * units && start < (int64_t)(before + mine) * units) {
+            int b = b_lo;
+            int64_t first = (int64_t)before * units;
+            while (true) {
+                const int64_t next = first + (int64_t)units * tree_cost(clamped_len(
+                                                 __ldg(p.context_lens + b), p.cap));
+                if (start < next) break;
+                first = next;
+                ++b;
+            }
+            s_start[0] = b;
+            s_start[1] = (int)(start - first);
+        }
+        __syncthreads();
+        if (start < stop) {
+            walk.b = s_start[0];
+            walk.n = clamped_len(__ldg(p.context_lens + walk.b), p.cap);
+            in_seq = s_start[1];
+        }
     }
-    __syncthreads();
     const uint32_t tmem = *tmem_slot;
     const uint32_t ring_addr = ptx::smem_addr(ring);
     const uint32_t q_addr = ptx::smem_addr(sq);
 
-    TreeWalk walk;
     walk.at = start;
     walk.end = stop;
     if (start < stop) {
-        walk.b = s_start[0];
-        walk.n = clamped_len(__ldg(p.context_lens + walk.b), p.cap);
         const int cost = tree_cost(walk.n);
-        walk.unit = s_start[1] / cost;
-        walk.pos = s_start[1] - walk.unit * cost;
+        walk.unit = in_seq / cost;
+        walk.pos = in_seq - walk.unit * cost;
     }
 
     if (warp >= kTreeSoftmaxWarps) {
