@@ -179,6 +179,17 @@ def test_attention_matches_the_definition(key):
     ref.assert_close(out, *ref.attention(c), key)
 
 
+@pytest.mark.parametrize("t,group", [(6, 2), (40, 4)])
+@pytest.mark.parametrize("b", [31, 32, 33, 64])
+def test_attention_of_about_a_warp_of_sequences(b, t, group):
+    """Ragged, with empty places at the start, in the middle and at the end."""
+    lens = [0 if i in (0, b // 2, b - 1) else t + 131 * i % 700 for i in range(b)]
+    c = ref.make_case(b + t, lens, t, 2 * group, 2, 64, 16, "fp16")
+    out, err = _run(c)
+    assert err == 0
+    ref.assert_close(out, *ref.attention(c), f"{b} sequences")
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.11, 2.0])
 def test_attention_scales(scale):
     c = ref.make_case(3, **ATTENTION["rows_300"]) | {"scale": scale}
