@@ -1007,36 +1007,66 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
 }
 
 // Joins the partials of the units that were cut: w_c = 2^(lse_c - max),
-// out = sum_c w_c O_c / sum_c w_c over the CTAs of the unit, two partials at a
-// time with a running maximum.  Eight lanes take a row of the output, all of
-// a partial's loads in flight at once (a warp a row, one partial after another,
-// took 20 us for the 65536 rows of 32 nodes on the Llama-70B layer).
+// out = sum_c w_c O_c / sum_c w_c over the CTAs of the unit, with a running
+// maximum.  Eight lanes take a row's columns, all of two partials' loads in flight
+// at once (a warp a row, one partial after another, took 20 us for the 65536 rows
+// of 32 nodes on the Llama-70B layer), and G such groups share a row's partials
+// where rows are few: launch_tree_t has the rule.
 constexpr int kTreeMergeThreads = 128;
-constexpr int kTreeMergeRows = kTreeMergeThreads / 8;
+constexpr int kTreeMergeGroups = kTreeMergeThreads / 8;
 
-template <typename T, int D>
+template <int E>
+struct TreeSum {  // of partials: O's 4 E columns of a lane, weights to base 2^m
+    float m, den;
+    float4 acc[E];
+
+    __device__ __forceinline__ void scale(float f) {
+        den *= f;
+#pragma unroll
+        for (int e = 0; e < E; ++e)  // a zero weight adds nothing, whatever it weighs
+            acc[e] = f == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                              : make_float4(acc[e].x * f, acc[e].y * f, acc[e].z * f,
+                                            acc[e].w * f);
+    }
+    __device__ __forceinline__ void add(float w, const float4 (&x)[E]) {
+        den += w;
+        if (w == 0.f) return;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            acc[e].x = fmaf(w, x[e].x, acc[e].x);
+            acc[e].y = fmaf(w, x[e].y, acc[e].y);
+            acc[e].z = fmaf(w, x[e].z, acc[e].z);
+            acc[e].w = fmaf(w, x[e].w, acc[e].w);
+        }
+    }
+};
+
+template <typename T, int D, int G>
 __global__ void __launch_bounds__(kTreeMergeThreads)
 tree_merge_kernel(const TreeParams p, int unit_rows) {
     constexpr int E = D / 32;  // float4 columns of a lane: 8 k + lane % 8
+    static_assert(G == 1 || G == 4 || G == kTreeMergeGroups, "a group, a warp or a CTA a row");
     ptx::launch_dependents();
-    ptx::grid_dependency_wait();
     const int q8 = threadIdx.x & 7;
-    const int64_t row = (int64_t)blockIdx.x * kTreeMergeRows + (threadIdx.x >> 3);
-    if (row >= (int64_t)p.num_seqs * p.tree_len * p.num_q_heads) return;
-    const int h = (int)(row % p.num_q_heads);
-    const int64_t bi = row / p.num_q_heads;
-    const int b = (int)(bi / p.tree_len), node = (int)(bi - (int64_t)b * p.tree_len);
-    const int g = h / p.group;
-    const int r = node * p.group + h - g * p.group;
-    const int rb = r / unit_rows;
+    const int group = threadIdx.x >> 3;
+    // (rows fit 30 bits: 65535 sequences and KV heads, 1024 nodes, groups of 16)
+    const uint32_t row = blockIdx.x * (kTreeMergeGroups / G) + group / G;
+    const uint32_t bi = row / p.num_q_heads, h = row - bi * p.num_q_heads;
+    const uint32_t b = bi / p.tree_len, node = bi - b * p.tree_len;
+    const uint32_t g = h / p.group;
+    const uint32_t r = node * p.group + h - g * p.group;
+    const uint32_t rb = r / unit_rows;
+    const int urow = (int)(r - rb * unit_rows);
+    ptx::grid_dependency_wait();
+    if (b >= (uint32_t)p.num_seqs) return;
     const int2 ctas = __ldg(p.unit_ctas + ((int64_t)b * p.num_kv_heads + g) * p.row_blocks + rb);
     if (ctas.x == ctas.y) return;  // written whole
-    const int urow = r - rb * unit_rows;
-    float m = -INFINITY, den = 0.f;
-    float4 acc[E];
+    TreeSum<E> sum;
+    sum.m = -INFINITY;
+    sum.den = 0.f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = ctas.x; c <= ctas.y; c += 2) {
+    for (int e = 0; e < E; ++e) sum.acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = ctas.x + 2 * (group % G); c <= ctas.y; c += 2 * G) {
         // a unit's first CTA leaves its last partial, the others their first
         const bool two = c < ctas.y;
         const int64_t at0 = (int64_t)(2 * c + (c == ctas.x ? 1 : 0)) * unit_rows + urow;
@@ -1051,35 +1081,65 @@ tree_merge_kernel(const TreeParams p, int unit_rows) {
             x[e] = __ldg(o0 + 8 * e);
             y[e] = __ldg(o1 + 8 * e);
         }
-        const float mn = fmaxf(m, fmaxf(lse0, lse1));
+        const float mn = fmaxf(sum.m, fmaxf(lse0, lse1));
         const float ref = mn == -INFINITY ? 0.f : mn;
-        const float f = exp2f(m - ref), w0 = exp2f(lse0 - ref), w1 = exp2f(lse1 - ref);
-        m = mn;
-        den = den * f + w0 + w1;
-        // a zero weight adds nothing, whatever its partial holds
+        sum.scale(exp2f(sum.m - ref));
+        sum.m = mn;
+        sum.add(exp2f(lse0 - ref), x);
+        sum.add(exp2f(lse1 - ref), y);
+    }
+    if constexpr (G > 1) {  // a warp's four groups
+        const float mw = fmaxf(sum.m, __shfl_xor_sync(0xffffffffu, sum.m, 8));
+        const float mn = fmaxf(mw, __shfl_xor_sync(0xffffffffu, mw, 16));
+        sum.scale(exp2f(sum.m - (mn == -INFINITY ? 0.f : mn)));
+        sum.m = mn;
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            acc[e] = make_float4(acc[e].x * f, acc[e].y * f, acc[e].z * f, acc[e].w * f);
-            if (w0 != 0.f) {
-                acc[e].x = fmaf(w0, x[e].x, acc[e].x);
-                acc[e].y = fmaf(w0, x[e].y, acc[e].y);
-                acc[e].z = fmaf(w0, x[e].z, acc[e].z);
-                acc[e].w = fmaf(w0, x[e].w, acc[e].w);
-            }
-            if (w1 != 0.f) {
-                acc[e].x = fmaf(w1, y[e].x, acc[e].x);
-                acc[e].y = fmaf(w1, y[e].y, acc[e].y);
-                acc[e].z = fmaf(w1, y[e].z, acc[e].z);
-                acc[e].w = fmaf(w1, y[e].w, acc[e].w);
+        for (int o = 8; o <= 16; o *= 2) {
+            sum.den += __shfl_xor_sync(0xffffffffu, sum.den, o);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                sum.acc[e].x += __shfl_xor_sync(0xffffffffu, sum.acc[e].x, o);
+                sum.acc[e].y += __shfl_xor_sync(0xffffffffu, sum.acc[e].y, o);
+                sum.acc[e].z += __shfl_xor_sync(0xffffffffu, sum.acc[e].z, o);
+                sum.acc[e].w += __shfl_xor_sync(0xffffffffu, sum.acc[e].w, o);
             }
         }
     }
-    const float inv = den == 0.f ? 0.f : 1.f / den;
-    uint2* out = reinterpret_cast<uint2*>(static_cast<T*>(p.out) + row * D) + q8;
+    if constexpr (G == kTreeMergeGroups) {  // the CTA's four warps
+        constexpr int kWarps = kTreeMergeThreads / 32;
+        __shared__ float4 s_acc[kWarps][E][8];
+        __shared__ float2 s_mden[kWarps];
+        const int warp = threadIdx.x >> 5;
+        if ((threadIdx.x & 31) < 8) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) s_acc[warp][e][q8] = sum.acc[e];
+            if (q8 == 0) s_mden[warp] = make_float2(sum.m, sum.den);
+        }
+        __syncthreads();
+        if (threadIdx.x >= 8) return;
+        float mn = sum.m;
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) mn = fmaxf(mn, s_mden[w].x);
+        const float ref = mn == -INFINITY ? 0.f : mn;
+        sum.scale(exp2f(sum.m - ref));
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) {
+            const float f = exp2f(s_mden[w].x - ref);
+            const float den = sum.den + s_mden[w].y * f;
+            float4 x[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) x[e] = s_acc[w][e][q8];
+            sum.add(f, x);
+            sum.den = den;
+        }
+    }
+    if (group % G % 4 != 0) return;
+    const float inv = sum.den == 0.f ? 0.f : 1.f / sum.den;
+    uint2* out = reinterpret_cast<uint2*>(static_cast<T*>(p.out) + (int64_t)row * D) + q8;
 #pragma unroll
     for (int e = 0; e < E; ++e)
-        out[8 * e] = make_uint2(pack2(acc[e].x * inv, acc[e].y * inv, T()),
-                                pack2(acc[e].z * inv, acc[e].w * inv, T()));
+        out[8 * e] = make_uint2(pack2(sum.acc[e].x * inv, sum.acc[e].y * inv, T()),
+                                pack2(sum.acc[e].z * inv, sum.acc[e].w * inv, T()));
 }
 
 // ---------------------------------------------------------------------------
@@ -1094,6 +1154,7 @@ struct TreeCallPlan {
     int row_blocks;
     int unit_rows;
     int ctas;
+    int max_tiles;       // of a unit, in places
     bool cut;            // a unit may be cut: partials and a merge
     size_t units_bytes;
     size_t workspace_bytes;
@@ -1126,6 +1187,7 @@ static pkv_status plan_tree(int num_seqs, int tree_len, int num_q_heads, int num
     if ((int64_t)num_kv_heads * plan->row_blocks * tree_cost(max_context_len) > INT_MAX)
         return PKV_ERR_UNSUPPORTED;
     plan->ctas = (int)std::max<int64_t>(1, std::min<int64_t>(sms, units * tiles));
+    plan->max_tiles = tiles;
     plan->cut = tiles > 1;
     plan->units_bytes = ((size_t)units * sizeof(int2) + 255) & ~size_t(255);
     plan->workspace_bytes =
@@ -1164,12 +1226,24 @@ static cudaError_t launch_tree_t(const CUtensorMap& mk, const CUtensorMap& mv, c
     e = cudaLaunchKernelEx(&cfg, kern, mk, mv, p);
     if (e != cudaSuccess || !plan.cut) return e;
     const int64_t rows = (int64_t)p.num_seqs * p.tree_len * p.num_q_heads;
-    const int64_t ctas = (rows + kTreeMergeRows - 1) / kTreeMergeRows;
+    // Groups a row: while few rows leave the SMs room (about 20000 groups run at a
+    // time) and a unit may have partials for them.  1, 4 and 16 groups: 36 rows of
+    // some 90 partials 37, 18 and 13 us (the whole call), 252 rows of 70 36, 24 and
+    // 17, 1792 rows of ten 18.3, 15.0 and 14.5, 12960 rows of two 23, 26 and 38.
+    const int partials = std::min(plan.ctas, plan.max_tiles);
+    const int groups = rows * 16 <= 32768 && partials > 8 ? kTreeMergeGroups
+                       : rows * 4 <= 32768 && partials > 2 ? 4
+                                                           : 1;
+    const int64_t ctas = (rows * groups + kTreeMergeGroups - 1) / kTreeMergeGroups;
     if (ctas > INT_MAX) return cudaErrorInvalidValue;
     cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3(kTreeMergeThreads);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, tree_merge_kernel<T, D>, p, plan.unit_rows);
+    return cudaLaunchKernelEx(&cfg,
+                              groups == 1   ? tree_merge_kernel<T, D, 1>
+                              : groups == 4 ? tree_merge_kernel<T, D, 4>
+                                            : tree_merge_kernel<T, D, kTreeMergeGroups>,
+                              p, plan.unit_rows);
 }
 
 template <typename T>
