@@ -6,8 +6,8 @@ checks tensor types, passes device pointers, sizes and the current CUDA stream,
 and turns status codes into exceptions.  PyTorch provides device memory and
 streams.  The calls of the tree step, whose kernels take 2 us at small batches,
 have a quick form of the same checks in C++ (``pkv_binding.so``); what it does
-not take is checked here.  There is no CPU fallback: if the library is not built, or a tensor is
-not on a CUDA device, the call raises.
+not take is checked here.  There is no CPU fallback: if the library is not
+built, or a tensor is not on a CUDA device, the call raises.
 
 Calls (same names as the C entry points, without the ``pkv_`` prefix):
 
