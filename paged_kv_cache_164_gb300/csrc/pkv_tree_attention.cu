@@ -956,30 +956,42 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                     return *reinterpret_cast<const float4*>(tray + row * 128 +
                                                             ((i ^ (row & 7)) << 4));
                 };
+                // everything is read before the first store, which might alias it for all
+                // that the compiler knows (900 cycles a turn of partials, so 650 to 700;
+                // 32 nodes on the Llama-70B layer 154 us, so 148)
                 if (direct) {
                     const int64_t first = (int64_t)s.b * p.tree_len * p.num_q_heads;
+                    uint4 x[4];
+                    int rr[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {  // 8 rows of 32 columns at a time
                         const int row = i * 8 + lane / 4, q4 = lane % 4;
-                        const int rr = __shfl_sync(0xffffffffu, rel, row);
-                        const float4 x = chunk(row, 2 * q4), y = chunk(row, 2 * q4 + 1);
-                        if (rr >= 0)
-                            reinterpret_cast<uint4*>(static_cast<T*>(p.out) + (first + rr) * D +
-                                                     col0 + c)[q4] =
-                                make_uint4(pack2(x.x, x.y, T()), pack2(x.z, x.w, T()),
-                                           pack2(y.x, y.y, T()), pack2(y.z, y.w, T()));
+                        rr[i] = __shfl_sync(0xffffffffu, rel, row);
+                        const float4 lo = chunk(row, 2 * q4), hi = chunk(row, 2 * q4 + 1);
+                        x[i] = make_uint4(pack2(lo.x, lo.y, T()), pack2(lo.z, lo.w, T()),
+                                          pack2(hi.x, hi.y, T()), pack2(hi.z, hi.w, T()));
                     }
+                    uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + first * D +
+                                                          col0 + c) + lane % 4;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (rr[i] >= 0) out[(int64_t)rr[i] * (D / 8)] = x[i];
                 } else {
-                    float* part = p.partial_o +
-                                  ((int64_t)slot * kUnitRows + urow - lane) * D + col0 + c;
+                    float4* part = reinterpret_cast<float4*>(
+                                       p.partial_o +
+                                       ((int64_t)slot * kUnitRows + urow - lane) * D + col0 + c) +
+                                   lane % 8;
+                    float4 x[8];
+                    int rr[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {  // 4 rows
                         const int row = i * 4 + lane / 8;
-                        const int rr = __shfl_sync(0xffffffffu, rel, row);
-                        if (rr >= 0)
-                            reinterpret_cast<float4*>(part + row * D)[lane % 8] =
-                                chunk(row, lane % 8);
+                        rr[i] = __shfl_sync(0xffffffffu, rel, row);
+                        x[i] = chunk(row, lane % 8);
                     }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (rr[i] >= 0) part[(i * 4 + lane / 8) * (D / 4)] = x[i];
                 }
             }
             if (live && !direct && (ROWS || wg == 0))
