@@ -40,7 +40,7 @@
 // 2.69 GB (6.7 to 6.9 TB/s, 98 to 102 % of the copy rate), 8 nodes on the
 // Llama-7B layer (16 contexts of 520 to 4096) 97 to 100 us for 607 MB (90 to
 // 92 %).  With 256 rows, the tensor cores and the softmax beside them: 32 nodes
-// on the Llama-70B layer (32 x 4096 tokens) 149 us, of which the products alone,
+// on the Llama-70B layer (32 x 4096 tokens) 148 us, of which the products alone,
 // with P twice, would take 109 at the dense rate (tensor pipe 65 % active); a
 // single 16-bit P would take 129.  Head dim 64 is bound by the softmax threads.
 //
