@@ -53,6 +53,7 @@
 
 #include "pkv_common.cuh"
 #include "pkv_device.cuh"
+#include "pkv_tree_parts.cuh"
 
 namespace pkv {
 
@@ -66,8 +67,9 @@ struct TreeParams {
     int64_t mask_stride;
     int32_t* err_flag;
     int2* unit_ctas;     // per unit: the first and last CTA of its tiles; null: no unit is cut
-    float* partial_o;    // [2 * CTAs][rows per unit][D]
-    float* partial_lse;  // [2 * CTAs][rows per unit], base 2
+    float* partial_o;    // [tree_partials(ctas)][rows per unit][D]
+    float* partial_lse;  // [tree_partials(ctas)][rows per unit], base 2
+    int ctas;            // of the attention kernel
     int max_blocks_per_seq;
     int num_blocks;
     int block_size;
@@ -903,7 +905,7 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             }
             ptx::tc_fence_after_sync();
             const bool direct = s.tiles == s.unit_tiles;
-            const int slot = 2 * blockIdx.x + (s.tile0 == 0 ? 1 : 0);
+            const int slot = tree_partial(blockIdx.x, s.tile0 == 0);
             const bool bad_v = s_bad[nseg & 3] == nseg + 1;
             // Columns: ROWS: the whole row; else this warpgroup's half.  They leave
             // through shared memory, 32 at a time, so that a warp writes whole lines
@@ -1076,6 +1078,7 @@ tree_merge_kernel(const TreeParams p, int unit_rows) {
     if (b >= (uint32_t)p.num_seqs) return;
     const int2 ctas = __ldg(p.unit_ctas + ((int64_t)b * p.num_kv_heads + g) * p.row_blocks + rb);
     if (ctas.x == ctas.y) return;  // written whole
+    if (!tree_parts_valid(ctas.x, ctas.y, p.ctas)) return;  // a wait expired: flagged there
     TreeSum<E> sum;
     sum.m = -INFINITY;
     sum.den = 0.f;
@@ -1084,8 +1087,8 @@ tree_merge_kernel(const TreeParams p, int unit_rows) {
     for (int c = ctas.x + 2 * (group % G); c <= ctas.y; c += 2 * G) {
         // a unit's first CTA leaves its last partial, the others their first
         const bool two = c < ctas.y;
-        const int64_t at0 = (int64_t)(2 * c + (c == ctas.x ? 1 : 0)) * unit_rows + urow;
-        const int64_t at1 = two ? (int64_t)(2 * c + 2) * unit_rows + urow : at0;
+        const int64_t at0 = (int64_t)tree_partial(c, c == ctas.x) * unit_rows + urow;
+        const int64_t at1 = two ? (int64_t)tree_partial(c + 1, false) * unit_rows + urow : at0;
         const float lse0 = __ldg(p.partial_lse + at0);
         const float lse1 = two ? __ldg(p.partial_lse + at1) : -INFINITY;
         const float4* o0 = reinterpret_cast<const float4*>(p.partial_o + at0 * D) + q8;
@@ -1206,8 +1209,8 @@ static pkv_status plan_tree(int num_seqs, int tree_len, int num_q_heads, int num
     plan->cut = tiles > 1;
     plan->units_bytes = ((size_t)units * sizeof(int2) + 255) & ~size_t(255);
     plan->workspace_bytes =
-        256 + (plan->cut ? plan->units_bytes + (size_t)2 * plan->ctas * plan->unit_rows *
-                                                   (head_dim + 1) * sizeof(float)
+        256 + (plan->cut ? plan->units_bytes + (size_t)tree_partials(plan->ctas) *
+                                                   plan->unit_rows * (head_dim + 1) * sizeof(float)
                          : 0);
     return PKV_OK;
 }
@@ -1334,7 +1337,9 @@ extern "C" pkv_status pkv_tree_attention(
     if (plan.cut) {
         p.unit_ctas = static_cast<int2*>(workspace);
         p.partial_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.units_bytes);
-        p.partial_lse = p.partial_o + (size_t)2 * plan.ctas * plan.unit_rows * head_dim;
+        p.partial_lse =
+            p.partial_o + (size_t)tree_partials(plan.ctas) * plan.unit_rows * head_dim;
+        p.ctas = plan.ctas;
     }
     p.max_blocks_per_seq = max_blocks_per_seq;
     p.num_blocks = num_blocks;
