@@ -532,7 +532,7 @@ pkv_status pkv_tree_attention(void* out, const void* q, const void* k_cache, con
  *                  accepted_lens[b] are not read
  *   accepted_lens  int32 [num_seqs], 0 .. min(max_accepted, tree_len)
  *   new_context_lens  int32 [num_seqs] (written), nullable; must not overlap
- *                  context_lens
+ *                  anything that the call reads
  * A malformed path or count is flagged (PKV_EFLAG_TREE): nothing of that
  * sequence moves, and its new length is the committed one.  The same goes for
  * a flagged context length (new length max(0, min(n_b, longest) - tree_len))

@@ -87,6 +87,12 @@ pkv_status decode_workspace_16bit(int num_seqs, int num_q_heads, int num_kv_head
 // served to a context that replaced a destroyed one.
 bool current_context_id(unsigned long long* id);
 
+// Whether [a, a + an) and [b, b + bn) share a byte.
+inline bool overlap(const void* a, int64_t an, const void* b, int64_t bn) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + (uintptr_t)bn && y < x + (uintptr_t)an;
+}
+
 // SMs of the current device, or -1.
 int current_sm_count();
 

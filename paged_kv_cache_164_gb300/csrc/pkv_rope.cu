@@ -265,12 +265,6 @@ static cudaError_t launch_rope(RopeParams p, int num_tokens, int sms, cudaStream
                          : launch_rope_t<T, D, F8, false>(p, grid, stream);
 }
 
-// Whether [a, a + an) and [b, b + bn) share a byte.
-static bool overlap(const void* a, int64_t an, const void* b, int64_t bn) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + (uintptr_t)bn && y < x + (uintptr_t)an;
-}
-
 static pkv_status norm_rope_impl(RopeParams p, int num_tokens, int num_blocks, int head_dim,
                                  pkv_dtype dtype, bool f8, void* stream) {
     p.hnd = take_layout(dtype);

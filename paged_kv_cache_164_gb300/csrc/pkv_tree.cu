@@ -333,9 +333,17 @@ extern "C" pkv_status pkv_tree_commit(void* k_cache, void* v_cache, const int32_
           reinterpret_cast<uintptr_t>(accepted) | reinterpret_cast<uintptr_t>(accepted_lens) |
           reinterpret_cast<uintptr_t>(new_context_lens)) & 3u))
         return PKV_ERR_INVALID_ARG;
-    // every CTA of a sequence reads its length: the new one goes elsewhere
-    if (new_context_lens != nullptr && new_context_lens < context_lens + num_seqs &&
-        context_lens < new_context_lens + num_seqs)
+    // every CTA of a sequence reads its length, its count, its path and its table, and
+    // the first writes the new length when it is through with them: that goes elsewhere
+    const int64_t lens_bytes = (int64_t)num_seqs * 4;
+    const int64_t cache_bytes = (int64_t)num_blocks * block_size * num_kv_heads * head_dim * 2;
+    const auto over = [&](const void* a, int64_t bytes) {
+        return new_context_lens != nullptr && overlap(new_context_lens, lens_bytes, a, bytes);
+    };
+    if (over(context_lens, lens_bytes) || over(accepted_lens, lens_bytes) ||
+        over(accepted, lens_bytes * max_accepted) ||
+        over(block_tables, lens_bytes * max_blocks_per_seq) || over(k_cache, cache_bytes) ||
+        over(v_cache, cache_bytes))
         return PKV_ERR_INVALID_ARG;
     TreeCommitParams p = {};
     p.k_cache = static_cast<uint4*>(k_cache);

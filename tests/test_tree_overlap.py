@@ -1,0 +1,40 @@
+"""Outputs of the tree step's calls that lie over what the call reads are refused before any
+launch (CPU): the CTAs of a sequence have no order among them."""
+import ctypes
+
+import pytest
+
+import paged_kv_cache_164_gb300 as pkv
+from paged_kv_cache_164_gb300 import build as pkv_build
+
+NULL = ctypes.c_void_p(0)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    pkv_build.build()
+    return pkv.load()
+
+
+def _at(place, offset=0):
+    """Addresses a gigabyte apart that nothing dereferences."""
+    return ctypes.c_void_p((place + 1 << 30) + offset)
+
+
+B, T, WIDTH, MOST, NB, BS, H_KV, D = 3, 5, 4, 3, 8, 16, 2, 64
+CACHE = NB * BS * H_KV * D * 2
+COMMIT = {"k": (0, CACHE), "v": (1, CACHE), "tables": (2, B * WIDTH * 4), "lens": (3, B * 4),
+          "accepted": (4, B * MOST * 4), "counts": (5, B * 4)}
+
+
+def _commit(lib, new):
+    k, v, tables, lens, accepted, counts = (_at(i) for i in range(6))
+    return lib.pkv_tree_commit(k, v, tables, WIDTH, lens, T, accepted, counts, MOST, new, B, NB,
+                               BS, H_KV, D, 1, NULL, NULL)
+
+
+@pytest.mark.parametrize("name", COMMIT)
+def test_commit_refuses_new_lengths_over_what_it_reads(lib, name):
+    place, size = COMMIT[name]
+    for offset in (0, size - 4, -4 * (B - 1)):
+        assert _commit(lib, _at(place, offset)) == 1
