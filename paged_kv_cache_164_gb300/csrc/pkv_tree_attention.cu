@@ -101,6 +101,11 @@ static_assert(2 * kTreeSoftmaxRegs + 2 * kTreeOtherRegs <= 4 * kTreeLaunchRegs, 
 // stays below 2^8, and O / l and the log-sum-exp come out the same.
 constexpr float kTreeLazyLog2 = 8.f;
 constexpr int kTreeBoxes = kTreeTokens / kStageTokens;  // TMA boxes along a tile's tokens
+// Marks of stretches with a V that is not finite, a ring of them.  With ROWS the slots
+// alone hold the warpgroups together: while one has yet to read the mark of a stretch
+// whose slots are free, the other may be at the V of as many stretches further on as
+// the ring has room for, two tiles (four slots) each at least.
+constexpr int kTreeMarks = 8;
 
 template <int D>
 struct TreeTileCfg {
@@ -120,6 +125,7 @@ struct TreeTileCfg {
     static constexpr int kSmemBytes = 2 * kQTileBytes + kSlots * kSlotBytes + kStageBytes +
                                       kXchBytes + kBarriers * 8 + 256;
     static constexpr uint32_t kColO = 4 * kTreeTokens;  // S of (warpgroup, buffer), then O
+    static_assert(kSlots / 4 < kTreeMarks, "marks of the stretches that may be under way");
     static_assert(kColO + 2 * D <= 512, "tensor memory layout");
     static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
 };
@@ -283,8 +289,9 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
     volatile int* abort_flag = words;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(words + 1);
     int* s_start = words + 2;           // first sequence, and the first place in its part
-    volatile int* s_bad = words + 6;    // [4]: 1 + the stretch (its place: mod 4) with a bad V
-    int* s_scan = words + 10;           // [16]
+    volatile int* s_bad = words + 6;    // [kTreeMarks]: 1 + the stretch (its place: the
+                                        // remainder) with a bad V
+    int* s_scan = words + 6 + kTreeMarks;  // [16]
 
     const int tid = threadIdx.x;
     const int warp = tid >> 5;
@@ -311,7 +318,7 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
         ptx::mbar_init(ptx::smem_addr(met), 2 * TR);
         ptx::mbar_init(ptx::smem_addr(o_free), 2 * TR);
         *abort_flag = 0;
-        for (int i = 0; i < 4; ++i) s_bad[i] = 0;
+        for (int i = 0; i < kTreeMarks; ++i) s_bad[i] = 0;
         ptx::fence_barrier_init();
         ptx::prefetch_tensormap(&tm_k);
         ptx::prefetch_tensormap(&tm_v);
@@ -763,7 +770,7 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                                                  drop_not_finite(x.z, T()) |
                                                  drop_not_finite(x.w, T());
                             if (bad) {
-                                s_bad[nseg & 3] = nseg + 1;
+                                s_bad[nseg % kTreeMarks] = nseg + 1;
                                 __threadfence_block();  // before the value is gone
                                 *cell = x;
                             }
@@ -906,7 +913,7 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             ptx::tc_fence_after_sync();
             const bool direct = s.tiles == s.unit_tiles;
             const int slot = tree_partial(blockIdx.x, s.tile0 == 0);
-            const bool bad_v = s_bad[nseg & 3] == nseg + 1;
+            const bool bad_v = s_bad[nseg % kTreeMarks] == nseg + 1;
             // Columns: ROWS: the whole row; else this warpgroup's half.  They leave
             // through shared memory, 32 at a time, so that a warp writes whole lines
             // (a row a thread: 4 cycles of the load/store unit for every one).
