@@ -711,11 +711,18 @@ def _caches(k_cache: torch.Tensor, v_cache: torch.Tensor, layout: str, dtype):
     raise ValueError(f"layout must be one of {_LAYOUTS}, got {layout!r}")
 
 
-def _keep(t: torch.Tensor, stream) -> torch.Tensor:
-    """A tensor allocated here for a call on ``stream``: when that is another
-    stream than the allocator's current one, its memory must outlast the call."""
-    if stream is not None:
-        t.record_stream(stream)
+def _new(shape, dtype, device, stream) -> torch.Tensor:
+    """A tensor made here for a call on ``stream`` (None: the current one).  It is taken
+    from the memory of that stream: a block freed on the current one may still be in use
+    by work queued there.  What the caller does with it on the current stream is
+    waited for before its memory is used again."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    if current != stream:
+        t.record_stream(current)
     return t
 
 
@@ -761,7 +768,7 @@ def _norm_rope(name, q, k, v, positions, cos_sin, k_cache, v_cache, slot_mapping
     if (qw and q_weight.shape != (d,)) or (kw and k_weight.shape != (d,)):
         raise ValueError("a norm's weight must be [head_dim]")
     if q_out is None:
-        q_out = _keep(torch.empty((t, h_q, d), dtype=dt, device=q.device), stream)
+        q_out = _new((t, h_q, d), dt, q.device, stream)
     elif q_out.shape != qshape:
         raise ValueError("q_out must have the shape of q")
     cache_dt = torch.uint8 if scales else dt
@@ -851,12 +858,11 @@ def tree_plan(parents: torch.Tensor, context_lens: torch.Tensor, block_tables: t
     if tables != b:
         raise ValueError("inconsistent tree-plan shapes")
     if tree_mask is None:
-        tree_mask = _keep(torch.empty((b, t, words), dtype=i32, device=parents.device), stream)
+        tree_mask = _new((b, t, words), i32, parents.device, stream)
     if positions is None:
-        positions = _keep(torch.empty((b, t), dtype=i32, device=parents.device), stream)
+        positions = _new((b, t), i32, parents.device, stream)
     if slot_mapping is None:
-        slot_mapping = _keep(torch.empty((b, t), dtype=torch.int64, device=parents.device),
-                             stream)
+        slot_mapping = _new((b, t), torch.int64, parents.device, stream)
     if tree_mask.shape != (b, t, words) or positions.shape != shape or \
             slot_mapping.shape != shape:
         raise ValueError("inconsistent tree-plan outputs")
@@ -926,13 +932,13 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = _keep(torch.empty_like(q), stream)
+        out = _new(qshape, dt, q.device, stream)
     elif out.shape != qshape:
         raise ValueError("out must have the shape of q")
     if workspace is None:  # a given workspace is checked by the library itself
         with torch.cuda.device(dev):
             need = tree_attention_workspace_size(b, t, h_q, h_kv, d, bs, max_context_len)
-        workspace = _keep(torch.empty(need, dtype=torch.uint8, device=q.device), stream)
+        workspace = _new((need,), torch.uint8, q.device, stream)
     r = _run(lib.pkv_tree_attention, dev, (
         _arg(out, "out", dt, dev), _arg(q, "q", dt, dev),
         _arg(k_cache, "k_cache", dt, dev), _arg(v_cache, "v_cache", dt, dev),
@@ -978,7 +984,7 @@ def tree_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torc
     if context_lens.shape != seqs or paths != b or accepted_lens.shape != seqs:
         raise ValueError("inconsistent tree-commit shapes")
     if new_context_lens is None:
-        new_context_lens = _keep(torch.empty(b, dtype=i32, device=k_cache.device), stream)
+        new_context_lens = _new((b,), i32, k_cache.device, stream)
     elif new_context_lens.shape != seqs:
         raise ValueError("new_context_lens must be [sequences]")
     r = _run(lib.pkv_tree_commit, dev, (

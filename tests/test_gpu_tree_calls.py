@@ -41,3 +41,51 @@ def test_commit_refuses_the_counts_as_the_place_of_the_new_lengths(quick, monkey
                     new_context_lens=torch.empty_like(cnt))
     want = ref.commit(c, 6, accepted, counts)
     assert _same_bits(g["k"], want[0]) and _same_bits(g["v"], want[1])
+
+
+def test_outputs_made_for_another_stream_lie_in_no_memory_that_is_in_use():
+    """Blocks that are freed on the current stream, where work that writes them is still
+    queued, while the calls run at once on another stream."""
+    t, h_q, h_kv, d, bs = 40, 4, 2, 64, 16
+    c = ref.make_case(71, [60, 300], t, h_q, h_kv, d, bs, "fp16")
+    g, nb = ref.on_gpu(c), c["k"].shape[0]
+    accepted = torch.tensor([[0, 3, 15], [2, 3, 9]], dtype=torch.int32, device="cuda")
+    counts = torch.tensor([3, 2], dtype=torch.int32, device="cuda")
+    x = torch.randn(2 * t, h_q + 2 * h_kv, d, device="cuda").half()
+    pos = torch.arange(2 * t, dtype=torch.int32, device="cuda")
+    slots = pos.long()
+    angle = torch.rand(2 * t, d // 2, device="cuda")
+    table = torch.cat([angle.cos(), angle.sin()], 1)
+    kc, vc = g["k"].clone(), g["v"].clone()
+
+    def plan(stream):
+        return pkv.tree_plan(g["parents"], g["lens"], g["tables"], nb, bs, 300, stream=stream)
+
+    def rope(stream):
+        return [pkv.norm_rope_append(x[:, :h_q], x[:, h_q:h_q + h_kv], x[:, h_q + h_kv:], pos,
+                                     table, kc, vc, slots, stream=stream)]
+
+    def attention(stream):
+        return [pkv.tree_attention(g["q"], g["k"], g["v"], g["tables"], g["lens"], 300, g["mask"],
+                                   scale=c["scale"], stream=stream)]
+
+    def commit(stream):  # (the same rows each time: nothing moves twice)
+        return [pkv.tree_commit(kc, vc, g["tables"], g["lens"], t, accepted, counts,
+                                stream=stream)]
+
+    need = pkv.tree_attention_workspace_size(2, t, h_q, h_kv, d, bs, 300)
+    side = torch.cuda.Stream()
+    for call in (plan, rope, attention, commit):
+        want = [y.clone() for y in call(None)]
+        torch.cuda.synchronize()
+        old = [torch.empty_like(y) for y in want for _ in range(3)]
+        old += [torch.empty(need, dtype=torch.uint8, device="cuda") for _ in range(3)]
+        torch.cuda._sleep(50_000_000)
+        for y in old:
+            y.fill_(7)
+        del old, y
+        got = call(side)
+        side.synchronize()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), call.__name__
