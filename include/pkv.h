@@ -455,11 +455,12 @@ pkv_status pkv_norm_rope_append_fp8(void* q_out, const void* q, int64_t q_stride
  * committed ones, then one per tree node, node i at position
  * n_b - tree_len + i.  The calls of a step:
  *     pkv_tree_plan, pkv_norm_rope_append (or pkv_append), pkv_tree_attention,
- *     pkv_tree_commit
+ *     pkv_tree_commit_within (or pkv_tree_commit)
  * A sequence with n_b = 0 is an empty place of the batch: its nodes are
  * absent, its attention rows are zero and nothing of it is moved.  Any other
  * n_b below tree_len, negative or beyond the block table or max_context_len is
- * flagged (PKV_EFLAG_CONTEXT_LEN).
+ * flagged (PKV_EFLAG_CONTEXT_LEN); the calls that take max_context_len are given
+ * the same one.
  */
 #define PKV_TREE_ABSENT (-2)          /* parents entry of a node that is not there */
 #define PKV_MAX_TREE_LEN 1024
@@ -535,9 +536,21 @@ pkv_status pkv_tree_attention(void* out, const void* q, const void* k_cache, con
  *                  anything that the call reads
  * A malformed path or count is flagged (PKV_EFLAG_TREE): nothing of that
  * sequence moves, and its new length is the committed one.  The same goes for
- * a flagged context length (new length max(0, min(n_b, longest) - tree_len))
- * and for a path that meets a bad block id (PKV_EFLAG_BLOCK_ID).
+ * a flagged context length (new length max(0, min(n_b, longest) - tree_len),
+ * longest that of the block table or max_context_len) and for a path that meets a
+ * bad block id (PKV_EFLAG_BLOCK_ID).
+ * pkv_tree_commit has no max_context_len: the block table alone bounds a context,
+ * and one beyond the step's max_context_len, which the other calls flag and whose
+ * nodes they leave out, is committed like any other.
  */
+pkv_status pkv_tree_commit_within(void* k_cache, void* v_cache, const int32_t* block_tables,
+                                  int max_blocks_per_seq, const int32_t* context_lens,
+                                  int max_context_len, int tree_len, const int32_t* accepted,
+                                  const int32_t* accepted_lens, int max_accepted,
+                                  int32_t* new_context_lens, int num_seqs, int num_blocks,
+                                  int block_size, int num_kv_heads, int head_dim,
+                                  pkv_dtype dtype, int32_t* err_flag, void* stream);
+
 pkv_status pkv_tree_commit(void* k_cache, void* v_cache, const int32_t* block_tables,
                            int max_blocks_per_seq, const int32_t* context_lens, int tree_len,
                            const int32_t* accepted, const int32_t* accepted_lens,

@@ -109,6 +109,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.pkv_tree_attention_workspace_size.restype = sz
     lib.pkv_tree_attention.argtypes = [p, p, p, p, p, i, p, i, p, i64, i, i, i, i, i, i, i, f, p,
                                        sz, i, p, p]
+    lib.pkv_tree_commit_within.argtypes = [p, p, p, i, p, i, i, p, p, i, p, i, i, i, i, i, i, p, p]
     lib.pkv_tree_commit.argtypes = [p, p, p, i, p, i, p, p, i, p, i, i, i, i, i, i, p, p]
     lib.pkv_check_error.argtypes = [p, p, ctypes.POINTER(ctypes.c_int32)]
     lib.pkv_status_string.argtypes = [i]
@@ -122,7 +123,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                  "pkv_append_fp8", "pkv_decode_attention_fp8",
                  "pkv_decode_attention_prefix_shared", "pkv_multi_query_attention",
                  "pkv_norm_rope_append", "pkv_norm_rope_append_fp8", "pkv_tree_plan",
-                 "pkv_tree_attention", "pkv_tree_commit",
+                 "pkv_tree_attention", "pkv_tree_commit", "pkv_tree_commit_within",
                  "pkv_merge", "pkv_gather", "pkv_selftest_wait_timeout",
                  "pkv_check_error", "pkv_max_group_size", "pkv_multi_query_plan"):
         getattr(lib, name).restype = i
@@ -145,7 +146,7 @@ def _load_quick(lib: ctypes.CDLL) -> None:
     if module.torch_version == torch.__version__:
         module.bind(*(ctypes.cast(getattr(lib, "pkv_" + name), ctypes.c_void_p).value
                       for name in ("norm_rope_append", "norm_rope_append_fp8", "tree_plan",
-                                   "tree_attention", "tree_commit")))
+                                   "tree_attention", "tree_commit_within")))
         _quick = module
 
 
@@ -958,16 +959,18 @@ def tree_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torc
                 context_lens: torch.Tensor, tree_len: int, accepted: torch.Tensor,
                 accepted_lens: torch.Tensor, new_context_lens: Optional[torch.Tensor] = None,
                 err_flag: Optional[torch.Tensor] = None, stream=None,
-                layout: str = "nhd") -> torch.Tensor:
+                layout: str = "nhd", max_context_len: Optional[int] = None) -> torch.Tensor:
     """Moves the accepted path's cache rows behind the committed context, in place.
 
     accepted int32 [B, A]: each sequence's accepted nodes, strictly increasing,
     accepted_lens int32 [B] of them.  Returns the new context lengths (int32 [B]):
-    context_lens - tree_len + accepted_lens.
+    context_lens - tree_len + accepted_lens.  ``max_context_len``: the step's; a longer
+    context is flagged and not committed (None: the block table alone bounds it).
     """
     if _quick is not None and stream is None:
         r = _quick.tree_commit(k_cache, v_cache, block_tables, context_lens, tree_len, accepted,
-                               accepted_lens, new_context_lens, err_flag, layout)
+                               accepted_lens, new_context_lens, err_flag, layout,
+                               max_context_len)
         if r is not None:
             if r:
                 _check(r, "pkv_tree_commit")
@@ -987,10 +990,12 @@ def tree_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torc
         new_context_lens = _new((b,), i32, k_cache.device, stream)
     elif new_context_lens.shape != seqs:
         raise ValueError("new_context_lens must be [sequences]")
-    r = _run(lib.pkv_tree_commit, dev, (
+    longest = 2 ** 31 - 1 if max_context_len is None else _c_int(max_context_len,
+                                                                 "max_context_len")
+    r = _run(lib.pkv_tree_commit_within, dev, (
         _arg(k_cache, "k_cache", dt, dev), _arg(v_cache, "v_cache", dt, dev),
         _arg(block_tables, "block_tables", i32, dev), width,
-        _arg(context_lens, "context_lens", i32, dev), _c_int(tree_len, "tree_len"),
+        _arg(context_lens, "context_lens", i32, dev), longest, _c_int(tree_len, "tree_len"),
         _arg(accepted, "accepted", i32, dev), _arg(accepted_lens, "accepted_lens", i32, dev),
         most, _arg(new_context_lens, "new_context_lens", i32, dev), b, nb, bs,
         h_kv, d, code,

@@ -21,7 +21,7 @@ decltype(&pkv_norm_rope_append) fn_norm_rope_append = nullptr;
 decltype(&pkv_norm_rope_append_fp8) fn_norm_rope_append_fp8 = nullptr;
 decltype(&pkv_tree_plan) fn_tree_plan = nullptr;
 decltype(&pkv_tree_attention) fn_tree_attention = nullptr;
-decltype(&pkv_tree_commit) fn_tree_commit = nullptr;
+decltype(&pkv_tree_commit_within) fn_tree_commit = nullptr;
 
 // Reads a call's arguments; `ok` stays true while they have the usual form.
 struct Reader {
@@ -277,9 +277,9 @@ PyObject* tree_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // (k_cache, v_cache, block_tables, context_lens, tree_len, accepted, accepted_lens,
-//  new_context_lens, err_flag, layout)
+//  new_context_lens, err_flag, layout, max_context_len)
 PyObject* tree_commit(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    if (n != 10 || fn_tree_commit == nullptr) Py_RETURN_NONE;
+    if (n != 11 || fn_tree_commit == nullptr) Py_RETURN_NONE;
     Reader r;
     const at::Tensor* k = r.first(a[0], 4);
     if (!r.ok) Py_RETURN_NONE;
@@ -296,12 +296,14 @@ PyObject* tree_commit(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const void* counts = r.dense(a[6], at::kInt, seqs);
     void* fresh = r.dense(a[7], at::kInt, seqs);
     int32_t* flag = r.flag(a[8]);
+    const int cap = a[10] == Py_None ? INT_MAX : r.integer(a[10]);
     const int width = r.narrow(tables->size(1)), batch = r.narrow(b),
               most = r.narrow(accepted->size(1));
     if (!r.ok) Py_RETURN_NONE;
     return PyLong_FromLong(fn_tree_commit(
         c.k, c.v, static_cast<const int32_t*>(tables->data_ptr()), width,
-        static_cast<const int32_t*>(lens), len, static_cast<const int32_t*>(accepted->data_ptr()),
+        static_cast<const int32_t*>(lens), cap, len,
+        static_cast<const int32_t*>(accepted->data_ptr()),
         static_cast<const int32_t*>(counts), most, static_cast<int32_t*>(fresh), batch,
         c.num_blocks, c.block_size, c.heads, c.d, c.code, flag, stream_of(r.device)));
 }
@@ -317,7 +319,7 @@ PyObject* guarded(PyObject* self, PyObject* const* args, Py_ssize_t n) {
 }
 
 // bind(addresses of norm_rope_append, norm_rope_append_fp8, tree_plan,
-//      tree_attention, tree_commit)
+//      tree_attention, tree_commit_within)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* p[5];
     if (n != 5) {

@@ -309,15 +309,14 @@ extern "C" pkv_status pkv_tree_plan(int32_t* tree_mask, int32_t* positions, int6
                       plan_smem_bytes(tree_len));
 }
 
-extern "C" pkv_status pkv_tree_commit(void* k_cache, void* v_cache, const int32_t* block_tables,
-                                      int max_blocks_per_seq, const int32_t* context_lens,
-                                      int tree_len, const int32_t* accepted,
-                                      const int32_t* accepted_lens, int max_accepted,
-                                      int32_t* new_context_lens, int num_seqs, int num_blocks,
-                                      int block_size, int num_kv_heads, int head_dim,
-                                      pkv_dtype dtype, int32_t* err_flag, void* stream) {
+extern "C" pkv_status pkv_tree_commit_within(
+    void* k_cache, void* v_cache, const int32_t* block_tables, int max_blocks_per_seq,
+    const int32_t* context_lens, int max_context_len, int tree_len, const int32_t* accepted,
+    const int32_t* accepted_lens, int max_accepted, int32_t* new_context_lens, int num_seqs,
+    int num_blocks, int block_size, int num_kv_heads, int head_dim, pkv_dtype dtype,
+    int32_t* err_flag, void* stream) {
     const bool hnd = take_layout(dtype);
-    if (num_seqs < 0 || tree_len <= 0 || max_accepted <= 0 || max_blocks_per_seq <= 0 ||
+    if (num_seqs < 0 || max_context_len < 0 || tree_len <= 0 || max_accepted <= 0 || max_blocks_per_seq <= 0 ||
         num_blocks <= 0 || block_size <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
         (dtype != PKV_FP16 && dtype != PKV_BF16))
         return PKV_ERR_INVALID_ARG;
@@ -361,11 +360,24 @@ extern "C" pkv_status pkv_tree_commit(void* k_cache, void* v_cache, const int32_
     p.block_size = block_size;
     p.num_kv_heads = num_kv_heads;
     p.head_vecs = head_dim / 8;
-    p.cap = max_blocks_per_seq * block_size;
+    p.cap = std::min(max_blocks_per_seq * block_size, max_context_len);
     p.hnd = hnd;
     const int cols = 2 * num_kv_heads * p.head_vecs;
     return launch_pdl(tree_commit_kernel, p,
                       dim3((cols + kCommitThreads - 1) / kCommitThreads, num_seqs), kCommitThreads,
                       stream,
                       2 * std::min(max_accepted, tree_len) * (int)sizeof(int64_t));
+}
+
+extern "C" pkv_status pkv_tree_commit(void* k_cache, void* v_cache, const int32_t* block_tables,
+                                      int max_blocks_per_seq, const int32_t* context_lens,
+                                      int tree_len, const int32_t* accepted,
+                                      const int32_t* accepted_lens, int max_accepted,
+                                      int32_t* new_context_lens, int num_seqs, int num_blocks,
+                                      int block_size, int num_kv_heads, int head_dim,
+                                      pkv_dtype dtype, int32_t* err_flag, void* stream) {
+    return pkv_tree_commit_within(k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens,
+                                  INT_MAX, tree_len, accepted, accepted_lens, max_accepted,
+                                  new_context_lens, num_seqs, num_blocks, block_size, num_kv_heads,
+                                  head_dim, dtype, err_flag, stream);
 }

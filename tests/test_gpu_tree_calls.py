@@ -89,3 +89,42 @@ def test_outputs_made_for_another_stream_lie_in_no_memory_that_is_in_use():
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), call.__name__
+
+
+@pytest.mark.parametrize("quick", [True, False])
+def test_a_context_beyond_the_steps_longest_is_not_committed(quick, monkeypatch):
+    """Longer than max_context_len and shorter than the block table: the plan gives its nodes
+    no slots and the attention leaves them out, so that the commit has no rows to move."""
+    pkv.load()
+    if not quick:
+        monkeypatch.setattr(pkv, "_quick", None)
+    t, cap = 6, 80
+    c, accepted, counts = _commit_case(t, [40, 96, 80], [[0, 3, 5], [1, 2], [2]])
+    assert 16 * c["tables"].shape[1] > 96
+    g, acc, cnt = ref.on_gpu(c), accepted.cuda(), counts.cuda()
+    nb = c["k"].shape[0]
+    flag = pkv.new_error_flag("cuda")
+    slots = pkv.tree_plan(g["parents"], g["lens"], g["tables"], nb, 16, cap, err_flag=flag)[2]
+    assert pkv.check_error(flag) == pkv.EFLAG_CONTEXT_LEN
+    assert (slots[1] == -1).all() and (slots[[0, 2]] >= 0).all()
+    flag.zero_()
+    new = torch.empty_like(cnt)
+    pkv.tree_commit(g["k"], g["v"], g["tables"], g["lens"], t, acc, cnt, new_context_lens=new,
+                    err_flag=flag, max_context_len=cap)
+    assert pkv.check_error(flag) == pkv.EFLAG_CONTEXT_LEN
+    empty = dict(c, lens=torch.tensor([40, 0, 80], dtype=torch.int32))
+    k, v, want = ref.commit(empty, t, accepted, counts)
+    want[1] = cap - t
+    assert torch.equal(new.cpu(), want) and _same_bits(g["k"], k) and _same_bits(g["v"], v)
+    # without it the block table alone bounds a context
+    again = ref.on_gpu(c)
+    flag.zero_()
+    pkv.tree_commit(again["k"], again["v"], again["tables"], again["lens"], t, acc, cnt,
+                    new_context_lens=new, err_flag=flag)
+    k, v, want = ref.commit(c, t, accepted, counts)
+    assert pkv.check_error(flag) == 0
+    assert torch.equal(new.cpu(), want) and _same_bits(again["k"], k)
+    for bad, error in ((-1, pkv.PkvError), (2 ** 31, ValueError)):
+        with pytest.raises(error):
+            pkv.tree_commit(g["k"], g["v"], g["tables"], g["lens"], t, acc, cnt,
+                            new_context_lens=new, max_context_len=bad)
