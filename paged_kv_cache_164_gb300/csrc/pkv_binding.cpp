@@ -154,6 +154,17 @@ struct Caches {
     }
 };
 
+// A call of the C ABI without Python's lock: a launch waits where the device's queue
+// is full, and other threads go on meanwhile.  (All arguments are read before it.)
+template <typename F>
+PyObject* unlocked(F call) {
+    pkv_status s;
+    Py_BEGIN_ALLOW_THREADS
+    s = call();
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(s);
+}
+
 void* stream_of(int device) {
     return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device)).stream();
 }
@@ -194,14 +205,15 @@ PyObject* norm_rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const float* tab = static_cast<const float*>(table->data_ptr());
     const int32_t* ps = static_cast<const int32_t*>(pos);
     const int64_t* sl = static_cast<const int64_t*>(slots);
-    const pkv_status s =
-        f8 ? fn_norm_rope_append_fp8(out, qp, qs, kp, ks, vp, vs, qw, kw, eps, tab, npos, rd, inter,
-                                     ps, c.k, c.v, sl, tokens, c.num_blocks, c.block_size, heads,
-                                     c.heads, c.d, k_scale, v_scale, c.code, flag, st)
-           : fn_norm_rope_append(out, qp, qs, kp, ks, vp, vs, qw, kw, eps, tab, npos, rd, inter, ps,
-                                 c.k, c.v, sl, tokens, c.num_blocks, c.block_size, heads, c.heads,
-                                 c.d, c.code, flag, st);
-    return PyLong_FromLong(s);
+    return unlocked([&] {
+        return f8 ? fn_norm_rope_append_fp8(out, qp, qs, kp, ks, vp, vs, qw, kw, eps, tab, npos,
+                                            rd, inter, ps, c.k, c.v, sl, tokens, c.num_blocks,
+                                            c.block_size, heads, c.heads, c.d, k_scale, v_scale,
+                                            c.code, flag, st)
+                  : fn_norm_rope_append(out, qp, qs, kp, ks, vp, vs, qw, kw, eps, tab, npos, rd,
+                                        inter, ps, c.k, c.v, sl, tokens, c.num_blocks,
+                                        c.block_size, heads, c.heads, c.d, c.code, flag, st);
+    });
 }
 
 // (parents, context_lens, block_tables, num_blocks, block_size, max_context_len,
@@ -225,11 +237,14 @@ PyObject* tree_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
     int32_t* flag = r.flag(a[9]);
     const int width = r.narrow(tables->size(1)), batch = r.narrow(b), len = r.narrow(t);
     if (!r.ok) Py_RETURN_NONE;
-    return PyLong_FromLong(fn_tree_plan(
-        static_cast<int32_t*>(mask), static_cast<int32_t*>(pos), static_cast<int64_t*>(slots),
-        static_cast<const int32_t*>(par), static_cast<const int32_t*>(lens),
-        static_cast<const int32_t*>(tables->data_ptr()), width, cap, batch, len, nb, bs, flag,
-        stream_of(r.device)));
+    const int32_t* tab = static_cast<const int32_t*>(tables->data_ptr());
+    void* st = stream_of(r.device);
+    return unlocked([&] {
+        return fn_tree_plan(static_cast<int32_t*>(mask), static_cast<int32_t*>(pos),
+                            static_cast<int64_t*>(slots), static_cast<const int32_t*>(par),
+                            static_cast<const int32_t*>(lens), tab, width, cap, batch, len, nb,
+                            bs, flag, st);
+    });
 }
 
 // (q, k_cache, v_cache, block_tables, context_lens, max_context_len, tree_mask,
@@ -269,11 +284,16 @@ PyObject* tree_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int width = r.narrow(tables->size(1)), batch = r.narrow(b), len = r.narrow(t),
               heads = r.narrow(h_q);
     if (!r.ok) Py_RETURN_NONE;
-    return PyLong_FromLong(fn_tree_attention(
-        out, qp, c.k, c.v, static_cast<const int32_t*>(tables->data_ptr()), width,
-        static_cast<const int32_t*>(lens), cap, static_cast<const int32_t*>(mask->data_ptr()),
-        mask_stride, batch, len, c.num_blocks, c.block_size, heads, c.heads, c.d, scale,
-        ws->data_ptr(), ws->nbytes(), c.code, flag, stream_of(r.device)));
+    const int32_t* tab = static_cast<const int32_t*>(tables->data_ptr());
+    const int32_t* bits = static_cast<const int32_t*>(mask->data_ptr());
+    void* ws_ptr = ws->data_ptr();
+    const size_t ws_bytes = ws->nbytes();
+    void* st = stream_of(r.device);
+    return unlocked([&] {
+        return fn_tree_attention(out, qp, c.k, c.v, tab, width, static_cast<const int32_t*>(lens),
+                                 cap, bits, mask_stride, batch, len, c.num_blocks, c.block_size,
+                                 heads, c.heads, c.d, scale, ws_ptr, ws_bytes, c.code, flag, st);
+    });
 }
 
 // (k_cache, v_cache, block_tables, context_lens, tree_len, accepted, accepted_lens,
@@ -300,12 +320,15 @@ PyObject* tree_commit(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int width = r.narrow(tables->size(1)), batch = r.narrow(b),
               most = r.narrow(accepted->size(1));
     if (!r.ok) Py_RETURN_NONE;
-    return PyLong_FromLong(fn_tree_commit(
-        c.k, c.v, static_cast<const int32_t*>(tables->data_ptr()), width,
-        static_cast<const int32_t*>(lens), cap, len,
-        static_cast<const int32_t*>(accepted->data_ptr()),
-        static_cast<const int32_t*>(counts), most, static_cast<int32_t*>(fresh), batch,
-        c.num_blocks, c.block_size, c.heads, c.d, c.code, flag, stream_of(r.device)));
+    const int32_t* tab = static_cast<const int32_t*>(tables->data_ptr());
+    const int32_t* path = static_cast<const int32_t*>(accepted->data_ptr());
+    void* st = stream_of(r.device);
+    return unlocked([&] {
+        return fn_tree_commit(c.k, c.v, tab, width, static_cast<const int32_t*>(lens), cap, len,
+                              path, static_cast<const int32_t*>(counts), most,
+                              static_cast<int32_t*>(fresh), batch, c.num_blocks, c.block_size,
+                              c.heads, c.d, c.code, flag, st);
+    });
 }
 
 // C++ exceptions (a tensor without storage, a CUDA error) become "not the usual form".

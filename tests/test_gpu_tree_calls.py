@@ -1,4 +1,7 @@
 """Calls of the tree step that are easily made and were once answered wrongly or refused (GPU)."""
+import threading
+import time
+
 import pytest
 import torch
 
@@ -128,3 +131,45 @@ def test_a_context_beyond_the_steps_longest_is_not_committed(quick, monkeypatch)
         with pytest.raises(error):
             pkv.tree_commit(g["k"], g["v"], g["tables"], g["lens"], t, acc, cnt,
                             new_context_lens=new, max_context_len=bad)
+
+
+@pytest.mark.parametrize("quick", [True, False])
+def test_a_launch_that_waits_for_the_queue_lets_other_threads_run(quick, monkeypatch):
+    """Plans queued behind a kernel of about half a second, more of them than the device's
+    queue holds: a thread that ticks every millisecond goes on meanwhile."""
+    pkv.load()
+    if not quick:
+        monkeypatch.setattr(pkv, "_quick", None)
+    t = 4
+    c, _, _ = _commit_case(t, [40, 90], [[0], [0]])
+    g, nb = ref.on_gpu(c), c["k"].shape[0]
+    args = (g["parents"], g["lens"], g["tables"], nb, 16, 100)
+    outs = pkv.tree_plan(*args)
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    start.record()
+    torch.cuda._sleep(100_000_000)
+    end.record()
+    end.synchronize()
+    cycles = int(100_000_000 * 500 / start.elapsed_time(end))
+    gaps, stop = [], threading.Event()
+
+    def tick():
+        last = time.perf_counter()
+        while not stop.is_set():
+            time.sleep(0.001)
+            now = time.perf_counter()
+            gaps.append(now - last)
+            last = now
+
+    thread = threading.Thread(target=tick)
+    thread.start()
+    begun = time.perf_counter()
+    torch.cuda._sleep(cycles)
+    for _ in range(6000):
+        pkv.tree_plan(*args, *outs)
+    queued = time.perf_counter() - begun
+    stop.set()
+    thread.join()
+    torch.cuda.synchronize()
+    assert queued > 0.3, "the queue took every launch: nothing was tested"
+    assert max(gaps) < 0.15, f"the other thread stood still for {max(gaps):.2f} s"
