@@ -12,6 +12,7 @@ on in Python.
 from __future__ import annotations
 
 import concurrent.futures
+import contextlib
 import glob
 import hashlib
 import os
@@ -90,18 +91,26 @@ def build_binding(force: bool = False) -> bool:
                 if f.read().strip() == h.hexdigest():
                     return True
         os.makedirs(OUT_DIR, exist_ok=True)
-        if os.path.exists(BINDING):  # never one of other headers than these
-            os.remove(BINDING)
         r = subprocess.run([*cmd, "-o", tmp], capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(r.stderr[-2000:])
+        # (another process may be building too: each step holds whatever that one has done)
+        _remove(stamp)
         os.replace(tmp, BINDING)
-        with open(stamp, "w") as f:
+        with open(tmp, "w") as f:
             f.write(h.hexdigest())
+        os.replace(tmp, stamp)
         return True
     except (ImportError, AttributeError, OSError, RuntimeError) as e:
         print(f"pkv: the quick binding is left out: {e}", file=sys.stderr)
+        for f in (tmp, BINDING):  # never one of other headers than these
+            _remove(f)
         return False
+
+
+def _remove(path: str) -> None:
+    with contextlib.suppress(OSError):
+        os.remove(path)
 
 
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
