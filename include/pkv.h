@@ -482,6 +482,7 @@ pkv_status pkv_norm_rope_append_fp8(void* q_out, const void* q, int64_t q_stride
  *                 node's position, -1 for an absent node, and for all nodes of a
  *                 sequence whose context length is flagged, or whose block id is
  *                 (PKV_EFLAG_BLOCK_ID)
+ * None of the three may overlap an input.
  */
 pkv_status pkv_tree_plan(int32_t* tree_mask, int32_t* positions, int64_t* slot_mapping,
                          const int32_t* parents, const int32_t* context_lens,

@@ -289,6 +289,16 @@ extern "C" pkv_status pkv_tree_plan(int32_t* tree_mask, int32_t* positions, int6
           reinterpret_cast<uintptr_t>(block_tables)) & 3u) ||
         (reinterpret_cast<uintptr_t>(slot_mapping) & 7u))
         return PKV_ERR_INVALID_ARG;
+    // a sequence of more than kPlanRows nodes has several CTAs, which all read its
+    // parents, length and table and each write their own rows
+    const int64_t seqs = num_seqs, nodes = seqs * tree_len;
+    const int64_t out_bytes[3] = {nodes * ((tree_len + 31) / 32) * 4, nodes * 4, nodes * 8};
+    const void* outs[3] = {tree_mask, positions, slot_mapping};
+    for (int i = 0; i < 3; ++i)
+        if (overlap(outs[i], out_bytes[i], parents, nodes * 4) ||
+            overlap(outs[i], out_bytes[i], context_lens, seqs * 4) ||
+            overlap(outs[i], out_bytes[i], block_tables, seqs * max_blocks_per_seq * 4))
+            return PKV_ERR_INVALID_ARG;
     TreePlanParams p = {};
     p.tree_mask = tree_mask;
     p.positions = positions;

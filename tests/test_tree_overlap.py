@@ -33,6 +33,22 @@ def _commit(lib, new):
                                BS, H_KV, D, 1, NULL, NULL)
 
 
+PLAN_IN = {"parents": (3, B * T * 4), "lens": (4, B * 4), "tables": (5, B * WIDTH * 4)}
+PLAN_OUT = {"mask": (0, B * T * 4), "positions": (1, B * T * 4), "slots": (2, B * T * 8)}
+
+
+@pytest.mark.parametrize("name", PLAN_IN)
+@pytest.mark.parametrize("out", PLAN_OUT)
+def test_plan_refuses_outputs_over_what_it_reads(lib, out, name):
+    place, size = PLAN_IN[name]
+    for offset in (0, (size - 4) // 8 * 8, -((PLAN_OUT[out][1] - 4) // 8 * 8)):
+        mask, positions, slots = (_at(place, offset) if n == out else _at(at)
+                                  for n, (at, _) in PLAN_OUT.items())
+        parents, lens, tables = (_at(at) for at, _ in PLAN_IN.values())
+        assert lib.pkv_tree_plan(mask, positions, slots, parents, lens, tables, WIDTH, 64, B, T,
+                                 NB, BS, NULL, NULL) == 1
+
+
 @pytest.mark.parametrize("name", COMMIT)
 def test_commit_refuses_new_lengths_over_what_it_reads(lib, name):
     place, size = COMMIT[name]
