@@ -426,7 +426,10 @@ pkv_status pkv_multi_query_attention(
  *                 (PKV_EFLAG_SLOT), the token skipped
  * pkv_norm_rope_append_fp8 writes E4M3 caches: E4M3(y / k_scale) and
  * E4M3(v / v_scale), the fp32 quotient rounded to the nearest E4M3 value (ties
- * to even), saturating at +-448 (V's codes are those of pkv_append_fp8).
+ * to even), saturating at +-448 (V's codes are those of pkv_append_fp8).  The calls
+ * that read such a cache are pkv_decode_attention_fp8 and
+ * pkv_append_decode_attention_fp8: pkv_tree_attention and pkv_tree_commit take
+ * 16-bit caches only, so a tree step has no E4M3 form.
  */
 pkv_status pkv_norm_rope_append(void* q_out, const void* q, int64_t q_stride, const void* k,
                                 int64_t k_stride, const void* v, int64_t v_stride,
@@ -498,7 +501,10 @@ pkv_status pkv_tree_plan(int32_t* tree_mask, int32_t* positions, int64_t* slot_m
  * any bits (pkv_tree_plan writes the ancestors'); bits past tree_len are
  * ignored.  A row that attends to nothing becomes zero.  What the cache holds
  * at a position that a row does not attend to never reaches that row, whatever
- * its bits (infinities and NaN included).
+ * its bits (infinities and NaN included).  An infinity in a committed position's V,
+ * which every row attends to, makes that dim of the rows infinite or NaN.
+ * Scores, softmax sums and accumulators are fp32; a softmax weight meets V as two
+ * terms of the cache's type, which keep it to 2^-16 (bf16) or 2^-22 (fp16) of itself.
  *
  *   q, out        [num_seqs][tree_len][num_q_heads][head_dim], dtype
  *   tree_mask     int32 [num_seqs][tree_len][ceil(tree_len / 32)], rows of
@@ -530,8 +536,8 @@ pkv_status pkv_tree_attention(void* out, const void* q, const void* k_cache, con
  * hold the nodes are the sequence's own (as for any append).
  *
  *   accepted       int32 [num_seqs][max_accepted]: a sequence's accepted nodes,
- *                  strictly increasing (a path down the tree is); entries past
- *                  accepted_lens[b] are not read
+ *                  strictly increasing (a path down the tree is); what entries past
+ *                  accepted_lens[b] hold does not matter
  *   accepted_lens  int32 [num_seqs], 0 .. min(max_accepted, tree_len)
  *   new_context_lens  int32 [num_seqs] (written), nullable; must not overlap
  *                  anything that the call reads
