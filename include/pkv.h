@@ -415,7 +415,7 @@ pkv_status pkv_multi_query_attention(
  *                 the three may be parts of one packed projection; strides are
  *                 multiples of 8 elements, at least a token's heads
  *   q_out         [num_tokens][num_q_heads][head_dim]; may be q itself when
- *                 q_stride is a token's heads, must not overlap q, k or v otherwise
+ *                 q_stride is a token's heads, must not overlap any other argument
  *   q_weight, k_weight  [head_dim], dtype; NULL: no norm
  *   eps           finite, >= 0
  *   cos_sin       float32 [max_position][rotary_dim]: cosines, then sines

@@ -303,6 +303,16 @@ static pkv_status norm_rope_impl(RopeParams p, int num_tokens, int num_blocks, i
         overlap(p.q_out, out_bytes, p.k, (last * p.k_stride + (int64_t)hkv * head_dim) * 2) ||
         overlap(p.q_out, out_bytes, p.v, (last * p.v_stride + (int64_t)hkv * head_dim) * 2))
         return PKV_ERR_INVALID_ARG;
+    const int64_t cache_bytes = (int64_t)num_blocks * bs * hkv * head_dim * (f8 ? 1 : 2);
+    const auto over = [&](const void* a, int64_t bytes) {
+        return a != nullptr && overlap(p.q_out, out_bytes, a, bytes);
+    };
+    if (over(p.q_weight, head_dim * 2) || over(p.k_weight, head_dim * 2) ||
+        over(p.cos_sin, (int64_t)p.max_position * p.rotary_dim * 4) ||
+        over(p.positions, (int64_t)num_tokens * 4) ||
+        over(p.slot_mapping, (int64_t)num_tokens * 8) || over(p.k_cache, cache_bytes) ||
+        over(p.v_cache, cache_bytes))
+        return PKV_ERR_INVALID_ARG;
     const int sms = current_sm_count();
     if (sms <= 0) return PKV_ERR_CUDA;
     p.num_slots = (int64_t)num_blocks * bs;

@@ -54,3 +54,27 @@ def test_commit_refuses_new_lengths_over_what_it_reads(lib, name):
     place, size = COMMIT[name]
     for offset in (0, size - 4, -4 * (B - 1)):
         assert _commit(lib, _at(place, offset)) == 1
+
+
+TOKENS, H_Q, NPOS = 4, 6, 100
+ROPE = {"q": (1, TOKENS * H_Q * D * 2), "k": (2, TOKENS * H_KV * D * 2),
+        "v": (3, TOKENS * H_KV * D * 2), "q_weight": (4, D * 2), "k_weight": (5, D * 2),
+        "cos_sin": (6, NPOS * D * 4), "positions": (7, TOKENS * 4), "k_cache": (8, CACHE),
+        "v_cache": (9, CACHE), "slots": (10, TOKENS * 8)}
+
+
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("name", ROPE)
+def test_norm_rope_append_refuses_its_output_over_what_it_reads(lib, name, f8):
+    place, size = ROPE[name]
+    if f8 and "cache" in name:
+        size //= 2
+    q, k, v, wq, wk, table, pos, kc, vc, slots = (_at(i) for i in range(1, 11))
+    before = TOKENS * H_Q * D * 2 - 16
+    for offset in ([0] if name != "q" else []) + [16 * ((size - 1) // 16), -before]:
+        head = (_at(place, offset), q, H_Q * D, k, H_KV * D, v, H_KV * D, wq, wk, 1e-6, table,
+                NPOS, D, 0, pos, kc, vc, slots, TOKENS, NB, BS, H_Q, H_KV, D)
+        if f8:
+            assert lib.pkv_norm_rope_append_fp8(*head, 0.1, 0.1, 1, NULL, NULL) == 1
+        else:
+            assert lib.pkv_norm_rope_append(*head, 1, NULL, NULL) == 1
