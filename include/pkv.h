@@ -506,7 +506,8 @@ pkv_status pkv_tree_plan(int32_t* tree_mask, int32_t* positions, int64_t* slot_m
  * Scores, softmax sums and accumulators are fp32; a softmax weight meets V as two
  * terms of the cache's type, which keep it to 2^-16 (bf16) or 2^-22 (fp16) of itself.
  *
- *   q, out        [num_seqs][tree_len][num_q_heads][head_dim], dtype
+ *   q, out        [num_seqs][tree_len][num_q_heads][head_dim], dtype; out may be q
+ *                 itself, must not overlap any argument otherwise
  *   tree_mask     int32 [num_seqs][tree_len][ceil(tree_len / 32)], rows of
  *                 sequence b mask_stride words after those of b - 1 (0: one
  *                 mask for all sequences)

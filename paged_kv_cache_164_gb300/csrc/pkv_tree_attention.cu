@@ -1321,12 +1321,26 @@ extern "C" pkv_status pkv_tree_attention(
         ((reinterpret_cast<uintptr_t>(block_tables) | reinterpret_cast<uintptr_t>(context_lens) |
           reinterpret_cast<uintptr_t>(tree_mask)) & 3u))
         return PKV_ERR_INVALID_ARG;
-    if ((int64_t)max_blocks_per_seq * block_size > kTreeMaxContext) return PKV_ERR_UNSUPPORTED;
+    if ((int64_t)max_blocks_per_seq * block_size > kTreeMaxContext ||
+        max_context_len > kTreeMaxContext)
+        return PKV_ERR_UNSUPPORTED;
+    // the output is q itself (a unit's rows are read by its CTAs alone, and written when
+    // they are through), or apart from everything that is read
+    const int64_t seqs = num_seqs;
+    const int64_t q_bytes = seqs * tree_len * num_q_heads * head_dim * 2;
+    const int64_t mask_bytes = ((seqs - 1) * mask_stride + mask_words) * 4;
+    const int64_t cache_bytes = (int64_t)num_blocks * block_size * num_kv_heads * head_dim * 2;
+    const auto over = [&](const void* a, int64_t bytes) { return overlap(out, q_bytes, a, bytes); };
+    if ((out != q && over(q, q_bytes)) || over(block_tables, seqs * max_blocks_per_seq * 4) ||
+        over(context_lens, seqs * 4) || over(tree_mask, mask_bytes) ||
+        over(k_cache, cache_bytes) || over(v_cache, cache_bytes))
+        return PKV_ERR_INVALID_ARG;
     TreeCallPlan plan;
     st = plan_tree(num_seqs, tree_len, num_q_heads, num_kv_heads, head_dim, block_size,
                    max_context_len, &plan);
     if (st != PKV_OK) return st;
     if (workspace_bytes < plan.workspace_bytes) return PKV_ERR_WORKSPACE;
+    if (over(workspace, (int64_t)plan.workspace_bytes)) return PKV_ERR_INVALID_ARG;
 
     CUtensorMap mk, mv;
     if (!make_cache_map(&mk, k_cache, dtype, num_blocks, block_size, num_kv_heads, head_dim, hnd) ||

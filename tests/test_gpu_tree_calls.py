@@ -173,3 +173,59 @@ def test_a_launch_that_waits_for_the_queue_lets_other_threads_run(quick, monkeyp
     torch.cuda.synchronize()
     assert queued > 0.3, "the queue took every launch: nothing was tested"
     assert max(gaps) < 0.15, f"the other thread stood still for {max(gaps):.2f} s"
+
+
+@pytest.mark.parametrize("key", ["one_tile_d64", "one_tile", "whole_units", "cut", "cut_256_rows",
+                                 "three_blocks"])
+def test_attention_in_place(key):
+    """The output over the queries, where a unit is written at once and where it is cut."""
+    c = ref.make_case(len(key), **{
+        "one_tile_d64": dict(lens=[20, 33, 9], t=9, h_q=6, h_kv=3, d=64, bs=16, dtype="fp16"),
+        "one_tile": dict(lens=[90, 77], t=40, h_q=8, h_kv=1, d=128, bs=16, dtype="bf16"),
+        "whole_units": dict(lens=[300] * 40, t=5, h_q=8, h_kv=8, d=128, bs=16, dtype="bf16"),
+        "cut": dict(lens=[9000, 40, 2500], t=7, h_q=8, h_kv=2, d=64, bs=32, dtype="bf16"),
+        "cut_256_rows": dict(lens=[2000, 130], t=32, h_q=16, h_kv=2, d=128, bs=16, dtype="bf16"),
+        "three_blocks": dict(lens=[700, 64], t=48, h_q=8, h_kv=1, d=128, bs=16, dtype="fp16"),
+    }[key])
+    g = ref.on_gpu(c)
+    args = (g["k"], g["v"], g["tables"], g["lens"], c["max_len"], g["mask"])
+    want = pkv.tree_attention(g["q"], *args, scale=c["scale"])
+    ref.assert_close(want, *ref.attention(c), key)
+    q = g["q"].clone()
+    assert pkv.tree_attention(q, *args, scale=c["scale"], out=q) is q
+    assert _same_bits(q, want)
+    both = torch.empty(2 * q.numel() + 8, dtype=q.dtype, device="cuda")
+    shifted = both[8:8 + q.numel()].view(q.shape)
+    with pytest.raises(pkv.PkvError, match="INVALID_ARG"):
+        pkv.tree_attention(both[:q.numel()].view(q.shape), *args, out=shifted)
+
+
+def test_empty_batches_and_norms_of_one_side():
+    t = 5
+    c, accepted, counts = _commit_case(t, [40, 30], [[0], [1]])
+    g, nb = ref.on_gpu(c), c["k"].shape[0]
+    none = pkv.tree_plan(g["parents"][:0], g["lens"][:0], g["tables"][:0], nb, 16, 64)
+    assert [tuple(x.shape) for x in none] == [(0, t, 1), (0, t), (0, t)]
+    out = pkv.tree_attention(g["q"][:0], g["k"], g["v"], g["tables"][:0], g["lens"][:0], 64,
+                             g["mask"][:0])
+    assert out.shape == (0, t, 8, 128)
+    new = pkv.tree_commit(g["k"], g["v"], g["tables"][:0], g["lens"][:0], t, accepted[:0].cuda(),
+                          counts[:0].cuda())
+    assert new.shape == (0,)
+    x = torch.randn(7, 12, 128, device="cuda").bfloat16()
+    w = (1 + 0.1 * torch.randn(128, device="cuda")).bfloat16()
+    angle = torch.rand(50, 64, device="cuda")
+    table = torch.cat([angle.cos(), angle.sin()], 1)
+    pos = torch.arange(7, dtype=torch.int32, device="cuda") * 7
+    slots = torch.arange(7, device="cuda") * 3
+    for wq, wk in ((w, None), (None, w), (None, None), (w, w)):
+        kc, vc = (torch.zeros(4, 16, 2, 128, dtype=torch.bfloat16, device="cuda") for _ in "kv")
+        q = pkv.norm_rope_append(x[:, :8], x[:, 8:10], x[:, 10:], pos, table, kc, vc, slots,
+                                 q_weight=wq, k_weight=wk)
+        cpu = [y.cpu() if y is not None else None for y in (wq, wk)]
+        eq, ek, ev, bq, bk = ref.norm_rope(x[:, :8].cpu(), x[:, 8:10].cpu(), x[:, 10:].cpu(),
+                                           pos.cpu(), table.cpu(), *cpu, 1e-6, "half")
+        for got, exact, lost in ((q, eq, bq), (kc.view(-1, 2, 128)[slots], ek, bk),
+                                 (vc.view(-1, 2, 128)[slots], ev, 0 * ev)):
+            off = (got.cpu().double() - exact).abs()
+            assert (off <= 2.0 ** -8 * (exact.abs() + lost) + lost).all()

@@ -78,3 +78,18 @@ def test_norm_rope_append_refuses_its_output_over_what_it_reads(lib, name, f8):
             assert lib.pkv_norm_rope_append_fp8(*head, 0.1, 0.1, 1, NULL, NULL) == 1
         else:
             assert lib.pkv_norm_rope_append(*head, 1, NULL, NULL) == 1
+
+
+Q_BYTES = B * T * H_Q * D * 2
+ATTENTION = {"q": (1, Q_BYTES), "k": (2, CACHE), "v": (3, CACHE), "tables": (4, B * WIDTH * 4),
+             "lens": (5, B * 4), "mask": (6, 4 * ((B - 1) * 9 + T))}
+
+
+@pytest.mark.parametrize("name", ATTENTION)
+def test_attention_refuses_its_output_over_what_it_reads(lib, name):
+    place, size = ATTENTION[name]
+    q, k, v, tables, lens, mask, ws = (_at(i) for i in range(1, 8))
+    for offset in ([0] if name != "q" else []) + [16 * ((size - 1) // 16), -(Q_BYTES - 16)]:
+        assert lib.pkv_tree_attention(_at(place, offset), q, k, v, tables, WIDTH, lens, 64, mask,
+                                      9, B, T, NB, BS, H_Q, H_KV, D, 0.1, ws, 1 << 29, 1, NULL,
+                                      NULL) == 1
