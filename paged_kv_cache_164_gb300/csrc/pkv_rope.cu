@@ -6,9 +6,10 @@
 //     y_a' = y_a cos - y_b sin,  y_b' = y_b cos + y_a sin  for each rotated pair
 // It is bound by memory: every row is read once and written once (q to q_out,
 // k and v into the cache), a few operations an element.  16411 packed tokens of
-// the Llama-7B layer (815 MB) take 124 us, 6.57 TB/s (97 % of the copy rate);
-// 2043 tokens of the Llama-70B layer (80 MB) 18.3 us into E4M3 pages, 17.7 us into
-// 16-bit ones, where starting and draining the SMs shows; 32 tokens 2 us, a
+// the Llama-7B layer (815 MB) take 125 us, 6.5 TB/s (96 % of the copy rate);
+// 2043 tokens of the Llama-70B layer (80 MB) 18.4 us into E4M3 pages, 17.7 us into
+// 16-bit ones, 1.55 and 1.44 times their bytes at that rate: 6129 CTAs, four and a
+// half waves of them, each of which loads, waits and stores once; 32 tokens 2 us, a
 // launch's least.
 //
 // A group of head_dim / 8 lanes takes a row, two blocks of 4 dims a

@@ -20,9 +20,10 @@ namespace pkv {
 // the chain is sound); then a thread hops from word to word instead of from node
 // to node, and the bits it gathers count its depth.  The rows go through shared
 // memory, so that their stores are dense: a row is 4 to 128 bytes.
-// Latency is all it costs.  One sequence's 64 nodes: 1.7 us, a launch's least;
-// 256 sequences of 250 nodes, some 55 deep: 5.1 us (8.7 with a walk of the whole
-// chain for its soundness and another for its bits, and each thread storing its row).
+// Latency is all it costs.  One sequence's 64 nodes: 2 us, a launch's least; 256
+// sequences of 250 nodes, some 55 deep: 5.5 us a call, 4.3 in a graph of such calls.
+// (A walk of the whole chain for its soundness, another for its bits, and each
+// thread storing its row: 8.7 us where this form took 5.1, by the same clock.)
 
 struct TreePlanParams {
     int32_t* tree_mask;

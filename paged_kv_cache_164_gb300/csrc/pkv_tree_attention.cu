@@ -35,14 +35,21 @@
 // (normalised O and its log-sum-exp) per CTA, at most two a CTA, and
 // tree_merge_kernel joins them.
 //
-// What bounds it: up to 128 rows per KV head, memory: 16 nodes on the Llama-70B
-// layer over 8 ragged contexts of 33000 to 131000 tokens take 390 to 404 us for
-// 2.69 GB (6.7 to 6.9 TB/s, 98 to 102 % of the copy rate), 8 nodes on the
-// Llama-7B layer (16 contexts of 520 to 4096) 97 to 100 us for 607 MB (90 to
-// 92 %).  With 256 rows, the tensor cores and the softmax beside them: 32 nodes
-// on the Llama-70B layer (32 x 4096 tokens) 148 us, of which the products alone,
-// with P twice, would take 109 at the dense rate (tensor pipe 65 % active); a
-// single 16-bit P would take 129.  Head dim 64 is bound by the softmax threads.
+// What bounds it (times of a few dozen calls, then of calls that go on for seconds,
+// where the power cap lowers the clock):
+// Up to 128 rows per KV head, memory: 16 nodes on the Llama-70B layer over 8 ragged
+// contexts of 33000 to 131000 tokens take 390 to 412 us, then 450, for 2.69 GB (96
+// to 102 % of the copy rate, then 88 %), 8 nodes on the Llama-7B layer (16 contexts
+// of 520 to 4096) 97 to 101 us, then 100, for 607 MB (89 to 92 %).
+// With 256 rows, 32 nodes on the Llama-70B layer (32 x 4096 tokens), 147 us, then
+// 166.  No unit is full: the tensor pipe is active 63 % of the time, the memory 48 %.
+// The products alone, with P twice, would take 109 at the dense rate (a single 16-bit
+// P would take 129 in all); the softmax threads take about as long beside them, and
+// the join of the cut units 16.
+// Head dim 64 takes as long at the softmax of a score for half the products: the same
+// 256 rows 126 us, 128 rows (16 nodes) 75, for floors of 42 and 41; tensor pipe 34 %
+// active, 0.53 instructions a cycle and scheduler from its two softmax warps, and a
+// token-major cache's rows of 128 bytes read 1.5 times (410 MB of 268).
 //
 // Every wait is bounded, as in the decode kernels.
 #include <algorithm>
@@ -970,7 +977,7 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 };
                 // everything is read before the first store, which might alias it for all
                 // that the compiler knows (900 cycles a turn of partials, so 650 to 700;
-                // 32 nodes on the Llama-70B layer 154 us, so 148)
+                // 32 nodes on the Llama-70B layer 154 us, so 148, of a few dozen calls)
                 if (direct) {
                     const int64_t first = (int64_t)s.b * p.tree_len * p.num_q_heads;
                     uint4 x[4];
@@ -1252,9 +1259,12 @@ static cudaError_t launch_tree_t(const CUtensorMap& mk, const CUtensorMap& mv, c
     if (e != cudaSuccess || !plan.cut) return e;
     const int64_t rows = (int64_t)p.num_seqs * p.tree_len * p.num_q_heads;
     // Groups a row: while few rows leave the SMs room (about 20000 groups run at a
-    // time) and a unit may have partials for them.  1, 4 and 16 groups: 36 rows of
-    // some 90 partials 37, 18 and 13 us (the whole call), 252 rows of 70 36, 24 and
-    // 17, 1792 rows of ten 18.3, 15.0 and 14.5, 12960 rows of two 23, 26 and 38.
+    // time) and a unit may have partials for them.  1, 4 and 16 groups, the whole call
+    // in a graph (bf16, head dim 128, 16-token pages):
+    //   9 nodes, 4/1 heads, 1 x 12579 tokens (36 rows of 99 partials)     40, 19.5, 13.1
+    //   63 nodes, 4/1 heads, 1 x 17963 tokens (252 rows of 141)           61, 34, 27.8
+    //   16 nodes, 8/1 heads, 14 x 4016 tokens (1792 rows of some 11)    24.8, 19.2, 19.7
+    //   60 nodes, 8/4 heads, 27 x 2060 tokens (12960 rows of two or three)  34, 37, 51
     const int partials = std::min(plan.ctas, plan.max_tiles);
     const int groups = rows * 16 <= 32768 && partials > 8 ? kTreeMergeGroups
                        : rows * 4 <= 32768 && partials > 2 ? 4
