@@ -156,13 +156,18 @@ struct Caches {
 
 // A call of the C ABI without Python's lock: a launch waits where the device's queue
 // is full, and other threads go on meanwhile.  (All arguments are read before it.)
+struct Unlocked {  // (the lock is back however the call is left)
+    PyThreadState* state = PyEval_SaveThread();
+    ~Unlocked() { PyEval_RestoreThread(state); }
+};
+template <typename F>
+pkv_status run_unlocked(F call) {
+    Unlocked u;
+    return call();
+}
 template <typename F>
 PyObject* unlocked(F call) {
-    pkv_status s;
-    Py_BEGIN_ALLOW_THREADS
-    s = call();
-    Py_END_ALLOW_THREADS
-    return PyLong_FromLong(s);
+    return PyLong_FromLong(run_unlocked(call));
 }
 
 void* stream_of(int device) {

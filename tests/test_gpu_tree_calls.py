@@ -1,4 +1,6 @@
 """Calls of the tree step that are easily made and were once answered wrongly or refused (GPU)."""
+import ctypes
+import subprocess
 import threading
 import time
 
@@ -229,3 +231,68 @@ def test_empty_batches_and_norms_of_one_side():
                                  (vc.view(-1, 2, 128)[slots], ev, 0 * ev)):
             off = (got.cpu().double() - exact).abs()
             assert (off <= 2.0 ** -8 * (exact.abs() + lost) + lost).all()
+
+
+THROWS = """#include <stdexcept>
+extern "C" int throws() { throw std::runtime_error("no"); }
+"""
+
+
+def test_an_exception_in_a_call_gives_the_lock_back(tmp_path, monkeypatch):
+    """The quick form answers "not mine" and Python's lock is held again: the call in Python
+    that follows needs it."""
+    lib = pkv.load()
+    if pkv._quick is None:
+        pytest.skip("built without the headers of Python and torch")
+    (tmp_path / "throws.cpp").write_text(THROWS)
+    out = str(tmp_path / "throws.so")
+    subprocess.run(["g++", "-shared", "-fPIC", "-o", out, str(tmp_path / "throws.cpp")], check=True)
+    fake = ctypes.cast(ctypes.CDLL(out).throws, ctypes.c_void_p).value
+    real = [ctypes.cast(getattr(lib, "pkv_" + n), ctypes.c_void_p).value
+            for n in ("norm_rope_append", "norm_rope_append_fp8", "tree_plan", "tree_attention",
+                      "tree_commit_within")]
+    c, _, _ = _commit_case(4, [40, 90], [[0], [0]])
+    g, nb = ref.on_gpu(c), c["k"].shape[0]
+    args = (g["parents"], g["lens"], g["tables"], nb, 16, 100)
+    want = pkv.tree_plan(*args)
+    outs = [torch.full_like(x, -9) for x in want]
+    pkv._quick.bind(*[fake] * 5)
+    try:
+        assert pkv._quick.tree_plan(*args, *outs, None) is None
+        for _ in range(50):
+            pkv.tree_plan(*args, *outs)
+    finally:
+        pkv._quick.bind(*real)
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+def test_outputs_made_on_a_forked_stream_in_a_graph():
+    """Captured on a stream that joins the capture, outputs and workspace allocated there;
+    other tensors are made and written between the replays."""
+    t = 9
+    c = ref.make_case(77, [700, 90], t, 8, 2, 128, 16, "bf16")
+    g, nb = ref.on_gpu(c), c["k"].shape[0]
+
+    def step(stream):
+        mask, pos, slots = pkv.tree_plan(g["parents"], g["lens"], g["tables"], nb, 16, 700,
+                                         stream=stream)
+        out = pkv.tree_attention(g["q"], g["k"], g["v"], g["tables"], g["lens"], 700, mask,
+                                 scale=c["scale"], stream=stream)
+        return mask, pos, slots, out
+
+    want = [x.clone() for x in step(None)]
+    torch.cuda.synchronize()
+    graph, fork = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        fork.wait_stream(torch.cuda.current_stream())
+        got = step(fork)
+        torch.cuda.current_stream().wait_stream(fork)
+    for _ in range(3):
+        junk = [torch.full((1 << 16,), 7, dtype=torch.int64, device="cuda") for _ in range(20)]
+        for x in got:
+            x.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all((x == 7).all() for x in junk)
+        for a, b in zip(got, want):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
