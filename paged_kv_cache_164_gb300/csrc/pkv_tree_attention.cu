@@ -1026,6 +1026,8 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             s = next;
             have = have_next;
         }
+        // a warp that gave up a wait may have the next stretch's queries on their way
+        ptx::cp_async_wait_all();
     }
 
     ptx::tc_fence_before_sync();
