@@ -68,6 +68,12 @@ typedef enum { PKV_FP16 = 0, PKV_BF16 = 1 } pkv_dtype;
                                         decoded without the shared prefix) */
 #define PKV_EFLAG_POSITION      0x20 /* rotary position outside the cos / sin table */
 #define PKV_EFLAG_TREE          0x40 /* a malformed tree of drafted tokens or accepted path */
+#define PKV_EFLAG_QUERY         0x80 /* rows of a ragged batch that do not increase, or lead
+                                        beyond the rows given */
+#define PKV_EFLAG_POOL          0x100 /* pages or token places ran out (batch_plan), or a free
+                                         count outside its list */
+#define PKV_EFLAG_TOKEN         0x200 /* a drafted token outside the vocabulary, or a row of
+                                         probabilities without any mass */
 
 #define PKV_MAX_SPLITS 1024           /* upper bound on split-K partitions per sequence */
 
@@ -565,6 +571,148 @@ pkv_status pkv_tree_commit(void* k_cache, void* v_cache, const int32_t* block_ta
                            int max_accepted, int32_t* new_context_lens, int num_seqs,
                            int num_blocks, int block_size, int num_kv_heads, int head_dim,
                            pkv_dtype dtype, int32_t* err_flag, void* stream);
+
+/*
+ * A ragged step: its sequences bring different numbers of new tokens (chunks of
+ * prompts, single tokens, drafted tails), packed one after another; sequence b's
+ * rows are query_starts[b] .. query_starts[b + 1] - 1 ([inference] "Chunked
+ * Prefill"; continuous batching).  The calls of a step:
+ *     pkv_batch_plan, pkv_norm_rope_append (or pkv_append), pkv_chunk_attention,
+ *     pkv_verify_drafts where tokens were drafted (its new lengths are the next
+ *     step's keep_lens)
+ *
+ * The plan of a step: pages taken from and given back to a free list, block
+ * tables, positions and slots, from the requests' lengths ([inference]
+ * PageAllocator: allocate and free of physical blocks).  In this order, as if one
+ * sequence after another:
+ *   1. Sequence b keeps keep_lens[b] of its context_lens[b] tokens.  Its pages
+ *      behind them, table entries ceil(keep / block_size), but not before
+ *      shared_pages[b], up to ceil(context / block_size) - 1, are pushed onto the
+ *      free list in the table's order.
+ *   2. It receives new_lens[b] tokens, and the pages for them, each popped from the
+ *      list and written behind its table's kept entries.  From the first sequence
+ *      on for which pages or token places (max_tokens) do not last, none receives
+ *      any (PKV_EFLAG_POOL): its new tokens are none.
+ *   3. query_starts is the exclusive sum of the tokens received, and
+ *      new_context_lens[b] = keep + those.  Token j of sequence b has position
+ *      keep + j and that position's slot; the places behind the last token get
+ *      position 0 and slot -1 (padding).
+ *
+ *   context_lens, new_lens  int32 [num_seqs]
+ *   keep_lens     int32 [num_seqs], 0 .. context_lens; NULL: all is kept
+ *   shared_pages  int32 [num_seqs]; NULL: none.  A sequence's first pages that
+ *                 others hold too (a shared prefix): never given back
+ *   block_tables  int32 [num_seqs][max_blocks_per_seq] (read and written)
+ *   free_blocks   int32 [free_capacity] (read and written): the list, its top at
+ *                 free_count[0] - 1; what was popped keeps its bytes
+ *   free_count    int32 [1]
+ *   query_starts  int32 [num_seqs + 1] (written)
+ *   positions     int32 [max_tokens] (written);  slot_mapping  int64 [max_tokens] (written)
+ *   new_context_lens, new_free_count  (written); may be context_lens and free_count
+ * No other two arguments may overlap where one is written.
+ * A context length beyond the block table (PKV_EFLAG_CONTEXT_LEN; then nothing of
+ * the sequence changes, and its new length is the clamped one), a keep length
+ * outside 0 .. context (the same), new tokens that are negative or lead beyond the
+ * table (none received), a block id outside the pool (PKV_EFLAG_BLOCK_ID; slot -1)
+ * and a free list that overflows (PKV_EFLAG_POOL; what does not fit is dropped) are
+ * flagged.
+ */
+pkv_status pkv_batch_plan(int32_t* query_starts, int32_t* positions, int64_t* slot_mapping,
+                          int32_t* new_context_lens, int32_t* new_free_count,
+                          const int32_t* context_lens, const int32_t* new_lens,
+                          const int32_t* keep_lens, const int32_t* shared_pages,
+                          int32_t* block_tables, int max_blocks_per_seq, int32_t* free_blocks,
+                          int free_capacity, const int32_t* free_count, int num_seqs,
+                          int max_tokens, int num_blocks, int block_size, int32_t* err_flag,
+                          void* stream);
+
+/*
+ * Attention of a ragged step's new tokens over the paged cache (their K/V are
+ * appended first, so context_lens counts them).  Token i of sequence b, which
+ * brings t_b tokens, has position m = n_b - t_b + i and sees the positions
+ *     max(0, m + 1 - window) <= t < max(m + 1, min(prefix_lens[b], n_b))
+ * (causal; a window of 0 is none; a prefix is seen by every token, as a picture's
+ * or an instruction's places are).  Of those:
+ *     z_t = scale <q_i, K_t>;  z_t = softcap tanh(z_t / softcap) where softcap > 0;
+ *     z_t += slopes[h] (t - m) where slopes are given;  out = sum_t softmax(z)_t V_t
+ * A row that sees nothing becomes zero.  What the cache holds at a position that a
+ * row does not see never reaches that row, whatever its bits (infinities and NaN
+ * included).  Rows of q before query_starts[0] and from query_starts[num_seqs] on
+ * are left as they were.
+ *
+ *   q, out        [num_tokens][num_q_heads][head_dim], dtype; out may be q itself,
+ *                 must not overlap any argument otherwise
+ *   query_starts  int32 [num_seqs + 1], not decreasing, 0 .. num_tokens (otherwise
+ *                 clamped and flagged, PKV_EFLAG_QUERY)
+ *   context_lens  int32 [num_seqs], at least the sequence's tokens (a shorter one is
+ *                 flagged PKV_EFLAG_CONTEXT_LEN; rows of negative positions are zero)
+ *   prefix_lens   int32 [num_seqs]; NULL: none
+ *   slopes        float32 [num_q_heads], finite; NULL: none
+ *   softcap, window  >= 0 (0: none)
+ *   other arguments as for pkv_multi_query_attention; workspace of at least
+ *   pkv_chunk_attention_workspace_size(...) bytes (contents on entry do not matter)
+ */
+size_t pkv_chunk_attention_workspace_size(int num_seqs, int num_tokens, int num_q_heads,
+                                          int num_kv_heads, int head_dim, int block_size,
+                                          int max_context_len);
+
+pkv_status pkv_chunk_attention(void* out, const void* q, const void* k_cache, const void* v_cache,
+                               const int32_t* block_tables, int max_blocks_per_seq,
+                               const int32_t* query_starts, const int32_t* context_lens,
+                               int max_context_len, const int32_t* prefix_lens,
+                               const float* slopes, int num_seqs, int num_tokens, int num_blocks,
+                               int block_size, int num_q_heads, int num_kv_heads, int head_dim,
+                               float scale, float softcap, int window, void* workspace,
+                               size_t workspace_bytes, pkv_dtype dtype, int32_t* err_flag,
+                               void* stream);
+
+/*
+ * Verification of drafted tokens ([inference] "投机采样 (Speculative Decoding)":
+ * accept a draft with probability min(1, p / q), else draw from what is left of p).
+ * Sequence b's rows row_starts[b] .. row_starts[b + 1] - 1 are the nodes of a chain
+ * or a tree: node 0 is the token that the step before chose, node i hangs on
+ * parents[i] < i.  Row r of target_probs is the large model's distribution of what
+ * follows node r, row r of draft_probs the one from which r's children were drawn
+ * (NULL: drafts without a distribution, all of its mass on the token tried).
+ *     cur = 0, R = p_cur, Z = 1
+ *     for node i = 1, 2, .. whose parent is cur, token x, number u = uniforms[i]:
+ *         u q_cur(x) Z < R(x):  accepted; cur = i, R = p_cur, Z = 1
+ *         otherwise:            R = max(R - Z q_cur, 0), Z = sum R
+ *     next token: the first k with R(0) + .. + R(k) > uniforms[0] sum R
+ *         (R = p_cur where R is zero everywhere)
+ * Sums are exact to 2^-60 in any order, so the result does not depend on how the
+ * work is split.  Values are taken as they are in [0, 1]; NaN and negative ones as
+ * 0, larger ones as 1; a row's sum must be below 16 (it is 1).  Uniforms below 0 and
+ * NaN are taken as 0, from 1 on as the largest below 1.
+ *
+ *   target_probs, draft_probs  float32 [num_rows][vocab]
+ *   tokens, parents  int32 [num_rows]; parents within the sequence, node 0's ignored;
+ *                 NULL: a chain, node i on i - 1.  PKV_TREE_ABSENT, -1 and, flagged
+ *                 (PKV_EFLAG_TREE), any other value outside 0 .. i - 1: never tried.
+ *                 A token outside 0 .. vocab - 1 is flagged (PKV_EFLAG_TOKEN), never tried
+ *   row_starts    int32 [num_seqs + 1], not decreasing, 0 .. num_rows, at most
+ *                 PKV_MAX_TREE_LEN apart (otherwise flagged, PKV_EFLAG_QUERY, and the
+ *                 sequence taken as empty)
+ *   uniforms      float32 [num_rows]
+ *   accepted      int32 [num_seqs][max_accepted] (written): the accepted nodes, node 0
+ *                 first, -1 behind them; at most max_accepted are accepted (the walk
+ *                 ends there, and the next token is drawn from the last one's p)
+ *   accepted_lens int32 [num_seqs] (written);  next_tokens  int32 [num_seqs] (written)
+ *   context_lens, new_context_lens  int32 [num_seqs], both or neither NULL:
+ *                 new = context_lens[b] - the sequence's rows + accepted_lens[b]
+ *                 (a chain's tokens lie at its positions already; a tree's path is moved
+ *                 by pkv_tree_commit, which takes accepted and accepted_lens)
+ * An empty sequence: 0 accepted, next token -1, its context length as it is.  A row
+ * without any mass: next token -1, flagged (PKV_EFLAG_TOKEN).
+ * Nothing written may overlap another argument, but new_context_lens may be context_lens.
+ */
+pkv_status pkv_verify_drafts(int32_t* accepted, int32_t* accepted_lens, int32_t* next_tokens,
+                             int32_t* new_context_lens, const float* target_probs,
+                             const float* draft_probs, const int32_t* tokens,
+                             const int32_t* parents, const int32_t* row_starts,
+                             const float* uniforms, const int32_t* context_lens, int num_seqs,
+                             int num_rows, int vocab, int max_accepted, int32_t* err_flag,
+                             void* stream);
 
 /*
  * Log-sum-exp merge of split-K partials ([inference] combine_result and the

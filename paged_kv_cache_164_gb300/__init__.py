@@ -19,6 +19,10 @@ Calls (same names as the C entry points, without the ``pkv_`` prefix):
   tree_plan(parents, context_lens, block_tables, num_blocks, block_size, max_context_len)
   tree_attention(q, k_cache, v_cache, block_tables, context_lens, max_context_len, tree_mask)
   tree_commit(k_cache, v_cache, block_tables, context_lens, tree_len, accepted, accepted_lens)
+  batch_plan(context_lens, new_lens, block_tables, free_blocks, free_count, num_blocks, block_size,
+             max_tokens)
+  chunk_attention(q, k_cache, v_cache, block_tables, query_starts, context_lens, max_context_len)
+  verify_drafts(target_probs, draft_probs, tokens, row_starts, uniforms, max_accepted)
   check_error(err_flag)
 """
 from __future__ import annotations
@@ -41,7 +45,7 @@ STATUS_NAMES = {0: "PKV_OK", 1: "PKV_ERR_INVALID_ARG", 2: "PKV_ERR_UNSUPPORTED",
                 3: "PKV_ERR_WORKSPACE", 4: "PKV_ERR_CUDA", 5: "PKV_ERR_DEVICE_INDEX",
                 6: "PKV_ERR_DEVICE_TIMEOUT"}
 EFLAG_BLOCK_ID, EFLAG_SLOT, EFLAG_CONTEXT_LEN, EFLAG_TIMEOUT, EFLAG_GROUP = 0x1, 0x2, 0x4, 0x8, 0x10
-EFLAG_POSITION, EFLAG_TREE = 0x20, 0x40
+EFLAG_POSITION, EFLAG_TREE, EFLAG_QUERY, EFLAG_POOL, EFLAG_TOKEN = 0x20, 0x40, 0x80, 0x100, 0x200
 TREE_ABSENT, MAX_TREE_LEN = -2, 1024
 MAX_SPLITS = 1024
 _DTYPES = {torch.float16: 0, torch.bfloat16: 1}
@@ -111,6 +115,12 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                                        sz, i, p, p]
     lib.pkv_tree_commit_within.argtypes = [p, p, p, i, p, i, i, p, p, i, p, i, i, i, i, i, i, p, p]
     lib.pkv_tree_commit.argtypes = [p, p, p, i, p, i, p, p, i, p, i, i, i, i, i, i, p, p]
+    lib.pkv_batch_plan.argtypes = [p, p, p, p, p, p, p, p, p, p, i, p, i, p, i, i, i, i, p, p]
+    lib.pkv_chunk_attention_workspace_size.argtypes = [i, i, i, i, i, i, i]
+    lib.pkv_chunk_attention_workspace_size.restype = sz
+    lib.pkv_chunk_attention.argtypes = [p, p, p, p, p, i, p, p, i, p, p, i, i, i, i, i, i, i, f, f,
+                                        i, p, sz, i, p, p]
+    lib.pkv_verify_drafts.argtypes = [p, p, p, p, p, p, p, p, p, p, p, i, i, i, i, p, p]
     lib.pkv_check_error.argtypes = [p, p, ctypes.POINTER(ctypes.c_int32)]
     lib.pkv_status_string.argtypes = [i]
     lib.pkv_status_string.restype = ctypes.c_char_p
@@ -124,7 +134,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                  "pkv_decode_attention_prefix_shared", "pkv_multi_query_attention",
                  "pkv_norm_rope_append", "pkv_norm_rope_append_fp8", "pkv_tree_plan",
                  "pkv_tree_attention", "pkv_tree_commit", "pkv_tree_commit_within",
-                 "pkv_merge", "pkv_gather", "pkv_selftest_wait_timeout",
+                 "pkv_batch_plan", "pkv_chunk_attention", "pkv_verify_drafts", "pkv_merge", "pkv_gather", "pkv_selftest_wait_timeout",
                  "pkv_check_error", "pkv_max_group_size", "pkv_multi_query_plan"):
         getattr(lib, name).restype = i
     _lib = lib
@@ -1004,6 +1014,205 @@ def tree_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torc
     if r:
         _check(r, "pkv_tree_commit")
     return new_context_lens
+
+
+def _given(t: Optional[torch.Tensor], name: str, dtype, device: int, shape) -> int:
+    """The address of an optional dense argument of a shape (0: not given)."""
+    if t is None:
+        return 0
+    at = _arg(t, name, dtype, device)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return at
+
+
+def batch_plan(context_lens: torch.Tensor, new_lens: torch.Tensor, block_tables: torch.Tensor,
+               free_blocks: torch.Tensor, free_count: torch.Tensor, num_blocks: int,
+               block_size: int, max_tokens: int, keep_lens: Optional[torch.Tensor] = None,
+               shared_pages: Optional[torch.Tensor] = None,
+               query_starts: Optional[torch.Tensor] = None,
+               positions: Optional[torch.Tensor] = None,
+               slot_mapping: Optional[torch.Tensor] = None,
+               new_context_lens: Optional[torch.Tensor] = None,
+               new_free_count: Optional[torch.Tensor] = None,
+               err_flag: Optional[torch.Tensor] = None, stream=None):
+    """The plan of a ragged step: (query_starts, positions, slot_mapping, new_context_lens,
+    new_free_count).
+
+    Sequence b keeps ``keep_lens[b]`` (all, if not given) of its ``context_lens[b]``
+    tokens and receives ``new_lens[b]`` (int32 [B]).  Pages that are no longer needed
+    are pushed onto ``free_blocks`` (int32, the list; ``free_count`` int32 [1] of them
+    are free), but for a sequence's first ``shared_pages[b]``; new ones are popped into
+    ``block_tables`` (int32 [B, pages], updated in place).  query_starts int32 [B + 1],
+    positions int32 [max_tokens], slot_mapping int64 [max_tokens] (places behind the
+    last token: position 0, slot -1).  The lengths and the count may be updated in
+    place: ``new_context_lens=context_lens``, ``new_free_count=free_count``.
+
+    Where pages or token places run out, that sequence and those behind it receive no
+    tokens (``EFLAG_POOL``): their query rows are empty.
+    """
+    lib = load()
+    dev = _cuda_index(context_lens, "context_lens", 1)
+    i32, i64 = torch.int32, torch.int64
+    b, most = context_lens.shape[0], _c_int(max_tokens, "max_tokens")
+    seqs, one, places = (b,), (1,), (most,)
+    if block_tables.dim() != 2 or block_tables.shape[0] != b or free_blocks.dim() != 1 or most < 0:
+        raise ValueError("inconsistent batch-plan shapes")
+    if query_starts is None:
+        query_starts = _new((b + 1,), i32, context_lens.device, stream)
+    if positions is None:
+        positions = _new(places, i32, context_lens.device, stream)
+    if slot_mapping is None:
+        slot_mapping = _new(places, i64, context_lens.device, stream)
+    if new_context_lens is None:
+        new_context_lens = _new(seqs, i32, context_lens.device, stream)
+    if new_free_count is None:
+        new_free_count = _new(one, i32, context_lens.device, stream)
+    r = _run(lib.pkv_batch_plan, dev, (
+        _given(query_starts, "query_starts", i32, dev, (b + 1,)),
+        _given(positions, "positions", i32, dev, places),
+        _given(slot_mapping, "slot_mapping", i64, dev, places),
+        _given(new_context_lens, "new_context_lens", i32, dev, seqs),
+        _given(new_free_count, "new_free_count", i32, dev, one),
+        _arg(context_lens, "context_lens", i32, dev),
+        _given(new_lens, "new_lens", i32, dev, seqs),
+        _given(keep_lens, "keep_lens", i32, dev, seqs),
+        _given(shared_pages, "shared_pages", i32, dev, seqs),
+        _arg(block_tables, "block_tables", i32, dev), block_tables.shape[1],
+        _arg(free_blocks, "free_blocks", i32, dev), free_blocks.shape[0],
+        _given(free_count, "free_count", i32, dev, one), b, most,
+        _c_int(num_blocks, "num_blocks"), _c_int(block_size, "block_size"),
+        0 if err_flag is None else _arg(err_flag, "err_flag", i32, dev),
+        _raw_stream(dev) if stream is None else stream.cuda_stream))
+    if r:
+        _check(r, "pkv_batch_plan")
+    return query_starts, positions, slot_mapping, new_context_lens, new_free_count
+
+
+def chunk_attention_workspace_size(num_seqs: int, num_tokens: int, num_q_heads: int,
+                                   num_kv_heads: int, head_dim: int, block_size: int,
+                                   max_context_len: int) -> int:
+    """Bytes of workspace ``chunk_attention`` needs on the current device."""
+    n = load().pkv_chunk_attention_workspace_size(num_seqs, num_tokens, num_q_heads, num_kv_heads,
+                                                  head_dim, block_size, max_context_len)
+    if n == SIZE_MAX:
+        raise PkvError(1, "pkv_chunk_attention_workspace_size")
+    return int(n)
+
+
+def chunk_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                    block_tables: torch.Tensor, query_starts: torch.Tensor,
+                    context_lens: torch.Tensor, max_context_len: int,
+                    scale: Optional[float] = None, softcap: float = 0.0, window: int = 0,
+                    slopes: Optional[torch.Tensor] = None,
+                    prefix_lens: Optional[torch.Tensor] = None,
+                    out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                    err_flag: Optional[torch.Tensor] = None, stream=None,
+                    layout: str = "nhd") -> torch.Tensor:
+    """Attention of a ragged step's new tokens over the paged cache.
+
+    q [T, H_q, d]: the sequences' new tokens one after another, sequence b's from row
+    query_starts[b] (int32 [B + 1]) on; context_lens counts them (they are appended
+    first).  A token at position m sees the positions up to its own, of those the last
+    ``window`` (0: all), and those below prefix_lens[b] (int32 [B]) that the window
+    leaves, behind its own too.  Scores are capped by ``softcap`` * tanh(z / softcap)
+    (0: not), and get slopes[h] * (t - m) (float32 [H_q]).  Rows outside query_starts
+    are left as they were.  16-bit caches only.
+    """
+    lib = load()
+    dev = _cuda_index(q, "q", 3)
+    t, h_q, d = qshape = q.shape
+    dt, i32 = q.dtype, torch.int32
+    nb, bs, h_kv, d2, code = _caches(k_cache, v_cache, layout, dt)
+    if d2 != d or block_tables.dim() != 2 or context_lens.dim() != 1 or \
+            block_tables.shape[0] != context_lens.shape[0]:
+        raise ValueError("inconsistent chunk attention shapes")
+    b = context_lens.shape[0]
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if out is None:
+        out = _new(qshape, dt, q.device, stream)
+    if workspace is None:  # a given workspace is checked by the library itself
+        with torch.cuda.device(dev):
+            need = chunk_attention_workspace_size(b, t, h_q, h_kv, d, bs, max_context_len)
+        workspace = _new((need,), torch.uint8, q.device, stream)
+    r = _run(lib.pkv_chunk_attention, dev, (
+        _given(out, "out", dt, dev, qshape), _arg(q, "q", dt, dev),
+        _arg(k_cache, "k_cache", dt, dev), _arg(v_cache, "v_cache", dt, dev),
+        _arg(block_tables, "block_tables", i32, dev), block_tables.shape[1],
+        _given(query_starts, "query_starts", i32, dev, (b + 1,)),
+        _arg(context_lens, "context_lens", i32, dev),
+        _c_int(max_context_len, "max_context_len"),
+        _given(prefix_lens, "prefix_lens", i32, dev, (b,)),
+        _given(slopes, "slopes", torch.float32, dev, (h_q,)), b, t, nb, bs, h_q, h_kv, d,
+        float(scale), float(softcap), _c_int(window, "window"),
+        _arg(workspace, "workspace", workspace.dtype, dev), workspace.nbytes, code,
+        0 if err_flag is None else _arg(err_flag, "err_flag", i32, dev),
+        _raw_stream(dev) if stream is None else stream.cuda_stream))
+    if r:
+        _check(r, "pkv_chunk_attention")
+    return out
+
+
+def verify_drafts(target_probs: torch.Tensor, draft_probs: Optional[torch.Tensor],
+                  tokens: torch.Tensor, row_starts: torch.Tensor, uniforms: torch.Tensor,
+                  max_accepted: int, parents: Optional[torch.Tensor] = None,
+                  context_lens: Optional[torch.Tensor] = None,
+                  accepted: Optional[torch.Tensor] = None,
+                  accepted_lens: Optional[torch.Tensor] = None,
+                  next_tokens: Optional[torch.Tensor] = None,
+                  new_context_lens: Optional[torch.Tensor] = None,
+                  err_flag: Optional[torch.Tensor] = None, stream=None):
+    """(accepted, accepted_lens, next_tokens, new_context_lens) of drafted tokens.
+
+    Sequence b's nodes are the rows row_starts[b] .. row_starts[b + 1] - 1 (int32
+    [B + 1]): node 0 the token chosen before, the others drafts (``tokens`` int32 [R]),
+    each on an earlier node (``parents`` int32 [R], within the sequence; None: a
+    chain).  target_probs and draft_probs float32 [R, V]: what the large and the small
+    model say follows a node (draft_probs None: drafts of certainty).  uniforms float32
+    [R]: node i's test, and node 0's the draw of the next token.
+
+    accepted int32 [B, max_accepted]: the accepted nodes, node 0 first, -1 behind them,
+    as ``tree_commit`` takes them with accepted_lens int32 [B]; next_tokens int32 [B].
+    With ``context_lens``, new_context_lens int32 [B] (else None): context - rows +
+    accepted (``batch_plan``'s keep_lens).
+    """
+    lib = load()
+    dev = _cuda_index(target_probs, "target_probs", 2)
+    n, v = target_probs.shape
+    i32, f32 = torch.int32, torch.float32
+    most = _c_int(max_accepted, "max_accepted")
+    if not isinstance(row_starts, torch.Tensor) or row_starts.dim() != 1 or \
+            row_starts.shape[0] < 1 or most < 1:
+        raise ValueError("inconsistent verification shapes")
+    b = row_starts.shape[0] - 1
+    rows, seqs = (n,), (b,)
+    if accepted is None:
+        accepted = _new((b, most), i32, target_probs.device, stream)
+    if accepted_lens is None:
+        accepted_lens = _new(seqs, i32, target_probs.device, stream)
+    if next_tokens is None:
+        next_tokens = _new(seqs, i32, target_probs.device, stream)
+    if context_lens is None:
+        if new_context_lens is not None:
+            raise ValueError("new_context_lens needs context_lens")
+    elif new_context_lens is None:
+        new_context_lens = _new(seqs, i32, target_probs.device, stream)
+    r = _run(lib.pkv_verify_drafts, dev, (
+        _given(accepted, "accepted", i32, dev, (b, most)),
+        _given(accepted_lens, "accepted_lens", i32, dev, seqs),
+        _given(next_tokens, "next_tokens", i32, dev, seqs),
+        _given(new_context_lens, "new_context_lens", i32, dev, seqs),
+        _arg(target_probs, "target_probs", f32, dev),
+        _given(draft_probs, "draft_probs", f32, dev, (n, v)),
+        _given(tokens, "tokens", i32, dev, rows), _given(parents, "parents", i32, dev, rows),
+        _arg(row_starts, "row_starts", i32, dev), _given(uniforms, "uniforms", f32, dev, rows),
+        _given(context_lens, "context_lens", i32, dev, seqs), b, n, v, most,
+        0 if err_flag is None else _arg(err_flag, "err_flag", i32, dev),
+        _raw_stream(dev) if stream is None else stream.cuda_stream))
+    if r:
+        _check(r, "pkv_verify_drafts")
+    return accepted, accepted_lens, next_tokens, new_context_lens
 
 
 def check_error(err_flag: torch.Tensor, stream=None) -> int:
