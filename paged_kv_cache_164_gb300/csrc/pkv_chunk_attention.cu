@@ -1,17 +1,48 @@
-// Attention of a ragged step's new tokens over a paged KV cache.
+// Attention of a ragged step's new tokens over a paged KV cache (tcgen05).
 //
 // The math: token i of sequence b, which brings t_b tokens to n_b, has position
 // m = n_b - t_b + i and sees lo <= t < hi,
 //     lo = max(0, m + 1 - window), hi = max(m + 1, min(prefix_b, n_b));
 //     z_t = scale <q_i, K_t>, capped by softcap tanh(z / softcap), plus slope_h (t - m);
 //     out_i = softmax(z) V over those t.
+// The (token, query head) rows of a KV head form a dense matrix that meets every
+// position once: the two products run on the tensor cores (fp32 accumulators in tensor
+// memory), with the online softmax between them: running reference m, sum l and
+// accumulator O per row, one division at the end.
 //
-// The simplest form: a warp takes one (token, query head), 32 positions at a time, a
-// lane a position for the scores and D / 32 columns of V for the sum.
+// Tiles: 128 rows x 128 positions.  Two softmax warpgroups, a thread a row, each with
+// an S and an O of its own in tensor memory (all 512 columns at head dim 128):
+//   S_w = Q_w K^T   tcgen05.mma 128 x 128 x D, Q and K from shared memory
+//   softmax         a thread reads its row of S, writes P over it
+//   O_w += P_w V    P from tensor memory, V from shared memory
+// One warp issues everything in the order PV_0(j) S_0(j+1) PV_1(j) S_1(j+1), so that a
+// warpgroup is at its softmax while the other's two products run.  The tensor core
+// runs them in that order: S over a P comes after the product that reads it, and where
+// S(j) is complete so is PV(j-1).
+// A unit (row block of a KV head, pkv_chunk_line.cuh) of more than 128 rows gives each
+// warpgroup 128 of its rows, which meet the same tiles; a smaller one (single tokens,
+// drafted tails) gives both the same rows and every other tile, and they meet at the
+// end.  Four warps stream K and V by TMA through the block table into a ring of tiles.
+//
+// A softmax weight meets V as one 16-bit term in the larger units, where the products
+// are what takes the time (a second term costs half as much again), and as two in the
+// smaller ones, which wait for memory: a single token's output is as precise as
+// pkv_decode_attention's, a chunk's row has its weights' rounding beside its own.
+//
+// Work: the units' places lie on one line, cut into equal segments; a persistent CTA an
+// SM takes one of them, or one in each of a few rounds where the line is long (so that
+// the CTAs are near one another on the line, and what they read of K and V together
+// stays in L2).  A unit inside a segment is written to the output at once; one that is
+// cut leaves a partial (normalised O and its log-sum-exp) per segment, which
+// chunk_merge_kernel joins.
+//
+// Every wait is bounded, as in the decode kernels.
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <cmath>
 
+#include "pkv_chunk_line.cuh"
 #include "pkv_common.cuh"
 #include "pkv_device.cuh"
 
@@ -20,7 +51,6 @@ namespace pkv {
 struct ChunkParams {
     void* out;
     const void* q;
-    const void* k_cache;
     const void* v_cache;
     const int32_t* block_tables;
     const int32_t* query_starts;
@@ -28,112 +58,998 @@ struct ChunkParams {
     const int32_t* prefix_lens;
     const float* slopes;
     int32_t* err_flag;
+    ChunkRecord* records;  // [rounds * ctas]
+    int32_t* has;          // [chunk_partials]: whether a stretch of tiles left a partial
+    float* partial_o;      // [chunk_partials][2 kChunkRows][D]
+    float* partial_lse;    // [chunk_partials][2 kChunkRows], base 2
+    ChunkShape shape;
+    int rounds;            // at most
     int max_blocks_per_seq;
     int num_seqs;
     int num_tokens;
     int num_blocks;
     int block_size;
     int num_q_heads;
-    int num_kv_heads;
-    int group;
     int cap;
-    int window;
     bool hnd;
-    float scale;
+    float scale_log2;      // |scale| * log2(e) (of 1 where scale is 0)
+    float scale_sign;      // 1, -1 or 0
     float softcap;
+    float tanh_log2;       // 2 log2(e) scale / softcap
 };
 
-template <typename T, int D>
-__global__ void __launch_bounds__(128) chunk_attention_kernel(const ChunkParams p) {
-    constexpr int E = D / 32;
-    __shared__ float s_q[4][D];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    ptx::launch_dependents();
-    ptx::grid_dependency_wait();
-    const int token = blockIdx.x, h = blockIdx.y * 4 + warp;
-    if (h >= p.num_q_heads) return;
-    if (token == 0 && h == 0)
-        for (int i = lane; i <= p.num_seqs; i += 32) {
-            const int here = p.query_starts[i];
-            if (here < 0 || here > p.num_tokens || (i > 0 && here < p.query_starts[i - 1]))
-                flag_error(p.err_flag, PKV_EFLAG_QUERY);
-        }
-    int lo_b = 0, hi_b = p.num_seqs;  // the first sequence that ends behind the token
-    while (lo_b < hi_b) {
-        const int mid = (lo_b + hi_b) / 2;
-        if (p.query_starts[mid + 1] > token)
-            hi_b = mid;
-        else
-            lo_b = mid + 1;
-    }
-    const int b = lo_b;
-    if (b == p.num_seqs || p.query_starts[b] > token) return;
-    const int first = max(0, p.query_starts[b]);
-    const int t_b = min(p.num_tokens, p.query_starts[b + 1]) - first;
-    const int n_raw = p.context_lens[b], n = clamped_len(n_raw, p.cap);
-    if (lane == 0 && h == 0 && (n_raw != n || n < t_b)) flag_error(p.err_flag, PKV_EFLAG_CONTEXT_LEN);
-    const int m = n - t_b + token - first;
-    const int prefix = p.prefix_lens != nullptr ? min(p.prefix_lens[b], n) : 0;
-    const int hi = m < 0 ? 0 : max(m + 1, prefix);
-    const int lo = p.window > 0 ? max(0, m + 1 - p.window) : 0;
-    const T* q = static_cast<const T*>(p.q) + ((int64_t)token * p.num_q_heads + h) * D;
-    for (int e = lane; e < D; e += 32) s_q[warp][e] = (float)q[e];
-    __syncwarp();
-    const int g = h / p.group;
-    const float slope = p.slopes != nullptr ? p.slopes[h] : 0.f;
-    float top = -INFINITY, sum = 0.f, acc[E] = {};
-    auto row = [&](const void* cache, int t) -> const T* {
-        const int blk = p.block_tables[(int64_t)b * p.max_blocks_per_seq + t / p.block_size];
-        if (blk < 0 || blk >= p.num_blocks) return nullptr;
-        const int off = t % p.block_size;
-        return static_cast<const T*>(cache) +
-               (p.hnd ? ((int64_t)blk * p.num_kv_heads + g) * p.block_size + off
-                      : ((int64_t)blk * p.block_size + off) * p.num_kv_heads + g) * D;
-    };
-    for (int t0 = lo; t0 < hi; t0 += 32) {
-        const int t = t0 + lane;
-        float z = -INFINITY;
-        const T* k = t < hi ? row(p.k_cache, t) : nullptr;
-        if (t < hi && k == nullptr) flag_error(p.err_flag, PKV_EFLAG_BLOCK_ID);
-        if (k != nullptr) {
-            z = 0.f;
-            for (int e = 0; e < D; e += 2) {
-                const float2 x = pair_to_float2(*reinterpret_cast<const uint32_t*>(k + e), T());
-                z = fmaf(s_q[warp][e], x.x, z);
-                z = fmaf(s_q[warp][e + 1], x.y, z);
-            }
-            z *= p.scale;
-            if (p.softcap > 0.f) z = p.softcap * tanhf(z / p.softcap);
-            z += slope * (float)(t - m);
-        }
-        float mx = z;
-        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        const float next = fmaxf(top, mx);
-        const float ref = next == -INFINITY ? 0.f : next;
-        const float alpha = expf(top - ref), w = expf(z - ref);
-        top = next;
-        float ws = w;
-        for (int o = 16; o > 0; o >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, o);
-        sum = sum * alpha + ws;
-        for (int e = 0; e < E; ++e) acc[e] *= alpha;
-        for (int j = 0; j < 32; ++j) {
-            const float wj = __shfl_sync(0xffffffffu, w, j);
-            const T* v = t0 + j < hi ? row(p.v_cache, t0 + j) : nullptr;
-            if (v == nullptr) continue;
-            for (int e = 0; e < E; ++e) {
-                const float x = (float)v[e * 32 + lane];
-                // (a weight that underflows does not make an infinity that it sees a NaN)
-                acc[e] = isinf(x) ? acc[e] + x : fmaf(wj, x, acc[e]);
-            }
-        }
-    }
-    T* out = static_cast<T*>(p.out) + ((int64_t)token * p.num_q_heads + h) * D;
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    for (int e = 0; e < E; ++e) out[e * 32 + lane] = from_float(acc[e] * inv, T());
+constexpr int kChunkSoftmaxWarps = 8;                 // two warpgroups
+constexpr int kChunkTmaWarp = kChunkSoftmaxWarps;     // four producers
+constexpr int kChunkTmaWarps = 4;
+constexpr int kChunkMmaWarp = kChunkTmaWarp + kChunkTmaWarps;
+constexpr int kChunkThreads = (kChunkSoftmaxWarps + 8) * 32;  // the last three only fill up
+// Registers: the other warpgroups hand over what they do not need, so that a softmax
+// thread's row of S stays in registers.
+constexpr int kChunkLaunchRegs = 128, kChunkSoftmaxRegs = 184, kChunkOtherRegs = 72;
+static_assert(2 * kChunkSoftmaxRegs + 2 * kChunkOtherRegs <= 4 * kChunkLaunchRegs, "register shares");
+// Scores may exceed a row's reference by this much (base 2) before it moves.
+constexpr float kChunkLazyLog2 = 8.f;
+constexpr int kChunkBoxes = kChunkTile / kStageTokens;  // TMA boxes along a tile
+constexpr int kChunkMaxRounds = 4;
+// Marks of units with a V that is not finite, a ring of them: the warpgroups are at
+// most a unit apart (each needs the other's tiles released), and the ring is four.
+constexpr int kChunkMarks = 4;
+// A segment has at least this many places (a tile and what its unit costs besides), and
+// more rounds are taken only where theirs have this many.
+constexpr int kChunkLeastSegment = 512;
+constexpr int kChunkRoundSegment = 12288;
+
+template <int D>
+struct ChunkTileCfg {
+    static constexpr int kRegions = D / 64;                      // 128-byte column blocks
+    static constexpr int kRegionBytes = kChunkTile * 128;        // of a tile, and of Q
+    static constexpr int kTileBytes = kRegions * kRegionBytes;   // K or V of a tile; Q
+    static constexpr int kSlots = D == 128 ? 5 : 10;
+    static constexpr int kXchBytes = 2 * kChunkRows * 8;         // (m, l) of each half and row
+    // full[slots], empty[slots], s_full[2], p_ready[2], o_done[2], q_ready[2], met, o_free, drain
+    static constexpr int kBarriers = 2 * kSlots + 11;
+    static constexpr int kWords = 64;
+    static constexpr int kSmemBytes =
+        (2 + kSlots) * kTileBytes + kXchBytes + kBarriers * 8 + kWords * 4 + kChunkMaxRounds * 48;
+    static constexpr uint32_t kColO = 2 * kChunkTile;  // S of each warpgroup, then O
+    static_assert(kColO + 2 * D <= 512, "tensor memory layout");
+    static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
+};
+
+// Where K or V of tile j of a stretch of nt lies in the ring, counted from the stretch's
+// first place: the order in which the issuer takes them.  Both warpgroups on every tile:
+// K0 V0 K1 V1 ..; every other tile (split): K0 K1 V0 K2 V1 K3 ...
+__device__ __forceinline__ int chunk_place(bool split, bool is_v, int j, int nt) {
+    if (!split) return 2 * j + (is_v ? 1 : 0);
+    return is_v ? min(j + 2, nt) + j : (j < 2 ? j : 2 * j - 1);
 }
 
-// Sizes that the workspace and the launch share.
+// A segment's start, as one thread found it for all.
+struct ChunkStart {
+    int64_t at, end;
+    int b, g, rb, pos;
+    int pad[4];
+};
+static_assert(sizeof(ChunkStart) == 48, "starts in shared memory");
+
+__device__ __forceinline__ ChunkSeq chunk_load(const ChunkParams& p, int b) {
+    const int from = __ldg(p.query_starts + b), to = __ldg(p.query_starts + b + 1);
+    const int n = __ldg(p.context_lens + b);
+    const int prefix = p.prefix_lens != nullptr ? __ldg(p.prefix_lens + b) : 0;
+    ChunkSeq s;
+    s.first = clamped_len(from, p.num_tokens);
+    s.tokens = max(0, clamped_len(to, p.num_tokens) - s.first);
+    s.n = clamped_len(n, p.cap);
+    s.prefix = clamped_len(prefix, s.n);
+    return s;
+}
+
+__device__ __forceinline__ int64_t warp_scan64(int64_t x) {  // inclusive
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, x, o);
+        if ((threadIdx.x & 31) >= o) x += v;
+    }
+    return x;
+}
+
+template <typename T, int D, bool MOD>
+__global__ void __launch_bounds__(kChunkThreads, 1)
+chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_v, const ChunkParams p) {
+    using Cfg = ChunkTileCfg<D>;
+    constexpr int R = Cfg::kRegions;
+    constexpr int NS = Cfg::kSlots;
+    constexpr int TR = kChunkRows;
+    constexpr int TT = kChunkTile;
+
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t* sq = smem;  // two Q tiles [region][128 rows][128 B], swizzled
+    uint8_t* ring = sq + 2 * Cfg::kTileBytes;
+    float2* xch = reinterpret_cast<float2*>(ring + NS * Cfg::kTileBytes);
+    uint64_t* full_bar = reinterpret_cast<uint64_t*>(ring + NS * Cfg::kTileBytes + Cfg::kXchBytes);
+    uint64_t* empty_bar = full_bar + NS;
+    uint64_t* s_full = empty_bar + NS;  // [warpgroup]
+    uint64_t* p_ready = s_full + 2;     // [warpgroup]
+    uint64_t* o_done = p_ready + 2;     // [warpgroup]: a unit's last product is complete
+    uint64_t* q_ready = o_done + 2;     // [warpgroup]
+    uint64_t* met = q_ready + 2;        // both are through a split unit
+    uint64_t* o_free = met + 1;         // both have read O_0, O_1 and the exchange of one
+    uint64_t* drain = o_free + 1;
+    int* words = reinterpret_cast<int*>(full_bar + Cfg::kBarriers);
+    volatile int* abort_flag = words;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(words + 1);
+    volatile int* s_bad = words + 2;    // [kChunkMarks]: 1 + the unit (its place: the
+                                        // remainder) with a bad V
+    int* s_segments = words + 6;
+    int64_t* s_line = reinterpret_cast<int64_t*>(words + 8);
+    int64_t* s_scan = reinterpret_cast<int64_t*>(words + 10);  // [16]
+    ChunkStart* s_start = reinterpret_cast<ChunkStart*>(words + Cfg::kWords);
+
+    const int tid = threadIdx.x;
+    const int warp = tid >> 5;
+    const int lane = tid & 31;
+    const int bs = p.block_size;
+    const int bs_shift = __ffs(bs) - 1;
+
+    ptx::launch_dependents();
+    if (tid == 0) {
+        for (int i = 0; i < NS; ++i) {
+            ptx::mbar_init(ptx::smem_addr(&full_bar[i]), kChunkTmaWarps);
+            ptx::mbar_init(ptx::smem_addr(&empty_bar[i]), 1);
+        }
+        for (int w = 0; w < 2; ++w) {
+            ptx::mbar_init(ptx::smem_addr(&s_full[w]), 1);
+            ptx::mbar_init(ptx::smem_addr(&p_ready[w]), TR);
+            ptx::mbar_init(ptx::smem_addr(&o_done[w]), 1);
+            ptx::mbar_init(ptx::smem_addr(&q_ready[w]), TR);
+        }
+        ptx::mbar_init(ptx::smem_addr(met), 2 * TR);
+        ptx::mbar_init(ptx::smem_addr(o_free), 2 * TR);
+        ptx::mbar_init(ptx::smem_addr(drain), 1);
+        *abort_flag = 0;
+        for (int i = 0; i < kChunkMarks; ++i) s_bad[i] = 0;
+        ptx::fence_barrier_init();
+        ptx::prefetch_tensormap(&tm_k);
+        ptx::prefetch_tensormap(&tm_v);
+    }
+    if (warp == kChunkMmaWarp) {
+        ptx::tmem_alloc(ptx::smem_addr(tmem_slot), 512);
+        ptx::tmem_relinquish_alloc_permit();
+    }
+#ifdef PKV_DEBUG
+    poison_smem(ring, NS * Cfg::kTileBytes, tid, kChunkThreads);
+#endif
+    ptx::grid_dependency_wait();
+
+    auto load = [&](int b) { return chunk_load(p, b); };
+
+    // The line, and where on it this CTA's segments start: a thread sums the places of a
+    // run of sequences, a scan puts the runs in order, and the thread whose run holds a
+    // segment's first place stands there for all.  Up to 32 sequences a warp does it by
+    // itself, a lane a sequence.
+    {
+        const bool few = p.num_seqs <= 32;
+        const int runs = few ? 32 : kChunkThreads;
+        const int per = (p.num_seqs + runs - 1) / runs;
+        const int b_lo = min(p.num_seqs, tid * per);
+        const int b_hi = tid < runs ? min(p.num_seqs, b_lo + per) : b_lo;
+        int64_t mine = 0;
+        for (int b = b_lo; b < b_hi; ++b) {
+            mine += chunk_places(load(b), p.shape);
+            if (blockIdx.x == 0) {
+                const int from = __ldg(p.query_starts + b), to = __ldg(p.query_starts + b + 1);
+                if (from < 0 || to < from || to > p.num_tokens)
+                    flag_error(p.err_flag, PKV_EFLAG_QUERY);
+            }
+        }
+        int64_t before = 0, line = 0;
+        if (!few || warp == 0) {
+            const int64_t incl = warp_scan64(mine);
+            before = incl - mine;
+            line = __shfl_sync(0xffffffffu, incl, 31);
+        }
+        if (!few) {
+            if (lane == 31) s_scan[warp] = line;
+            __syncthreads();
+            line = 0;
+            for (int w = 0; w < kChunkThreads / 32; ++w) {
+                if (w < warp) before += s_scan[w];
+                line += s_scan[w];
+            }
+        }
+        if (!few || warp == 0) {
+            const int64_t most = (line + kChunkLeastSegment - 1) / kChunkLeastSegment;
+            const int ctas = (int)min((int64_t)gridDim.x, most);
+            const int64_t long_ones =
+                ctas > 0 ? line / ((int64_t)ctas * kChunkRoundSegment) : 0;
+            const int rounds = (int)max((int64_t)1, min((int64_t)p.rounds, long_ones));
+            const int segments = rounds * ctas;
+            if (tid == 0) {
+                *s_line = line;
+                *s_segments = segments;
+            }
+            for (int r = 0; r < rounds && (int)blockIdx.x < ctas; ++r) {
+                const int seg = r * ctas + blockIdx.x;
+                const int64_t at = chunk_segment_start(line, segments, seg);
+                if (at < before || at >= before + mine) continue;
+                int64_t first = before;
+                int b = b_lo;
+                ChunkSeq s;
+                while (true) {
+                    s = load(b);
+                    const int64_t places = chunk_places(s, p.shape);
+                    if (at < first + places) break;
+                    first += places;
+                    ++b;
+                }
+                ChunkWalk w;
+                w.enter(s, p.shape, b, at - first);
+                s_start[r].at = at;
+                s_start[r].end = chunk_segment_start(line, segments, seg + 1);
+                s_start[r].b = w.b;
+                s_start[r].g = w.g;
+                s_start[r].rb = w.rb;
+                s_start[r].pos = w.pos;
+            }
+        }
+        ptx::tc_fence_before_sync();
+        __syncthreads();
+        ptx::tc_fence_after_sync();
+    }
+    const int64_t line = *s_line;
+    const int segments = *s_segments;
+    const int ctas = (int)min((int64_t)gridDim.x,
+                              (line + kChunkLeastSegment - 1) / kChunkLeastSegment);
+    const int rounds = (int)blockIdx.x < ctas ? segments / ctas : 0;
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t ring_addr = ptx::smem_addr(ring);
+    const uint32_t q_addr = ptx::smem_addr(sq);
+    if (p.records != nullptr)  // segments that the line has not
+        for (int s = segments + blockIdx.x * kChunkThreads + tid; s < p.rounds * (int)gridDim.x;
+             s += gridDim.x * kChunkThreads)
+            p.records[s].first = -1;
+
+    ChunkWalk walk;
+    int round = 0;
+    walk.at = walk.end = 0;
+    // The next unit's stretch, of this round or the next.
+    auto next_any = [&](ChunkStretch& t) {
+        while (!walk.next_any(p.shape, load, t)) {
+            if (round == rounds) return false;
+            const ChunkStart& s = s_start[round++];
+            walk.at = s.at;
+            walk.end = s.end;
+            walk.b = s.b;
+            walk.g = s.g;
+            walk.rb = s.rb;
+            walk.pos = s.pos;
+            walk.seq = load(s.b);
+        }
+        t.segment = (round - 1) * ctas + blockIdx.x;
+        return true;
+    };
+    auto next = [&](ChunkStretch& t) {
+        do {
+            if (!next_any(t)) return false;
+        } while (t.tiles == 0);
+        return true;
+    };
+    const int group = p.shape.group;
+
+    if (warp >= kChunkSoftmaxWarps) {
+        ptx::reg_dec<kChunkOtherRegs>();
+        ChunkStretch t;
+        if (warp < kChunkMmaWarp) {
+            // ------------------------------------------------------------ producers
+            // A warp loads a quarter of every tile; a lane issues one box (16 positions x
+            // 64 dims).
+            constexpr int kMine = kChunkBoxes * R / kChunkTmaWarps;
+            const int box = (warp - kChunkTmaWarp) * kMine + lane;
+            const int bx = box / R, rr = box % R;
+            const bool loads = lane < kMine;
+            const uint64_t keep = ptx::l2_policy_evict_last();
+            const uint64_t once = ptx::l2_policy_evict_first();
+            int place = 0;       // of the ring, since the start
+            uint32_t filled = 0; // slots with a copy of this warp's that may be in flight,
+            uint32_t parity = 0; // and its phase's parity
+            bool ok = true;
+            while (ok && next_any(t)) {
+                if (p.records != nullptr && warp == kChunkTmaWarp && lane == 0) {
+                    // what the join reads: whether this stretch leaves a partial, and, once
+                    // a segment, the unit whose partials it joins: one that was cut by the
+                    // segment's start and ends here
+                    const bool cut = t.tiles < t.unit_tiles;
+                    p.has[chunk_partial(t.segment, t.begins)] = cut && t.tiles > 0;
+                    if (t.at == s_start[round - 1].at) {
+                        const bool joins = !t.begins && cut && t.skipped + t.tiles == t.unit_tiles;
+                        p.records[t.segment] = ChunkRecord{
+                            joins ? chunk_segment_of(line, segments, t.unit_at) : -1, t.b, t.g,
+                            t.rb};
+                    }
+                }
+                if (t.tiles == 0) continue;
+                const int nt = t.tiles;
+                const bool split = t.tokens * group <= TR;
+                const int32_t* table = p.block_tables + (int64_t)t.b * p.max_blocks_per_seq;
+                const uint64_t policy = t.seq.tokens > p.shape.block_tokens ? keep : once;
+                if (warp == kChunkTmaWarp && lane == 0 && t.skipped == 0 && t.g == 0 && t.rb == 0) {
+                    const int n_raw = __ldg(p.context_lens + t.b);
+                    if (n_raw != t.seq.n || n_raw < t.seq.tokens)
+                        flag_error(p.err_flag, PKV_EFLAG_CONTEXT_LEN);
+                }
+                // the block of this lane's box of tile j, as the table has it (-1: none)
+                auto box_block = [&](int j) {
+                    const int at = (t.tile + j) * TT + bx * kStageTokens;
+                    return loads && j < nt && at + kStageTokens > t.lo && at < t.hi
+                               ? __ldg(table + (at >> bs_shift))
+                               : -1;
+                };
+                auto fill = [&](bool is_v, int j, int blk) {
+                    const int at = (t.tile + j) * TT + bx * kStageTokens;
+                    if (blk < 0 || blk >= p.num_blocks) {
+                        if (!is_v && loads && at + kStageTokens > t.lo && at < t.hi)
+                            flag_error(p.err_flag, PKV_EFLAG_BLOCK_ID);
+                        blk = -1;
+                    }
+                    const int slot = place % NS, phase = place / NS;
+                    ++place;
+                    if (phase > 0 && !warp_wait_phase(ptx::smem_addr(&empty_bar[slot]),
+                                                      (phase - 1) & 1, abort_flag, p.err_flag))
+                        return false;
+                    const uint32_t fb = ptx::smem_addr(&full_bar[slot]);
+                    const uint32_t dst = ring_addr + slot * Cfg::kTileBytes +
+                                         rr * Cfg::kRegionBytes + bx * kStageTokens * 128;
+#ifdef PKV_DEBUG
+                    if (phase > 0) {
+                        ptx::tc_fence_after_sync();
+                        for (int i = 0; i < kMine; ++i) {
+                            const uint32_t d = __shfl_sync(0xffffffffu, dst, i);
+                            poison_smem(ring + (d - ring_addr), kStageTokens * 128, lane, 32);
+                        }
+                        __syncwarp();
+                    }
+#endif
+                    const uint32_t boxes = __ballot_sync(0xffffffffu, blk >= 0);
+                    if (lane == 0) {
+                        if (boxes == 0)
+                            ptx::mbar_arrive(fb);  // every position of the quarter is masked
+                        else
+                            ptx::mbar_arrive_expect_tx(fb, __popc(boxes) * kStageTokens * 128);
+                    }
+                    __syncwarp();
+                    if (blk >= 0)
+                        load_kv_box(dst, is_v ? &tm_v : &tm_k, fb, rr * 64, t.g, at & (bs - 1),
+                                    blk, p.hnd, policy);
+                    filled |= 1u << slot;
+                    parity = (parity & ~(1u << slot)) | ((uint32_t)(phase & 1) << slot);
+                    return true;
+                };
+                // table entries are read two tiles ahead
+                int b0 = box_block(0), b1 = box_block(1), b2 = box_block(2);
+                if (split) ok = fill(false, 0, b0) && (nt < 2 || fill(false, 1, b1));
+                for (int j = 0; j < nt && ok; ++j) {
+                    const int far = box_block(j + 3);
+                    if (split)
+                        ok = fill(true, j, b0) && (j + 2 >= nt || fill(false, j + 2, b2));
+                    else
+                        ok = fill(false, j, b0) && fill(true, j, b0);
+                    b0 = b1;
+                    b1 = b2;
+                    b2 = far;
+                }
+            }
+            if (lane == 0 && *abort_flag) {
+                // wait (bounded) for this warp's copies in flight before leaving
+                const uint64_t t0 = ptx::globaltimer();
+                for (int i = 0; i < NS; ++i) {
+                    if (!((filled >> i) & 1u)) continue;
+                    while (!ptx::mbar_try_wait(ptx::smem_addr(&full_bar[i]), (parity >> i) & 1u) &&
+                           ptx::globaltimer() - t0 < kWaitLimitNs) {
+                    }
+                }
+            }
+        } else if (warp == kChunkMmaWarp) {
+            // ------------------------------------------------------------ MMA issuer
+            // The whole warp walks the steps, so that addresses and descriptors are
+            // uniform values; one elected lane issues.
+            constexpr uint32_t fmt = F16Format<T>::value;
+            constexpr uint32_t idesc_s = mma_idesc(fmt, TR, TT, false);
+            constexpr uint32_t idesc_o = mma_idesc(fmt, TR, D, true);
+            // descriptors of the first slots: a byte offset adds its sixteenth
+            const uint64_t qdesc = ptx::smem_desc_sw128(q_addr, 16, 1024);
+            const uint64_t kdesc = ptx::smem_desc_sw128(ring_addr, 16, 1024);
+            const uint64_t vdesc = ptx::smem_desc_sw128(ring_addr, Cfg::kRegionBytes, 1024);
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            int place0 = 0;
+            int step[2] = {0, 0};   // S tiles of each warpgroup so far
+            int unit[2] = {0, 0};   // units with tiles for it
+            bool ok = true;
+            while (ok && next(t)) {
+                const int nt = __shfl_sync(0xffffffffu, t.tiles, 0);
+                const bool split = __shfl_sync(0xffffffffu, t.tokens * group <= TR ? 1 : 0, 0);
+                auto wait = [&](uint64_t* bar, int parity) {
+                    return warp_wait_phase(ptx::smem_addr(bar), parity & 1, abort_flag,
+                                           p.err_flag);
+                };
+                // S of warpgroup w for tile j; `last`: it is the tile's last reader
+                auto issue_s = [&](int w, int j, bool last) {
+                    const int at = place0 + chunk_place(split, false, j, nt);
+                    const int slot = at % NS;
+                    if (!wait(&full_bar[slot], at / NS)) return false;
+                    ptx::tc_fence_after_sync();
+                    const uint64_t kd = kdesc + (uint32_t)(slot * (Cfg::kTileBytes / 16));
+                    const uint64_t qd = qdesc + (uint32_t)(w * (Cfg::kTileBytes / 16));
+                    if (ptx::elect_one()) {
+#pragma unroll
+                        for (int ks = 0; ks < D / 16; ++ks)
+                            ptx::tc_mma_f16(
+                                tm + w * TT, qd + (ks / 4) * (Cfg::kRegionBytes / 16) + (ks % 4) * 2,
+                                kd + (ks / 4) * (Cfg::kRegionBytes / 16) + (ks % 4) * 2, idesc_s,
+                                ks > 0 ? 1u : 0u);
+                        ptx::tc_commit(ptx::smem_addr(&s_full[w]));
+                        if (last) ptx::tc_commit(ptx::smem_addr(&empty_bar[slot]));
+                    }
+                    __syncwarp();
+                    return true;
+                };
+                auto issue_pv = [&](int w, int j, bool first, bool ends, bool last) {
+                    const int at = place0 + chunk_place(split, true, j, nt);
+                    const int slot = at % NS;
+                    if (!wait(&full_bar[slot], at / NS) || !wait(&p_ready[w], step[w]))
+                        return false;
+                    ++step[w];
+                    ptx::tc_fence_after_sync();
+                    const uint64_t vd = vdesc + (uint32_t)(slot * (Cfg::kTileBytes / 16));
+                    const uint32_t pt = tm + w * TT;
+                    const uint32_t acc = tm + Cfg::kColO + w * D;
+                    if (ptx::elect_one()) {
+#pragma unroll
+                        for (int kt = 0; kt < TT / 16; ++kt) {
+                            const uint64_t v = vd + (uint32_t)(kt * 16 * 128 / 16);
+                            ptx::tc_mma_f16_ts(acc, pt + kt * 8, v, idesc_o,
+                                               (!first || kt > 0) ? 1u : 0u);
+                            // (a split unit's weights have a second term)
+                            if (split) ptx::tc_mma_f16_ts(acc, pt + TT / 2 + kt * 8, v, idesc_o, 1u);
+                        }
+                        if (ends) ptx::tc_commit(ptx::smem_addr(&o_done[w]));
+                        if (last) ptx::tc_commit(ptx::smem_addr(&empty_bar[slot]));
+                    }
+                    __syncwarp();
+                    return true;
+                };
+                if (split) {
+                    ok = wait(&q_ready[0], unit[0]) && issue_s(0, 0, true) &&
+                         (nt < 2 || (wait(&q_ready[1], unit[1]) && issue_s(1, 1, true)));
+                    for (int j = 0; j < nt && ok; ++j)
+                        ok = issue_pv(j & 1, j, j < 2, j + 2 >= nt, true) &&
+                             (j + 2 >= nt || issue_s(j & 1, j + 2, true));
+                    ++unit[0];
+                    unit[1] += nt > 1;
+                } else {
+                    ok = wait(&q_ready[0], unit[0]) && issue_s(0, 0, false) &&
+                         wait(&q_ready[1], unit[1]) && issue_s(1, 0, true);
+                    for (int j = 0; j < nt && ok; ++j) {
+                        const bool more = j + 1 < nt;
+                        ok = issue_pv(0, j, j == 0, !more, false) &&
+                             (!more || issue_s(0, j + 1, false)) &&
+                             issue_pv(1, j, j == 0, !more, true) &&
+                             (!more || issue_s(1, j + 1, true));
+                    }
+                    ++unit[0];
+                    ++unit[1];
+                }
+                place0 += 2 * nt;
+            }
+            // every product has completed before the tensor memory is released
+            if (ptx::elect_one()) ptx::tc_commit(ptx::smem_addr(drain));
+            __syncwarp();
+            const uint64_t t0 = ptx::globaltimer();
+            while (!ptx::mbar_try_wait(ptx::smem_addr(drain), 0) &&
+                   ptx::globaltimer() - t0 < kWaitLimitNs) {
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ softmax rows
+        ptx::reg_inc<kChunkSoftmaxRegs>();
+        const int wg = warp / 4;                  // warpgroup
+        const int srow = 32 * (warp % 4) + lane;  // row of the tile = tensor-memory lane
+        const uint32_t lane_base = (uint32_t)(32 * (warp % 4)) << 16;
+        const uint32_t s_col = tmem + lane_base + wg * TT;
+        const uint32_t o_col = tmem + lane_base + Cfg::kColO;
+        int place0 = 0, nunit = 0;
+        int step = 0;                     // this warpgroup's tiles so far
+        int own = 0;                      // units with tiles for it
+        int splits = 0;                   // split units so far
+        bool free_due = false;            // O and the exchange of the last one may be read
+        bool ok = true;
+
+        auto is_split = [&](const ChunkStretch& t) { return t.tokens * group <= TR; };
+        auto tiles_of = [&](const ChunkStretch& t) {
+            return is_split(t) ? (t.tiles + 1 - wg) / 2 : t.tiles;
+        };
+        // this thread's row of a unit: (token of the row block, query head), or a token
+        // of -1 past its rows
+        auto row_of = [&](const ChunkStretch& t, int& head) {
+            const int r = is_split(t) ? srow : wg * TR + srow;
+            const int token = r / group;
+            head = t.g * group + r - token * group;
+            return r < t.tokens * group ? token : -1;
+        };
+        // its row of Q into this warpgroup's tile
+        auto load_q = [&](const ChunkStretch& t) {
+            int head;
+            const int token = row_of(t, head);
+            const uint4* src = reinterpret_cast<const uint4*>(
+                static_cast<const T*>(p.q) +
+                ((int64_t)(t.seq.first + t.token0 + max(token, 0)) * p.num_q_heads + head) * D);
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c)
+                ptx::cp_async_16(q_addr + wg * Cfg::kTileBytes + (c / 8) * Cfg::kRegionBytes +
+                                     srow * 128 + (((c % 8) ^ (srow & 7)) << 4),
+                                 token >= 0 ? src + c : src, token >= 0);
+        };
+        auto q_loaded = [&] {
+            ptx::cp_async_wait_all();
+            ptx::fence_proxy_async_smem();
+            ptx::mbar_arrive(ptx::smem_addr(&q_ready[wg]));
+        };
+
+        ChunkStretch t, ahead;
+        bool have = next(t);
+        if (have && tiles_of(t) > 0) {
+            load_q(t);
+            q_loaded();
+        }
+        while (have && ok) {
+            const bool split = is_split(t);
+            const int nt = t.tiles, mine = tiles_of(t);
+            int head;
+            const int token = row_of(t, head);
+            const bool live = token >= 0;
+            const bool warp_live = __any_sync(0xffffffffu, live);
+            const int m = t.seq.n - t.seq.tokens + t.token0 + max(token, 0);
+            const int lo = chunk_lo(p.shape, m), hi = live ? chunk_hi(t.seq, m) : 0;
+            const bool have_ahead = next(ahead);
+            const bool load_ahead = have_ahead && tiles_of(ahead) > 0;
+            const int32_t* table = p.block_tables + (int64_t)t.b * p.max_blocks_per_seq;
+            const float slope =
+                MOD && p.slopes != nullptr && live ? __ldg(p.slopes + head) * kLog2e : 0.f;
+            // lanes 0-7: the block of box `lane` of tile j, as the table has it (-1: none)
+            auto box_block = [&](int j) {
+                const int at = (t.tile + j) * TT + lane * kStageTokens;
+                return lane < kChunkBoxes && j < nt && at + kStageTokens > t.lo && at < t.hi
+                           ? __ldg(table + (at >> bs_shift))
+                           : -1;
+            };
+
+            float m_ref = -INFINITY, l = 0.f;
+            const int j0 = split ? wg : 0, by = split ? 2 : 1;
+            int blk = box_block(j0), blk_next = box_block(j0 + by);  // two steps ahead
+            for (int j = j0; j < nt; j += by, ++step) {
+                const uint32_t boxes = __ballot_sync(0xffffffffu, blk >= 0 && blk < p.num_blocks);
+                blk = blk_next;
+                blk_next = box_block(j + 2 * by);
+                const int t0 = (t.tile + j) * TT;
+                // every row of the unit sees the whole tile
+                const bool plain = boxes == (1u << kChunkBoxes) - 1u && t0 >= t.lo_all &&
+                                   t0 + TT <= t.hi_all;
+                if (!warp_wait_phase(ptx::smem_addr(&s_full[wg]), step & 1, abort_flag,
+                                     p.err_flag)) {
+                    ok = false;
+                    break;
+                }
+                ptx::tc_fence_after_sync();
+                if (j + by >= nt && load_ahead) load_q(ahead);  // (its tile's last reader is done)
+                if (!plain) {
+                    // V rows that are not there hold stale bytes, and one that only some
+                    // rows see may hold infinities or NaN: zeroed in shared memory, so that
+                    // 0 * V is 0; the rows that do see such a value get it back at the end.
+                    const int at = place0 + chunk_place(split, true, j, nt);
+                    const int slot = at % NS;
+                    if (!warp_wait_phase(ptx::smem_addr(&full_bar[slot]), (at / NS) & 1,
+                                         abort_flag, p.err_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* vst = ring + slot * Cfg::kTileBytes;
+                    for (int idx = srow; idx < TT * R * 8; idx += TR) {
+                        const int row = idx / (R * 8), rem = idx - row * (R * 8);
+                        const int at_row = t0 + row;
+                        const bool there = (boxes >> (row / kStageTokens)) & 1u;
+                        if (there && at_row >= t.lo_all && at_row < t.hi_all) continue;
+                        uint4* cell = reinterpret_cast<uint4*>(
+                            vst + (rem / 8) * Cfg::kRegionBytes + row * 128 + (rem % 8) * 16);
+                        if (!there || at_row < t.lo || at_row >= t.hi) {
+                            *cell = make_uint4(0u, 0u, 0u, 0u);
+                        } else {
+                            uint4 x = *cell;
+                            const uint32_t bad = drop_not_finite(x.x, T()) |
+                                                 drop_not_finite(x.y, T()) |
+                                                 drop_not_finite(x.z, T()) |
+                                                 drop_not_finite(x.w, T());
+                            if (bad) {
+                                s_bad[nunit % kChunkMarks] = nunit + 1;
+                                __threadfence_block();  // before the value is gone
+                                *cell = x;
+                            }
+                        }
+                    }
+                    ptx::fence_proxy_async_smem();
+                }
+                if (free_due) {
+                    // both warpgroups have read O_0, O_1 and the exchange of the split unit
+                    // before; neither is written anew until then
+                    if (!warp_wait_phase(ptx::smem_addr(o_free), (splits - 1) & 1, abort_flag,
+                                         p.err_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    free_due = false;
+                }
+                if (warp_live) {
+                    uint32_t sc[TT / 32][32];
+                    __syncwarp();
+#pragma unroll
+                    for (int c = 0; c < TT / 32; ++c) ptx::tmem_ld32_async(s_col + c * 32, sc[c]);
+                    ptx::tmem_wait_ld();
+#pragma unroll
+                    for (int c = 0; c < TT / 32; ++c) ptx::tmem_loaded(sc[c]);
+                    float scale = p.scale_log2;
+                    if constexpr (MOD) {
+                        // the scores themselves, in base-2 units
+                        scale = 1.f;
+                        const float k1 = p.scale_log2 * p.scale_sign;
+                        if (p.softcap > 0.f) {
+                            // cap tanh(x) = cap - 2 cap / (1 + e^(2x))
+                            const float cap2 = p.softcap * kLog2e;
+#pragma unroll
+                            for (int c = 0; c < TT / 32; ++c)
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) {
+                                    const float e = ptx::ex2_approx(
+                                        __uint_as_float(sc[c][i]) * p.tanh_log2);
+                                    sc[c][i] = __float_as_uint(
+                                        fmaf(-2.f * cap2, __fdividef(1.f, 1.f + e), cap2));
+                                }
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < TT / 32; ++c)
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    sc[c][i] = __float_as_uint(__uint_as_float(sc[c][i]) * k1);
+                        }
+                        if (p.slopes != nullptr) {
+                            const float away = (float)(t0 - m);
+#pragma unroll
+                            for (int c = 0; c < TT / 32; ++c)
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    sc[c][i] = __float_as_uint(
+                                        fmaf(slope, away + (float)(c * 32 + i),
+                                             __uint_as_float(sc[c][i])));
+                        }
+                    } else if (p.scale_sign != 1.f) {
+#pragma unroll
+                        for (int c = 0; c < TT / 32; ++c)
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                sc[c][i] = __float_as_uint(__uint_as_float(sc[c][i]) * p.scale_sign);
+                    }
+                    if (!plain) {
+#pragma unroll
+                        for (int c = 0; c < TT / 32; ++c) {
+                            const int from = lo - (t0 + c * 32), to = hi - (t0 + c * 32);
+                            uint32_t allow = to >= 32 ? ~0u : to <= 0 ? 0u : (1u << to) - 1u;
+                            allow &= from <= 0 ? ~0u : from >= 32 ? 0u : ~0u << from;
+                            const uint32_t bb = boxes >> (2 * c);
+                            allow &= ((bb & 1u) ? 0x0000ffffu : 0u) |
+                                     ((bb & 2u) ? 0xffff0000u : 0u);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (!((allow >> i) & 1u)) sc[c][i] = __float_as_uint(-INFINITY);
+                        }
+                    }
+                    float mx[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        mx[c] = fmaxf(__uint_as_float(sc[c][0]), __uint_as_float(sc[c][1]));
+#pragma unroll
+                    for (int i = 2; i < 32; i += 2)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            mx[c] = fmaxf(fmaxf(mx[c], __uint_as_float(sc[c][i])),
+                                          __uint_as_float(sc[c][i + 1]));
+                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+                    float alpha = 1.f;
+                    if (m_ref == -INFINITY) {
+                        m_ref = top;  // O and l are still zero for this row
+                    } else if (top > m_ref + kChunkLazyLog2) {
+                        alpha = ptx::ex2_approx(m_ref - top);
+                        m_ref = top;
+                    }
+                    const float ref = (m_ref == -INFINITY ? 0.f : m_ref) - WeightBias<T>::value;
+                    // O is rescaled when a reference moved (the last O += P V is complete:
+                    // S of this step is, and was issued behind it)
+                    if (__any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t ov[32];
+                            __syncwarp();
+                            ptx::tmem_ld32(o_col + wg * D + c * 32, ov);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+                            ptx::tmem_st32(o_col + wg * D + c * 32, ov);
+                        }
+                        l *= alpha;
+                    }
+                    const float2 scale2 = make_float2(scale, scale);
+                    const float2 ref2 = make_float2(-ref, -ref);
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    auto weight = [&](int c, int e) {
+                        float2 y = ptx::fma2(make_float2(__uint_as_float(sc[c][2 * e]),
+                                                         __uint_as_float(sc[c][2 * e + 1])),
+                                             scale2, ref2);
+                        y.x = ptx::ex2_approx(y.x);
+                        y.y = ptx::ex2_approx(y.y);
+                        sum[e % 2] = ptx::add2(sum[e % 2], y);
+                        return y;
+                    };
+                    if (split) {
+#pragma unroll
+                        for (int c = 0; c < TT / 32; ++c) {
+                            uint32_t ph[16], pl[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) split_pair(weight(c, e), ph[e], pl[e], T());
+                            ptx::tmem_st16_async(s_col + c * 16, ph);
+                            ptx::tmem_st16_async(s_col + TT / 2 + c * 16, pl);
+                        }
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < TT / 32; ++c) {
+                            uint32_t ph[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                const float2 y = weight(c, e);
+                                ph[e] = pack2(y.x, y.y, T());
+                            }
+                            ptx::tmem_st16_async(s_col + c * 16, ph);
+                        }
+                    }
+                    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                    ptx::tmem_wait_st();
+                }
+                ptx::tc_fence_before_sync();
+                ptx::mbar_arrive(ptx::smem_addr(&p_ready[wg]));
+            }
+            if (!ok) break;
+            place0 += 2 * nt;
+            if (load_ahead) {
+                if (mine == 0) load_q(ahead);
+                q_loaded();
+            }
+
+            // the unit's last O += P V
+            if (mine > 0) {
+                if (!warp_wait_phase(ptx::smem_addr(&o_done[wg]), own & 1, abort_flag, p.err_flag))
+                    break;
+                ++own;
+            }
+            float fa, fb = 0.f, lse;  // out = O_0 fa + O_1 fb (not split: O_w fa)
+            bool two = false;         // O_1 has something
+            if (!split) {
+                fa = l == 0.f ? 0.f : 1.f / l;
+                lse = l == 0.f ? -INFINITY : m_ref - WeightBias<T>::value + log2f(l);
+            } else {
+                // both warpgroups are through: their halves of the softmax meet
+                if (free_due) {
+                    if (!warp_wait_phase(ptx::smem_addr(o_free), (splits - 1) & 1, abort_flag,
+                                         p.err_flag))
+                        break;
+                    free_due = false;
+                }
+                xch[wg * TR + srow] = make_float2(m_ref, l);
+                ptx::tc_fence_before_sync();
+                ptx::mbar_arrive(ptx::smem_addr(met));
+                if (!warp_wait_phase(ptx::smem_addr(met), splits & 1, abort_flag, p.err_flag))
+                    break;
+                const float2 ha = xch[srow], hb = xch[TR + srow];
+                two = nt > 1;
+                const float mm = fmaxf(ha.x, hb.x);
+                fa = ha.x == -INFINITY ? 0.f : ptx::ex2_approx(ha.x - mm);
+                fb = hb.x == -INFINITY ? 0.f : ptx::ex2_approx(hb.x - mm);
+                const float sum = ha.y * fa + hb.y * fb;
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                fa *= inv;
+                fb *= inv;
+                lse = sum == 0.f ? -INFINITY : mm - WeightBias<T>::value + log2f(sum);
+            }
+            ptx::tc_fence_after_sync();
+            const bool direct = nt == t.unit_tiles;
+            const int slot = chunk_partial(t.segment, t.begins);
+            const bool bad_v = s_bad[nunit % kChunkMarks] == nunit + 1;
+            // Columns: the whole row; of a split unit this warpgroup's half.
+            const int cols = split ? D / 2 : D;
+            const int col0 = split ? wg * cols : 0;
+            const int64_t out_row =
+                (int64_t)(t.seq.first + t.token0 + max(token, 0)) * p.num_q_heads + head;
+            const int urow = split ? srow : wg * TR + srow;
+#pragma unroll 1
+            for (int c = 0; c < cols; c += 32) {
+                if (!warp_live) break;
+                float v[32];
+                uint32_t ov[32];
+                __syncwarp();
+                ptx::tmem_ld32(o_col + (split ? 0 : wg * D) + col0 + c, ov);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(ov[i]) * fa;
+                if (two) {
+                    ptx::tmem_ld32(o_col + D + col0 + c, ov);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = fmaf(__uint_as_float(ov[i]), fb, v[i]);
+                }
+                if (!live) continue;
+                if (bad_v) {
+                    // infinities and NaN in the V of positions that this row sees and others
+                    // do not: those before lo_all and from hi_all on
+                    const int from = max(lo, t.tile * TT), to = min(hi, (t.tile + nt) * TT);
+                    for (int x = from; x < to; ++x) {
+                        if (x >= t.lo_all && x < t.hi_all) {
+                            x = min(t.hi_all, to) - 1;
+                            continue;
+                        }
+                        const int vb = __ldg(table + (x >> bs_shift));
+                        if (vb < 0 || vb >= p.num_blocks) continue;
+                        const int off = x & (bs - 1);
+                        const uint16_t* vr =
+                            static_cast<const uint16_t*>(p.v_cache) +
+                            (p.hnd ? ((int64_t)vb * p.shape.heads + t.g) * bs + off
+                                   : ((int64_t)vb * bs + off) * p.shape.heads + t.g) * D +
+                            col0 + c;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const uint16_t e = __ldg(vr + i);
+                            if (not_finite(e, T())) v[i] += unpack2(e, T()).x;
+                        }
+                    }
+                }
+                if (direct) {
+                    uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + out_row * D +
+                                                          col0 + c);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        out[i] = make_uint4(pack2(v[8 * i], v[8 * i + 1], T()),
+                                            pack2(v[8 * i + 2], v[8 * i + 3], T()),
+                                            pack2(v[8 * i + 4], v[8 * i + 5], T()),
+                                            pack2(v[8 * i + 6], v[8 * i + 7], T()));
+                } else {
+                    float4* part = reinterpret_cast<float4*>(
+                        p.partial_o + ((int64_t)slot * 2 * TR + urow) * D + col0 + c);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        part[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                }
+            }
+            if (live && !direct && (!split || wg == 0))
+                p.partial_lse[(int64_t)slot * 2 * TR + urow] = lse;
+            if (split) {
+                ptx::tc_fence_before_sync();
+                ptx::mbar_arrive(ptx::smem_addr(o_free));
+                free_due = true;
+                ++splits;
+            }
+            ++nunit;
+            t = ahead;
+            have = have_ahead;
+        }
+        // a warp that gave up a wait may have the next unit's queries on their way
+        ptx::cp_async_wait_all();
+    }
+
+    ptx::tc_fence_before_sync();
+    __syncthreads();
+    if (warp == kChunkMmaWarp) {
+        __syncwarp();
+        ptx::tc_fence_after_sync();
+        ptx::tmem_dealloc(tmem, 512);
+    }
+}
+
+// Joins the partials of the units that were cut: w_c = 2^(lse_c - max),
+// out = sum_c w_c O_c / sum_c w_c over the unit's segments, with a running maximum.  The
+// segment that ends a unit has its record; a CTA takes 16 of its rows, eight lanes a row.
+constexpr int kChunkMergeThreads = 128;
+constexpr int kChunkMergeRows = kChunkMergeThreads / 8;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kChunkMergeThreads) chunk_merge_kernel(const ChunkParams p) {
+    constexpr int E = D / 32;  // float4 columns of a lane: 8 k + lane % 8
+    constexpr int F = 4;       // partials in flight
+    ptx::launch_dependents();
+    ptx::grid_dependency_wait();
+    const int segment = blockIdx.x;
+    const int row = blockIdx.y * kChunkMergeRows + (threadIdx.x >> 3), q8 = threadIdx.x & 7;
+    const int4 words = __ldg(reinterpret_cast<const int4*>(p.records) + segment);
+    const ChunkRecord r = {words.x, words.y, words.z, words.w};
+    if (!chunk_record_valid(r, segment, p.num_seqs, p.shape.heads)) return;
+    const ChunkSeq s = chunk_load(p, r.b);
+    const int64_t token0 = (int64_t)r.rb * p.shape.block_tokens;
+    const int token = row / p.shape.group;
+    if (token >= p.shape.block_tokens || token0 + token >= s.tokens) return;
+    float m = -INFINITY, den = 0.f;
+    float4 acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = r.first; c <= segment; c += F) {
+        float lse[F];
+        float4 x[F][E];
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+            // a unit's first segment leaves the partial that it begins, the others that
+            // which was begun before them
+            const int slot = chunk_partial(min(c + f, segment), c + f == r.first);
+            const int64_t at = (int64_t)slot * 2 * kChunkRows + row;
+            const bool has = c + f <= segment && __ldg(p.has + slot) == 1;
+            lse[f] = has ? __ldg(p.partial_lse + at) : -INFINITY;
+            const float4* o = reinterpret_cast<const float4*>(p.partial_o + at * D) + q8;
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                x[f][e] = has ? __ldg(o + 8 * e) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        float mn = m;
+#pragma unroll
+        for (int f = 0; f < F; ++f) mn = fmaxf(mn, lse[f]);
+        const float ref = mn == -INFINITY ? 0.f : mn;
+        const float old = exp2f(m - ref);
+        m = mn;
+        den *= old;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            acc[e].x *= old;
+            acc[e].y *= old;
+            acc[e].z *= old;
+            acc[e].w *= old;
+        }
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+            const float w = exp2f(lse[f] - ref);
+            den += w;
+            if (w == 0.f) continue;  // adds nothing, whatever it weighs
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                acc[e].x = fmaf(w, x[f][e].x, acc[e].x);
+                acc[e].y = fmaf(w, x[f][e].y, acc[e].y);
+                acc[e].z = fmaf(w, x[f][e].z, acc[e].z);
+                acc[e].w = fmaf(w, x[f][e].w, acc[e].w);
+            }
+        }
+    }
+    const float inv = den == 0.f ? 0.f : 1.f / den;
+    const int64_t out_row = (s.first + token0 + token) * p.num_q_heads + r.g * p.shape.group + row -
+                            token * p.shape.group;
+    uint2* out = reinterpret_cast<uint2*>(static_cast<T*>(p.out) + out_row * D) + q8;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        out[8 * e] = make_uint2(pack2(acc[e].x * inv, acc[e].y * inv, T()),
+                                pack2(acc[e].z * inv, acc[e].w * inv, T()));
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+
+// The plan of a call: the CTAs, the rounds at most, and the workspace.
 constexpr int kChunkMaxContext = INT_MAX - 1024;  // positions of the last tile fit an int
+struct ChunkCallPlan {
+    int ctas;
+    int rounds;
+    bool cut;  // a unit may be cut: partials and a join
+    size_t records_bytes;
+    size_t has_bytes;
+    size_t workspace_bytes;
+};
+
 static pkv_status check_chunk(int num_seqs, int num_tokens, int num_q_heads, int num_kv_heads,
                               int head_dim, int block_size, int max_context_len) {
     const pkv_status st = check_shapes(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
@@ -144,23 +1060,81 @@ static pkv_status check_chunk(int num_seqs, int num_tokens, int num_q_heads, int
     return PKV_OK;
 }
 
-template <typename T, int D>
-static cudaError_t launch_chunk_t(const ChunkParams& p, cudaStream_t stream) {
+static pkv_status plan_chunk(int num_seqs, int num_tokens, int num_q_heads, int num_kv_heads,
+                             int head_dim, int block_size, int max_context_len,
+                             ChunkCallPlan* plan) {
+    const pkv_status st = check_chunk(num_seqs, num_tokens, num_q_heads, num_kv_heads, head_dim,
+                                      block_size, max_context_len);
+    if (st != PKV_OK) return st;
+    const int sms = current_sm_count();
+    if (sms <= 0) return PKV_ERR_CUDA;
+    // the line at most: every unit as long as the longest context
+    const int block_tokens = 2 * kChunkRows / (num_q_heads / num_kv_heads);
+    const double units = (double)num_kv_heads *
+                         ((double)num_tokens / block_tokens + std::min(num_seqs, num_tokens));
+    const double places = units * ((double)kChunkUnitCost + max_context_len);
+    if (places > 1e15) return PKV_ERR_UNSUPPORTED;  // (times the segments, within 64 bits)
+    plan->ctas = (int)std::max(1.0, std::min((double)sms, std::ceil(places / kChunkLeastSegment)));
+    plan->rounds = (int)std::max(
+        1.0, std::min((double)kChunkMaxRounds, places / ((double)plan->ctas * kChunkRoundSegment)));
+    plan->cut = max_context_len > kChunkTile;
+    const size_t segments = (size_t)plan->ctas * plan->rounds;
+    plan->records_bytes = (segments * sizeof(ChunkRecord) + 255) & ~size_t(255);
+    plan->has_bytes = (chunk_partials((int)segments) * sizeof(int32_t) + 255) & ~size_t(255);
+    plan->workspace_bytes =
+        256 + (plan->cut ? plan->records_bytes + plan->has_bytes +
+                               (size_t)chunk_partials((int)segments) * 2 * kChunkRows *
+                                   (head_dim + 1) * sizeof(float)
+                         : 0);
+    return PKV_OK;
+}
+
+template <typename T, int D, bool MOD>
+static cudaError_t launch_chunk_t(const CUtensorMap& mk, const CUtensorMap& mv,
+                                  const ChunkParams& p, const ChunkCallPlan& plan,
+                                  cudaStream_t stream) {
+    using Cfg = ChunkTileCfg<D>;
+    auto kern = chunk_attention_kernel<T, D, MOD>;
+    // the attribute belongs to a device's copy of the kernel
+    static std::atomic<bool> set[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !set[dev].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 Cfg::kSmemBytes);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) set[dev].store(true, std::memory_order_release);
+    }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.num_tokens, (p.num_q_heads + 3) / 4);
-    cfg.blockDim = dim3(128);
+    cfg.gridDim = dim3(plan.ctas);
+    cfg.blockDim = dim3(kChunkThreads);
+    cfg.dynamicSmemBytes = Cfg::kSmemBytes;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, chunk_attention_kernel<T, D>, p);
+    e = cudaLaunchKernelEx(&cfg, kern, mk, mv, p);
+    if (e != cudaSuccess || !plan.cut) return e;
+    const int64_t rows = std::min<int64_t>(2 * kChunkRows, (int64_t)p.num_tokens * p.shape.group);
+    cfg.gridDim = dim3(plan.ctas * plan.rounds,
+                       (unsigned)((rows + kChunkMergeRows - 1) / kChunkMergeRows));
+    cfg.blockDim = dim3(kChunkMergeThreads);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, chunk_merge_kernel<T, D>, p);
 }
 
 template <typename T>
-static cudaError_t launch_chunk(const ChunkParams& p, int head_dim, cudaStream_t stream) {
-    return head_dim == 64 ? launch_chunk_t<T, 64>(p, stream) : launch_chunk_t<T, 128>(p, stream);
+static cudaError_t launch_chunk(const CUtensorMap& mk, const CUtensorMap& mv, const ChunkParams& p,
+                                const ChunkCallPlan& plan, int head_dim, cudaStream_t stream) {
+    const bool mod = p.softcap > 0.f || p.slopes != nullptr;
+    if (head_dim == 64)
+        return mod ? launch_chunk_t<T, 64, true>(mk, mv, p, plan, stream)
+                   : launch_chunk_t<T, 64, false>(mk, mv, p, plan, stream);
+    return mod ? launch_chunk_t<T, 128, true>(mk, mv, p, plan, stream)
+               : launch_chunk_t<T, 128, false>(mk, mv, p, plan, stream);
 }
 
 }  // namespace pkv
@@ -170,10 +1144,11 @@ using namespace pkv;
 extern "C" size_t pkv_chunk_attention_workspace_size(int num_seqs, int num_tokens, int num_q_heads,
                                                      int num_kv_heads, int head_dim,
                                                      int block_size, int max_context_len) {
-    if (check_chunk(num_seqs, num_tokens, num_q_heads, num_kv_heads, head_dim, block_size,
-                    max_context_len) != PKV_OK)
+    ChunkCallPlan plan;
+    if (plan_chunk(num_seqs, num_tokens, num_q_heads, num_kv_heads, head_dim, block_size,
+                   max_context_len, &plan) != PKV_OK)
         return SIZE_MAX;
-    return 256;
+    return plan.workspace_bytes;
 }
 
 extern "C" pkv_status pkv_chunk_attention(
@@ -205,7 +1180,6 @@ extern "C" pkv_status pkv_chunk_attention(
     const int64_t seqs = num_seqs;
     const int64_t q_bytes = (int64_t)num_tokens * num_q_heads * head_dim * 2;
     const int64_t cache_bytes = (int64_t)num_blocks * block_size * num_kv_heads * head_dim * 2;
-    const size_t need = 256;
     const auto over = [&](const void* a, int64_t bytes) {
         return a != nullptr && overlap(out, q_bytes, a, bytes);
     };
@@ -214,12 +1188,20 @@ extern "C" pkv_status pkv_chunk_attention(
         over(prefix_lens, seqs * 4) || over(slopes, (int64_t)num_q_heads * 4) ||
         over(k_cache, cache_bytes) || over(v_cache, cache_bytes))
         return PKV_ERR_INVALID_ARG;
-    if (workspace_bytes < need) return PKV_ERR_WORKSPACE;
-    if (over(workspace, (int64_t)need)) return PKV_ERR_INVALID_ARG;
+    ChunkCallPlan plan;
+    st = plan_chunk(num_seqs, num_tokens, num_q_heads, num_kv_heads, head_dim, block_size,
+                    max_context_len, &plan);
+    if (st != PKV_OK) return st;
+    if (workspace_bytes < plan.workspace_bytes) return PKV_ERR_WORKSPACE;
+    if (over(workspace, (int64_t)plan.workspace_bytes)) return PKV_ERR_INVALID_ARG;
+
+    CUtensorMap mk, mv;
+    if (!make_cache_map(&mk, k_cache, dtype, num_blocks, block_size, num_kv_heads, head_dim, hnd) ||
+        !make_cache_map(&mv, v_cache, dtype, num_blocks, block_size, num_kv_heads, head_dim, hnd))
+        return PKV_ERR_CUDA;
     ChunkParams p = {};
     p.out = out;
     p.q = q;
-    p.k_cache = k_cache;
     p.v_cache = v_cache;
     p.block_tables = block_tables;
     p.query_starts = query_starts;
@@ -227,22 +1209,34 @@ extern "C" pkv_status pkv_chunk_attention(
     p.prefix_lens = prefix_lens;
     p.slopes = slopes;
     p.err_flag = err_flag;
+    if (plan.cut) {
+        char* at = static_cast<char*>(workspace);
+        p.records = reinterpret_cast<ChunkRecord*>(at);
+        p.has = reinterpret_cast<int32_t*>(at + plan.records_bytes);
+        p.partial_o = reinterpret_cast<float*>(at + plan.records_bytes + plan.has_bytes);
+        p.partial_lse = p.partial_o + (size_t)chunk_partials(plan.ctas * plan.rounds) * 2 *
+                                          kChunkRows * head_dim;
+    }
+    p.shape.group = num_q_heads / num_kv_heads;
+    p.shape.block_tokens = 2 * kChunkRows / p.shape.group;
+    p.shape.heads = num_kv_heads;
+    p.shape.window = window;
+    p.rounds = plan.rounds;
     p.max_blocks_per_seq = max_blocks_per_seq;
     p.num_seqs = num_seqs;
     p.num_tokens = num_tokens;
     p.num_blocks = num_blocks;
     p.block_size = block_size;
     p.num_q_heads = num_q_heads;
-    p.num_kv_heads = num_kv_heads;
-    p.group = num_q_heads / num_kv_heads;
     p.cap = std::min(max_blocks_per_seq * block_size, max_context_len);
-    p.window = window;
     p.hnd = hnd;
-    p.scale = scale;
+    p.scale_log2 = (scale == 0.f ? 1.f : std::fabs(scale)) * kLog2e;
+    p.scale_sign = scale > 0.f ? 1.f : scale < 0.f ? -1.f : 0.f;
     p.softcap = softcap;
+    p.tanh_log2 = softcap > 0.f ? 2.f * kLog2e * scale / softcap : 0.f;
     cudaStream_t s = (cudaStream_t)stream;
-    const cudaError_t e = dtype == PKV_FP16 ? launch_chunk<__half>(p, head_dim, s)
-                                            : launch_chunk<__nv_bfloat16>(p, head_dim, s);
+    const cudaError_t e = dtype == PKV_FP16 ? launch_chunk<__half>(mk, mv, p, plan, head_dim, s)
+                                            : launch_chunk<__nv_bfloat16>(mk, mv, p, plan, head_dim, s);
     if (e != cudaSuccess) {
         cudaGetLastError();
         return PKV_ERR_CUDA;

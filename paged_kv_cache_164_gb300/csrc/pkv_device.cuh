@@ -2,6 +2,8 @@
 // on mbarriers, the TMA boxes of a paged cache, tcgen05 descriptors.
 #pragma once
 
+#include <type_traits>
+
 #include "pkv_common.cuh"
 #include "pkv_ptx.cuh"
 
@@ -107,6 +109,49 @@ __device__ __forceinline__ void split_hi_lo(float p0, float p1, uint32_t& hi, ui
     hi = pack2(p0, p1, __half());
     const float2 back = unpack2(hi, __half());
     lo = pack2(p0 - back.x, p1 - back.y, __half());
+}
+
+// A row's weights are 2^(score - reference + bias).  fp16 has few exponents:
+// with the bias its largest weight is 2^(8 + 7), and what subnormals lose of
+// one is below 2^-32 of the row's largest.
+template <typename T> struct WeightBias { static constexpr float value = 0.f; };
+template <> struct WeightBias<__half> { static constexpr float value = 7.f; };
+
+// Two softmax weights as hi + lo 16-bit pairs: hi the weight cut to the type's
+// fraction bits, lo the rest, rounded (of a bf16 weight 2^-16 may be lost, of a fp16
+// one 2^-22).  hi + lo is as often above the weight as below it: the row's sum adds
+// the weights themselves, and terms that are all low leave a bias in the quotient.
+// (bf16 with lo cut too: up to 2^-15, always low; the same time.  With hi rounded as
+// well: up to 2^-17; 32 nodes on the Llama-70B layer 153 us, so 149.)
+__device__ __forceinline__ void split_pair(float2 x, uint32_t& hi, uint32_t& lo, __nv_bfloat16) {
+    const uint32_t a = __float_as_uint(x.x), b = __float_as_uint(x.y);
+    hi = __byte_perm(a, b, 0x7632);
+    const float2 r = ptx::fma2(make_float2(__uint_as_float(a & 0xffff0000u),
+                                           __uint_as_float(b & 0xffff0000u)),
+                               make_float2(-1.f, -1.f), x);
+    lo = pack2(r.x, r.y, __nv_bfloat16());
+}
+__device__ __forceinline__ void split_pair(float2 x, uint32_t& hi, uint32_t& lo, __half) {
+    const float2 h = make_float2(__uint_as_float(__float_as_uint(x.x) & 0xffffe000u),
+                                 __uint_as_float(__float_as_uint(x.y) & 0xffffe000u));
+    hi = pack2(h.x, h.y, __half());
+    const float2 r = ptx::fma2(h, make_float2(-1.f, -1.f), x);
+    lo = pack2(r.x, r.y, __half());
+}
+
+// Whether a 16-bit value is an infinity or a NaN.
+__device__ __forceinline__ bool not_finite(uint16_t x, __nv_bfloat16) {
+    return (x & 0x7f80u) == 0x7f80u;
+}
+__device__ __forceinline__ bool not_finite(uint16_t x, __half) { return (x & 0x7c00u) == 0x7c00u; }
+
+// Zeroes what is not finite in a pair of 16-bit values; not 0 if something was.
+template <typename T>
+__device__ __forceinline__ uint32_t drop_not_finite(uint32_t& x, T) {
+    constexpr uint32_t k = std::is_same<T, __half>::value ? 0x7c007c00u : 0x7f807f80u;
+    const uint32_t bad = __vcmpeq2(x & k, k);
+    x &= ~bad;
+    return bad;
 }
 
 }  // namespace pkv
