@@ -23,6 +23,9 @@
 // warpgroup 128 of its rows, which meet the same tiles; a smaller one (single tokens,
 // drafted tails) gives both the same rows and every other tile, and they meet at the
 // end.  Four warps stream K and V by TMA through the block table into a ring of tiles.
+// One warp walks the segments and leaves what the others need of a unit in a ring in
+// shared memory, a few units ahead: walked by every warp for itself, the reads of a new
+// sequence and its tables stood before each unit's first softmax, 6 to 7 us a unit.
 //
 // A softmax weight meets V as one 16-bit term in the larger units, where the products
 // are what takes the time (a second term costs half as much again), and as two in the
@@ -82,7 +85,9 @@ constexpr int kChunkSoftmaxWarps = 8;                 // two warpgroups
 constexpr int kChunkTmaWarp = kChunkSoftmaxWarps;     // four producers
 constexpr int kChunkTmaWarps = 4;
 constexpr int kChunkMmaWarp = kChunkTmaWarp + kChunkTmaWarps;
-constexpr int kChunkThreads = (kChunkSoftmaxWarps + 8) * 32;  // the last three only fill up
+constexpr int kChunkWalkWarp = kChunkMmaWarp + 1;
+constexpr int kChunkThreads = (kChunkSoftmaxWarps + 8) * 32;  // the last two only fill up
+constexpr int kChunkReaders = kChunkSoftmaxWarps + kChunkTmaWarps + 1;  // of a unit's notes
 // Registers: the other warpgroups hand over what they do not need, so that a softmax
 // thread's row of S stays in registers.
 constexpr int kChunkLaunchRegs = 128, kChunkSoftmaxRegs = 184, kChunkOtherRegs = 72;
@@ -91,13 +96,37 @@ static_assert(2 * kChunkSoftmaxRegs + 2 * kChunkOtherRegs <= 4 * kChunkLaunchReg
 constexpr float kChunkLazyLog2 = 8.f;
 constexpr int kChunkBoxes = kChunkTile / kStageTokens;  // TMA boxes along a tile
 constexpr int kChunkMaxRounds = 4;
-// Marks of units with a V that is not finite, a ring of them: the warpgroups are at
-// most a unit apart (each needs the other's tiles released), and the ring is four.
-constexpr int kChunkMarks = 4;
+// Notes of units, a ring of them; with each the mark of a V that is not finite in it.
+constexpr int kChunkNotes = 4;
 // A segment has at least this many places (a tile and what its unit costs besides), and
 // more rounds are taken only where theirs have this many.
 constexpr int kChunkLeastSegment = 512;
 constexpr int kChunkRoundSegment = 12288;
+
+// What the walking warp notes of a unit's stretch.
+struct ChunkNote {
+    int b, g;
+    int q_row;           // row of q of the row block's first token
+    int tokens;          // of the row block
+    int m;               // the first one's position
+    int prefix;
+    int lo, hi;          // positions that any row sees
+    int lo_all, hi_all;  // that all rows see
+    int tile, tiles;     // tiles of the stretch; -1 tiles: the end
+    int partial;         // the stretch's partial, or -1: it is the whole unit
+    int flags;
+    int bad_v;           // (set by who finds a V that is not finite)
+    int blocks[2 * kChunkBoxes];  // of the first two tiles' boxes, as the table has them
+};
+constexpr int kNotePagesThere = 1;  // every page of the stretch is within the pool
+constexpr int kNoteAgain = 2;       // other row blocks read the same tiles
+static_assert(sizeof(ChunkNote) == 124, "notes in shared memory");
+
+// A segment's start, as one thread found it for all.
+struct ChunkStart {
+    int64_t at;
+    int b, g, rb, pos;
+};
 
 template <int D>
 struct ChunkTileCfg {
@@ -106,11 +135,12 @@ struct ChunkTileCfg {
     static constexpr int kTileBytes = kRegions * kRegionBytes;   // K or V of a tile; Q
     static constexpr int kSlots = D == 128 ? 5 : 10;
     static constexpr int kXchBytes = 2 * kChunkRows * 8;         // (m, l) of each half and row
-    // full[slots], empty[slots], s_full[2], p_ready[2], o_done[2], q_ready[2], met, o_free, drain
-    static constexpr int kBarriers = 2 * kSlots + 11;
-    static constexpr int kWords = 64;
-    static constexpr int kSmemBytes =
-        (2 + kSlots) * kTileBytes + kXchBytes + kBarriers * 8 + kWords * 4 + kChunkMaxRounds * 48;
+    // full[slots], empty[slots], s_full[2], p_ready[2], o_done[2], q_ready[2], met, o_free,
+    // drain, noted[notes], read[notes]
+    static constexpr int kBarriers = 2 * kSlots + 11 + 2 * kChunkNotes;
+    static constexpr int kSmemBytes = (2 + kSlots) * kTileBytes + kXchBytes + kBarriers * 8 + 24 +
+                                      kChunkMaxRounds * (int)sizeof(ChunkStart) +
+                                      kChunkNotes * (int)sizeof(ChunkNote);
     static constexpr uint32_t kColO = 2 * kChunkTile;  // S of each warpgroup, then O
     static_assert(kColO + 2 * D <= 512, "tensor memory layout");
     static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
@@ -123,14 +153,6 @@ __device__ __forceinline__ int chunk_place(bool split, bool is_v, int j, int nt)
     if (!split) return 2 * j + (is_v ? 1 : 0);
     return is_v ? min(j + 2, nt) + j : (j < 2 ? j : 2 * j - 1);
 }
-
-// A segment's start, as one thread found it for all.
-struct ChunkStart {
-    int64_t at, end;
-    int b, g, rb, pos;
-    int pad[4];
-};
-static_assert(sizeof(ChunkStart) == 48, "starts in shared memory");
 
 __device__ __forceinline__ ChunkSeq chunk_load(const ChunkParams& p, int b) {
     const int from = __ldg(p.query_starts + b), to = __ldg(p.query_starts + b + 1);
@@ -176,15 +198,16 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
     uint64_t* met = q_ready + 2;        // both are through a split unit
     uint64_t* o_free = met + 1;         // both have read O_0, O_1 and the exchange of one
     uint64_t* drain = o_free + 1;
-    int* words = reinterpret_cast<int*>(full_bar + Cfg::kBarriers);
+    uint64_t* noted = drain + 1;        // [notes]
+    uint64_t* read = noted + kChunkNotes;  // [notes]: by all readers
+    int64_t* s_line = reinterpret_cast<int64_t*>(full_bar + Cfg::kBarriers);
+    int* words = reinterpret_cast<int*>(s_line + 1);
     volatile int* abort_flag = words;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(words + 1);
-    volatile int* s_bad = words + 2;    // [kChunkMarks]: 1 + the unit (its place: the
-                                        // remainder) with a bad V
-    int* s_segments = words + 6;
-    int64_t* s_line = reinterpret_cast<int64_t*>(words + 8);
-    int64_t* s_scan = reinterpret_cast<int64_t*>(words + 10);  // [16]
-    ChunkStart* s_start = reinterpret_cast<ChunkStart*>(words + Cfg::kWords);
+    int* s_segments = words + 2;
+    ChunkStart* s_start = reinterpret_cast<ChunkStart*>(words + 4);
+    ChunkNote* notes = reinterpret_cast<ChunkNote*>(s_start + kChunkMaxRounds);
+    int64_t* s_scan = reinterpret_cast<int64_t*>(xch);  // [16], before the first exchange
 
     const int tid = threadIdx.x;
     const int warp = tid >> 5;
@@ -207,8 +230,11 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
         ptx::mbar_init(ptx::smem_addr(met), 2 * TR);
         ptx::mbar_init(ptx::smem_addr(o_free), 2 * TR);
         ptx::mbar_init(ptx::smem_addr(drain), 1);
+        for (int i = 0; i < kChunkNotes; ++i) {
+            ptx::mbar_init(ptx::smem_addr(&noted[i]), 1);
+            ptx::mbar_init(ptx::smem_addr(&read[i]), kChunkReaders);
+        }
         *abort_flag = 0;
-        for (int i = 0; i < kChunkMarks; ++i) s_bad[i] = 0;
         ptx::fence_barrier_init();
         ptx::prefetch_tensormap(&tm_k);
         ptx::prefetch_tensormap(&tm_v);
@@ -223,6 +249,9 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
     ptx::grid_dependency_wait();
 
     auto load = [&](int b) { return chunk_load(p, b); };
+    auto chunk_ctas = [&](int64_t line) {
+        return (int)min((int64_t)gridDim.x, (line + kChunkLeastSegment - 1) / kChunkLeastSegment);
+    };
 
     // The line, and where on it this CTA's segments start: a thread sums the places of a
     // run of sequences, a scan puts the runs in order, and the thread whose run holds a
@@ -259,8 +288,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             }
         }
         if (!few || warp == 0) {
-            const int64_t most = (line + kChunkLeastSegment - 1) / kChunkLeastSegment;
-            const int ctas = (int)min((int64_t)gridDim.x, most);
+            const int ctas = chunk_ctas(line);
             const int64_t long_ones =
                 ctas > 0 ? line / ((int64_t)ctas * kChunkRoundSegment) : 0;
             const int rounds = (int)max((int64_t)1, min((int64_t)p.rounds, long_ones));
@@ -285,61 +313,29 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 }
                 ChunkWalk w;
                 w.enter(s, p.shape, b, at - first);
-                s_start[r].at = at;
-                s_start[r].end = chunk_segment_start(line, segments, seg + 1);
-                s_start[r].b = w.b;
-                s_start[r].g = w.g;
-                s_start[r].rb = w.rb;
-                s_start[r].pos = w.pos;
+                s_start[r] = ChunkStart{at, w.b, w.g, w.rb, w.pos};
             }
         }
         ptx::tc_fence_before_sync();
         __syncthreads();
         ptx::tc_fence_after_sync();
     }
-    const int64_t line = *s_line;
-    const int segments = *s_segments;
-    const int ctas = (int)min((int64_t)gridDim.x,
-                              (line + kChunkLeastSegment - 1) / kChunkLeastSegment);
-    const int rounds = (int)blockIdx.x < ctas ? segments / ctas : 0;
     const uint32_t tmem = *tmem_slot;
     const uint32_t ring_addr = ptx::smem_addr(ring);
     const uint32_t q_addr = ptx::smem_addr(sq);
-    if (p.records != nullptr)  // segments that the line has not
-        for (int s = segments + blockIdx.x * kChunkThreads + tid; s < p.rounds * (int)gridDim.x;
-             s += gridDim.x * kChunkThreads)
-            p.records[s].first = -1;
-
-    ChunkWalk walk;
-    int round = 0;
-    walk.at = walk.end = 0;
-    // The next unit's stretch, of this round or the next.
-    auto next_any = [&](ChunkStretch& t) {
-        while (!walk.next_any(p.shape, load, t)) {
-            if (round == rounds) return false;
-            const ChunkStart& s = s_start[round++];
-            walk.at = s.at;
-            walk.end = s.end;
-            walk.b = s.b;
-            walk.g = s.g;
-            walk.rb = s.rb;
-            walk.pos = s.pos;
-            walk.seq = load(s.b);
-        }
-        t.segment = (round - 1) * ctas + blockIdx.x;
-        return true;
+    // A reader's wait for note i of the CTA's, and its leave of it.
+    auto note_there = [&](int i) {
+        return warp_wait_phase(ptx::smem_addr(&noted[i % kChunkNotes]), (i / kChunkNotes) & 1,
+                               abort_flag, p.err_flag);
     };
-    auto next = [&](ChunkStretch& t) {
-        do {
-            if (!next_any(t)) return false;
-        } while (t.tiles == 0);
-        return true;
+    auto note_read = [&](int i) {
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&read[i % kChunkNotes]));
     };
     const int group = p.shape.group;
 
     if (warp >= kChunkSoftmaxWarps) {
         ptx::reg_dec<kChunkOtherRegs>();
-        ChunkStretch t;
         if (warp < kChunkMmaWarp) {
             // ------------------------------------------------------------ producers
             // A warp loads a quarter of every tile; a lane issues one box (16 positions x
@@ -354,41 +350,28 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             uint32_t filled = 0; // slots with a copy of this warp's that may be in flight,
             uint32_t parity = 0; // and its phase's parity
             bool ok = true;
-            while (ok && next_any(t)) {
-                if (p.records != nullptr && warp == kChunkTmaWarp && lane == 0) {
-                    // what the join reads: whether this stretch leaves a partial, and, once
-                    // a segment, the unit whose partials it joins: one that was cut by the
-                    // segment's start and ends here
-                    const bool cut = t.tiles < t.unit_tiles;
-                    p.has[chunk_partial(t.segment, t.begins)] = cut && t.tiles > 0;
-                    if (t.at == s_start[round - 1].at) {
-                        const bool joins = !t.begins && cut && t.skipped + t.tiles == t.unit_tiles;
-                        p.records[t.segment] = ChunkRecord{
-                            joins ? chunk_segment_of(line, segments, t.unit_at) : -1, t.b, t.g,
-                            t.rb};
-                    }
-                }
-                if (t.tiles == 0) continue;
-                const int nt = t.tiles;
-                const bool split = t.tokens * group <= TR;
-                const int32_t* table = p.block_tables + (int64_t)t.b * p.max_blocks_per_seq;
-                const uint64_t policy = t.seq.tokens > p.shape.block_tokens ? keep : once;
-                if (warp == kChunkTmaWarp && lane == 0 && t.skipped == 0 && t.g == 0 && t.rb == 0) {
-                    const int n_raw = __ldg(p.context_lens + t.b);
-                    if (n_raw != t.seq.n || n_raw < t.seq.tokens)
-                        flag_error(p.err_flag, PKV_EFLAG_CONTEXT_LEN);
-                }
+            for (int u = 0; ok && note_there(u); ++u) {
+                const ChunkNote& note = notes[u % kChunkNotes];
+                const int nt = note.tiles, g = note.g, lo = note.lo, hi = note.hi;
+                const int base = note.tile * TT + bx * kStageTokens;
+                const bool split = note.tokens * group <= TR;
+                const int32_t* table = p.block_tables + (int64_t)note.b * p.max_blocks_per_seq;
+                const uint64_t policy = note.flags & kNoteAgain ? keep : once;
+                const int first0 = loads ? note.blocks[bx] : -1;
+                const int first1 = loads ? note.blocks[kChunkBoxes + bx] : -1;
+                note_read(u);
+                if (nt < 0) break;
                 // the block of this lane's box of tile j, as the table has it (-1: none)
                 auto box_block = [&](int j) {
-                    const int at = (t.tile + j) * TT + bx * kStageTokens;
-                    return loads && j < nt && at + kStageTokens > t.lo && at < t.hi
+                    const int at = base + j * TT;
+                    return loads && j < nt && at + kStageTokens > lo && at < hi
                                ? __ldg(table + (at >> bs_shift))
                                : -1;
                 };
                 auto fill = [&](bool is_v, int j, int blk) {
-                    const int at = (t.tile + j) * TT + bx * kStageTokens;
+                    const int at = base + j * TT;
                     if (blk < 0 || blk >= p.num_blocks) {
-                        if (!is_v && loads && at + kStageTokens > t.lo && at < t.hi)
+                        if (!is_v && loads && at + kStageTokens > lo && at < hi)
                             flag_error(p.err_flag, PKV_EFLAG_BLOCK_ID);
                         blk = -1;
                     }
@@ -419,14 +402,14 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                     }
                     __syncwarp();
                     if (blk >= 0)
-                        load_kv_box(dst, is_v ? &tm_v : &tm_k, fb, rr * 64, t.g, at & (bs - 1),
+                        load_kv_box(dst, is_v ? &tm_v : &tm_k, fb, rr * 64, g, at & (bs - 1),
                                     blk, p.hnd, policy);
                     filled |= 1u << slot;
                     parity = (parity & ~(1u << slot)) | ((uint32_t)(phase & 1) << slot);
                     return true;
                 };
                 // table entries are read two tiles ahead
-                int b0 = box_block(0), b1 = box_block(1), b2 = box_block(2);
+                int b0 = first0, b1 = first1, b2 = box_block(2);
                 if (split) ok = fill(false, 0, b0) && (nt < 2 || fill(false, 1, b1));
                 for (int j = 0; j < nt && ok; ++j) {
                     const int far = box_block(j + 3);
@@ -465,9 +448,13 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             int step[2] = {0, 0};   // S tiles of each warpgroup so far
             int unit[2] = {0, 0};   // units with tiles for it
             bool ok = true;
-            while (ok && next(t)) {
-                const int nt = __shfl_sync(0xffffffffu, t.tiles, 0);
-                const bool split = __shfl_sync(0xffffffffu, t.tokens * group <= TR ? 1 : 0, 0);
+            for (int u = 0; ok && note_there(u); ++u) {
+                const ChunkNote& note = notes[u % kChunkNotes];
+                const int nt = __shfl_sync(0xffffffffu, note.tiles, 0);
+                const bool split =
+                    __shfl_sync(0xffffffffu, note.tokens * group <= TR ? 1 : 0, 0);
+                note_read(u);
+                if (nt < 0) break;
                 auto wait = [&](uint64_t* bar, int parity) {
                     return warp_wait_phase(ptx::smem_addr(bar), parity & 1, abort_flag,
                                            p.err_flag);
@@ -548,6 +535,111 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             while (!ptx::mbar_try_wait(ptx::smem_addr(drain), 0) &&
                    ptx::globaltimer() - t0 < kWaitLimitNs) {
             }
+        } else if (warp == kChunkWalkWarp) {
+            // ------------------------------------------------------------ the walk
+            const int64_t line = *s_line;
+            const int segments = *s_segments;
+            const int ctas = chunk_ctas(line);
+            const int rounds = (int)blockIdx.x < ctas ? segments / ctas : 0;
+            if (p.records != nullptr)  // segments that the line has not
+                for (int i = segments + blockIdx.x * 32 + lane; i < p.rounds * (int)gridDim.x;
+                     i += gridDim.x * 32)
+                    p.records[i].first = -1;
+            ChunkWalk walk;
+            ChunkStretch t;
+            int u = 0;
+            bool ok = true;
+            auto place = [&](int i) {  // where note i is written, once it was read
+                return i < kChunkNotes ||
+                       warp_wait_phase(ptx::smem_addr(&read[i % kChunkNotes]),
+                                       (i / kChunkNotes - 1) & 1, abort_flag, p.err_flag);
+            };
+            for (int round = 0; round < rounds && ok; ++round) {
+                const ChunkStart start = s_start[round];
+                const int segment = round * ctas + blockIdx.x;
+                walk.at = start.at;
+                walk.end = chunk_segment_start(line, segments, segment + 1);
+                walk.b = start.b;
+                walk.g = start.g;
+                walk.rb = start.rb;
+                walk.pos = start.pos;
+                walk.seq = load(start.b);
+                while (walk.next_any(p.shape, load, t)) {
+                    const bool cut = t.tiles < t.unit_tiles;
+                    if (p.records != nullptr && lane == 0) {
+                        // what the join reads: whether this stretch leaves a partial, and,
+                        // once a segment, the unit whose partials it joins: one that was cut
+                        // by the segment's start and ends here
+                        p.has[chunk_partial(segment, t.begins)] = cut && t.tiles > 0;
+                        if (t.at == start.at) {
+                            const bool joins =
+                                !t.begins && cut && t.skipped + t.tiles == t.unit_tiles;
+                            p.records[segment] = ChunkRecord{
+                                joins ? chunk_segment_of(line, segments, t.unit_at) : -1, t.b,
+                                t.g, t.rb};
+                        }
+                    }
+                    if (t.tiles == 0) continue;
+                    if (t.skipped == 0 && t.g == 0 && t.rb == 0 && lane == 0) {
+                        const int n_raw = __ldg(p.context_lens + t.b);
+                        if (n_raw != t.seq.n || n_raw < t.seq.tokens)
+                            flag_error(p.err_flag, PKV_EFLAG_CONTEXT_LEN);
+                    }
+                    const int32_t* table = p.block_tables + (int64_t)t.b * p.max_blocks_per_seq;
+                    // lanes 0-15: boxes of the first two tiles
+                    const int at = t.tile * TT + lane * kStageTokens;
+                    const int end = min(t.hi, (t.tile + t.tiles) * TT);
+                    const int blk = lane < 2 * kChunkBoxes && at + kStageTokens > t.lo && at < end
+                                        ? __ldg(table + (at >> bs_shift))
+                                        : -1;
+                    // a few loads a lane tell whether all pages are there; of a longer
+                    // stretch the softmax warps look at each tile's
+                    const int page0 = max(t.lo, t.tile * TT) >> bs_shift;
+                    const int pages = ((end - 1) >> bs_shift) - page0 + 1;
+                    bool there = end > t.lo && pages <= 256;
+                    if (there) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int x = i * 32 + lane < pages
+                                              ? __ldg(table + page0 + i * 32 + lane)
+                                              : 0;
+                            there &= x >= 0 && x < p.num_blocks;
+                        }
+                    }
+                    there = __all_sync(0xffffffffu, there);
+                    if (!place(u)) {
+                        ok = false;
+                        break;
+                    }
+                    ChunkNote& note = notes[u % kChunkNotes];
+                    if (lane < 2 * kChunkBoxes) note.blocks[lane] = blk;
+                    if (lane == 0) {
+                        note.b = t.b;
+                        note.g = t.g;
+                        note.q_row = t.seq.first + t.token0;
+                        note.tokens = t.tokens;
+                        note.m = t.seq.n - t.seq.tokens + t.token0;
+                        note.prefix = t.seq.prefix;
+                        note.lo = t.lo;
+                        note.hi = t.hi;
+                        note.lo_all = t.lo_all;
+                        note.hi_all = t.hi_all;
+                        note.tile = t.tile;
+                        note.tiles = t.tiles;
+                        note.partial = cut ? chunk_partial(segment, t.begins) : -1;
+                        note.flags = (there ? kNotePagesThere : 0) |
+                                     (t.seq.tokens > p.shape.block_tokens ? kNoteAgain : 0);
+                        note.bad_v = 0;
+                    }
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&noted[u % kChunkNotes]));
+                    ++u;
+                }
+            }
+            if (ok && place(u) && lane == 0) {
+                notes[u % kChunkNotes].tiles = -1;
+                ptx::mbar_arrive(ptx::smem_addr(&noted[u % kChunkNotes]));
+            }
         }
     } else {
         // ------------------------------------------------------------ softmax rows
@@ -557,32 +649,32 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
         const uint32_t lane_base = (uint32_t)(32 * (warp % 4)) << 16;
         const uint32_t s_col = tmem + lane_base + wg * TT;
         const uint32_t o_col = tmem + lane_base + Cfg::kColO;
-        int place0 = 0, nunit = 0;
+        int place0 = 0;
         int step = 0;                     // this warpgroup's tiles so far
         int own = 0;                      // units with tiles for it
         int splits = 0;                   // split units so far
         bool free_due = false;            // O and the exchange of the last one may be read
         bool ok = true;
 
-        auto is_split = [&](const ChunkStretch& t) { return t.tokens * group <= TR; };
-        auto tiles_of = [&](const ChunkStretch& t) {
-            return is_split(t) ? (t.tiles + 1 - wg) / 2 : t.tiles;
+        auto is_split = [&](const ChunkNote& t) { return t.tokens * group <= TR; };
+        auto tiles_of = [&](const ChunkNote& t) {
+            return t.tiles < 0 ? 0 : is_split(t) ? (t.tiles + 1 - wg) / 2 : t.tiles;
         };
         // this thread's row of a unit: (token of the row block, query head), or a token
         // of -1 past its rows
-        auto row_of = [&](const ChunkStretch& t, int& head) {
+        auto row_of = [&](const ChunkNote& t, int& head) {
             const int r = is_split(t) ? srow : wg * TR + srow;
             const int token = r / group;
             head = t.g * group + r - token * group;
             return r < t.tokens * group ? token : -1;
         };
         // its row of Q into this warpgroup's tile
-        auto load_q = [&](const ChunkStretch& t) {
+        auto load_q = [&](const ChunkNote& t) {
             int head;
             const int token = row_of(t, head);
             const uint4* src = reinterpret_cast<const uint4*>(
                 static_cast<const T*>(p.q) +
-                ((int64_t)(t.seq.first + t.token0 + max(token, 0)) * p.num_q_heads + head) * D);
+                ((int64_t)(t.q_row + max(token, 0)) * p.num_q_heads + head) * D);
 #pragma unroll
             for (int c = 0; c < D / 8; ++c)
                 ptx::cp_async_16(q_addr + wg * Cfg::kTileBytes + (c / 8) * Cfg::kRegionBytes +
@@ -595,30 +687,35 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             ptx::mbar_arrive(ptx::smem_addr(&q_ready[wg]));
         };
 
-        ChunkStretch t, ahead;
-        bool have = next(t);
-        if (have && tiles_of(t) > 0) {
-            load_q(t);
-            q_loaded();
+        if (note_there(0)) {
+            if (tiles_of(notes[0]) > 0) {
+                load_q(notes[0]);
+                q_loaded();
+            }
+        } else {
+            ok = false;
         }
-        while (have && ok) {
+        for (int u = 0; ok && notes[u % kChunkNotes].tiles >= 0; ++u) {
+            ChunkNote& t = notes[u % kChunkNotes];
+            const ChunkNote& ahead = notes[(u + 1) % kChunkNotes];
             const bool split = is_split(t);
-            const int nt = t.tiles, mine = tiles_of(t);
+            const int nt = t.tiles, mine = tiles_of(t), tile = t.tile;
+            const int lo_all = t.lo_all, hi_all = t.hi_all;
             int head;
             const int token = row_of(t, head);
             const bool live = token >= 0;
             const bool warp_live = __any_sync(0xffffffffu, live);
-            const int m = t.seq.n - t.seq.tokens + t.token0 + max(token, 0);
-            const int lo = chunk_lo(p.shape, m), hi = live ? chunk_hi(t.seq, m) : 0;
-            const bool have_ahead = next(ahead);
-            const bool load_ahead = have_ahead && tiles_of(ahead) > 0;
+            const int m = t.m + max(token, 0);
+            const int lo = chunk_lo(p.shape, m), hi = live && m >= 0 ? max(m + 1, t.prefix) : 0;
+            const bool look = !(t.flags & kNotePagesThere);
             const int32_t* table = p.block_tables + (int64_t)t.b * p.max_blocks_per_seq;
             const float slope =
                 MOD && p.slopes != nullptr && live ? __ldg(p.slopes + head) * kLog2e : 0.f;
-            // lanes 0-7: the block of box `lane` of tile j, as the table has it (-1: none)
+            // lanes 0-7, where the notes do not say that all pages are there: the block of
+            // box `lane` of tile j, as the table has it (-1: none)
             auto box_block = [&](int j) {
-                const int at = (t.tile + j) * TT + lane * kStageTokens;
-                return lane < kChunkBoxes && j < nt && at + kStageTokens > t.lo && at < t.hi
+                const int at = (tile + j) * TT + lane * kStageTokens;
+                return look && lane < kChunkBoxes && j < nt && at + kStageTokens > t.lo && at < t.hi
                            ? __ldg(table + (at >> bs_shift))
                            : -1;
             };
@@ -627,20 +724,29 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             const int j0 = split ? wg : 0, by = split ? 2 : 1;
             int blk = box_block(j0), blk_next = box_block(j0 + by);  // two steps ahead
             for (int j = j0; j < nt; j += by, ++step) {
-                const uint32_t boxes = __ballot_sync(0xffffffffu, blk >= 0 && blk < p.num_blocks);
-                blk = blk_next;
-                blk_next = box_block(j + 2 * by);
-                const int t0 = (t.tile + j) * TT;
+                const int t0 = (tile + j) * TT;
+                uint32_t boxes = (1u << kChunkBoxes) - 1u;  // (beyond lo and hi all is masked)
+                if (look) {
+                    boxes = __ballot_sync(0xffffffffu, blk >= 0 && blk < p.num_blocks);
+                    blk = blk_next;
+                    blk_next = box_block(j + 2 * by);
+                }
                 // every row of the unit sees the whole tile
-                const bool plain = boxes == (1u << kChunkBoxes) - 1u && t0 >= t.lo_all &&
-                                   t0 + TT <= t.hi_all;
+                const bool plain = boxes == (1u << kChunkBoxes) - 1u && t0 >= lo_all &&
+                                   t0 + TT <= hi_all;
                 if (!warp_wait_phase(ptx::smem_addr(&s_full[wg]), step & 1, abort_flag,
                                      p.err_flag)) {
                     ok = false;
                     break;
                 }
                 ptx::tc_fence_after_sync();
-                if (j + by >= nt && load_ahead) load_q(ahead);  // (its tile's last reader is done)
+                if (j + by >= nt) {  // (the last reader of Q's tile is done)
+                    if (!note_there(u + 1)) {
+                        ok = false;
+                        break;
+                    }
+                    if (tiles_of(ahead) > 0) load_q(ahead);
+                }
                 if (!plain) {
                     // V rows that are not there hold stale bytes, and one that only some
                     // rows see may hold infinities or NaN: zeroed in shared memory, so that
@@ -657,7 +763,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                         const int row = idx / (R * 8), rem = idx - row * (R * 8);
                         const int at_row = t0 + row;
                         const bool there = (boxes >> (row / kStageTokens)) & 1u;
-                        if (there && at_row >= t.lo_all && at_row < t.hi_all) continue;
+                        if (there && at_row >= lo_all && at_row < hi_all) continue;
                         uint4* cell = reinterpret_cast<uint4*>(
                             vst + (rem / 8) * Cfg::kRegionBytes + row * 128 + (rem % 8) * 16);
                         if (!there || at_row < t.lo || at_row >= t.hi) {
@@ -669,7 +775,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                                                  drop_not_finite(x.z, T()) |
                                                  drop_not_finite(x.w, T());
                             if (bad) {
-                                s_bad[nunit % kChunkMarks] = nunit + 1;
+                                *const_cast<volatile int*>(&t.bad_v) = 1;
                                 __threadfence_block();  // before the value is gone
                                 *cell = x;
                             }
@@ -825,7 +931,8 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             }
             if (!ok) break;
             place0 += 2 * nt;
-            if (load_ahead) {
+            if (mine == 0 && !note_there(u + 1)) break;
+            if (tiles_of(ahead) > 0) {
                 if (mine == 0) load_q(ahead);
                 q_loaded();
             }
@@ -866,14 +973,14 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 lse = sum == 0.f ? -INFINITY : mm - WeightBias<T>::value + log2f(sum);
             }
             ptx::tc_fence_after_sync();
-            const bool direct = nt == t.unit_tiles;
-            const int slot = chunk_partial(t.segment, t.begins);
-            const bool bad_v = s_bad[nunit % kChunkMarks] == nunit + 1;
+            const int partial = t.partial;
+            const bool direct = partial < 0;
+            const bool bad_v = *const_cast<volatile int*>(&t.bad_v) != 0;
             // Columns: the whole row; of a split unit this warpgroup's half.
             const int cols = split ? D / 2 : D;
             const int col0 = split ? wg * cols : 0;
             const int64_t out_row =
-                (int64_t)(t.seq.first + t.token0 + max(token, 0)) * p.num_q_heads + head;
+                (int64_t)(t.q_row + max(token, 0)) * p.num_q_heads + head;
             const int urow = split ? srow : wg * TR + srow;
 #pragma unroll 1
             for (int c = 0; c < cols; c += 32) {
@@ -893,10 +1000,10 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 if (bad_v) {
                     // infinities and NaN in the V of positions that this row sees and others
                     // do not: those before lo_all and from hi_all on
-                    const int from = max(lo, t.tile * TT), to = min(hi, (t.tile + nt) * TT);
+                    const int from = max(lo, tile * TT), to = min(hi, (tile + nt) * TT);
                     for (int x = from; x < to; ++x) {
-                        if (x >= t.lo_all && x < t.hi_all) {
-                            x = min(t.hi_all, to) - 1;
+                        if (x >= lo_all && x < hi_all) {
+                            x = min(hi_all, to) - 1;
                             continue;
                         }
                         const int vb = __ldg(table + (x >> bs_shift));
@@ -925,23 +1032,21 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                                             pack2(v[8 * i + 6], v[8 * i + 7], T()));
                 } else {
                     float4* part = reinterpret_cast<float4*>(
-                        p.partial_o + ((int64_t)slot * 2 * TR + urow) * D + col0 + c);
+                        p.partial_o + ((int64_t)partial * 2 * TR + urow) * D + col0 + c);
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         part[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
                 }
             }
             if (live && !direct && (!split || wg == 0))
-                p.partial_lse[(int64_t)slot * 2 * TR + urow] = lse;
+                p.partial_lse[(int64_t)partial * 2 * TR + urow] = lse;
             if (split) {
                 ptx::tc_fence_before_sync();
                 ptx::mbar_arrive(ptx::smem_addr(o_free));
                 free_due = true;
                 ++splits;
             }
-            ++nunit;
-            t = ahead;
-            have = have_ahead;
+            note_read(u);
         }
         // a warp that gave up a wait may have the next unit's queries on their way
         ptx::cp_async_wait_all();
