@@ -68,6 +68,20 @@ def test_large_vocabularies(vocab):
     _check(_case(11, [4, 6], vocab, True, sharp=1.0))
 
 
+@pytest.mark.parametrize("vocab,draft", [(140001, True), (200000, True), (140001, False)])
+def test_vocabularies_beyond_what_a_cluster_holds_in_registers(vocab, draft):
+    c = _case(15, [3], vocab, True, draft, sharp=1.0)
+    c["parents"] = torch.tensor([-1, 0, 0], dtype=torch.int32)
+    for u in (0.02, 0.97):
+        c["u"] = torch.tensor([u, 0.9999, 0.9999])
+        _check(c)
+
+
+@pytest.mark.parametrize("batch", [1, 2, 5, 19, 40, 90, 200])
+def test_batches_that_take_clusters_of_every_size(batch):
+    _check(_case(16, [4] * batch, 2056, True))
+
+
 def test_flat_distributions_at_many_borders():
     """Tokens of probability 1 / V each: a sum in 32 bits would miss its neighbour."""
     n, v = 200, 3000
