@@ -680,10 +680,10 @@ pkv_status pkv_chunk_attention(void* out, const void* q, const void* k_cache, co
  *         otherwise:            R = max(R - Z q_cur, 0), Z = sum R
  *     next token: the first k with R(0) + .. + R(k) > uniforms[0] sum R
  *         (R = p_cur where R is zero everywhere)
- * R and its sums are whole multiples of 2^-45 (a value's nearest one), the same in any
+ * R and its sums are whole multiples of 2^-44 (a value's nearest one), the same in any
  * order, so the result does not depend on how the work is split.  Values are taken as
  * they are in [0, 1]; NaN and negative ones as 0, larger ones as 1; a row's sum must be
- * below 2^17 (it is 1).  Uniforms below 0 and
+ * below 2 (it is 1).  Uniforms below 0 and
  * NaN are taken as 0, from 1 on as the largest below 1.
  *
  *   target_probs, draft_probs  float32 [num_rows][vocab]

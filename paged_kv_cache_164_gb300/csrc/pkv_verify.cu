@@ -19,9 +19,9 @@ namespace pkv {
 // known beforehand and fetched by a thread a node; a pass over the vocabulary is made
 // only where a child is rejected, and the last one's sums already say where the next
 // token lies.  A cluster of CTAs shares a sequence's vocabulary: each takes the walk by
-// itself, holds its part of the rest in registers (16 elements a thread) and exchanges
-// its sum with the others' through their shared memory.
-// Sums: 64-bit whole numbers of 2^-45, so that they are the same in any order and a
+// itself, sums its part of the rest (from L2 where a node has a second pass) and
+// exchanges its sum with the others' through their shared memory.
+// Sums: 64-bit whole numbers of 2^-44, so that they are the same in any order and a
 // draw at a border does not depend on the split of the work (a sum in fp32 is off by
 // more than the probability of a token of a flat distribution).  Two additions of fp32
 // take a probability apart into them (to_fixed); 2^-60, by shifts of the fraction, took
@@ -47,16 +47,15 @@ struct VerifyParams {
     int slice;  // of the vocabulary, a CTA's
 };
 
-constexpr int kVerifyThreads = 1024;
+constexpr int kVerifyThreads = 512;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
-constexpr int kVerifyEach = 16;  // elements that a thread holds
-constexpr int kVerifyBlock = kVerifyThreads * kVerifyEach;
+constexpr int kVerifyCtas = 2;     // an SM
 constexpr int kVerifyCluster = 8;  // CTAs of a sequence at most
 
-// x in [0, 1] as a multiple of 2^-45, to nearest: a sum with 2 has the bits of x down to
-// 2^-22 as its fraction, and what is left of x, 2^23 times as large, beside 3 the next 23
+// x in [0, 1] as a multiple of 2^-44, to nearest: a sum with 2 has the bits of x down to
+// 2^-22 as its fraction, and what is left of x, 2^22 times as large, beside 3 the next 22
 // (every step but the last is exact).  NaN and negative values are 0, larger ones 1.
-constexpr int kFixedBits = 45;
+constexpr int kFixedBits = 44;
 constexpr int kFixedHigh = 0x40000000, kFixedLow = 0x40400000;  // the bits of 2 and of 3
 __device__ __forceinline__ int64_t fixed_of(int hi, int lo) {
     return (int64_t)hi * (1 << (kFixedBits - 22)) + lo;
@@ -65,7 +64,7 @@ __device__ __forceinline__ uint64_t to_fixed(float x) {
     x = __saturatef(x);
     const float a = __fadd_rn(x, 2.f);
     const float r = __fsub_rn(x, __fsub_rn(a, 2.f));  // at most 2^-23
-    const float c = __fmaf_rn(r, 0x1p23f, 3.f);
+    const float c = __fmaf_rn(r, 0x1p22f, 3.f);
     return (uint64_t)fixed_of(__float_as_int(a) - kFixedHigh, __float_as_int(c) - kFixedLow);
 }
 // to_fixed(x) - to_fixed(y), at least 0: both taken apart at once.
@@ -74,12 +73,12 @@ __device__ __forceinline__ uint64_t fixed_rest(float x, float y) {
     const float2 a = ptx::add2(v, make_float2(2.f, 2.f));
     const float2 t = ptx::add2(a, make_float2(-2.f, -2.f));
     const float2 r = ptx::fma2(t, make_float2(-1.f, -1.f), v);
-    const float2 c = ptx::fma2(r, make_float2(0x1p23f, 0x1p23f), make_float2(3.f, 3.f));
+    const float2 c = ptx::fma2(r, make_float2(0x1p22f, 0x1p22f), make_float2(3.f, 3.f));
     const int64_t d = fixed_of(__float_as_int(a.x) - __float_as_int(a.y),
                                __float_as_int(c.x) - __float_as_int(c.y));
     return (uint64_t)(d > 0 ? d : 0);
 }
-// x z, both in 2^-45, x at most 1
+// x z, both in 2^-44, x at most 1
 __device__ __forceinline__ uint64_t fixed_product(uint64_t x, uint64_t z) {
     return __umul64hi(x << (64 - kFixedBits - 1), z << 1);
 }
@@ -97,20 +96,27 @@ __device__ __forceinline__ uint64_t warp_sum64(uint64_t x) {
     return x;
 }
 
-// What is left of an element once the first `count` of a node's children were rejected:
-// `mass` holds Z_0 .., `gone` their tokens (of a draft without a distribution).
 __device__ __forceinline__ uint64_t fixed_less(uint64_t r, uint64_t gone) {
     return r > gone ? r - gone : 0;
 }
-__device__ __forceinline__ uint64_t rest_of(uint64_t p, uint64_t q, bool draft, int k,
-                                            const uint64_t* mass, const int32_t* gone, int count) {
-    for (int j = 0; j < count; ++j) {
-        if (draft)
-            p = fixed_less(p, j == 0 ? q : fixed_product(q, mass[j]));
-        else if (gone[j] == k)
-            p = 0;
-    }
-    return p;
+// Z as two fp32 terms, and Z q for two q: exact to 2^-47 before it is a multiple of 2^-44.
+__device__ __forceinline__ float2 mass_terms(uint64_t z) {
+    const float hi = __ull2float_rn(z);
+    const int64_t rest = (int64_t)(z - __float2ull_rn(hi));
+    return make_float2(hi * 0x1p-44f, __ll2float_rn(rest) * 0x1p-44f);
+}
+__device__ __forceinline__ void fixed_products(float2 z, float2 q, uint64_t& first,
+                                               uint64_t& second) {
+    const float2 zh = make_float2(z.x, z.x), zl = make_float2(z.y, z.y);
+    const float2 hi = ptx::mul2(zh, q);
+    const float2 lo =
+        ptx::fma2(zl, q, ptx::fma2(zh, q, make_float2(-hi.x, -hi.y)));
+    const float2 a = ptx::add2(hi, make_float2(2.f, 2.f));
+    const float2 t = ptx::add2(a, make_float2(-2.f, -2.f));
+    const float2 r = ptx::add2(ptx::fma2(t, make_float2(-1.f, -1.f), hi), lo);
+    const float2 c = ptx::fma2(r, make_float2(0x1p22f, 0x1p22f), make_float2(3.f, 3.f));
+    first = (uint64_t)fixed_of(__float_as_int(a.x) - kFixedHigh, __float_as_int(c.x) - kFixedLow);
+    second = (uint64_t)fixed_of(__float_as_int(a.y) - kFixedHigh, __float_as_int(c.y) - kFixedLow);
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -134,24 +140,23 @@ __device__ __forceinline__ void store_cluster(uint64_t* local, uint32_t rank, ui
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(x) : "memory");
 }
 
-// VEC: elements that a thread loads at a time (4 where rows and their parts are 16-byte
-// aligned, else 1).  A block of a slice: kVerifyEach / VEC groups of VEC a thread, so that
-// the order of the elements is (group, thread, element).
+// VEC: elements that a lane loads at a time (4 where rows and their parts are 16-byte
+// aligned, else 1).  A warp takes a run of its CTA's elements.
 template <int VEC>
-__global__ void __launch_bounds__(kVerifyThreads, 1) verify_kernel(const VerifyParams p) {
-    constexpr int G = kVerifyEach / VEC;
+__global__ void __launch_bounds__(kVerifyThreads, kVerifyCtas)
+verify_kernel(const VerifyParams p) {
     __shared__ int s_parent[PKV_MAX_TREE_LEN], s_token[PKV_MAX_TREE_LEN];
     __shared__ float s_u[PKV_MAX_TREE_LEN], s_p[PKV_MAX_TREE_LEN], s_q[PKV_MAX_TREE_LEN];
-    __shared__ uint64_t s_mass[PKV_MAX_TREE_LEN];
+    __shared__ float2 s_mass[PKV_MAX_TREE_LEN];  // Z of the rejections
     __shared__ int32_t s_gone[PKV_MAX_TREE_LEN];
-    __shared__ uint64_t s_warp[G][kVerifyWarps];
+    __shared__ uint64_t s_warp[kVerifyWarps];
     __shared__ uint64_t s_cta[2][kVerifyCluster];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = cluster_rank(), ctas = cluster_size();
     const int b = blockIdx.x / ctas;
     const int v = p.vocab;
     const int lo = min(v, rank * p.slice), hi = min(v, lo + p.slice);  // this CTA's elements
-    const bool once = p.slice <= kVerifyBlock;  // they stay in registers
+    const int run = (p.slice / 4 + kVerifyWarps - 1) / kVerifyWarps * 4;  // of a warp
     ptx::launch_dependents();
     ptx::grid_dependency_wait();
     int bad = 0;
@@ -164,12 +169,12 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) verify_kernel(const VerifyP
     } else {
         count = end - first;
     }
-    if (tid < count) {  // (a node a thread)
-        int parent = tid - 1;
-        const int token = tid > 0 ? p.tokens[first + tid] : 0;
-        if (p.parents != nullptr && tid > 0) {
-            parent = p.parents[first + tid];
-            if (parent < 0 || parent >= tid) {
+    for (int i = tid; i < count; i += kVerifyThreads) {  // (a node a thread)
+        int parent = i - 1;
+        const int token = i > 0 ? p.tokens[first + i] : 0;
+        if (p.parents != nullptr && i > 0) {
+            parent = p.parents[first + i];
+            if (parent < 0 || parent >= i) {
                 if (parent != -1 && parent != PKV_TREE_ABSENT) bad |= PKV_EFLAG_TREE;
                 parent = -1;
             }
@@ -178,117 +183,113 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) verify_kernel(const VerifyP
             bad |= PKV_EFLAG_TOKEN;
             parent = -1;
         }
-        s_parent[tid] = parent;
-        s_token[tid] = token;
-        s_u[tid] = within(p.uniforms[first + tid], 0x1.fffffep-1f);
+        s_parent[i] = parent;
+        s_token[i] = token;
+        s_u[i] = within(p.uniforms[first + i], 0x1.fffffep-1f);
         if (parent >= 0) {
             const int64_t at = (int64_t)(first + parent) * v + token;
-            s_p[tid] = within(p.target[at], 1.f);
-            s_q[tid] = p.draft != nullptr ? within(p.draft[at], 1.f) : 1.f;
+            s_p[i] = within(p.target[at], 1.f);
+            s_q[i] = p.draft != nullptr ? within(p.draft[at], 1.f) : 1.f;
         }
     }
     int32_t* path = p.accepted + (int64_t)b * p.max_accepted;
     if (bad && rank == 0) flag_error(p.err_flag, bad);
     __syncthreads();
 
-    // The rest of this CTA's block of elements from `base` on, and the draft's part of it.
-    uint64_t left[kVerifyEach] = {};
-    float draft[kVerifyEach];
     const bool has_draft = p.draft != nullptr;
-    auto element = [&](int base, int i) {  // (of this thread's i-th)
-        return base + (i / VEC) * kVerifyThreads * VEC + tid * VEC + i % VEC;
-    };
-    // (what lies beyond the slice is 0)
-    float target[kVerifyEach];
-    auto fetch = [&](int node, int base, bool with_draft) {
-        const float* tp = p.target + (int64_t)(first + node) * v;
-        const float* dp = with_draft ? p.draft + (int64_t)(first + node) * v : nullptr;
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-            const int k = element(base, g * VEC);
-            if constexpr (VEC == 4) {
-                float4 a = make_float4(0.f, 0.f, 0.f, 0.f), d = a;
-                if (k < hi) {
-                    a = __ldg(reinterpret_cast<const float4*>(tp + k));
-                    if (with_draft) d = __ldg(reinterpret_cast<const float4*>(dp + k));
-                }
-                target[4 * g] = a.x, target[4 * g + 1] = a.y;
-                target[4 * g + 2] = a.z, target[4 * g + 3] = a.w;
-                draft[4 * g] = d.x, draft[4 * g + 1] = d.y;
-                draft[4 * g + 2] = d.z, draft[4 * g + 3] = d.w;
-            } else {
-                target[g] = k < hi ? __ldg(tp + k) : 0.f;
-                draft[g] = with_draft && k < hi ? __ldg(dp + k) : 0.f;
+    const float *tp = nullptr, *dp = nullptr;  // the rows of the pass
+    int rejected = 0;
+    // What is left of two elements, k of target x.x and draft y.x and k2 of x.y and y.y,
+    // after `rejected` children.
+    auto rest2 = [&](int k, int k2, float2 x, float2 y, uint64_t& r, uint64_t& r2) {
+        if (!has_draft || rejected == 0) {
+            r = to_fixed(x.x);
+            r2 = to_fixed(x.y);
+            for (int j = 0; j < rejected; ++j) {
+                if (s_gone[j] == k) r = 0;
+                if (s_gone[j] == k2) r2 = 0;
+            }
+            return;
+        }
+        r = fixed_rest(x.x, y.x);
+        r2 = fixed_rest(x.y, y.y);
+        if (rejected > 1) {
+            const float2 q = make_float2(__saturatef(y.x), __saturatef(y.y));
+            for (int j = 1; j < rejected; ++j) {
+                uint64_t g, g2;
+                fixed_products(s_mass[j], q, g, g2);
+                r = fixed_less(r, g);
+                r2 = fixed_less(r2, g2);
             }
         }
     };
-    // f(i) for this thread's elements of a block, group by group while there are any.
-    auto each = [&](int base, auto f) {
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-            if (base + g * kVerifyThreads * VEC >= hi) break;
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) f(g * VEC + i);
-        }
+    auto rest = [&](int k, float x, float y) {
+        uint64_t r, r2;
+        rest2(k, -1, make_float2(x, 0.f), make_float2(y, 0.f), r, r2);
+        return r;
     };
-    auto cta_sum = [&](uint64_t mine) {  // of all threads, for all
-        mine = warp_sum64(mine);
-        __syncthreads();  // (the sums before these are used)
-        if (lane == 0) s_warp[0][warp] = mine;
-        __syncthreads();
-        return warp_sum64(s_warp[0][lane]);
+    // The sum of elements from .. to - 1 over a warp; kSteps loads of a lane in flight.
+    constexpr int kSteps = 16 / VEC;
+    auto warp_run = [&](int from, int to) {
+        uint64_t mine = 0;
+        for (int k0 = from + lane * VEC; k0 < to; k0 += 32 * VEC * kSteps) {
+            float x[kSteps * VEC], y[kSteps * VEC];
+#pragma unroll
+            for (int u = 0; u < kSteps; ++u) {
+                const int k = k0 + u * 32 * VEC;
+                if constexpr (VEC == 4) {
+                    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), d = a;
+                    if (k < to) {
+                        a = __ldg(reinterpret_cast<const float4*>(tp + k));
+                        if (dp != nullptr) d = __ldg(reinterpret_cast<const float4*>(dp + k));
+                    }
+                    x[4 * u] = a.x, x[4 * u + 1] = a.y, x[4 * u + 2] = a.z, x[4 * u + 3] = a.w;
+                    y[4 * u] = d.x, y[4 * u + 1] = d.y, y[4 * u + 2] = d.z, y[4 * u + 3] = d.w;
+                } else {
+                    x[u] = k < to ? __ldg(tp + k) : 0.f;
+                    y[u] = k < to && dp != nullptr ? __ldg(dp + k) : 0.f;
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kSteps; ++u) {
+                const int k = k0 + u * 32 * VEC;
+                if (k >= to) break;
+                if constexpr (VEC == 4) {
+                    uint64_t r[4];
+                    rest2(k, k + 1, make_float2(x[4 * u], x[4 * u + 1]),
+                          make_float2(y[4 * u], y[4 * u + 1]), r[0], r[1]);
+                    rest2(k + 2, k + 3, make_float2(x[4 * u + 2], x[4 * u + 3]),
+                          make_float2(y[4 * u + 2], y[4 * u + 3]), r[2], r[3]);
+                    mine += (r[0] + r[1]) + (r[2] + r[3]);
+                } else {
+                    mine += rest(k, x[u], y[u]);
+                }
+            }
+        }
+        return warp_sum64(mine);
     };
     int passes = 0;
-    // What is left of block `base` at the node that was fetched, into `left`, and its sum.
-    auto start = [&](int base, int rejected) {
-        uint64_t mine = 0;
-        each(base, [&](int i) {
-            if (has_draft && rejected > 0)
-                left[i] = fixed_rest(target[i], draft[i]);
-            else
-                left[i] = rest_of(to_fixed(target[i]), 0, false, element(base, i), s_mass, s_gone,
-                                  rejected);
-            if (has_draft && rejected > 1) {
-                const uint64_t f = to_fixed(draft[i]);
-                for (int j = 1; j < rejected; ++j)
-                    left[i] = fixed_less(left[i], fixed_product(f, s_mass[j]));
-            }
-            mine += left[i];
-        });
-        return mine;
-    };
-    // What is left at `node` after `rejected` children, its sum over the cluster.
-    auto pass = [&](int node, int rejected) {
-        uint64_t mine = 0;
-        if (!once) {
-            for (int base = lo; base < hi; base += kVerifyBlock) {
-                fetch(node, base, has_draft && rejected > 0);
-                mine += start(base, rejected);
-            }
-        } else if (rejected <= 1) {
-            fetch(node, lo, has_draft && rejected > 0);
-            mine = start(lo, rejected);
-        } else {  // (the rest is there)
-            const uint64_t z = s_mass[rejected - 1];
-            const int token = s_gone[rejected - 1];
-            each(lo, [&](int i) {
-                if (has_draft)
-                    left[i] = fixed_less(left[i], fixed_product(to_fixed(draft[i]), z));
-                else if (element(lo, i) == token)
-                    left[i] = 0;
-                mine += left[i];
-            });
-        }
-        const uint64_t sum = cta_sum(mine);
+    // What is left at `node`, its sum over the cluster; the warps' parts in s_warp.
+    auto pass = [&](int node) {
+        tp = p.target + (int64_t)(first + node) * v;
+        dp = has_draft && rejected > 0 ? p.draft + (int64_t)(first + node) * v : nullptr;
+        const int from = lo + warp * run;
+        const uint64_t mine = warp_run(from, min(hi, from + run));
+        __syncthreads();  // (the sums before these are used)
+        if (lane == 0) s_warp[warp] = mine;
+        __syncthreads();
         const int par = passes++ & 1;
-        if (tid < ctas) store_cluster(&s_cta[par][rank], tid, sum);
+        if (warp == 0) {
+            const uint64_t sum = warp_sum64(lane < kVerifyWarps ? s_warp[lane] : 0);
+            if (lane < ctas) store_cluster(&s_cta[par][rank], lane, sum);
+        }
         cluster_sync();
         uint64_t total = 0;
         for (int c = 0; c < ctas; ++c) total += s_cta[par][c];
         return total;
     };
 
-    int cur = 0, length = 0, rejected = 0;
+    int cur = 0, length = 0;
     uint64_t total = 0;  // of the rest, where a child was rejected
     if (count > 0) {
         if (tid == 0 && rank == 0) path[0] = 0;
@@ -300,8 +301,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) verify_kernel(const VerifyP
         if (rejected == 0) {
             taken = product_below(s_u[i], s_q[i], s_p[i]);
         } else {
-            const uint64_t r = rest_of(to_fixed(s_p[i]), to_fixed(s_q[i]), has_draft, s_token[i],
-                                       s_mass, s_gone, rejected);
+            const uint64_t r = rest(s_token[i], s_p[i], s_q[i]);
             taken = fixed_product(fixed_product(to_fixed(s_u[i]), to_fixed(s_q[i])), total) < r;
         }
         if (taken) {
@@ -313,99 +313,70 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) verify_kernel(const VerifyP
         }
         __syncthreads();  // (the last pass's readers of these are through)
         if (tid == 0) {
-            s_mass[rejected] = total;  // (of the first, which is 1, nothing is read)
+            s_mass[rejected] = mass_terms(total);  // (of the first, which is 1, nothing is read)
             s_gone[rejected] = s_token[i];
         }
         ++rejected;
         __syncthreads();
-        total = pass(cur, rejected);
+        total = pass(cur);
     }
 
     if (count > 0 && (rejected == 0 || total == 0)) {
         rejected = 0;
-        total = pass(cur, 0);
+        total = pass(cur);
     }
     // The first element whose running sum is above u times the total: the CTA that holds
-    // it, the block, the warp's part of a group, and there the lane's element.
-    bool found = false;
+    // it, the warp's run, of that a warp's share, there the element.
     if (total > 0) {
         uint64_t aim = fixed_product(to_fixed(s_u[0]), total);
         int owner = 0;
         const int par = (passes - 1) & 1;
         while (owner + 1 < ctas && s_cta[par][owner] <= aim) aim -= s_cta[par][owner++];
-        for (int base = lo; owner == rank && base < hi && !found; base += kVerifyBlock) {
-            if (!once) {
-                fetch(cur, base, has_draft && rejected > 0);
-#pragma unroll
-                for (int i = 0; i < kVerifyEach; ++i) left[i] = 0;
-                const uint64_t sum = cta_sum(start(base, rejected));
-                if (sum <= aim && base + kVerifyBlock < hi) {
-                    aim -= sum;
-                    continue;
-                }
-            }
-            found = true;  // in this block
-            __syncthreads();
-#pragma unroll
-            for (int g = 0; g < G; ++g) {
-                uint64_t x = 0;
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) x += left[g * VEC + i];
-                x = warp_sum64(x);
-                if (lane == 0) s_warp[g][warp] = x;
-            }
-            __syncthreads();
-            // every warp finds the part, a group at a time; the part's own goes on
-            int group = 0, owns = 0;
-            for (; group < G; ++group) {
-                uint64_t incl = s_warp[group][lane];
-                const uint64_t own = incl;
+        if (owner == rank) {
+            // the first of the warps' sums that the aim lies in, and what is left of it there
+            auto narrow = [&]() {
+                const uint64_t own = lane < kVerifyWarps ? s_warp[lane] : 0;
+                uint64_t incl = own;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
                     const uint64_t x = __shfl_up_sync(0xffffffffu, incl, o);
                     if (lane >= o) incl += x;
                 }
                 const uint32_t over = __ballot_sync(0xffffffffu, incl > aim);
-                if (over != 0) {
-                    owns = __ffs(over) - 1;
-                    aim -= __shfl_sync(0xffffffffu, incl - own, owns);
-                    break;
-                }
-                aim -= __shfl_sync(0xffffffffu, incl, 31);
-            }
-            if (warp == owns) {
-                uint64_t mine[VEC] = {};
+                const int at = over != 0 ? __ffs(over) - 1 : kVerifyWarps - 1;
+                aim -= __shfl_sync(0xffffffffu, incl - own, at);
+                return at;
+            };
+            const int from = lo + narrow() * run, to = min(hi, from + run);
+            const int share = (run + kVerifyWarps - 1) / kVerifyWarps;
+            uint64_t mine = 0;
+            for (int k = from + warp * share + lane; k < min(to, from + (warp + 1) * share); k += 32)
+                mine += rest(k, __ldg(tp + k), dp != nullptr ? __ldg(dp + k) : 0.f);
+            mine = warp_sum64(mine);
+            __syncthreads();
+            if (lane == 0) s_warp[warp] = mine;
+            __syncthreads();
+            if (warp == 0) {
+                const int part = narrow();
+                const int last = min(to, from + (part + 1) * share);
+                int next = -1;
+                for (int k0 = from + part * share; k0 < last && next < 0; k0 += 32) {
+                    const int k = k0 + lane;
+                    uint64_t r = k < last ? rest(k, __ldg(tp + k), dp != nullptr ? __ldg(dp + k) : 0.f)
+                                          : 0;
 #pragma unroll
-                for (int g = 0; g < G; ++g)
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i)
-                        if (g == group) mine[i] = left[g * VEC + i];
-                uint64_t sum = 0;
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) sum += mine[i];
-                uint64_t incl = sum;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const uint64_t x = __shfl_up_sync(0xffffffffu, incl, o);
-                    if (lane >= o) incl += x;
-                }
-                const uint32_t over = __ballot_sync(0xffffffffu, incl > aim);
-                if (over == 0) {  // (a row whose sum is no distribution's)
-                    if (lane == 0) {
-                        flag_error(p.err_flag, PKV_EFLAG_TOKEN);
-                        p.next_tokens[b] = -1;
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const uint64_t x = __shfl_up_sync(0xffffffffu, r, o);
+                        if (lane >= o) r += x;
                     }
-                } else if (lane == __ffs(over) - 1) {
-                    aim -= incl - sum;
-                    int i = 0;
-#pragma unroll
-                    for (int j = 0; j + 1 < VEC; ++j)
-                        if (i == j && mine[j] <= aim) {
-                            aim -= mine[j];
-                            ++i;
-                        }
-                    p.next_tokens[b] = base + group * kVerifyThreads * VEC +
-                                       tid * VEC + i;
+                    const uint32_t over = __ballot_sync(0xffffffffu, r > aim);
+                    if (over != 0) next = k0 + __ffs(over) - 1;
+                    aim -= __shfl_sync(0xffffffffu, r, 31);
+                }
+                if (lane == 0) {
+                    p.next_tokens[b] = next;
+                    if (next < 0)  // a row whose sum is no distribution's
+                        flag_error(p.err_flag, PKV_EFLAG_TOKEN);
                 }
             }
         }
@@ -475,13 +446,12 @@ extern "C" pkv_status pkv_verify_drafts(int32_t* accepted, int32_t* accepted_len
     p.num_rows = num_rows;
     p.vocab = vocab;
     p.max_accepted = max_accepted;
-    // CTAs of a sequence: as many as hold its vocabulary in registers, and more while the
-    // sequences leave SMs idle
+    // CTAs of a sequence: while there are elements for them, as many as run at once
     const int sms = current_sm_count();
     if (sms <= 0) return PKV_ERR_CUDA;
     int ctas = 1;
-    while (ctas < kVerifyCluster && ((int64_t)ctas * kVerifyBlock < vocab ||
-                                     (ctas * 1024 < vocab && num_seqs * 2ll * ctas <= sms)))
+    while (ctas < kVerifyCluster && ctas * 1024 < vocab &&
+           num_seqs * 2ll * ctas <= (int64_t)sms * kVerifyCtas)
         ctas *= 2;
     if (num_seqs > INT_MAX / ctas) return PKV_ERR_UNSUPPORTED;
     p.slice = ((vocab + ctas - 1) / ctas + 3) & ~3;
