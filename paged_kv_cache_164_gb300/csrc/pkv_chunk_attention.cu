@@ -16,9 +16,12 @@
 //   softmax         a thread reads its row of S, writes P over it
 //   O_w += P_w V    P from tensor memory, V from shared memory
 // One warp issues everything in the order PV_0(j) S_0(j+1) PV_1(j) S_1(j+1), so that a
-// warpgroup is at its softmax while the other's two products run.  The tensor core
-// runs them in that order: S over a P comes after the product that reads it, and where
-// S(j) is complete so is PV(j-1).
+// warpgroup is at its softmax while the other's two products run; the order keeps them
+// apart (with an issuer for each, both fell into step, and a chunk behind 61440 tokens
+// took 7.7 ms instead of 6.4).  The tensor core runs the products in that order: S over a
+// P comes after the product that reads it, and where S(j) is complete so is PV(j-1).  P
+// goes over in two halves of 64 positions: the first is multiplied while the second is
+// made.
 // A unit (row block of a KV head, pkv_chunk_line.cuh) of more than 128 rows gives each
 // warpgroup 128 of its rows, which meet the same tiles; a smaller one (single tokens,
 // drafted tails) gives both the same rows and every other tile, and they meet at the
@@ -135,9 +138,9 @@ struct ChunkTileCfg {
     static constexpr int kTileBytes = kRegions * kRegionBytes;   // K or V of a tile; Q
     static constexpr int kSlots = D == 128 ? 5 : 10;
     static constexpr int kXchBytes = 2 * kChunkRows * 8;         // (m, l) of each half and row
-    // full[slots], empty[slots], s_full[2], p_ready[2], o_done[2], q_ready[2], met, o_free,
-    // drain, noted[notes], read[notes]
-    static constexpr int kBarriers = 2 * kSlots + 11 + 2 * kChunkNotes;
+    // full[slots], empty[slots], s_full[2], p_half[2], p_ready[2], o_done[2], q_ready[2],
+    // met, o_free, drain, noted[notes], read[notes]
+    static constexpr int kBarriers = 2 * kSlots + 13 + 2 * kChunkNotes;
     static constexpr int kSmemBytes = (2 + kSlots) * kTileBytes + kXchBytes + kBarriers * 8 + 24 +
                                       kChunkMaxRounds * (int)sizeof(ChunkStart) +
                                       kChunkNotes * (int)sizeof(ChunkNote);
@@ -175,6 +178,26 @@ __device__ __forceinline__ int64_t warp_scan64(int64_t x) {  // inclusive
     return x;
 }
 
+// Four lanes with four 16-byte pieces each: lane k's piece i becomes lane i's piece k.
+__device__ __forceinline__ uint4 shfl_xor4(uint4 x, int o) {
+    return make_uint4(__shfl_xor_sync(0xffffffffu, x.x, o), __shfl_xor_sync(0xffffffffu, x.y, o),
+                      __shfl_xor_sync(0xffffffffu, x.z, o), __shfl_xor_sync(0xffffffffu, x.w, o));
+}
+__device__ __forceinline__ void trade_pieces(uint4 (&x)[4], int lane) {
+#pragma unroll
+    for (int o = 1; o <= 2; o <<= 1)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i & o) continue;
+            const bool up = lane & o;
+            const uint4 got = shfl_xor4(up ? x[i] : x[i + o], o);
+            if (up)
+                x[i] = got;
+            else
+                x[i + o] = got;
+        }
+}
+
 template <typename T, int D, bool MOD>
 __global__ void __launch_bounds__(kChunkThreads, 1)
 chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
@@ -192,8 +215,9 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
     uint64_t* full_bar = reinterpret_cast<uint64_t*>(ring + NS * Cfg::kTileBytes + Cfg::kXchBytes);
     uint64_t* empty_bar = full_bar + NS;
     uint64_t* s_full = empty_bar + NS;  // [warpgroup]
-    uint64_t* p_ready = s_full + 2;     // [warpgroup]
-    uint64_t* o_done = p_ready + 2;     // [warpgroup]: a unit's last product is complete
+    uint64_t* p_half = s_full + 2;      // [warpgroup]: the first 64 positions' weights
+    uint64_t* p_ready = p_half + 2;     // [warpgroup]: all of them
+    uint64_t* o_done = p_ready + 2;   // [warpgroup]: a unit's last product is complete
     uint64_t* q_ready = o_done + 2;     // [warpgroup]
     uint64_t* met = q_ready + 2;        // both are through a split unit
     uint64_t* o_free = met + 1;         // both have read O_0, O_1 and the exchange of one
@@ -223,7 +247,8 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
         }
         for (int w = 0; w < 2; ++w) {
             ptx::mbar_init(ptx::smem_addr(&s_full[w]), 1);
-            ptx::mbar_init(ptx::smem_addr(&p_ready[w]), TR);
+            ptx::mbar_init(ptx::smem_addr(&p_half[w]), TR / 32);
+            ptx::mbar_init(ptx::smem_addr(&p_ready[w]), TR / 32);
             ptx::mbar_init(ptx::smem_addr(&o_done[w]), 1);
             ptx::mbar_init(ptx::smem_addr(&q_ready[w]), TR);
         }
@@ -444,10 +469,71 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             const uint64_t kdesc = ptx::smem_desc_sw128(ring_addr, 16, 1024);
             const uint64_t vdesc = ptx::smem_desc_sw128(ring_addr, Cfg::kRegionBytes, 1024);
             const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-            int place0 = 0;
-            int step[2] = {0, 0};   // S tiles of each warpgroup so far
-            int unit[2] = {0, 0};   // units with tiles for it
+            int slot = 0, phase = 0;  // of the ring's next place
+            int step[2] = {0, 0};     // tiles of each warpgroup so far
+            int unit[2] = {0, 0};     // units with tiles for it
             bool ok = true;
+            auto wait = [&](uint64_t* bar, int parity) {
+                return warp_wait_phase(ptx::smem_addr(bar), parity & 1, abort_flag, p.err_flag);
+            };
+            // the ring's next place, once it is full; -1: a wait gave up
+            auto take = [&] {
+                if (!wait(&full_bar[slot], phase)) return -1;
+                const int at = slot;
+                if (++slot == NS) {
+                    slot = 0;
+                    phase ^= 1;
+                }
+                return at;
+            };
+            // S of warpgroup w from the K in slot `at`; `last`: its last reader
+            auto issue_s = [&](int w, int at, bool last) {
+                ptx::tc_fence_after_sync();
+                const uint64_t kd = kdesc + (uint32_t)(at * (Cfg::kTileBytes / 16));
+                const uint64_t qd = qdesc + (uint32_t)(w * (Cfg::kTileBytes / 16));
+                if (ptx::elect_one()) {
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks)
+                        ptx::tc_mma_f16(
+                            tm + w * TT, qd + (ks / 4) * (Cfg::kRegionBytes / 16) + (ks % 4) * 2,
+                            kd + (ks / 4) * (Cfg::kRegionBytes / 16) + (ks % 4) * 2, idesc_s,
+                            ks > 0 ? 1u : 0u);
+                    ptx::tc_commit(ptx::smem_addr(&s_full[w]));
+                    if (last) ptx::tc_commit(ptx::smem_addr(&empty_bar[at]));
+                }
+                __syncwarp();
+            };
+            // O += P V of warpgroup w from the V in slot `at`
+            auto issue_pv = [&](int w, int at, bool split, bool first, bool ends, bool last) {
+                const uint64_t vd = vdesc + (uint32_t)(at * (Cfg::kTileBytes / 16));
+                const uint32_t pt = tm + w * TT;
+                const uint32_t acc = tm + Cfg::kColO + w * D;
+                auto half = [&](int h) {
+#pragma unroll
+                    for (int i = 0; i < TT / 32; ++i) {
+                        const int kt = h * (TT / 32) + i;
+                        const uint64_t v = vd + (uint32_t)(kt * 16 * 128 / 16);
+                        ptx::tc_mma_f16_ts(acc, pt + kt * 8, v, idesc_o,
+                                           (!first || kt > 0) ? 1u : 0u);
+                        // (a split unit's weights have a second term)
+                        if (split) ptx::tc_mma_f16_ts(acc, pt + TT / 2 + kt * 8, v, idesc_o, 1u);
+                    }
+                };
+                if (!wait(&p_half[w], step[w])) return false;
+                ptx::tc_fence_after_sync();
+                if (ptx::elect_one()) half(0);
+                __syncwarp();
+                if (!wait(&p_ready[w], step[w])) return false;
+                ++step[w];
+                ptx::tc_fence_after_sync();
+                if (ptx::elect_one()) {
+                    half(1);
+                    if (ends) ptx::tc_commit(ptx::smem_addr(&o_done[w]));
+                    if (last) ptx::tc_commit(ptx::smem_addr(&empty_bar[at]));
+                }
+                __syncwarp();
+                return true;
+            };
             for (int u = 0; ok && note_there(u); ++u) {
                 const ChunkNote& note = notes[u % kChunkNotes];
                 const int nt = __shfl_sync(0xffffffffu, note.tiles, 0);
@@ -455,78 +541,46 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                     __shfl_sync(0xffffffffu, note.tokens * group <= TR ? 1 : 0, 0);
                 note_read(u);
                 if (nt < 0) break;
-                auto wait = [&](uint64_t* bar, int parity) {
-                    return warp_wait_phase(ptx::smem_addr(bar), parity & 1, abort_flag,
-                                           p.err_flag);
-                };
-                // S of warpgroup w for tile j; `last`: it is the tile's last reader
-                auto issue_s = [&](int w, int j, bool last) {
-                    const int at = place0 + chunk_place(split, false, j, nt);
-                    const int slot = at % NS;
-                    if (!wait(&full_bar[slot], at / NS)) return false;
-                    ptx::tc_fence_after_sync();
-                    const uint64_t kd = kdesc + (uint32_t)(slot * (Cfg::kTileBytes / 16));
-                    const uint64_t qd = qdesc + (uint32_t)(w * (Cfg::kTileBytes / 16));
-                    if (ptx::elect_one()) {
-#pragma unroll
-                        for (int ks = 0; ks < D / 16; ++ks)
-                            ptx::tc_mma_f16(
-                                tm + w * TT, qd + (ks / 4) * (Cfg::kRegionBytes / 16) + (ks % 4) * 2,
-                                kd + (ks / 4) * (Cfg::kRegionBytes / 16) + (ks % 4) * 2, idesc_s,
-                                ks > 0 ? 1u : 0u);
-                        ptx::tc_commit(ptx::smem_addr(&s_full[w]));
-                        if (last) ptx::tc_commit(ptx::smem_addr(&empty_bar[slot]));
-                    }
-                    __syncwarp();
-                    return true;
-                };
-                auto issue_pv = [&](int w, int j, bool first, bool ends, bool last) {
-                    const int at = place0 + chunk_place(split, true, j, nt);
-                    const int slot = at % NS;
-                    if (!wait(&full_bar[slot], at / NS) || !wait(&p_ready[w], step[w]))
-                        return false;
-                    ++step[w];
-                    ptx::tc_fence_after_sync();
-                    const uint64_t vd = vdesc + (uint32_t)(slot * (Cfg::kTileBytes / 16));
-                    const uint32_t pt = tm + w * TT;
-                    const uint32_t acc = tm + Cfg::kColO + w * D;
-                    if (ptx::elect_one()) {
-#pragma unroll
-                        for (int kt = 0; kt < TT / 16; ++kt) {
-                            const uint64_t v = vd + (uint32_t)(kt * 16 * 128 / 16);
-                            ptx::tc_mma_f16_ts(acc, pt + kt * 8, v, idesc_o,
-                                               (!first || kt > 0) ? 1u : 0u);
-                            // (a split unit's weights have a second term)
-                            if (split) ptx::tc_mma_f16_ts(acc, pt + TT / 2 + kt * 8, v, idesc_o, 1u);
-                        }
-                        if (ends) ptx::tc_commit(ptx::smem_addr(&o_done[w]));
-                        if (last) ptx::tc_commit(ptx::smem_addr(&empty_bar[slot]));
-                    }
-                    __syncwarp();
-                    return true;
-                };
+                ok = wait(&q_ready[0], unit[0]++);
+                int at = ok ? take() : -1;
+                if (at < 0) break;
+                issue_s(0, at, split);
                 if (split) {
-                    ok = wait(&q_ready[0], unit[0]) && issue_s(0, 0, true) &&
-                         (nt < 2 || (wait(&q_ready[1], unit[1]) && issue_s(1, 1, true)));
-                    for (int j = 0; j < nt && ok; ++j)
-                        ok = issue_pv(j & 1, j, j < 2, j + 2 >= nt, true) &&
-                             (j + 2 >= nt || issue_s(j & 1, j + 2, true));
-                    ++unit[0];
-                    unit[1] += nt > 1;
+                    // K0 K1 V0 K2 V1 K3 ..
+                    if (nt > 1) {
+                        ok = wait(&q_ready[1], unit[1]++) && (at = take()) >= 0;
+                        if (!ok) break;
+                        issue_s(1, at, true);
+                    }
+                    for (int j = 0; j < nt && ok; ++j) {
+                        const int w = j & 1;
+                        at = take();
+                        ok = at >= 0 && issue_pv(w, at, true, j < 2, j + 2 >= nt, true);
+                        if (ok && j + 2 < nt) {
+                            at = take();
+                            ok = at >= 0;
+                            if (ok) issue_s(w, at, true);
+                        }
+                    }
                 } else {
-                    ok = wait(&q_ready[0], unit[0]) && issue_s(0, 0, false) &&
-                         wait(&q_ready[1], unit[1]) && issue_s(1, 0, true);
+                    // K0 V0 K1 V1 ..
+                    ok = wait(&q_ready[1], unit[1]++);
+                    if (!ok) break;
+                    issue_s(1, at, true);
                     for (int j = 0; j < nt && ok; ++j) {
                         const bool more = j + 1 < nt;
-                        ok = issue_pv(0, j, j == 0, !more, false) &&
-                             (!more || issue_s(0, j + 1, false)) &&
-                             issue_pv(1, j, j == 0, !more, true) &&
-                             (!more || issue_s(1, j + 1, true));
+                        const int v = take();
+                        ok = v >= 0 && issue_pv(0, v, false, j == 0, !more, false);
+                        int k = -1;
+                        if (ok && more) {
+                            k = take();
+                            ok = k >= 0;
+                            if (ok) issue_s(0, k, false);
+                        }
+                        ok = ok && issue_pv(1, v, false, j == 0, !more, true);
+                        if (ok && more) issue_s(1, k, true);
                     }
-                    ++unit[0];
-                    ++unit[1];
                 }
-                place0 += 2 * nt;
             }
             // every product has completed before the tensor memory is released
             if (ptx::elect_one()) ptx::tc_commit(ptx::smem_addr(drain));
@@ -704,7 +758,8 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             int head;
             const int token = row_of(t, head);
             const bool live = token >= 0;
-            const bool warp_live = __any_sync(0xffffffffu, live);
+            const uint32_t live_lanes = __ballot_sync(0xffffffffu, live);
+            const bool warp_live = live_lanes != 0;
             const int m = t.m + max(token, 0);
             const int lo = chunk_lo(p.shape, m), hi = live && m >= 0 ? max(m + 1, t.prefix) : 0;
             const bool look = !(t.flags & kNotePagesThere);
@@ -759,27 +814,49 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                         break;
                     }
                     uint8_t* vst = ring + slot * Cfg::kTileBytes;
-                    for (int idx = srow; idx < TT * R * 8; idx += TR) {
-                        const int row = idx / (R * 8), rem = idx - row * (R * 8);
-                        const int at_row = t0 + row;
-                        const bool there = (boxes >> (row / kStageTokens)) & 1u;
-                        if (there && at_row >= lo_all && at_row < hi_all) continue;
-                        uint4* cell = reinterpret_cast<uint4*>(
-                            vst + (rem / 8) * Cfg::kRegionBytes + row * 128 + (rem % 8) * 16);
-                        if (!there || at_row < t.lo || at_row >= t.hi) {
-                            *cell = make_uint4(0u, 0u, 0u, 0u);
-                        } else {
-                            uint4 x = *cell;
-                            const uint32_t bad = drop_not_finite(x.x, T()) |
-                                                 drop_not_finite(x.y, T()) |
-                                                 drop_not_finite(x.z, T()) |
-                                                 drop_not_finite(x.w, T());
-                            if (bad) {
-                                *const_cast<volatile int*>(&t.bad_v) = 1;
-                                __threadfence_block();  // before the value is gone
-                                *cell = x;
+                    constexpr int kCells = R * 8;  // 16-byte cells of a row
+                    auto clean = [&](int row0, int row1) {
+                        for (int i0 = row0 * kCells + srow; i0 < row1 * kCells; i0 += 4 * TR) {
+                            uint4 x[4];
+                            uint4* cell[4];
+                            int is[4];  // 0: nothing, 1: zeroed, 2: looked through
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const int idx = i0 + k * TR;
+                                const int row = idx / kCells, rem = idx % kCells;
+                                cell[k] = reinterpret_cast<uint4*>(
+                                    vst + (rem / 8) * Cfg::kRegionBytes + row * 128 + (rem % 8) * 16);
+                                const int pos = t0 + row;
+                                is[k] = idx >= row1 * kCells ? 0
+                                        : pos < t.lo || pos >= t.hi ||
+                                                !((boxes >> (row / kStageTokens)) & 1u)
+                                            ? 1
+                                        : pos >= lo_all && pos < hi_all ? 0
+                                                                        : 2;
+                                x[k] = is[k] == 2 ? *cell[k] : make_uint4(0u, 0u, 0u, 0u);
+                            }
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                if (is[k] == 1) *cell[k] = x[k];
+                                if (is[k] == 2 && any_not_finite(x[k], T())) {
+                                    drop_not_finite(x[k].x, T());
+                                    drop_not_finite(x[k].y, T());
+                                    drop_not_finite(x[k].z, T());
+                                    drop_not_finite(x[k].w, T());
+                                    *const_cast<volatile int*>(&t.bad_v) = 1;
+                                    __threadfence_block();  // before the value is gone
+                                    *cell[k] = x[k];
+                                }
                             }
                         }
+                    };
+                    if (boxes == (1u << kChunkBoxes) - 1u) {
+                        const int before = min(max(lo_all - t0, 0), TT);
+                        const int behind = max(min(max(hi_all - t0, 0), TT), before);
+                        clean(0, before);
+                        clean(behind, TT);
+                    } else {
+                        clean(0, TT);
                     }
                     ptx::fence_proxy_async_smem();
                 }
@@ -801,46 +878,53 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                     ptx::tmem_wait_ld();
 #pragma unroll
                     for (int c = 0; c < TT / 32; ++c) ptx::tmem_loaded(sc[c]);
-                    float scale = p.scale_log2;
-                    if constexpr (MOD) {
-                        // the scores themselves, in base-2 units
-                        scale = 1.f;
-                        const float k1 = p.scale_log2 * p.scale_sign;
-                        if (p.softcap > 0.f) {
-                            // cap tanh(x) = cap - 2 cap / (1 + e^(2x))
-                            const float cap2 = p.softcap * kLog2e;
-#pragma unroll
-                            for (int c = 0; c < TT / 32; ++c)
-#pragma unroll
-                                for (int i = 0; i < 32; ++i) {
-                                    const float e = ptx::ex2_approx(
-                                        __uint_as_float(sc[c][i]) * p.tanh_log2);
-                                    sc[c][i] = __float_as_uint(
-                                        fmaf(-2.f * cap2, __fdividef(1.f, 1.f + e), cap2));
-                                }
-                        } else {
-#pragma unroll
-                            for (int c = 0; c < TT / 32; ++c)
-#pragma unroll
-                                for (int i = 0; i < 32; ++i)
-                                    sc[c][i] = __float_as_uint(__uint_as_float(sc[c][i]) * k1);
-                        }
-                        if (p.slopes != nullptr) {
-                            const float away = (float)(t0 - m);
-#pragma unroll
-                            for (int c = 0; c < TT / 32; ++c)
-#pragma unroll
-                                for (int i = 0; i < 32; ++i)
-                                    sc[c][i] = __float_as_uint(
-                                        fmaf(slope, away + (float)(c * 32 + i),
-                                             __uint_as_float(sc[c][i])));
-                        }
-                    } else if (p.scale_sign != 1.f) {
+                    const float scale = MOD ? 1.f : p.scale_log2;
+                    // f over the row's pairs of neighbours
+                    auto pairs = [&](auto f) {
 #pragma unroll
                         for (int c = 0; c < TT / 32; ++c)
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                sc[c][i] = __float_as_uint(__uint_as_float(sc[c][i]) * p.scale_sign);
+                            for (int i = 0; i < 32; i += 2) {
+                                const float2 y = f(make_float2(__uint_as_float(sc[c][i]),
+                                                               __uint_as_float(sc[c][i + 1])),
+                                                   c * 32 + i);
+                                sc[c][i] = __float_as_uint(y.x);
+                                sc[c][i + 1] = __float_as_uint(y.y);
+                            }
+                    };
+                    if constexpr (MOD) {
+                        // the scores themselves, in base-2 units
+                        if (p.softcap > 0.f) {
+                            // cap tanh(x) = cap - 2 cap / (1 + e^(2x))
+                            const float cap2 = p.softcap * kLog2e;
+                            pairs([&](float2 y, int) {
+                                y = ptx::mul2(y, make_float2(p.tanh_log2, p.tanh_log2));
+                                y = ptx::add2(make_float2(ptx::ex2_approx(y.x), ptx::ex2_approx(y.y)),
+                                              make_float2(1.f, 1.f));
+                                return ptx::fma2(make_float2(-2.f * cap2, -2.f * cap2),
+                                                 make_float2(ptx::rcp_approx(y.x),
+                                                             ptx::rcp_approx(y.y)),
+                                                 make_float2(cap2, cap2));
+                            });
+                        } else {
+                            const float k1 = p.scale_log2 * p.scale_sign;
+                            pairs([&](float2 y, int) {
+                                return ptx::mul2(y, make_float2(k1, k1));
+                            });
+                        }
+                        if (p.slopes != nullptr) {
+                            const float away = (float)(t0 - m);
+                            pairs([&](float2 y, int i) {
+                                return ptx::fma2(make_float2(slope, slope),
+                                                 ptx::add2(make_float2(away, away),
+                                                           make_float2((float)i, (float)(i + 1))),
+                                                 y);
+                            });
+                        }
+                    } else if (p.scale_sign != 1.f) {
+                        pairs([&](float2 y, int) {
+                            return ptx::mul2(y, make_float2(p.scale_sign, p.scale_sign));
+                        });
                     }
                     if (!plain) {
 #pragma unroll
@@ -849,8 +933,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                             uint32_t allow = to >= 32 ? ~0u : to <= 0 ? 0u : (1u << to) - 1u;
                             allow &= from <= 0 ? ~0u : from >= 32 ? 0u : ~0u << from;
                             const uint32_t bb = boxes >> (2 * c);
-                            allow &= ((bb & 1u) ? 0x0000ffffu : 0u) |
-                                     ((bb & 2u) ? 0xffff0000u : 0u);
+                            allow &= ((bb & 1u) ? 0x0000ffffu : 0u) | ((bb & 2u) ? 0xffff0000u : 0u);
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
                                 if (!((allow >> i) & 1u)) sc[c][i] = __float_as_uint(-INFINITY);
@@ -875,7 +958,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                         m_ref = top;
                     }
                     const float ref = (m_ref == -INFINITY ? 0.f : m_ref) - WeightBias<T>::value;
-                    // O is rescaled when a reference moved (the last O += P V is complete:
+                    // O is rescaled where a reference moved (the last O += P V is complete:
                     // S of this step is, and was issued behind it)
                     if (__any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
@@ -902,6 +985,12 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                         sum[e % 2] = ptx::add2(sum[e % 2], y);
                         return y;
                     };
+                    auto over = [&](uint64_t* bar) {
+                        ptx::tmem_wait_st();
+                        ptx::tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(bar));
+                    };
                     if (split) {
 #pragma unroll
                         for (int c = 0; c < TT / 32; ++c) {
@@ -910,6 +999,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                             for (int e = 0; e < 16; ++e) split_pair(weight(c, e), ph[e], pl[e], T());
                             ptx::tmem_st16_async(s_col + c * 16, ph);
                             ptx::tmem_st16_async(s_col + TT / 2 + c * 16, pl);
+                            if (c == 1) over(&p_half[wg]);
                         }
                     } else {
 #pragma unroll
@@ -921,13 +1011,15 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                                 ph[e] = pack2(y.x, y.y, T());
                             }
                             ptx::tmem_st16_async(s_col + c * 16, ph);
+                            if (c == 1) over(&p_half[wg]);
                         }
                     }
                     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-                    ptx::tmem_wait_st();
+                    over(&p_ready[wg]);
+                } else if (lane == 0) {
+                    ptx::mbar_arrive(ptx::smem_addr(&p_half[wg]));
+                    ptx::mbar_arrive(ptx::smem_addr(&p_ready[wg]));
                 }
-                ptx::tc_fence_before_sync();
-                ptx::mbar_arrive(ptx::smem_addr(&p_ready[wg]));
             }
             if (!ok) break;
             place0 += 2 * nt;
@@ -996,8 +1088,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] = fmaf(__uint_as_float(ov[i]), fb, v[i]);
                 }
-                if (!live) continue;
-                if (bad_v) {
+                if (bad_v && live) {
                     // infinities and NaN in the V of positions that this row sees and others
                     // do not: those before lo_all and from hi_all on
                     const int from = max(lo, tile * TT), to = min(hi, (tile + nt) * TT);
@@ -1021,21 +1112,45 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                         }
                     }
                 }
+                // Four lanes trade 16-byte pieces of their rows, so that a store writes 64
+                // bytes of each of eight rows (a row a thread: 32 lines a store, and the
+                // load/store unit's time for them was the epilogue's, 7000 cycles a unit)
+                const int quad = lane & ~3, piece = lane & 3;
                 if (direct) {
-                    uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + out_row * D +
-                                                          col0 + c);
+                    uint4 x[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        out[i] = make_uint4(pack2(v[8 * i], v[8 * i + 1], T()),
-                                            pack2(v[8 * i + 2], v[8 * i + 3], T()),
-                                            pack2(v[8 * i + 4], v[8 * i + 5], T()),
-                                            pack2(v[8 * i + 6], v[8 * i + 7], T()));
-                } else {
-                    float4* part = reinterpret_cast<float4*>(
-                        p.partial_o + ((int64_t)partial * 2 * TR + urow) * D + col0 + c);
+                        x[i] = make_uint4(pack2(v[8 * i], v[8 * i + 1], T()),
+                                          pack2(v[8 * i + 2], v[8 * i + 3], T()),
+                                          pack2(v[8 * i + 4], v[8 * i + 5], T()),
+                                          pack2(v[8 * i + 6], v[8 * i + 7], T()));
+                    trade_pieces(x, lane);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        part[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                    for (int i = 0; i < 4; ++i) {
+                        const int64_t row = __shfl_sync(0xffffffffu, out_row, quad + i);
+                        if ((live_lanes >> (quad + i)) & 1u)
+                            reinterpret_cast<uint4*>(static_cast<T*>(p.out) + row * D + col0 +
+                                                     c)[piece] = x[i];
+                    }
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint4 x[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            x[i] = make_uint4(__float_as_uint(v[16 * h + 4 * i]),
+                                              __float_as_uint(v[16 * h + 4 * i + 1]),
+                                              __float_as_uint(v[16 * h + 4 * i + 2]),
+                                              __float_as_uint(v[16 * h + 4 * i + 3]));
+                        trade_pieces(x, lane);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if ((live_lanes >> (quad + i)) & 1u)
+                                reinterpret_cast<uint4*>(
+                                    p.partial_o +
+                                    ((int64_t)partial * 2 * TR + urow - lane + quad + i) * D + col0 +
+                                    c + 16 * h)[piece] = x[i];
+                    }
                 }
             }
             if (live && !direct && (!split || wg == 0))

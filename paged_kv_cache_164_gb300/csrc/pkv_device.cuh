@@ -154,4 +154,14 @@ __device__ __forceinline__ uint32_t drop_not_finite(uint32_t& x, T) {
     return bad;
 }
 
+// Whether any of eight 16-bit values is an infinity or a NaN: its exponent's bits are all
+// set, and one more in the lowest of them carries into the sign's place.
+template <typename T>
+__device__ __forceinline__ bool any_not_finite(const uint4& x, T) {
+    constexpr uint32_t k = std::is_same<T, __half>::value ? 0x7c007c00u : 0x7f807f80u;
+    constexpr uint32_t one = std::is_same<T, __half>::value ? 0x04000400u : 0x00800080u;
+    return ((((x.x & k) + one) | ((x.y & k) + one) | ((x.z & k) + one) | ((x.w & k) + one)) &
+            0x80008000u) != 0;
+}
+
 }  // namespace pkv

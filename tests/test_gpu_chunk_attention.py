@@ -248,3 +248,34 @@ def test_a_graph_follows_the_lengths_that_its_buffers_hold():
         graph.replay()
         torch.cuda.synchronize()
         ref.assert_close(out, *ref.attention(c), before)
+
+
+def test_scores_that_jump_within_a_tile():
+    """A largest score in either half of a tile, far above what the row had before."""
+    for dtype, jump in (("fp16", 3.0), ("bf16", 3.0), ("bf16", 40.0)):
+        for at in (5, 70, 130, 200, 300):
+            c = ref.make_chunk(24, [(400, 130), (400, 1)], 4, 1, 64, 16, dtype)
+            for s in range(2):
+                c["k"][int(c["tables"][s, at // 16]), at % 16] *= jump
+            _check(c)
+
+
+@pytest.mark.parametrize("softcap,bias", [(20.0, False), (0.0, True), (15.0, True)])
+def test_masked_keys_that_are_not_finite_beside_seen_ones(softcap, bias):
+    """NaN at every other position from the first one that no row sees on, and before windows."""
+    c = ref.make_chunk(25, [(151, 20), (77, 1)], 4, 1, 64, 16, "bf16", window=33, softcap=softcap,
+                       bias=bias)
+    for s, (n, t) in enumerate(((151, 20), (77, 1))):
+        for p in range(n - t - 33, -1, -2):
+            c["k"][int(c["tables"][s, p // 16]), p % 16] = math.nan
+            c["v"][int(c["tables"][s, p // 16]), p % 16] = math.inf
+    _check(c)
+
+
+def test_a_nan_key_makes_every_row_that_sees_it_nan_under_a_cap():
+    c = ref.make_chunk(26, [(150, 140)], 2, 1, 64, 16, "bf16", softcap=10.0)
+    out, bound = ref.attention(c)
+    c["k"][int(c["tables"][0, 120 // 16]), 120 % 16] = math.nan
+    got = _call(ref.on_gpu(c)).cpu()
+    ref.assert_close(got[:110], out[:110], bound[:110])
+    assert torch.isnan(got[110:140]).all()
