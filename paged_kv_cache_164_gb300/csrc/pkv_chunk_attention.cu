@@ -26,6 +26,7 @@
 // warpgroup 128 of its rows, which meet the same tiles; a smaller one (single tokens,
 // drafted tails) gives both the same rows and every other tile, and they meet at the
 // end.  Four warps stream K and V by TMA through the block table into a ring of tiles.
+// Two warps clean the V of tiles that some rows see only in part (below), once for all.
 // One warp walks the segments and leaves what the others need of a unit in a ring in
 // shared memory, a few units ahead: walked by every warp for itself, the reads of a new
 // sequence and its tables stood before each unit's first softmax, 6 to 7 us a unit.
@@ -66,7 +67,7 @@ struct ChunkParams {
     int32_t* err_flag;
     ChunkRecord* records;  // [rounds * ctas]
     int32_t* has;          // [chunk_partials]: whether a stretch of tiles left a partial
-    float* partial_o;      // [chunk_partials][2 kChunkRows][D]
+    float* partial_o;      // [chunk_partials][D / 4][2 kChunkRows][4]
     float* partial_lse;    // [chunk_partials][2 kChunkRows], base 2
     ChunkShape shape;
     int rounds;            // at most
@@ -89,8 +90,12 @@ constexpr int kChunkTmaWarp = kChunkSoftmaxWarps;     // four producers
 constexpr int kChunkTmaWarps = 4;
 constexpr int kChunkMmaWarp = kChunkTmaWarp + kChunkTmaWarps;
 constexpr int kChunkWalkWarp = kChunkMmaWarp + 1;
-constexpr int kChunkThreads = (kChunkSoftmaxWarps + 8) * 32;  // the last two only fill up
-constexpr int kChunkReaders = kChunkSoftmaxWarps + kChunkTmaWarps + 1;  // of a unit's notes
+constexpr int kChunkCleanWarp = kChunkWalkWarp + 1;
+constexpr int kChunkCleanWarps = 2;
+constexpr int kChunkThreads = (kChunkCleanWarp + kChunkCleanWarps) * 32;
+static_assert(kChunkThreads == 512, "four warpgroups");
+constexpr int kChunkReaders =  // of a unit's notes
+    kChunkSoftmaxWarps + kChunkTmaWarps + 1 + kChunkCleanWarps;
 // Registers: the other warpgroups hand over what they do not need, so that a softmax
 // thread's row of S stays in registers.
 constexpr int kChunkLaunchRegs = 128, kChunkSoftmaxRegs = 184, kChunkOtherRegs = 72;
@@ -118,12 +123,19 @@ struct ChunkNote {
     int tile, tiles;     // tiles of the stretch; -1 tiles: the end
     int partial;         // the stretch's partial, or -1: it is the whole unit
     int flags;
-    int bad_v;           // (set by who finds a V that is not finite)
+    int bad_from, bad_to;  // tiles of the stretch whose V was not finite (by the cleaners)
     int blocks[2 * kChunkBoxes];  // of the first two tiles' boxes, as the table has them
 };
 constexpr int kNotePagesThere = 1;  // every page of the stretch is within the pool
 constexpr int kNoteAgain = 2;       // other row blocks read the same tiles
-static_assert(sizeof(ChunkNote) == 124, "notes in shared memory");
+// The stretch's tiles that every row sees whole, where all pages are there: from .. to - 1.
+__device__ __forceinline__ int chunk_plain_from(const ChunkNote& t) {
+    return t.flags & kNotePagesThere ? (t.lo_all + kChunkTile - 1) / kChunkTile - t.tile : 0;
+}
+__device__ __forceinline__ int chunk_plain_to(const ChunkNote& t) {
+    return t.flags & kNotePagesThere ? t.hi_all / kChunkTile - t.tile : 0;
+}
+static_assert(sizeof(ChunkNote) == 128, "notes in shared memory");
 
 // A segment's start, as one thread found it for all.
 struct ChunkStart {
@@ -138,9 +150,9 @@ struct ChunkTileCfg {
     static constexpr int kTileBytes = kRegions * kRegionBytes;   // K or V of a tile; Q
     static constexpr int kSlots = D == 128 ? 5 : 10;
     static constexpr int kXchBytes = 2 * kChunkRows * 8;         // (m, l) of each half and row
-    // full[slots], empty[slots], s_full[2], p_half[2], p_ready[2], o_done[2], q_ready[2],
-    // met, o_free, drain, noted[notes], read[notes]
-    static constexpr int kBarriers = 2 * kSlots + 13 + 2 * kChunkNotes;
+    // full[slots], empty[slots], clean[slots], s_full[2], p_half[2], p_ready[2], o_done[2],
+    // q_ready[2], half_done[2], met, o_free, drain, noted[notes], read[notes], cleaned[notes]
+    static constexpr int kBarriers = 3 * kSlots + 15 + 3 * kChunkNotes;
     static constexpr int kSmemBytes = (2 + kSlots) * kTileBytes + kXchBytes + kBarriers * 8 + 24 +
                                       kChunkMaxRounds * (int)sizeof(ChunkStart) +
                                       kChunkNotes * (int)sizeof(ChunkNote);
@@ -176,6 +188,42 @@ __device__ __forceinline__ int64_t warp_scan64(int64_t x) {  // inclusive
         if ((threadIdx.x & 31) >= o) x += v;
     }
     return x;
+}
+
+// Adds to a finished row what it sees of the V that the cleaners took out: infinities and
+// NaN, but for positions lo_all .. hi_all - 1, whose V was left alone.  (Whatever finite
+// value stands there, the sum is the same.)
+struct ChunkSeen {
+    const int32_t* table;
+    int from, to;  // positions of the stretch that the row sees
+    int lo_all, hi_all;
+    int g;
+};
+__device__ __forceinline__ float as_float(__half x) { return __half2float(x); }
+__device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename T, int D, typename At>
+__device__ __forceinline__ void add_not_finite(const ChunkParams& p, const ChunkSeen& s, int col0,
+                                               int cols, At at) {
+    const int bs = p.block_size;
+#pragma unroll 1
+    for (int x = s.from; x < s.to; ++x) {
+        if (x >= s.lo_all && x < s.hi_all) {
+            x = min(s.hi_all, s.to) - 1;
+            continue;
+        }
+        const int blk = __ldg(s.table + x / bs);
+        if (blk < 0 || blk >= p.num_blocks) continue;
+        const int off = x % bs;
+        const uint16_t* v =
+            static_cast<const uint16_t*>(p.v_cache) +
+            (p.hnd ? ((int64_t)blk * p.shape.heads + s.g) * bs + off
+                   : ((int64_t)blk * bs + off) * p.shape.heads + s.g) * D;
+#pragma unroll 1
+        for (int c = col0; c < col0 + cols; ++c) {
+            const uint16_t e = __ldg(v + c);
+            if (not_finite(e, T())) at(c, unpack2(e, T()).x);
+        }
+    }
 }
 
 // Four lanes with four 16-byte pieces each: lane k's piece i becomes lane i's piece k.
@@ -214,16 +262,19 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
     float2* xch = reinterpret_cast<float2*>(ring + NS * Cfg::kTileBytes);
     uint64_t* full_bar = reinterpret_cast<uint64_t*>(ring + NS * Cfg::kTileBytes + Cfg::kXchBytes);
     uint64_t* empty_bar = full_bar + NS;
-    uint64_t* s_full = empty_bar + NS;  // [warpgroup]
+    uint64_t* clean_bar = empty_bar + NS;  // of a V that is cleaned
+    uint64_t* s_full = clean_bar + NS;  // [warpgroup]
     uint64_t* p_half = s_full + 2;      // [warpgroup]: the first 64 positions' weights
     uint64_t* p_ready = p_half + 2;     // [warpgroup]: all of them
     uint64_t* o_done = p_ready + 2;   // [warpgroup]: a unit's last product is complete
     uint64_t* q_ready = o_done + 2;     // [warpgroup]
-    uint64_t* met = q_ready + 2;        // both are through a split unit
+    uint64_t* half_done = q_ready + 2;  // [warpgroup]: the product with the first half is complete
+    uint64_t* met = half_done + 2;         // both are through a split unit
     uint64_t* o_free = met + 1;         // both have read O_0, O_1 and the exchange of one
     uint64_t* drain = o_free + 1;
     uint64_t* noted = drain + 1;        // [notes]
     uint64_t* read = noted + kChunkNotes;  // [notes]: by all readers
+    uint64_t* cleaned = read + kChunkNotes;  // [notes]: every tile of the unit
     int64_t* s_line = reinterpret_cast<int64_t*>(full_bar + Cfg::kBarriers);
     int* words = reinterpret_cast<int*>(s_line + 1);
     volatile int* abort_flag = words;
@@ -243,7 +294,8 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) {
             ptx::mbar_init(ptx::smem_addr(&full_bar[i]), kChunkTmaWarps);
-            ptx::mbar_init(ptx::smem_addr(&empty_bar[i]), 1);
+            ptx::mbar_init(ptx::smem_addr(&empty_bar[i]), 1 + kChunkCleanWarps);
+            ptx::mbar_init(ptx::smem_addr(&clean_bar[i]), kChunkCleanWarps);
         }
         for (int w = 0; w < 2; ++w) {
             ptx::mbar_init(ptx::smem_addr(&s_full[w]), 1);
@@ -251,6 +303,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             ptx::mbar_init(ptx::smem_addr(&p_ready[w]), TR / 32);
             ptx::mbar_init(ptx::smem_addr(&o_done[w]), 1);
             ptx::mbar_init(ptx::smem_addr(&q_ready[w]), TR);
+            ptx::mbar_init(ptx::smem_addr(&half_done[w]), 1);
         }
         ptx::mbar_init(ptx::smem_addr(met), 2 * TR);
         ptx::mbar_init(ptx::smem_addr(o_free), 2 * TR);
@@ -258,6 +311,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
         for (int i = 0; i < kChunkNotes; ++i) {
             ptx::mbar_init(ptx::smem_addr(&noted[i]), 1);
             ptx::mbar_init(ptx::smem_addr(&read[i]), kChunkReaders);
+            ptx::mbar_init(ptx::smem_addr(&cleaned[i]), kChunkCleanWarps);
         }
         *abort_flag = 0;
         ptx::fence_barrier_init();
@@ -472,6 +526,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             int slot = 0, phase = 0;  // of the ring's next place
             int step[2] = {0, 0};     // tiles of each warpgroup so far
             int unit[2] = {0, 0};     // units with tiles for it
+            uint32_t cleans = 0;      // parity of the slots' cleanings
             bool ok = true;
             auto wait = [&](uint64_t* bar, int parity) {
                 return warp_wait_phase(ptx::smem_addr(bar), parity & 1, abort_flag, p.err_flag);
@@ -503,6 +558,14 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 }
                 __syncwarp();
             };
+            // the V there, once it is clean where it has to be
+            auto take_v = [&](bool cleaned_first) {
+                const int at = take();
+                if (at < 0 || !cleaned_first) return at;
+                const int parity = (cleans >> at) & 1;
+                cleans ^= 1u << at;
+                return wait(&clean_bar[at], parity) ? at : -1;
+            };
             // O += P V of warpgroup w from the V in slot `at`
             auto issue_pv = [&](int w, int at, bool split, bool first, bool ends, bool last) {
                 const uint64_t vd = vdesc + (uint32_t)(at * (Cfg::kTileBytes / 16));
@@ -513,15 +576,19 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                     for (int i = 0; i < TT / 32; ++i) {
                         const int kt = h * (TT / 32) + i;
                         const uint64_t v = vd + (uint32_t)(kt * 16 * 128 / 16);
-                        ptx::tc_mma_f16_ts(acc, pt + kt * 8, v, idesc_o,
-                                           (!first || kt > 0) ? 1u : 0u);
-                        // (a split unit's weights have a second term)
-                        if (split) ptx::tc_mma_f16_ts(acc, pt + TT / 2 + kt * 8, v, idesc_o, 1u);
+                        // of each 32 positions of P, 16 columns of pairs and 16 of their
+                        // second terms, which a split unit's weights have
+                        const uint32_t a = pt + (kt / 2) * 32 + (kt % 2) * 8;
+                        ptx::tc_mma_f16_ts(acc, a, v, idesc_o, (!first || kt > 0) ? 1u : 0u);
+                        if (split) ptx::tc_mma_f16_ts(acc, a + 16, v, idesc_o, 1u);
                     }
                 };
                 if (!wait(&p_half[w], step[w])) return false;
                 ptx::tc_fence_after_sync();
-                if (ptx::elect_one()) half(0);
+                if (ptx::elect_one()) {
+                    half(0);
+                    ptx::tc_commit(ptx::smem_addr(&half_done[w]));
+                }
                 __syncwarp();
                 if (!wait(&p_ready[w], step[w])) return false;
                 ++step[w];
@@ -539,6 +606,10 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 const int nt = __shfl_sync(0xffffffffu, note.tiles, 0);
                 const bool split =
                     __shfl_sync(0xffffffffu, note.tokens * group <= TR ? 1 : 0, 0);
+                // tiles of the stretch that every row sees, of pages that are there
+                const int plain0 = __shfl_sync(0xffffffffu, chunk_plain_from(note), 0);
+                const int plain1 = __shfl_sync(0xffffffffu, chunk_plain_to(note), 0);
+                auto dirty = [&](int j) { return j < plain0 || j >= plain1; };
                 note_read(u);
                 if (nt < 0) break;
                 ok = wait(&q_ready[0], unit[0]++);
@@ -554,7 +625,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                     }
                     for (int j = 0; j < nt && ok; ++j) {
                         const int w = j & 1;
-                        at = take();
+                        at = take_v(dirty(j));
                         ok = at >= 0 && issue_pv(w, at, true, j < 2, j + 2 >= nt, true);
                         if (ok && j + 2 < nt) {
                             at = take();
@@ -569,7 +640,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                     issue_s(1, at, true);
                     for (int j = 0; j < nt && ok; ++j) {
                         const bool more = j + 1 < nt;
-                        const int v = take();
+                        const int v = take_v(dirty(j));
                         ok = v >= 0 && issue_pv(0, v, false, j == 0, !more, false);
                         int k = -1;
                         if (ok && more) {
@@ -683,7 +754,8 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                         note.partial = cut ? chunk_partial(segment, t.begins) : -1;
                         note.flags = (there ? kNotePagesThere : 0) |
                                      (t.seq.tokens > p.shape.block_tokens ? kNoteAgain : 0);
-                        note.bad_v = 0;
+                        note.bad_from = INT_MAX;
+                        note.bad_to = 0;
                     }
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&noted[u % kChunkNotes]));
@@ -694,6 +766,127 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 notes[u % kChunkNotes].tiles = -1;
                 ptx::mbar_arrive(ptx::smem_addr(&noted[u % kChunkNotes]));
             }
+        } else {
+            // ------------------------------------------------------------ cleaners
+            // V rows that are not there hold stale bytes, and one that only some rows see may
+            // hold infinities or NaN: zeroed in shared memory, so that 0 * V is 0; the rows
+            // that do see such a value get it back at the end.  They pass every place of
+            // the ring in its order and release it like the issuer (a reader that kept to
+            // the tiles it has work in could not tell a slot's fills apart by their parity).
+            const int half = warp - kChunkCleanWarp;
+            constexpr int kCells = R * 8;                    // 16-byte cells of a row
+            constexpr int kRowsEach = TT / kChunkCleanWarps;
+            int slot = 0, phase = 0;
+            bool ok = true;
+            auto full = [&] {
+                return warp_wait_phase(ptx::smem_addr(&full_bar[slot]), phase, abort_flag,
+                                       p.err_flag);
+            };
+            auto leave = [&] {
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&empty_bar[slot]));
+                if (++slot == NS) {
+                    slot = 0;
+                    phase ^= 1;
+                }
+            };
+            for (int u = 0; ok && note_there(u); ++u) {
+                ChunkNote& t = notes[u % kChunkNotes];
+                const int nt = t.tiles, tile = t.tile;
+                if (nt < 0) break;
+                const bool split = t.tokens * group <= TR;
+                const bool there = t.flags & kNotePagesThere;
+                const int lo = t.lo, hi = t.hi, lo_all = t.lo_all, hi_all = t.hi_all;
+                const int plain0 = chunk_plain_from(t), plain1 = chunk_plain_to(t);
+                const int32_t* table = p.block_tables + (int64_t)t.b * p.max_blocks_per_seq;
+                auto box_block = [&](int j) {  // lanes 0-7
+                    const int at = (tile + j) * TT + lane * kStageTokens;
+                    return !there && lane < kChunkBoxes && j < nt && at + kStageTokens > lo &&
+                                   at < hi
+                               ? __ldg(table + (at >> bs_shift))
+                               : -1;
+                };
+                int blk = box_block(0);
+                auto pass_k = [&] {
+                    if (!full()) return false;
+                    leave();
+                    return true;
+                };
+                auto clean_v = [&](int j) {
+                    const bool dirty = j < plain0 || j >= plain1;
+                    uint32_t boxes = (1u << kChunkBoxes) - 1u;
+                    if (!there) {
+                        boxes = __ballot_sync(0xffffffffu, blk >= 0 && blk < p.num_blocks);
+                        blk = box_block(j + 1);
+                    }
+                    if (!full()) return false;
+                    if (!dirty) {
+                        leave();
+                        return true;
+                    }
+                    const int t0 = (tile + j) * TT;
+                    // a lane keeps to its 16-byte column of every (32 / kCells)-th row
+                    uint8_t* column = ring + slot * Cfg::kTileBytes +
+                                      (lane % kCells / 8) * Cfg::kRegionBytes + (lane % 8) * 16;
+                    constexpr int kStep = 32 / kCells;
+                    auto zero = [&](int row0, int row1) {
+                        row1 = min(row1, (half + 1) * kRowsEach);
+                        for (int r = max(row0, half * kRowsEach) + lane / kCells; r < row1; r += kStep)
+                            *reinterpret_cast<uint4*>(column + r * 128) = make_uint4(0u, 0u, 0u, 0u);
+                    };
+                    auto look_through = [&](int row0, int row1) {
+                        row1 = min(row1, (half + 1) * kRowsEach);
+                        for (int r = max(row0, half * kRowsEach) + lane / kCells; r < row1;
+                             r += 4 * kStep) {
+                            uint4 x[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                x[k] = r + k * kStep < row1 ? *reinterpret_cast<const uint4*>(
+                                                                  column + (r + k * kStep) * 128)
+                                                            : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (any_not_finite(x[k], T())) {
+                                    drop_not_finite(x[k].x, T());
+                                    drop_not_finite(x[k].y, T());
+                                    drop_not_finite(x[k].z, T());
+                                    drop_not_finite(x[k].w, T());
+                                    atomicMin(&t.bad_from, j);
+                                    atomicMax(&t.bad_to, j + 1);
+                                    *reinterpret_cast<uint4*>(column + (r + k * kStep) * 128) = x[k];
+                                }
+                        }
+                    };
+                    // rows of the tile: none sees those before `a` and from `d` on, all see
+                    // those from `b` to `c`
+                    auto in_tile = [&](int x) { return min(max(x - t0, 0), TT); };
+                    const int a = in_tile(lo), d = max(in_tile(hi), a);
+                    const int b = min(max(in_tile(lo_all), a), d);
+                    const int c = min(max(in_tile(hi_all), b), d);
+                    zero(0, a);
+                    look_through(a, b);
+                    look_through(c, d);
+                    zero(d, TT);
+                    if (boxes != (1u << kChunkBoxes) - 1u)
+                        for (int x = 0; x < kChunkBoxes; ++x)
+                            if (!((boxes >> x) & 1u)) zero(x * kStageTokens, (x + 1) * kStageTokens);
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&clean_bar[slot]));
+                    leave();
+                    return true;
+                };
+                if (split) {
+                    ok = pass_k() && (nt < 2 || pass_k());
+                    for (int j = 0; j < nt && ok; ++j) ok = clean_v(j) && (j + 2 >= nt || pass_k());
+                } else {
+                    for (int j = 0; j < nt && ok; ++j) ok = pass_k() && clean_v(j);
+                }
+                if (!ok) break;
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&cleaned[u % kChunkNotes]));
+                note_read(u);
+            }
         }
     } else {
         // ------------------------------------------------------------ softmax rows
@@ -703,7 +896,6 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
         const uint32_t lane_base = (uint32_t)(32 * (warp % 4)) << 16;
         const uint32_t s_col = tmem + lane_base + wg * TT;
         const uint32_t o_col = tmem + lane_base + Cfg::kColO;
-        int place0 = 0;
         int step = 0;                     // this warpgroup's tiles so far
         int own = 0;                      // units with tiles for it
         int splits = 0;                   // split units so far
@@ -726,21 +918,21 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
         auto load_q = [&](const ChunkNote& t) {
             int head;
             const int token = row_of(t, head);
+            const bool live = token >= 0;
             const uint4* src = reinterpret_cast<const uint4*>(
                 static_cast<const T*>(p.q) +
-                ((int64_t)(t.q_row + max(token, 0)) * p.num_q_heads + head) * D);
+                ((int64_t)(t.q_row + max(token, 0)) * p.num_q_heads + (live ? head : 0)) * D);
 #pragma unroll
             for (int c = 0; c < D / 8; ++c)
                 ptx::cp_async_16(q_addr + wg * Cfg::kTileBytes + (c / 8) * Cfg::kRegionBytes +
                                      srow * 128 + (((c % 8) ^ (srow & 7)) << 4),
-                                 token >= 0 ? src + c : src, token >= 0);
+                                 src + c, live);
         };
         auto q_loaded = [&] {
             ptx::cp_async_wait_all();
             ptx::fence_proxy_async_smem();
             ptx::mbar_arrive(ptx::smem_addr(&q_ready[wg]));
         };
-
         if (note_there(0)) {
             if (tiles_of(notes[0]) > 0) {
                 load_q(notes[0]);
@@ -774,7 +966,6 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                            ? __ldg(table + (at >> bs_shift))
                            : -1;
             };
-
             float m_ref = -INFINITY, l = 0.f;
             const int j0 = split ? wg : 0, by = split ? 2 : 1;
             int blk = box_block(j0), blk_next = box_block(j0 + by);  // two steps ahead
@@ -802,64 +993,6 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                     }
                     if (tiles_of(ahead) > 0) load_q(ahead);
                 }
-                if (!plain) {
-                    // V rows that are not there hold stale bytes, and one that only some
-                    // rows see may hold infinities or NaN: zeroed in shared memory, so that
-                    // 0 * V is 0; the rows that do see such a value get it back at the end.
-                    const int at = place0 + chunk_place(split, true, j, nt);
-                    const int slot = at % NS;
-                    if (!warp_wait_phase(ptx::smem_addr(&full_bar[slot]), (at / NS) & 1,
-                                         abort_flag, p.err_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    uint8_t* vst = ring + slot * Cfg::kTileBytes;
-                    constexpr int kCells = R * 8;  // 16-byte cells of a row
-                    auto clean = [&](int row0, int row1) {
-                        for (int i0 = row0 * kCells + srow; i0 < row1 * kCells; i0 += 4 * TR) {
-                            uint4 x[4];
-                            uint4* cell[4];
-                            int is[4];  // 0: nothing, 1: zeroed, 2: looked through
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const int idx = i0 + k * TR;
-                                const int row = idx / kCells, rem = idx % kCells;
-                                cell[k] = reinterpret_cast<uint4*>(
-                                    vst + (rem / 8) * Cfg::kRegionBytes + row * 128 + (rem % 8) * 16);
-                                const int pos = t0 + row;
-                                is[k] = idx >= row1 * kCells ? 0
-                                        : pos < t.lo || pos >= t.hi ||
-                                                !((boxes >> (row / kStageTokens)) & 1u)
-                                            ? 1
-                                        : pos >= lo_all && pos < hi_all ? 0
-                                                                        : 2;
-                                x[k] = is[k] == 2 ? *cell[k] : make_uint4(0u, 0u, 0u, 0u);
-                            }
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                if (is[k] == 1) *cell[k] = x[k];
-                                if (is[k] == 2 && any_not_finite(x[k], T())) {
-                                    drop_not_finite(x[k].x, T());
-                                    drop_not_finite(x[k].y, T());
-                                    drop_not_finite(x[k].z, T());
-                                    drop_not_finite(x[k].w, T());
-                                    *const_cast<volatile int*>(&t.bad_v) = 1;
-                                    __threadfence_block();  // before the value is gone
-                                    *cell[k] = x[k];
-                                }
-                            }
-                        }
-                    };
-                    if (boxes == (1u << kChunkBoxes) - 1u) {
-                        const int before = min(max(lo_all - t0, 0), TT);
-                        const int behind = max(min(max(hi_all - t0, 0), TT), before);
-                        clean(0, before);
-                        clean(behind, TT);
-                    } else {
-                        clean(0, TT);
-                    }
-                    ptx::fence_proxy_async_smem();
-                }
                 if (free_due) {
                     // both warpgroups have read O_0, O_1 and the exchange of the split unit
                     // before; neither is written anew until then
@@ -871,160 +1004,172 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                     free_due = false;
                 }
                 if (warp_live) {
-                    uint32_t sc[TT / 32][32];
-                    __syncwarp();
-#pragma unroll
-                    for (int c = 0; c < TT / 32; ++c) ptx::tmem_ld32_async(s_col + c * 32, sc[c]);
-                    ptx::tmem_wait_ld();
-#pragma unroll
-                    for (int c = 0; c < TT / 32; ++c) ptx::tmem_loaded(sc[c]);
                     const float scale = MOD ? 1.f : p.scale_log2;
-                    // f over the row's pairs of neighbours
-                    auto pairs = [&](auto f) {
+                    // Half a tile at a time, one loop for both: unrolled for the whole tile, the
+                    // instructions did not stay in their cache beside the other warps'.
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t r[2][32];
+                        const int at = t0 + h * (TT / 2);
+                        const uint32_t col = s_col + h * (TT / 2);
+                        __syncwarp();
+                        ptx::tmem_ld32_async(col, r[0]);
+                        ptx::tmem_ld32_async(col + 32, r[1]);
+                        ptx::tmem_wait_ld();
+                        ptx::tmem_loaded(r[0]);
+                        ptx::tmem_loaded(r[1]);
+                        // f over the pairs of neighbouring scores
+                        auto pairs = [&](auto f) {
 #pragma unroll
-                        for (int c = 0; c < TT / 32; ++c)
+                            for (int c = 0; c < 2; ++c)
 #pragma unroll
-                            for (int i = 0; i < 32; i += 2) {
-                                const float2 y = f(make_float2(__uint_as_float(sc[c][i]),
-                                                               __uint_as_float(sc[c][i + 1])),
-                                                   c * 32 + i);
-                                sc[c][i] = __float_as_uint(y.x);
-                                sc[c][i + 1] = __float_as_uint(y.y);
+                                for (int i = 0; i < 32; i += 2) {
+                                    const float2 y = f(make_float2(__uint_as_float(r[c][i]),
+                                                                   __uint_as_float(r[c][i + 1])),
+                                                       c * 32 + i);
+                                    r[c][i] = __float_as_uint(y.x);
+                                    r[c][i + 1] = __float_as_uint(y.y);
+                                }
+                        };
+                        if constexpr (MOD) {
+                            // the scores themselves, in base-2 units
+                            if (p.softcap > 0.f) {
+                                // cap tanh(x) = cap - 2 cap / (1 + e^(2x))
+                                const float cap2 = p.softcap * kLog2e;
+                                pairs([&](float2 y, int) {
+                                    y = ptx::mul2(y, make_float2(p.tanh_log2, p.tanh_log2));
+                                    y = ptx::add2(
+                                        make_float2(ptx::ex2_approx(y.x), ptx::ex2_approx(y.y)),
+                                        make_float2(1.f, 1.f));
+                                    return ptx::fma2(make_float2(-2.f * cap2, -2.f * cap2),
+                                                     make_float2(ptx::rcp_approx(y.x),
+                                                                 ptx::rcp_approx(y.y)),
+                                                     make_float2(cap2, cap2));
+                                });
+                            } else {
+                                const float k1 = p.scale_log2 * p.scale_sign;
+                                pairs([&](float2 y, int) {
+                                    return ptx::mul2(y, make_float2(k1, k1));
+                                });
                             }
-                    };
-                    if constexpr (MOD) {
-                        // the scores themselves, in base-2 units
-                        if (p.softcap > 0.f) {
-                            // cap tanh(x) = cap - 2 cap / (1 + e^(2x))
-                            const float cap2 = p.softcap * kLog2e;
+                            if (p.slopes != nullptr) {
+                                const float away = (float)(at - m);
+                                pairs([&](float2 y, int i) {
+                                    return ptx::fma2(make_float2(slope, slope),
+                                                     ptx::add2(make_float2(away, away),
+                                                               make_float2((float)i, (float)(i + 1))),
+                                                     y);
+                                });
+                            }
+                        } else if (p.scale_sign != 1.f) {
                             pairs([&](float2 y, int) {
-                                y = ptx::mul2(y, make_float2(p.tanh_log2, p.tanh_log2));
-                                y = ptx::add2(make_float2(ptx::ex2_approx(y.x), ptx::ex2_approx(y.y)),
-                                              make_float2(1.f, 1.f));
-                                return ptx::fma2(make_float2(-2.f * cap2, -2.f * cap2),
-                                                 make_float2(ptx::rcp_approx(y.x),
-                                                             ptx::rcp_approx(y.y)),
-                                                 make_float2(cap2, cap2));
-                            });
-                        } else {
-                            const float k1 = p.scale_log2 * p.scale_sign;
-                            pairs([&](float2 y, int) {
-                                return ptx::mul2(y, make_float2(k1, k1));
+                                return ptx::mul2(y, make_float2(p.scale_sign, p.scale_sign));
                             });
                         }
-                        if (p.slopes != nullptr) {
-                            const float away = (float)(t0 - m);
-                            pairs([&](float2 y, int i) {
-                                return ptx::fma2(make_float2(slope, slope),
-                                                 ptx::add2(make_float2(away, away),
-                                                           make_float2((float)i, (float)(i + 1))),
-                                                 y);
-                            });
+                        if (!plain) {
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                const int from = lo - (at + c * 32), to = hi - (at + c * 32);
+                                uint32_t allow = to >= 32 ? ~0u : to <= 0 ? 0u : (1u << to) - 1u;
+                                allow &= from <= 0 ? ~0u : from >= 32 ? 0u : ~0u << from;
+                                const uint32_t bb = boxes >> (4 * h + 2 * c);
+                                allow &= ((bb & 1u) ? 0x0000ffffu : 0u) |
+                                         ((bb & 2u) ? 0xffff0000u : 0u);
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    if (!((allow >> i) & 1u)) r[c][i] = __float_as_uint(-INFINITY);
+                            }
                         }
-                    } else if (p.scale_sign != 1.f) {
-                        pairs([&](float2 y, int) {
-                            return ptx::mul2(y, make_float2(p.scale_sign, p.scale_sign));
-                        });
-                    }
-                    if (!plain) {
-#pragma unroll
-                        for (int c = 0; c < TT / 32; ++c) {
-                            const int from = lo - (t0 + c * 32), to = hi - (t0 + c * 32);
-                            uint32_t allow = to >= 32 ? ~0u : to <= 0 ? 0u : (1u << to) - 1u;
-                            allow &= from <= 0 ? ~0u : from >= 32 ? 0u : ~0u << from;
-                            const uint32_t bb = boxes >> (2 * c);
-                            allow &= ((bb & 1u) ? 0x0000ffffu : 0u) | ((bb & 2u) ? 0xffff0000u : 0u);
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (!((allow >> i) & 1u)) sc[c][i] = __float_as_uint(-INFINITY);
-                        }
-                    }
-                    float mx[4];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        mx[c] = fmaxf(__uint_as_float(sc[c][0]), __uint_as_float(sc[c][1]));
-#pragma unroll
-                    for (int i = 2; i < 32; i += 2)
+                        float mx[4];
 #pragma unroll
                         for (int c = 0; c < 4; ++c)
-                            mx[c] = fmaxf(fmaxf(mx[c], __uint_as_float(sc[c][i])),
-                                          __uint_as_float(sc[c][i + 1]));
-                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
-                    float alpha = 1.f;
-                    if (m_ref == -INFINITY) {
-                        m_ref = top;  // O and l are still zero for this row
-                    } else if (top > m_ref + kChunkLazyLog2) {
-                        alpha = ptx::ex2_approx(m_ref - top);
-                        m_ref = top;
-                    }
-                    const float ref = (m_ref == -INFINITY ? 0.f : m_ref) - WeightBias<T>::value;
-                    // O is rescaled where a reference moved (the last O += P V is complete:
-                    // S of this step is, and was issued behind it)
-                    if (__any_sync(0xffffffffu, alpha != 1.f)) {
-#pragma unroll 1
-                        for (int c = 0; c < D / 32; ++c) {
-                            uint32_t ov[32];
-                            __syncwarp();
-                            ptx::tmem_ld32(o_col + wg * D + c * 32, ov);
+                            mx[c] = fmaxf(__uint_as_float(r[c / 2][(c & 1) * 16]),
+                                          __uint_as_float(r[c / 2][(c & 1) * 16 + 1]));
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
-                            ptx::tmem_st32(o_col + wg * D + c * 32, ov);
+                        for (int i = 2; i < 16; i += 2)
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)
+                                mx[c] = fmaxf(
+                                    fmaxf(mx[c], __uint_as_float(r[c / 2][(c & 1) * 16 + i])),
+                                    __uint_as_float(r[c / 2][(c & 1) * 16 + i + 1]));
+                        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+                        float alpha = 1.f;
+                        if (m_ref == -INFINITY) {
+                            m_ref = top;  // O and l are still zero for this row
+                        } else if (top > m_ref + kChunkLazyLog2) {
+                            alpha = ptx::ex2_approx(m_ref - top);
+                            m_ref = top;
                         }
-                        l *= alpha;
-                    }
-                    const float2 scale2 = make_float2(scale, scale);
-                    const float2 ref2 = make_float2(-ref, -ref);
-                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                    auto weight = [&](int c, int e) {
-                        float2 y = ptx::fma2(make_float2(__uint_as_float(sc[c][2 * e]),
-                                                         __uint_as_float(sc[c][2 * e + 1])),
-                                             scale2, ref2);
-                        y.x = ptx::ex2_approx(y.x);
-                        y.y = ptx::ex2_approx(y.y);
-                        sum[e % 2] = ptx::add2(sum[e % 2], y);
-                        return y;
-                    };
-                    auto over = [&](uint64_t* bar) {
+                        // O is rescaled where a reference moved, once the product before is
+                        // complete (that of the tile before is: S of this one is, and was
+                        // issued behind it)
+                        if (__any_sync(0xffffffffu, alpha != 1.f)) {
+                            if (h > 0) {
+                                ok = warp_wait_phase(ptx::smem_addr(&half_done[wg]), step & 1,
+                                                     abort_flag, p.err_flag);
+                                if (!ok) break;
+                                ptx::tc_fence_after_sync();
+                            }
+#pragma unroll 1
+                            for (int c = 0; c < D / 16; ++c) {
+                                uint32_t ov[16];
+                                __syncwarp();
+                                ptx::tmem_ld16(o_col + wg * D + c * 16, ov);
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+                                ptx::tmem_st16_async(o_col + wg * D + c * 16, ov);
+                            }
+                            l *= alpha;
+                        }
+                        const float ref =
+                            (m_ref == -INFINITY ? 0.f : m_ref) - WeightBias<T>::value;
+                        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                        pairs([&](float2 y, int i) {
+                            y = ptx::fma2(y, make_float2(scale, scale), make_float2(-ref, -ref));
+                            y = make_float2(ptx::ex2_approx(y.x), ptx::ex2_approx(y.y));
+                            sum[i / 2 % 2] = ptx::add2(sum[i / 2 % 2], y);
+                            return y;
+                        });
+                        if (split) {
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                uint32_t pp[32];
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    split_pair(make_float2(__uint_as_float(r[c][2 * e]),
+                                                           __uint_as_float(r[c][2 * e + 1])),
+                                               pp[e], pp[16 + e], T());
+                                ptx::tmem_st32_async(col + c * 32, pp);
+                            }
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                uint32_t ph[16];
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    ph[e] = pack2(__uint_as_float(r[c][2 * e]),
+                                                  __uint_as_float(r[c][2 * e + 1]), T());
+                                ptx::tmem_st16_async(col + c * 32, ph);
+                            }
+                        }
+                        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                         ptx::tmem_wait_st();
                         ptx::tc_fence_before_sync();
                         __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(bar));
-                    };
-                    if (split) {
-#pragma unroll
-                        for (int c = 0; c < TT / 32; ++c) {
-                            uint32_t ph[16], pl[16];
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) split_pair(weight(c, e), ph[e], pl[e], T());
-                            ptx::tmem_st16_async(s_col + c * 16, ph);
-                            ptx::tmem_st16_async(s_col + TT / 2 + c * 16, pl);
-                            if (c == 1) over(&p_half[wg]);
-                        }
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < TT / 32; ++c) {
-                            uint32_t ph[16];
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                const float2 y = weight(c, e);
-                                ph[e] = pack2(y.x, y.y, T());
-                            }
-                            ptx::tmem_st16_async(s_col + c * 16, ph);
-                            if (c == 1) over(&p_half[wg]);
-                        }
+                        if (lane == 0)
+                            ptx::mbar_arrive(ptx::smem_addr(h == 0 ? &p_half[wg] : &p_ready[wg]));
                     }
-                    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-                    over(&p_ready[wg]);
+                    if (!ok) break;
                 } else if (lane == 0) {
                     ptx::mbar_arrive(ptx::smem_addr(&p_half[wg]));
                     ptx::mbar_arrive(ptx::smem_addr(&p_ready[wg]));
                 }
             }
             if (!ok) break;
-            place0 += 2 * nt;
             if (mine == 0 && !note_there(u + 1)) break;
-            if (tiles_of(ahead) > 0) {
+            const bool load_ahead = tiles_of(ahead) > 0;
+            if (load_ahead) {
                 if (mine == 0) load_q(ahead);
                 q_loaded();
             }
@@ -1036,12 +1181,12 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 ++own;
             }
             float fa, fb = 0.f, lse;  // out = O_0 fa + O_1 fb (not split: O_w fa)
-            bool two = false;         // O_1 has something
+            const bool two = split && nt > 1;  // O_1 has something
             if (!split) {
                 fa = l == 0.f ? 0.f : 1.f / l;
                 lse = l == 0.f ? -INFINITY : m_ref - WeightBias<T>::value + log2f(l);
             } else {
-                // both warpgroups are through: their halves of the softmax meet
+                // both warpgroups are through: their parts of the softmax meet
                 if (free_due) {
                     if (!warp_wait_phase(ptx::smem_addr(o_free), (splits - 1) & 1, abort_flag,
                                          p.err_flag))
@@ -1054,7 +1199,6 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 if (!warp_wait_phase(ptx::smem_addr(met), splits & 1, abort_flag, p.err_flag))
                     break;
                 const float2 ha = xch[srow], hb = xch[TR + srow];
-                two = nt > 1;
                 const float mm = fmaxf(ha.x, hb.x);
                 fa = ha.x == -INFINITY ? 0.f : ptx::ex2_approx(ha.x - mm);
                 fb = hb.x == -INFINITY ? 0.f : ptx::ex2_approx(hb.x - mm);
@@ -1067,13 +1211,21 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             ptx::tc_fence_after_sync();
             const int partial = t.partial;
             const bool direct = partial < 0;
-            const bool bad_v = *const_cast<volatile int*>(&t.bad_v) != 0;
+            if (!warp_wait_phase(ptx::smem_addr(&cleaned[u % kChunkNotes]), (u / kChunkNotes) & 1,
+                                 abort_flag, p.err_flag))
+                break;
+            const bool bad_v = t.bad_to != 0;
             // Columns: the whole row; of a split unit this warpgroup's half.
             const int cols = split ? D / 2 : D;
             const int col0 = split ? wg * cols : 0;
             const int64_t out_row =
-                (int64_t)(t.q_row + max(token, 0)) * p.num_q_heads + head;
+                (int64_t)(t.q_row + max(token, 0)) * p.num_q_heads + (live ? head : 0);
             const int urow = split ? srow : wg * TR + srow;
+            // where columns 4 c .. of row r of the partial lie
+            auto partial_at = [&](int c, int r) {
+                return reinterpret_cast<float4*>(p.partial_o) +
+                       ((int64_t)partial * (D / 4) + c) * 2 * TR + r;
+            };
 #pragma unroll 1
             for (int c = 0; c < cols; c += 32) {
                 if (!warp_live) break;
@@ -1088,35 +1240,10 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] = fmaf(__uint_as_float(ov[i]), fb, v[i]);
                 }
-                if (bad_v && live) {
-                    // infinities and NaN in the V of positions that this row sees and others
-                    // do not: those before lo_all and from hi_all on
-                    const int from = max(lo, tile * TT), to = min(hi, (tile + nt) * TT);
-                    for (int x = from; x < to; ++x) {
-                        if (x >= lo_all && x < hi_all) {
-                            x = min(hi_all, to) - 1;
-                            continue;
-                        }
-                        const int vb = __ldg(table + (x >> bs_shift));
-                        if (vb < 0 || vb >= p.num_blocks) continue;
-                        const int off = x & (bs - 1);
-                        const uint16_t* vr =
-                            static_cast<const uint16_t*>(p.v_cache) +
-                            (p.hnd ? ((int64_t)vb * p.shape.heads + t.g) * bs + off
-                                   : ((int64_t)vb * bs + off) * p.shape.heads + t.g) * D +
-                            col0 + c;
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const uint16_t e = __ldg(vr + i);
-                            if (not_finite(e, T())) v[i] += unpack2(e, T()).x;
-                        }
-                    }
-                }
-                // Four lanes trade 16-byte pieces of their rows, so that a store writes 64
-                // bytes of each of eight rows (a row a thread: 32 lines a store, and the
-                // load/store unit's time for them was the epilogue's, 7000 cycles a unit)
-                const int quad = lane & ~3, piece = lane & 3;
                 if (direct) {
+                    // Four lanes trade 16-byte pieces of their rows, so that a store writes
+                    // 64 bytes of each of eight rows, not 16 of 32
+                    const int quad = lane & ~3, piece = lane & 3;
                     uint4 x[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
@@ -1132,26 +1259,25 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                             reinterpret_cast<uint4*>(static_cast<T*>(p.out) + row * D + col0 +
                                                      c)[piece] = x[i];
                     }
-                } else {
+                } else if (live) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint4 x[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            x[i] = make_uint4(__float_as_uint(v[16 * h + 4 * i]),
-                                              __float_as_uint(v[16 * h + 4 * i + 1]),
-                                              __float_as_uint(v[16 * h + 4 * i + 2]),
-                                              __float_as_uint(v[16 * h + 4 * i + 3]));
-                        trade_pieces(x, lane);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if ((live_lanes >> (quad + i)) & 1u)
-                                reinterpret_cast<uint4*>(
-                                    p.partial_o +
-                                    ((int64_t)partial * 2 * TR + urow - lane + quad + i) * D + col0 +
-                                    c + 16 * h)[piece] = x[i];
-                    }
+                    for (int i = 0; i < 8; ++i)
+                        *partial_at((col0 + c) / 4 + i, urow) =
+                            make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
                 }
+            }
+            __syncwarp();  // (what the lanes wrote of each other's rows is there)
+            if (bad_v && live) {
+                const ChunkSeen seen = {table, max(lo, (tile + t.bad_from) * TT),
+                                        min(hi, (tile + t.bad_to) * TT), lo_all, hi_all, t.g};
+                add_not_finite<T, D>(p, seen, col0, cols, [&](int c, float x) {
+                    if (direct) {
+                        T* o = static_cast<T*>(p.out) + out_row * D + c;
+                        *o = from_float(as_float(*o) + x, T());
+                    } else {
+                        reinterpret_cast<float*>(partial_at(c / 4, urow))[c % 4] += x;
+                    }
+                });
             }
             if (live && !direct && (!split || wg == 0))
                 p.partial_lse[(int64_t)partial * 2 * TR + urow] = lse;
@@ -1212,10 +1338,11 @@ __global__ void __launch_bounds__(kChunkMergeThreads) chunk_merge_kernel(const C
             const int64_t at = (int64_t)slot * 2 * kChunkRows + row;
             const bool has = c + f <= segment && __ldg(p.has + slot) == 1;
             lse[f] = has ? __ldg(p.partial_lse + at) : -INFINITY;
-            const float4* o = reinterpret_cast<const float4*>(p.partial_o + at * D) + q8;
+            const float4* o = reinterpret_cast<const float4*>(p.partial_o) +
+                              ((int64_t)slot * (D / 4) + q8) * 2 * kChunkRows + row;
 #pragma unroll
             for (int e = 0; e < E; ++e)
-                x[f][e] = has ? __ldg(o + 8 * e) : make_float4(0.f, 0.f, 0.f, 0.f);
+                x[f][e] = has ? __ldg(o + e * 16 * kChunkRows) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
         float mn = m;
 #pragma unroll
