@@ -79,8 +79,7 @@ struct ChunkParams {
     int num_q_heads;
     int cap;
     bool hnd;
-    float scale_log2;      // |scale| * log2(e) (of 1 where scale is 0)
-    float scale_sign;      // 1, -1 or 0
+    float scale_log2;      // scale * log2(e)
     float softcap;
     float tanh_log2;       // 2 log2(e) scale / softcap
 };
@@ -1047,7 +1046,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                                                      make_float2(cap2, cap2));
                                 });
                             } else {
-                                const float k1 = p.scale_log2 * p.scale_sign;
+                                const float k1 = p.scale_log2;
                                 pairs([&](float2 y, int) {
                                     return ptx::mul2(y, make_float2(k1, k1));
                                 });
@@ -1061,10 +1060,6 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                                                      y);
                                 });
                             }
-                        } else if (p.scale_sign != 1.f) {
-                            pairs([&](float2 y, int) {
-                                return ptx::mul2(y, make_float2(p.scale_sign, p.scale_sign));
-                            });
                         }
                         if (!plain) {
 #pragma unroll
@@ -1476,7 +1471,8 @@ static cudaError_t launch_chunk_t(const CUtensorMap& mk, const CUtensorMap& mv,
 template <typename T>
 static cudaError_t launch_chunk(const CUtensorMap& mk, const CUtensorMap& mv, const ChunkParams& p,
                                 const ChunkCallPlan& plan, int head_dim, cudaStream_t stream) {
-    const bool mod = p.softcap > 0.f || p.slopes != nullptr;
+    // the plain kernel takes the largest score before it multiplies by the scale
+    const bool mod = p.softcap > 0.f || p.slopes != nullptr || !(p.scale_log2 > 0.f);
     if (head_dim == 64)
         return mod ? launch_chunk_t<T, 64, true>(mk, mv, p, plan, stream)
                    : launch_chunk_t<T, 64, false>(mk, mv, p, plan, stream);
@@ -1577,8 +1573,7 @@ extern "C" pkv_status pkv_chunk_attention(
     p.num_q_heads = num_q_heads;
     p.cap = std::min(max_blocks_per_seq * block_size, max_context_len);
     p.hnd = hnd;
-    p.scale_log2 = (scale == 0.f ? 1.f : std::fabs(scale)) * kLog2e;
-    p.scale_sign = scale > 0.f ? 1.f : scale < 0.f ? -1.f : 0.f;
+    p.scale_log2 = scale * kLog2e;
     p.softcap = softcap;
     p.tanh_log2 = softcap > 0.f ? 2.f * kLog2e * scale / softcap : 0.f;
     cudaStream_t s = (cudaStream_t)stream;
