@@ -96,8 +96,10 @@ static_assert(kChunkThreads == 512, "four warpgroups");
 constexpr int kChunkReaders =  // of a unit's notes
     kChunkSoftmaxWarps + kChunkTmaWarps + 1 + kChunkCleanWarps;
 // Registers: the other warpgroups hand over what they do not need, so that a softmax
-// thread's row of S stays in registers.
-constexpr int kChunkLaunchRegs = 128, kChunkSoftmaxRegs = 184, kChunkOtherRegs = 72;
+// thread's half row of S stays in registers.  Nothing is spilled at this split (at 184 and
+// 72 the walker's and the issuer's values were, and a chunk behind 61440 tokens took 7.0 ms
+// instead of 6.5: beside 226 KB of shared memory little is left to cache a stack in).
+constexpr int kChunkLaunchRegs = 128, kChunkSoftmaxRegs = 168, kChunkOtherRegs = 88;
 static_assert(2 * kChunkSoftmaxRegs + 2 * kChunkOtherRegs <= 4 * kChunkLaunchRegs, "register shares");
 // Scores may exceed a row's reference by this much (base 2) before it moves.
 constexpr float kChunkLazyLog2 = 8.f;

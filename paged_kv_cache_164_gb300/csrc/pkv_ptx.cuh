@@ -303,10 +303,10 @@ __device__ __forceinline__ float ex2_approx(float x) {
     return y;
 }
 
-// The smaller of two, NaN where one is.
-__device__ __forceinline__ float min_nan(float a, float b) {
+// The largest of three in one instruction.
+__device__ __forceinline__ float max3(float a, float b, float c) {
     float y;
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
     return y;
 }
 
