@@ -152,8 +152,8 @@ struct ChunkTileCfg {
     static constexpr int kSlots = D == 128 ? 5 : 10;
     static constexpr int kXchBytes = 2 * kChunkRows * 8;         // (m, l) of each half and row
     // full[slots], empty[slots], clean[slots], s_full[2], p_half[2], p_ready[2], o_done[2],
-    // q_ready[2], half_done[2], met, o_free, drain, noted[notes], read[notes], cleaned[notes]
-    static constexpr int kBarriers = 3 * kSlots + 15 + 3 * kChunkNotes;
+    // q_ready[2], met, o_free, drain, noted[notes], read[notes], cleaned[notes]
+    static constexpr int kBarriers = 3 * kSlots + 13 + 3 * kChunkNotes;
     static constexpr int kSmemBytes = (2 + kSlots) * kTileBytes + kXchBytes + kBarriers * 8 + 24 +
                                       kChunkMaxRounds * (int)sizeof(ChunkStart) +
                                       kChunkNotes * (int)sizeof(ChunkNote);
@@ -269,8 +269,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
     uint64_t* p_ready = p_half + 2;     // [warpgroup]: all of them
     uint64_t* o_done = p_ready + 2;   // [warpgroup]: a unit's last product is complete
     uint64_t* q_ready = o_done + 2;     // [warpgroup]
-    uint64_t* half_done = q_ready + 2;  // [warpgroup]: the product with the first half is complete
-    uint64_t* met = half_done + 2;         // both are through a split unit
+    uint64_t* met = q_ready + 2;        // both are through a split unit
     uint64_t* o_free = met + 1;         // both have read O_0, O_1 and the exchange of one
     uint64_t* drain = o_free + 1;
     uint64_t* noted = drain + 1;        // [notes]
@@ -304,7 +303,6 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             ptx::mbar_init(ptx::smem_addr(&p_ready[w]), TR / 32);
             ptx::mbar_init(ptx::smem_addr(&o_done[w]), 1);
             ptx::mbar_init(ptx::smem_addr(&q_ready[w]), TR);
-            ptx::mbar_init(ptx::smem_addr(&half_done[w]), 1);
         }
         ptx::mbar_init(ptx::smem_addr(met), 2 * TR);
         ptx::mbar_init(ptx::smem_addr(o_free), 2 * TR);
@@ -586,10 +584,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 };
                 if (!wait(&p_half[w], step[w])) return false;
                 ptx::tc_fence_after_sync();
-                if (ptx::elect_one()) {
-                    half(0);
-                    ptx::tc_commit(ptx::smem_addr(&half_done[w]));
-                }
+                if (ptx::elect_one()) half(0);
                 __syncwarp();
                 if (!wait(&p_ready[w], step[w])) return false;
                 ++step[w];
@@ -1006,38 +1001,34 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 }
                 if (warp_live) {
                     const float scale = MOD ? 1.f : p.scale_log2;
-                    // Half a tile at a time, one loop for both: unrolled for the whole tile, the
-                    // instructions did not stay in their cache beside the other warps'.
+                    // Two small loops over the row's scores, which are read twice, 32 at a
+                    // time: unrolled further, the instructions did not stay in their cache
+                    // beside the other warps' (64 tokens of 64 sequences of 2000: 123 us, 142
+                    // with 64 at a time, 188 with the tile in one piece).
+
+                    // f over the pairs of neighbouring scores
+                    auto pairs = [](auto& r, auto f) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            const float2 y =
+                                f(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), i);
+                            r[i] = __float_as_uint(y.x);
+                            r[i + 1] = __float_as_uint(y.y);
+                        }
+                    };
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t r[2][32];
-                        const int at = t0 + h * (TT / 2);
-                        const uint32_t col = s_col + h * (TT / 2);
+                    for (int c = 0; c < TT / 32; ++c) {
+                        uint32_t r[32];
                         __syncwarp();
-                        ptx::tmem_ld32_async(col, r[0]);
-                        ptx::tmem_ld32_async(col + 32, r[1]);
-                        ptx::tmem_wait_ld();
-                        ptx::tmem_loaded(r[0]);
-                        ptx::tmem_loaded(r[1]);
-                        // f over the pairs of neighbouring scores
-                        auto pairs = [&](auto f) {
-#pragma unroll
-                            for (int c = 0; c < 2; ++c)
-#pragma unroll
-                                for (int i = 0; i < 32; i += 2) {
-                                    const float2 y = f(make_float2(__uint_as_float(r[c][i]),
-                                                                   __uint_as_float(r[c][i + 1])),
-                                                       c * 32 + i);
-                                    r[c][i] = __float_as_uint(y.x);
-                                    r[c][i + 1] = __float_as_uint(y.y);
-                                }
-                        };
+                        ptx::tmem_ld32(s_col + c * 32, r);
+                        const int at = t0 + c * 32;
                         if constexpr (MOD) {
                             // the scores themselves, in base-2 units
                             if (p.softcap > 0.f) {
                                 // cap tanh(x) = cap - 2 cap / (1 + e^(2x))
                                 const float cap2 = p.softcap * kLog2e;
-                                pairs([&](float2 y, int) {
+                                pairs(r, [&](float2 y, int) {
                                     y = ptx::mul2(y, make_float2(p.tanh_log2, p.tanh_log2));
                                     y = ptx::add2(
                                         make_float2(ptx::ex2_approx(y.x), ptx::ex2_approx(y.y)),
@@ -1049,13 +1040,13 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                                 });
                             } else {
                                 const float k1 = p.scale_log2;
-                                pairs([&](float2 y, int) {
+                                pairs(r, [&](float2 y, int) {
                                     return ptx::mul2(y, make_float2(k1, k1));
                                 });
                             }
                             if (p.slopes != nullptr) {
                                 const float away = (float)(at - m);
-                                pairs([&](float2 y, int i) {
+                                pairs(r, [&](float2 y, int i) {
                                     return ptx::fma2(make_float2(slope, slope),
                                                      ptx::add2(make_float2(away, away),
                                                                make_float2((float)i, (float)(i + 1))),
@@ -1064,100 +1055,88 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                             }
                         }
                         if (!plain) {
+                            const int from = lo - at, to = hi - at;
+                            uint32_t allow = to >= 32 ? ~0u : to <= 0 ? 0u : (1u << to) - 1u;
+                            allow &= from <= 0 ? ~0u : from >= 32 ? 0u : ~0u << from;
+                            const uint32_t bb = boxes >> (2 * c);
+                            allow &= ((bb & 1u) ? 0x0000ffffu : 0u) |
+                                     ((bb & 2u) ? 0xffff0000u : 0u);
 #pragma unroll
-                            for (int c = 0; c < 2; ++c) {
-                                const int from = lo - (at + c * 32), to = hi - (at + c * 32);
-                                uint32_t allow = to >= 32 ? ~0u : to <= 0 ? 0u : (1u << to) - 1u;
-                                allow &= from <= 0 ? ~0u : from >= 32 ? 0u : ~0u << from;
-                                const uint32_t bb = boxes >> (4 * h + 2 * c);
-                                allow &= ((bb & 1u) ? 0x0000ffffu : 0u) |
-                                         ((bb & 2u) ? 0xffff0000u : 0u);
-#pragma unroll
-                                for (int i = 0; i < 32; ++i)
-                                    if (!((allow >> i) & 1u)) r[c][i] = __float_as_uint(-INFINITY);
-                            }
+                            for (int i = 0; i < 32; ++i)
+                                if (!((allow >> i) & 1u)) r[i] = __float_as_uint(-INFINITY);
                         }
-                        float mx[4];
+                        if (MOD || !plain) ptx::tmem_st32_async(s_col + c * 32, r);
 #pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            mx[c] = fmaxf(__uint_as_float(r[c / 2][(c & 1) * 16]),
-                                          __uint_as_float(r[c / 2][(c & 1) * 16 + 1]));
+                        for (int i = 0; i < 32; i += 8)
 #pragma unroll
-                        for (int i = 2; i < 16; i += 2)
-#pragma unroll
-                            for (int c = 0; c < 4; ++c)
-                                mx[c] = fmaxf(
-                                    fmaxf(mx[c], __uint_as_float(r[c / 2][(c & 1) * 16 + i])),
-                                    __uint_as_float(r[c / 2][(c & 1) * 16 + i + 1]));
-                        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
-                        float alpha = 1.f;
-                        if (m_ref == -INFINITY) {
-                            m_ref = top;  // O and l are still zero for this row
-                        } else if (top > m_ref + kChunkLazyLog2) {
-                            alpha = ptx::ex2_approx(m_ref - top);
-                            m_ref = top;
-                        }
-                        // O is rescaled where a reference moved, once the product before is
-                        // complete (that of the tile before is: S of this one is, and was
-                        // issued behind it)
-                        if (__any_sync(0xffffffffu, alpha != 1.f)) {
-                            if (h > 0) {
-                                ok = warp_wait_phase(ptx::smem_addr(&half_done[wg]), step & 1,
-                                                     abort_flag, p.err_flag);
-                                if (!ok) break;
-                                ptx::tc_fence_after_sync();
-                            }
+                            for (int k = 0; k < 4; ++k)
+                                mx[k] = fmaxf(fmaxf(mx[k], __uint_as_float(r[i + 2 * k])),
+                                              __uint_as_float(r[i + 2 * k + 1]));
+                    }
+                    if (MOD || !plain) ptx::tmem_wait_st();
+                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+                    float alpha = 1.f;
+                    if (m_ref == -INFINITY) {
+                        m_ref = top;  // O and l are still zero for this row
+                    } else if (top > m_ref + kChunkLazyLog2) {
+                        alpha = ptx::ex2_approx(m_ref - top);
+                        m_ref = top;
+                    }
+                    // O is rescaled where a reference moved (the product of the tile before is
+                    // complete: S of this one is, and was issued behind it)
+                    if (__any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
-                            for (int c = 0; c < D / 16; ++c) {
-                                uint32_t ov[16];
-                                __syncwarp();
-                                ptx::tmem_ld16(o_col + wg * D + c * 16, ov);
+                        for (int c = 0; c < D / 16; ++c) {
+                            uint32_t ov[16];
+                            __syncwarp();
+                            ptx::tmem_ld16(o_col + wg * D + c * 16, ov);
 #pragma unroll
-                                for (int i = 0; i < 16; ++i)
-                                    ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
-                                ptx::tmem_st16_async(o_col + wg * D + c * 16, ov);
-                            }
-                            l *= alpha;
+                            for (int i = 0; i < 16; ++i)
+                                ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+                            ptx::tmem_st16_async(o_col + wg * D + c * 16, ov);
                         }
-                        const float ref =
-                            (m_ref == -INFINITY ? 0.f : m_ref) - WeightBias<T>::value;
-                        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                        pairs([&](float2 y, int i) {
+                        l *= alpha;
+                    }
+                    const float ref = (m_ref == -INFINITY ? 0.f : m_ref) - WeightBias<T>::value;
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+                    for (int c = 0; c < TT / 32; ++c) {
+                        uint32_t r[32];
+                        const uint32_t col = s_col + c * 32;
+                        __syncwarp();
+                        ptx::tmem_ld32(col, r);
+                        pairs(r, [&](float2 y, int i) {
                             y = ptx::fma2(y, make_float2(scale, scale), make_float2(-ref, -ref));
                             y = make_float2(ptx::ex2_approx(y.x), ptx::ex2_approx(y.y));
                             sum[i / 2 % 2] = ptx::add2(sum[i / 2 % 2], y);
                             return y;
                         });
                         if (split) {
+                            uint32_t pp[32];
 #pragma unroll
-                            for (int c = 0; c < 2; ++c) {
-                                uint32_t pp[32];
-#pragma unroll
-                                for (int e = 0; e < 16; ++e)
-                                    split_pair(make_float2(__uint_as_float(r[c][2 * e]),
-                                                           __uint_as_float(r[c][2 * e + 1])),
-                                               pp[e], pp[16 + e], T());
-                                ptx::tmem_st32_async(col + c * 32, pp);
-                            }
+                            for (int e = 0; e < 16; ++e)
+                                split_pair(make_float2(__uint_as_float(r[2 * e]),
+                                                       __uint_as_float(r[2 * e + 1])),
+                                           pp[e], pp[16 + e], T());
+                            ptx::tmem_st32_async(col, pp);
                         } else {
+                            uint32_t ph[16];
 #pragma unroll
-                            for (int c = 0; c < 2; ++c) {
-                                uint32_t ph[16];
-#pragma unroll
-                                for (int e = 0; e < 16; ++e)
-                                    ph[e] = pack2(__uint_as_float(r[c][2 * e]),
-                                                  __uint_as_float(r[c][2 * e + 1]), T());
-                                ptx::tmem_st16_async(col + c * 32, ph);
-                            }
+                            for (int e = 0; e < 16; ++e)
+                                ph[e] = pack2(__uint_as_float(r[2 * e]),
+                                              __uint_as_float(r[2 * e + 1]), T());
+                            ptx::tmem_st16_async(col, ph);
                         }
-                        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-                        ptx::tmem_wait_st();
-                        ptx::tc_fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0)
-                            ptx::mbar_arrive(ptx::smem_addr(h == 0 ? &p_half[wg] : &p_ready[wg]));
+                        if (c % 2 == 1) {  // half a tile, or all of it
+                            ptx::tmem_wait_st();
+                            ptx::tc_fence_before_sync();
+                            __syncwarp();
+                            if (lane == 0)
+                                ptx::mbar_arrive(
+                                    ptx::smem_addr(c < TT / 64 ? &p_half[wg] : &p_ready[wg]));
+                        }
                     }
-                    if (!ok) break;
+                    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                 } else if (lane == 0) {
                     ptx::mbar_arrive(ptx::smem_addr(&p_half[wg]));
                     ptx::mbar_arrive(ptx::smem_addr(&p_ready[wg]));
