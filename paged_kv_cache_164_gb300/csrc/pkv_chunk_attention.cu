@@ -162,6 +162,18 @@ struct ChunkTileCfg {
     static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
 };
 
+// A bounded wait of a whole warp, as warp_wait_phase, in a few instructions: a dozen warps
+// wait at any time here, and what they execute meanwhile takes instruction cache from the
+// softmax.  Every wait has its limit, so no flag between the warps ends them.
+constexpr unsigned kChunkWaitCycles = 3800000000u;  // about 2 s
+__device__ __forceinline__ bool chunk_wait(uint32_t bar, uint32_t parity) {
+    const unsigned t0 = clock();
+    bool ok;
+    while (!(ok = ptx::mbar_try_wait(bar, parity)))
+        if ((unsigned)clock() - t0 > kChunkWaitCycles) break;
+    return __all_sync(0xffffffffu, ok);
+}
+
 // Where K or V of tile j of a stretch of nt lies in the ring, counted from the stretch's
 // first place: the order in which the issuer takes them.  Both warpgroups on every tile:
 // K0 V0 K1 V1 ..; every other tile (split): K0 K1 V0 K2 V1 K3 ...
@@ -277,9 +289,8 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
     uint64_t* cleaned = read + kChunkNotes;  // [notes]: every tile of the unit
     int64_t* s_line = reinterpret_cast<int64_t*>(full_bar + Cfg::kBarriers);
     int* words = reinterpret_cast<int*>(s_line + 1);
-    volatile int* abort_flag = words;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(words + 1);
-    int* s_segments = words + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(words);
+    int* s_segments = words + 1;
     ChunkStart* s_start = reinterpret_cast<ChunkStart*>(words + 4);
     ChunkNote* notes = reinterpret_cast<ChunkNote*>(s_start + kChunkMaxRounds);
     int64_t* s_scan = reinterpret_cast<int64_t*>(xch);  // [16], before the first exchange
@@ -312,7 +323,6 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             ptx::mbar_init(ptx::smem_addr(&read[i]), kChunkReaders);
             ptx::mbar_init(ptx::smem_addr(&cleaned[i]), kChunkCleanWarps);
         }
-        *abort_flag = 0;
         ptx::fence_barrier_init();
         ptx::prefetch_tensormap(&tm_k);
         ptx::prefetch_tensormap(&tm_v);
@@ -401,10 +411,15 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
     const uint32_t tmem = *tmem_slot;
     const uint32_t ring_addr = ptx::smem_addr(ring);
     const uint32_t q_addr = ptx::smem_addr(sq);
+    bool gave_up = false;
+    auto wait_for = [&](uint32_t bar, int parity) {
+        const bool done = chunk_wait(bar, parity);
+        gave_up |= !done;
+        return done;
+    };
     // A reader's wait for note i of the CTA's, and its leave of it.
     auto note_there = [&](int i) {
-        return warp_wait_phase(ptx::smem_addr(&noted[i % kChunkNotes]), (i / kChunkNotes) & 1,
-                               abort_flag, p.err_flag);
+        return wait_for(ptx::smem_addr(&noted[i % kChunkNotes]), (i / kChunkNotes) & 1);
     };
     auto note_read = [&](int i) {
         __syncwarp();
@@ -455,8 +470,8 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                     }
                     const int slot = place % NS, phase = place / NS;
                     ++place;
-                    if (phase > 0 && !warp_wait_phase(ptx::smem_addr(&empty_bar[slot]),
-                                                      (phase - 1) & 1, abort_flag, p.err_flag))
+                    if (phase > 0 && !wait_for(ptx::smem_addr(&empty_bar[slot]),
+                                                      (phase - 1) & 1))
                         return false;
                     const uint32_t fb = ptx::smem_addr(&full_bar[slot]);
                     const uint32_t dst = ring_addr + slot * Cfg::kTileBytes +
@@ -500,8 +515,9 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                     b2 = far;
                 }
             }
-            if (lane == 0 && *abort_flag) {
-                // wait (bounded) for this warp's copies in flight before leaving
+            if (lane == 0) {
+                // this warp's copies have arrived (they are still in flight where a reader
+                // gave up) before the CTA leaves
                 const uint64_t t0 = ptx::globaltimer();
                 for (int i = 0; i < NS; ++i) {
                     if (!((filled >> i) & 1u)) continue;
@@ -528,7 +544,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             uint32_t cleans = 0;      // parity of the slots' cleanings
             bool ok = true;
             auto wait = [&](uint64_t* bar, int parity) {
-                return warp_wait_phase(ptx::smem_addr(bar), parity & 1, abort_flag, p.err_flag);
+                return wait_for(ptx::smem_addr(bar), parity & 1);
             };
             // the ring's next place, once it is full; -1: a wait gave up
             auto take = [&] {
@@ -672,8 +688,8 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             bool ok = true;
             auto place = [&](int i) {  // where note i is written, once it was read
                 return i < kChunkNotes ||
-                       warp_wait_phase(ptx::smem_addr(&read[i % kChunkNotes]),
-                                       (i / kChunkNotes - 1) & 1, abort_flag, p.err_flag);
+                       wait_for(ptx::smem_addr(&read[i % kChunkNotes]),
+                                       (i / kChunkNotes - 1) & 1);
             };
             for (int round = 0; round < rounds && ok; ++round) {
                 const ChunkStart start = s_start[round];
@@ -775,8 +791,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             int slot = 0, phase = 0;
             bool ok = true;
             auto full = [&] {
-                return warp_wait_phase(ptx::smem_addr(&full_bar[slot]), phase, abort_flag,
-                                       p.err_flag);
+                return wait_for(ptx::smem_addr(&full_bar[slot]), phase);
             };
             auto leave = [&] {
                 __syncwarp();
@@ -976,8 +991,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 // every row of the unit sees the whole tile
                 const bool plain = boxes == (1u << kChunkBoxes) - 1u && t0 >= lo_all &&
                                    t0 + TT <= hi_all;
-                if (!warp_wait_phase(ptx::smem_addr(&s_full[wg]), step & 1, abort_flag,
-                                     p.err_flag)) {
+                if (!wait_for(ptx::smem_addr(&s_full[wg]), step & 1)) {
                     ok = false;
                     break;
                 }
@@ -992,8 +1006,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 if (free_due) {
                     // both warpgroups have read O_0, O_1 and the exchange of the split unit
                     // before; neither is written anew until then
-                    if (!warp_wait_phase(ptx::smem_addr(o_free), (splits - 1) & 1, abort_flag,
-                                         p.err_flag)) {
+                    if (!wait_for(ptx::smem_addr(o_free), (splits - 1) & 1)) {
                         ok = false;
                         break;
                     }
@@ -1152,8 +1165,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
 
             // the unit's last O += P V
             if (mine > 0) {
-                if (!warp_wait_phase(ptx::smem_addr(&o_done[wg]), own & 1, abort_flag, p.err_flag))
-                    break;
+                if (!wait_for(ptx::smem_addr(&o_done[wg]), own & 1)) break;
                 ++own;
             }
             float fa, fb = 0.f, lse;  // out = O_0 fa + O_1 fb (not split: O_w fa)
@@ -1164,16 +1176,13 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             } else {
                 // both warpgroups are through: their parts of the softmax meet
                 if (free_due) {
-                    if (!warp_wait_phase(ptx::smem_addr(o_free), (splits - 1) & 1, abort_flag,
-                                         p.err_flag))
-                        break;
+                    if (!wait_for(ptx::smem_addr(o_free), (splits - 1) & 1)) break;
                     free_due = false;
                 }
                 xch[wg * TR + srow] = make_float2(m_ref, l);
                 ptx::tc_fence_before_sync();
                 ptx::mbar_arrive(ptx::smem_addr(met));
-                if (!warp_wait_phase(ptx::smem_addr(met), splits & 1, abort_flag, p.err_flag))
-                    break;
+                if (!wait_for(ptx::smem_addr(met), splits & 1)) break;
                 const float2 ha = xch[srow], hb = xch[TR + srow];
                 const float mm = fmaxf(ha.x, hb.x);
                 fa = ha.x == -INFINITY ? 0.f : ptx::ex2_approx(ha.x - mm);
@@ -1187,8 +1196,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             ptx::tc_fence_after_sync();
             const int partial = t.partial;
             const bool direct = partial < 0;
-            if (!warp_wait_phase(ptx::smem_addr(&cleaned[u % kChunkNotes]), (u / kChunkNotes) & 1,
-                                 abort_flag, p.err_flag))
+            if (!wait_for(ptx::smem_addr(&cleaned[u % kChunkNotes]), (u / kChunkNotes) & 1))
                 break;
             const bool bad_v = t.bad_to != 0;
             // Columns: the whole row; of a split unit this warpgroup's half.
@@ -1269,6 +1277,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
         ptx::cp_async_wait_all();
     }
 
+    if (gave_up && lane == 0) flag_error(p.err_flag, PKV_EFLAG_TIMEOUT);
     ptx::tc_fence_before_sync();
     __syncthreads();
     if (warp == kChunkMmaWarp) {
