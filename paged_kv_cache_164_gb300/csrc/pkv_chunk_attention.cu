@@ -174,12 +174,13 @@ __device__ __forceinline__ bool chunk_wait(uint32_t bar, uint32_t parity) {
     return __all_sync(0xffffffffu, ok);
 }
 
-// Where K or V of tile j of a stretch of nt lies in the ring, counted from the stretch's
-// first place: the order in which the issuer takes them.  Both warpgroups on every tile:
-// K0 V0 K1 V1 ..; every other tile (split): K0 K1 V0 K2 V1 K3 ...
-__device__ __forceinline__ int chunk_place(bool split, bool is_v, int j, int nt) {
-    if (!split) return 2 * j + (is_v ? 1 : 0);
-    return is_v ? min(j + 2, nt) + j : (j < 2 ? j : 2 * j - 1);
+// What lies at place i of the ring, counted from the first of a stretch of nt tiles: the
+// order in which the issuer takes them.  Both warpgroups on every tile: K0 V0 K1 V1 ..;
+// every other tile (split): K0 K1 V0 K2 V1 K3 ..
+__device__ __forceinline__ int chunk_place_tile(bool split, int i, int nt, bool& is_v) {
+    is_v = split ? (i > 1 && i % 2 == 0) || i == 2 * nt - 1 : i % 2 == 1;
+    if (!split) return i / 2;
+    return i == 2 * nt - 1 ? nt - 1 : i < 2 ? i : is_v ? i / 2 - 1 : (i + 1) / 2;
 }
 
 __device__ __forceinline__ ChunkSeq chunk_load(const ChunkParams& p, int b) {
@@ -729,19 +730,19 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                     const int blk = lane < 2 * kChunkBoxes && at + kStageTokens > t.lo && at < end
                                         ? __ldg(table + (at >> bs_shift))
                                         : -1;
-                    // a few loads a lane tell whether all pages are there; of a longer
-                    // stretch the softmax warps look at each tile's
+                    // whether all pages are there: where one is not, the others look at each
+                    // tile's
                     const int page0 = max(t.lo, t.tile * TT) >> bs_shift;
                     const int pages = ((end - 1) >> bs_shift) - page0 + 1;
-                    bool there = end > t.lo && pages <= 256;
-                    if (there) {
+                    bool there = end > t.lo;
+#pragma unroll 1
+                    for (int i0 = lane; there && i0 < pages; i0 += 8 * 32) {
+                        int x[8];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int x = i * 32 + lane < pages
-                                              ? __ldg(table + page0 + i * 32 + lane)
-                                              : 0;
-                            there &= x >= 0 && x < p.num_blocks;
-                        }
+                        for (int i = 0; i < 8; ++i)
+                            x[i] = i0 + i * 32 < pages ? __ldg(table + page0 + i0 + i * 32) : 0;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) there &= x[i] >= 0 && x[i] < p.num_blocks;
                     }
                     there = __all_sync(0xffffffffu, there);
                     if (!place(u)) {
@@ -790,9 +791,6 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             constexpr int kRowsEach = TT / kChunkCleanWarps;
             int slot = 0, phase = 0;
             bool ok = true;
-            auto full = [&] {
-                return wait_for(ptx::smem_addr(&full_bar[slot]), phase);
-            };
             auto leave = [&] {
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&empty_bar[slot]));
@@ -818,22 +816,19 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                                : -1;
                 };
                 int blk = box_block(0);
-                auto pass_k = [&] {
-                    if (!full()) return false;
-                    leave();
-                    return true;
-                };
-                auto clean_v = [&](int j) {
-                    const bool dirty = j < plain0 || j >= plain1;
+                for (int i = 0; i < 2 * nt; ++i) {
+                    bool is_v;
+                    const int j = chunk_place_tile(split, i, nt, is_v);
                     uint32_t boxes = (1u << kChunkBoxes) - 1u;
-                    if (!there) {
+                    if (is_v && !there) {
                         boxes = __ballot_sync(0xffffffffu, blk >= 0 && blk < p.num_blocks);
                         blk = box_block(j + 1);
                     }
-                    if (!full()) return false;
-                    if (!dirty) {
+                    ok = wait_for(ptx::smem_addr(&full_bar[slot]), phase);
+                    if (!ok) break;
+                    if (!is_v || (j >= plain0 && j < plain1)) {
                         leave();
-                        return true;
+                        continue;
                     }
                     const int t0 = (tile + j) * TT;
                     // a lane keeps to its 16-byte column of every (32 / kCells)-th row
@@ -885,13 +880,6 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&clean_bar[slot]));
                     leave();
-                    return true;
-                };
-                if (split) {
-                    ok = pass_k() && (nt < 2 || pass_k());
-                    for (int j = 0; j < nt && ok; ++j) ok = clean_v(j) && (j + 2 >= nt || pass_k());
-                } else {
-                    for (int j = 0; j < nt && ok; ++j) ok = pass_k() && clean_v(j);
                 }
                 if (!ok) break;
                 __syncwarp();
