@@ -303,13 +303,6 @@ __device__ __forceinline__ float ex2_approx(float x) {
     return y;
 }
 
-// The largest of three in one instruction.
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float y;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
-    return y;
-}
-
 // 1 / x by the hardware approximation (relative error about 2^-23).
 __device__ __forceinline__ float rcp_approx(float x) {
     float y;
