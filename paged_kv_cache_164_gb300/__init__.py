@@ -4,7 +4,7 @@ A thin ctypes binding over the C ABI in ``include/pkv.h`` (``libpkv.so``).
 Every step of the path runs in the library's CUDA kernels; this module only
 checks tensor types, passes device pointers, sizes and the current CUDA stream,
 and turns status codes into exceptions.  PyTorch provides device memory and
-streams.  The calls of the tree step, whose kernels take 2 us at small batches,
+streams.  The calls of the tree and ragged steps, whose kernels take a few us at most,
 have a quick form of the same checks in C++ (``pkv_binding.so``); what it does
 not take is checked here.  There is no CPU fallback: if the library is not
 built, or a tensor is not on a CUDA device, the call raises.
@@ -59,7 +59,7 @@ class PkvError(RuntimeError):
 
 
 _lib: Optional[ctypes.CDLL] = None
-# The quick form of the tree step's calls (csrc/pkv_binding.cpp): for arguments of
+# The quick form of the tree step's and the ragged step's calls (csrc/pkv_binding.cpp): for arguments of
 # the usual form a call's status, None for all others; None itself where it was not
 # built, or for another torch than this one.
 _quick = None
@@ -157,6 +157,8 @@ def _load_quick(lib: ctypes.CDLL) -> None:
         module.bind(*(ctypes.cast(getattr(lib, "pkv_" + name), ctypes.c_void_p).value
                       for name in ("norm_rope_append", "norm_rope_append_fp8", "tree_plan",
                                    "tree_attention", "tree_commit_within")))
+        module.bind_ragged(*(ctypes.cast(getattr(lib, "pkv_" + name), ctypes.c_void_p).value
+                             for name in ("batch_plan", "chunk_attention", "verify_drafts")))
         _quick = module
 
 
@@ -1051,6 +1053,15 @@ def batch_plan(context_lens: torch.Tensor, new_lens: torch.Tensor, block_tables:
     Where pages or token places run out, that sequence and those behind it receive no
     tokens (``EFLAG_POOL``): their query rows are empty.
     """
+    if _quick is not None and stream is None:
+        r = _quick.batch_plan(context_lens, new_lens, block_tables, free_blocks, free_count,
+                              num_blocks, block_size, max_tokens, keep_lens, shared_pages,
+                              query_starts, positions, slot_mapping, new_context_lens,
+                              new_free_count, err_flag)
+        if r is not None:
+            if r:
+                _check(r, "pkv_batch_plan")
+            return query_starts, positions, slot_mapping, new_context_lens, new_free_count
     lib = load()
     dev = _cuda_index(context_lens, "context_lens", 1)
     i32, i64 = torch.int32, torch.int64
@@ -1119,6 +1130,14 @@ def chunk_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     (0: not), and get slopes[h] * (t - m) (float32 [H_q]).  Rows outside query_starts
     are left as they were.  16-bit caches only.
     """
+    if _quick is not None and stream is None:
+        r = _quick.chunk_attention(q, k_cache, v_cache, block_tables, query_starts, context_lens,
+                                   max_context_len, scale, softcap, window, slopes, prefix_lens,
+                                   out, workspace, err_flag, layout)
+        if r is not None:
+            if r:
+                _check(r, "pkv_chunk_attention")
+            return out
     lib = load()
     dev = _cuda_index(q, "q", 3)
     t, h_q, d = qshape = q.shape
@@ -1177,6 +1196,14 @@ def verify_drafts(target_probs: torch.Tensor, draft_probs: Optional[torch.Tensor
     With ``context_lens``, new_context_lens int32 [B] (else None): context - rows +
     accepted (``batch_plan``'s keep_lens).
     """
+    if _quick is not None and stream is None:
+        r = _quick.verify_drafts(target_probs, draft_probs, tokens, row_starts, uniforms,
+                                 max_accepted, parents, context_lens, accepted, accepted_lens,
+                                 next_tokens, new_context_lens, err_flag)
+        if r is not None:
+            if r:
+                _check(r, "pkv_verify_drafts")
+            return accepted, accepted_lens, next_tokens, new_context_lens
     lib = load()
     dev = _cuda_index(target_probs, "target_probs", 2)
     n, v = target_probs.shape

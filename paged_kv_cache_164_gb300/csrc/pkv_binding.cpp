@@ -1,4 +1,4 @@
-// The tree step's Python calls in their usual form, marshalled in C++: every
+// The tree step's and the ragged step's Python calls in their usual form, marshalled in C++: every
 // tensor given, dense, of the right type, on the current device, launched on its
 // current stream.  A call of that form goes straight to the C ABI (reading a
 // dozen tensors takes 1 us here and 5 to 9 us in Python, and the kernels of small
@@ -22,6 +22,9 @@ decltype(&pkv_norm_rope_append_fp8) fn_norm_rope_append_fp8 = nullptr;
 decltype(&pkv_tree_plan) fn_tree_plan = nullptr;
 decltype(&pkv_tree_attention) fn_tree_attention = nullptr;
 decltype(&pkv_tree_commit_within) fn_tree_commit = nullptr;
+decltype(&pkv_batch_plan) fn_batch_plan = nullptr;
+decltype(&pkv_chunk_attention) fn_chunk_attention = nullptr;
+decltype(&pkv_verify_drafts) fn_verify_drafts = nullptr;
 
 // Reads a call's arguments; `ok` stays true while they have the usual form.
 struct Reader {
@@ -336,6 +339,141 @@ PyObject* tree_commit(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// (context_lens, new_lens, block_tables, free_blocks, free_count, num_blocks, block_size,
+//  max_tokens, keep_lens, shared_pages, query_starts, positions, slot_mapping,
+//  new_context_lens, new_free_count, err_flag)
+PyObject* batch_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (n != 16 || fn_batch_plan == nullptr) Py_RETURN_NONE;
+    Reader r;
+    const at::Tensor* lens = r.first(a[0], 1);
+    if (!r.ok) Py_RETURN_NONE;
+    const int64_t b = lens->size(0);
+    const int64_t seqs[1] = {b}, starts[1] = {b + 1}, one[1] = {1};
+    const int nb = r.integer(a[5]), bs = r.integer(a[6]), most = r.integer(a[7]);
+    const int64_t places[1] = {most};
+    const void* ctx = r.dense(a[0], at::kInt, seqs);
+    const void* fresh = r.dense(a[1], at::kInt, seqs);
+    const at::Tensor* tables = r.typed(a[2], at::kInt);
+    if (!r.ok || tables->dim() != 2 || tables->size(0) != b || !tables->is_contiguous())
+        Py_RETURN_NONE;
+    const at::Tensor* free_list = r.typed(a[3], at::kInt);
+    if (!r.ok || free_list->dim() != 1 || !free_list->is_contiguous()) Py_RETURN_NONE;
+    const void* count = r.dense(a[4], at::kInt, one);
+    const void* keep = r.optional(a[8], at::kInt, seqs);
+    const void* shared = r.optional(a[9], at::kInt, seqs);
+    void* qs = r.dense(a[10], at::kInt, starts);
+    void* pos = r.dense(a[11], at::kInt, places);
+    void* slots = r.dense(a[12], at::kLong, places);
+    void* new_lens = r.dense(a[13], at::kInt, seqs);
+    void* new_count = r.dense(a[14], at::kInt, one);
+    int32_t* flag = r.flag(a[15]);
+    const int width = r.narrow(tables->size(1)), batch = r.narrow(b),
+              room = r.narrow(free_list->size(0));
+    if (!r.ok) Py_RETURN_NONE;
+    int32_t* tab = static_cast<int32_t*>(tables->data_ptr());
+    int32_t* list = static_cast<int32_t*>(free_list->data_ptr());
+    void* st = stream_of(r.device);
+    return unlocked([&] {
+        return fn_batch_plan(
+            static_cast<int32_t*>(qs), static_cast<int32_t*>(pos), static_cast<int64_t*>(slots),
+            static_cast<int32_t*>(new_lens), static_cast<int32_t*>(new_count),
+            static_cast<const int32_t*>(ctx), static_cast<const int32_t*>(fresh),
+            static_cast<const int32_t*>(keep), static_cast<const int32_t*>(shared), tab, width,
+            list, room, static_cast<const int32_t*>(count), batch, most, nb, bs, flag, st);
+    });
+}
+
+// (q, k_cache, v_cache, block_tables, query_starts, context_lens, max_context_len, scale,
+//  softcap, window, slopes, prefix_lens, out, workspace, err_flag, layout)
+PyObject* chunk_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (n != 16 || fn_chunk_attention == nullptr) Py_RETURN_NONE;
+    Reader r;
+    const at::Tensor* q = r.first(a[0], 3);
+    if (!r.ok) Py_RETURN_NONE;
+    const at::ScalarType type = q->scalar_type();
+    const int64_t t = q->size(0), h_q = q->size(1), d = q->size(2);
+    const Caches c(r, a[1], a[2], a[15], type, type);
+    if (!r.ok || c.d != d) Py_RETURN_NONE;
+    const void* qp = r.dense(a[0], type, q->sizes());
+    const at::Tensor* tables = r.typed(a[3], at::kInt);
+    if (!r.ok || tables->dim() != 2 || !tables->is_contiguous()) Py_RETURN_NONE;
+    const int64_t b = tables->size(0);
+    const int64_t seqs[1] = {b}, starts[1] = {b + 1}, heads_of[1] = {h_q};
+    const void* qs = r.dense(a[4], at::kInt, starts);
+    const void* lens = r.dense(a[5], at::kInt, seqs);
+    const int cap = r.integer(a[6]);
+    const float scale = a[7] == Py_None && d > 0
+                            ? static_cast<float>(1.0 / std::sqrt(static_cast<double>(d)))
+                            : r.real(a[7]);
+    const float softcap = r.real(a[8]);
+    const int window = r.integer(a[9]);
+    const void* slopes = r.optional(a[10], at::kFloat, heads_of);
+    const void* prefix = r.optional(a[11], at::kInt, seqs);
+    void* out = r.dense(a[12], type, q->sizes());
+    const at::Tensor* ws = r.ok ? r.tensor(a[13]) : nullptr;
+    if (!r.ok || !ws->is_cuda() || ws->get_device() != r.device || !ws->is_contiguous())
+        Py_RETURN_NONE;
+    int32_t* flag = r.flag(a[14]);
+    const int width = r.narrow(tables->size(1)), batch = r.narrow(b), tokens = r.narrow(t),
+              heads = r.narrow(h_q);
+    if (!r.ok) Py_RETURN_NONE;
+    const int32_t* tab = static_cast<const int32_t*>(tables->data_ptr());
+    void* ws_ptr = ws->data_ptr();
+    const size_t ws_bytes = ws->nbytes();
+    void* st = stream_of(r.device);
+    return unlocked([&] {
+        return fn_chunk_attention(out, qp, c.k, c.v, tab, width, static_cast<const int32_t*>(qs),
+                                  static_cast<const int32_t*>(lens), cap,
+                                  static_cast<const int32_t*>(prefix),
+                                  static_cast<const float*>(slopes), batch, tokens, c.num_blocks,
+                                  c.block_size, heads, c.heads, c.d, scale, softcap, window,
+                                  ws_ptr, ws_bytes, c.code, flag, st);
+    });
+}
+
+// (target_probs, draft_probs, tokens, row_starts, uniforms, max_accepted, parents,
+//  context_lens, accepted, accepted_lens, next_tokens, new_context_lens, err_flag)
+PyObject* verify_drafts(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (n != 13 || fn_verify_drafts == nullptr) Py_RETURN_NONE;
+    Reader r;
+    const at::Tensor* target = r.first(a[0], 2);
+    if (!r.ok) Py_RETURN_NONE;
+    const int64_t rows = target->size(0), v = target->size(1);
+    const void* tp = r.dense(a[0], at::kFloat, target->sizes());
+    const void* dp = r.optional(a[1], at::kFloat, target->sizes());
+    const int64_t nodes[1] = {rows};
+    const void* tokens = r.dense(a[2], at::kInt, nodes);
+    const at::Tensor* starts = r.typed(a[3], at::kInt);
+    if (!r.ok || starts->dim() != 1 || starts->size(0) < 1 || !starts->is_contiguous())
+        Py_RETURN_NONE;
+    const int64_t b = starts->size(0) - 1;
+    const void* uniforms = r.dense(a[4], at::kFloat, nodes);
+    const int most = r.integer(a[5]);
+    const void* parents = r.optional(a[6], at::kInt, nodes);
+    const int64_t seqs[1] = {b}, path[2] = {b, most};
+    const void* lens = r.optional(a[7], at::kInt, seqs);
+    void* accepted = r.dense(a[8], at::kInt, path);
+    void* counts = r.dense(a[9], at::kInt, seqs);
+    void* next = r.dense(a[10], at::kInt, seqs);
+    // the new lengths go with the old ones
+    if (!r.ok || most < 1 || (a[7] == Py_None) != (a[11] == Py_None)) Py_RETURN_NONE;
+    void* fresh = r.optional(a[11], at::kInt, seqs);
+    int32_t* flag = r.flag(a[12]);
+    const int batch = r.narrow(b), n_rows = r.narrow(rows), vocab = r.narrow(v);
+    if (!r.ok) Py_RETURN_NONE;
+    const int32_t* st_rows = static_cast<const int32_t*>(starts->data_ptr());
+    void* st = stream_of(r.device);
+    return unlocked([&] {
+        return fn_verify_drafts(
+            static_cast<int32_t*>(accepted), static_cast<int32_t*>(counts),
+            static_cast<int32_t*>(next), static_cast<int32_t*>(fresh),
+            static_cast<const float*>(tp), static_cast<const float*>(dp),
+            static_cast<const int32_t*>(tokens), static_cast<const int32_t*>(parents), st_rows,
+            static_cast<const float*>(uniforms), static_cast<const int32_t*>(lens), batch, n_rows,
+            vocab, most, flag, st);
+    });
+}
+
 // C++ exceptions (a tensor without storage, a CUDA error) become "not the usual form".
 template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
 PyObject* guarded(PyObject* self, PyObject* const* args, Py_ssize_t n) {
@@ -346,26 +484,42 @@ PyObject* guarded(PyObject* self, PyObject* const* args, Py_ssize_t n) {
     }
 }
 
+// Reads `count` addresses; false with Python's error set.
+bool addresses(PyObject* const* a, Py_ssize_t n, int count, const char* message, void** p) {
+    if (n != count) {
+        PyErr_SetString(PyExc_TypeError, message);
+        return false;
+    }
+    for (int i = 0; i < count; ++i) {
+        p[i] = PyLong_AsVoidPtr(a[i]);
+        if (p[i] == nullptr) {
+            if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "a null address");
+            return false;
+        }
+    }
+    return true;
+}
+
 // bind(addresses of norm_rope_append, norm_rope_append_fp8, tree_plan,
 //      tree_attention, tree_commit_within)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* p[5];
-    if (n != 5) {
-        PyErr_SetString(PyExc_TypeError, "bind takes five addresses");
-        return nullptr;
-    }
-    for (int i = 0; i < 5; ++i) {
-        p[i] = PyLong_AsVoidPtr(a[i]);
-        if (p[i] == nullptr) {
-            if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "a null address");
-            return nullptr;
-        }
-    }
+    if (!addresses(a, n, 5, "bind takes five addresses", p)) return nullptr;
     fn_norm_rope_append = reinterpret_cast<decltype(fn_norm_rope_append)>(p[0]);
     fn_norm_rope_append_fp8 = reinterpret_cast<decltype(fn_norm_rope_append_fp8)>(p[1]);
     fn_tree_plan = reinterpret_cast<decltype(fn_tree_plan)>(p[2]);
     fn_tree_attention = reinterpret_cast<decltype(fn_tree_attention)>(p[3]);
     fn_tree_commit = reinterpret_cast<decltype(fn_tree_commit)>(p[4]);
+    Py_RETURN_NONE;
+}
+
+// bind_ragged(addresses of batch_plan, chunk_attention, verify_drafts)
+PyObject* bind_ragged(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    void* p[3];
+    if (!addresses(a, n, 3, "bind_ragged takes three addresses", p)) return nullptr;
+    fn_batch_plan = reinterpret_cast<decltype(fn_batch_plan)>(p[0]);
+    fn_chunk_attention = reinterpret_cast<decltype(fn_chunk_attention)>(p[1]);
+    fn_verify_drafts = reinterpret_cast<decltype(fn_verify_drafts)>(p[2]);
     Py_RETURN_NONE;
 }
 
@@ -376,6 +530,10 @@ PyMethodDef methods[] = {
     {"tree_plan", PKV_FAST(guarded<tree_plan>), nullptr},
     {"tree_attention", PKV_FAST(guarded<tree_attention>), nullptr},
     {"tree_commit", PKV_FAST(guarded<tree_commit>), nullptr},
+    {"bind_ragged", PKV_FAST(bind_ragged), nullptr},
+    {"batch_plan", PKV_FAST(guarded<batch_plan>), nullptr},
+    {"chunk_attention", PKV_FAST(guarded<chunk_attention>), nullptr},
+    {"verify_drafts", PKV_FAST(guarded<verify_drafts>), nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "pkv_binding", nullptr, -1, methods,

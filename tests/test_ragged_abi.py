@@ -177,3 +177,20 @@ def test_the_reference_of_the_verification_draws_from_the_target():
                 for k in range(4):
                     mass[k] += reach * left[k] / z
         assert [float(m) for m in mass] == p[0].tolist()
+
+
+def test_quick_binding_leaves_what_it_does_not_know_to_python(lib):
+    if pkv._quick is None:
+        pytest.skip("built without the headers of Python and torch")
+    i = torch.zeros((1, 1), dtype=torch.int32)
+    k = torch.zeros((4, 16, 2, 64), dtype=torch.float16)
+    quick = pkv._quick
+    for call, n in ((quick.batch_plan, 16), (quick.chunk_attention, 16), (quick.verify_drafts, 13)):
+        for args in ((), (i,) * n, (i[0],) * n, (k,) * n, (k[0],) * n, (None,) * n, (1,) * n,
+                     ("nhd",) * n, (object(),) * (n + 1), (i.to_sparse(),) * n,
+                     (k[0].to("meta"),) * n):
+            assert call(*args) is None
+    with pytest.raises(TypeError):
+        quick.bind_ragged(1, 2)
+    with pytest.raises(ValueError):
+        quick.bind_ragged(0, 0, 0)
