@@ -303,28 +303,25 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
     const int bs_shift = __ffs(bs) - 1;
 
     ptx::launch_dependents();
-    if (tid == 0) {
-        for (int i = 0; i < NS; ++i) {
-            ptx::mbar_init(ptx::smem_addr(&full_bar[i]), kChunkTmaWarps);
-            ptx::mbar_init(ptx::smem_addr(&empty_bar[i]), 1 + kChunkCleanWarps);
-            ptx::mbar_init(ptx::smem_addr(&clean_bar[i]), kChunkCleanWarps);
-        }
-        for (int w = 0; w < 2; ++w) {
-            ptx::mbar_init(ptx::smem_addr(&s_full[w]), 1);
-            ptx::mbar_init(ptx::smem_addr(&p_half[w]), TR / 32);
-            ptx::mbar_init(ptx::smem_addr(&p_ready[w]), TR / 32);
-            ptx::mbar_init(ptx::smem_addr(&o_done[w]), 1);
-            ptx::mbar_init(ptx::smem_addr(&q_ready[w]), TR);
-        }
-        ptx::mbar_init(ptx::smem_addr(met), 2 * TR);
-        ptx::mbar_init(ptx::smem_addr(o_free), 2 * TR);
-        ptx::mbar_init(ptx::smem_addr(drain), 1);
-        for (int i = 0; i < kChunkNotes; ++i) {
-            ptx::mbar_init(ptx::smem_addr(&noted[i]), 1);
-            ptx::mbar_init(ptx::smem_addr(&read[i]), kChunkReaders);
-            ptx::mbar_init(ptx::smem_addr(&cleaned[i]), kChunkCleanWarps);
-        }
+    if (tid < Cfg::kBarriers) {  // a thread a barrier, in their order
+        const int i = tid;
+        const int count =
+            i < NS                ? kChunkTmaWarps
+            : i < 2 * NS          ? 1 + kChunkCleanWarps
+            : i < 3 * NS          ? kChunkCleanWarps
+            : i < 3 * NS + 2      ? 1            // s_full
+            : i < 3 * NS + 6      ? TR / 32      // p_half, p_ready
+            : i < 3 * NS + 8      ? 1            // o_done
+            : i < 3 * NS + 10     ? TR           // q_ready
+            : i < 3 * NS + 12     ? 2 * TR       // met, o_free
+            : i < 3 * NS + 13     ? 1            // drain
+            : i < 3 * NS + 13 + kChunkNotes     ? 1  // noted
+            : i < 3 * NS + 13 + 2 * kChunkNotes ? kChunkReaders
+                                                : kChunkCleanWarps;
+        ptx::mbar_init(ptx::smem_addr(&full_bar[i]), count);
         ptx::fence_barrier_init();
+    }
+    if (tid == 0) {
         ptx::prefetch_tensormap(&tm_k);
         ptx::prefetch_tensormap(&tm_v);
     }
@@ -344,14 +341,20 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
 
     // The line, and where on it this CTA's segments start: a thread sums the places of a
     // run of sequences, a scan puts the runs in order, and the thread whose run holds a
-    // segment's first place stands there for all.  Up to 32 sequences a warp does it by
-    // itself, a lane a sequence.
-    {
-        const bool few = p.num_seqs <= 32;
+    // segment's first place stands there for all.  Up to 32 sequences the walking warp
+    // does it by itself, a lane a sequence, and the others go on meanwhile.
+    const bool few = p.num_seqs <= 32;
+    if (few) {
+        ptx::tc_fence_before_sync();
+        __syncthreads();
+        ptx::tc_fence_after_sync();
+    }
+    if (!few || warp == kChunkWalkWarp) {
+        const int me = few ? lane : tid;
         const int runs = few ? 32 : kChunkThreads;
         const int per = (p.num_seqs + runs - 1) / runs;
-        const int b_lo = min(p.num_seqs, tid * per);
-        const int b_hi = tid < runs ? min(p.num_seqs, b_lo + per) : b_lo;
+        const int b_lo = min(p.num_seqs, me * per);
+        const int b_hi = min(p.num_seqs, b_lo + per);
         int64_t mine = 0;
         for (int b = b_lo; b < b_hi; ++b) {
             mine += chunk_places(load(b), p.shape);
@@ -361,12 +364,9 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                     flag_error(p.err_flag, PKV_EFLAG_QUERY);
             }
         }
-        int64_t before = 0, line = 0;
-        if (!few || warp == 0) {
-            const int64_t incl = warp_scan64(mine);
-            before = incl - mine;
-            line = __shfl_sync(0xffffffffu, incl, 31);
-        }
+        const int64_t incl = warp_scan64(mine);
+        int64_t before = incl - mine;
+        int64_t line = __shfl_sync(0xffffffffu, incl, 31);
         if (!few) {
             if (lane == 31) s_scan[warp] = line;
             __syncthreads();
@@ -376,13 +376,13 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 line += s_scan[w];
             }
         }
-        if (!few || warp == 0) {
+        {
             const int ctas = chunk_ctas(line);
             const int64_t long_ones =
                 ctas > 0 ? line / ((int64_t)ctas * kChunkRoundSegment) : 0;
             const int rounds = (int)max((int64_t)1, min((int64_t)p.rounds, long_ones));
             const int segments = rounds * ctas;
-            if (tid == 0) {
+            if (me == 0) {
                 *s_line = line;
                 *s_segments = segments;
             }
@@ -405,6 +405,9 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 s_start[r] = ChunkStart{at, w.b, w.g, w.rb, w.pos};
             }
         }
+        __syncwarp();
+    }
+    if (!few) {
         ptx::tc_fence_before_sync();
         __syncthreads();
         ptx::tc_fence_after_sync();
@@ -1156,11 +1159,13 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 if (!wait_for(ptx::smem_addr(&o_done[wg]), own & 1)) break;
                 ++own;
             }
-            float fa, fb = 0.f, lse;  // out = O_0 fa + O_1 fb (not split: O_w fa)
+            float fa, fb = 0.f;  // out = O_0 fa + O_1 fb (not split: O_w fa)
+            float sum, top;      // of the weights; their reference
             const bool two = split && nt > 1;  // O_1 has something
             if (!split) {
-                fa = l == 0.f ? 0.f : 1.f / l;
-                lse = l == 0.f ? -INFINITY : m_ref - WeightBias<T>::value + log2f(l);
+                sum = l;
+                top = m_ref;
+                fa = 1.f;
             } else {
                 // both warpgroups are through: their parts of the softmax meet
                 if (free_due) {
@@ -1172,15 +1177,15 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 ptx::mbar_arrive(ptx::smem_addr(met));
                 if (!wait_for(ptx::smem_addr(met), splits & 1)) break;
                 const float2 ha = xch[srow], hb = xch[TR + srow];
-                const float mm = fmaxf(ha.x, hb.x);
-                fa = ha.x == -INFINITY ? 0.f : ptx::ex2_approx(ha.x - mm);
-                fb = hb.x == -INFINITY ? 0.f : ptx::ex2_approx(hb.x - mm);
-                const float sum = ha.y * fa + hb.y * fb;
-                const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                fa *= inv;
-                fb *= inv;
-                lse = sum == 0.f ? -INFINITY : mm - WeightBias<T>::value + log2f(sum);
+                top = fmaxf(ha.x, hb.x);
+                fa = ha.x == -INFINITY ? 0.f : ptx::ex2_approx(ha.x - top);
+                fb = hb.x == -INFINITY ? 0.f : ptx::ex2_approx(hb.x - top);
+                sum = ha.y * fa + hb.y * fb;
             }
+            // (a sum is 0 or 1 at least: the score that set the reference is in it)
+            const float inv = sum == 0.f ? 0.f : ptx::rcp_approx(sum);
+            fa *= inv;
+            fb *= inv;
             ptx::tc_fence_after_sync();
             const int partial = t.partial;
             const bool direct = partial < 0;
@@ -1252,7 +1257,8 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 });
             }
             if (live && !direct && (!split || wg == 0))
-                p.partial_lse[(int64_t)partial * 2 * TR + urow] = lse;
+                p.partial_lse[(int64_t)partial * 2 * TR + urow] =
+                    sum == 0.f ? -INFINITY : top - WeightBias<T>::value + log2f(sum);
             if (split) {
                 ptx::tc_fence_before_sync();
                 ptx::mbar_arrive(ptx::smem_addr(o_free));
