@@ -107,10 +107,12 @@ constexpr int kChunkBoxes = kChunkTile / kStageTokens;  // TMA boxes along a til
 constexpr int kChunkMaxRounds = 4;
 // Notes of units, a ring of them; with each the mark of a V that is not finite in it.
 constexpr int kChunkNotes = 4;
-// A segment has at least this many places (a tile and what its unit costs besides), and
-// more rounds are taken only where theirs have this many.
-constexpr int kChunkLeastSegment = 512;
-constexpr int kChunkRoundSegment = 12288;
+// A segment has at least this many places, no more than the smallest unit, so that each
+// unit of a small batch has a CTA (two sequences of 40 tokens: 8.6 us, 10.7 at 512), and
+// more rounds are taken only where theirs have this many (whole prompts of 4096 tokens:
+// 924 us, 939 at 24576 and 966 at 12288, where more units are cut).
+constexpr int kChunkLeastSegment = kChunkUnitCost;
+constexpr int kChunkRoundSegment = 49152;
 
 // What the walking warp notes of a unit's stretch.
 struct ChunkNote {
@@ -1217,7 +1219,18 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] = fmaf(__uint_as_float(ov[i]), fb, v[i]);
                 }
-                if (direct) {
+                if (direct && t.tokens * group <= 32) {
+                    // few rows: each lane its own, in fewer instructions
+                    uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + out_row * D +
+                                                          col0 + c);
+                    if (live)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            dst[i] = make_uint4(pack2(v[8 * i], v[8 * i + 1], T()),
+                                                pack2(v[8 * i + 2], v[8 * i + 3], T()),
+                                                pack2(v[8 * i + 4], v[8 * i + 5], T()),
+                                                pack2(v[8 * i + 6], v[8 * i + 7], T()));
+                } else if (direct) {
                     // Four lanes trade 16-byte pieces of their rows, so that a store writes
                     // 64 bytes of each of eight rows, not 16 of 32
                     const int quad = lane & ~3, piece = lane & 3;
