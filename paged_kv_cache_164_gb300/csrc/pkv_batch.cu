@@ -15,7 +15,11 @@ namespace pkv {
 // bisection in the sums), so that one sequence's thousand pages take no longer than
 // a thousand sequences' one.  Steps of many tokens write their positions and slots
 // in a second kernel (batch_slots_kernel), which only reads what the first left.
-// Latency is all that it costs.
+// Latency is all that it costs (a call in a graph: 6.2 us for 256 sequences of single
+// tokens, 9 us for 200 of which 24 bring some 15000 together, whose positions the second
+// kernel writes): a launch, three rounds of loads that depend on one another and two
+// scans.  Under the profiler, with cold caches, 10.5 us, a third of the stalls on loads,
+// a quarter on instructions that are met for the first time.
 // ---------------------------------------------------------------------------
 
 struct BatchPlanParams {

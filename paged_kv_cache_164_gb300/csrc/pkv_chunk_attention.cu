@@ -17,8 +17,8 @@
 //   O_w += P_w V    P from tensor memory, V from shared memory
 // One warp issues everything in the order PV_0(j) S_0(j+1) PV_1(j) S_1(j+1), so that a
 // warpgroup is at its softmax while the other's two products run; the order keeps them
-// apart (with an issuer for each, both fell into step, and a chunk behind 61440 tokens
-// took 7.7 ms instead of 6.4).  The tensor core runs the products in that order: S over a
+// apart (with an issuer for each, both fell into step, and a chunk of 4096 tokens behind
+// 61440, 64/8 heads, took a fifth longer).  The tensor core runs the products in that order: S over a
 // P comes after the product that reads it, and where S(j) is complete so is PV(j-1).  P
 // goes over in two halves of 64 positions: the first is multiplied while the second is
 // made.
@@ -42,6 +42,15 @@
 // stays in L2).  A unit inside a segment is written to the output at once; one that is
 // cut leaves a partial (normalised O and its log-sum-exp) per segment, which
 // chunk_merge_kernel joins.
+//
+// Measured (64/8 heads, bf16, d 128, a call in a graph): single tokens of 64 sequences over
+// 2500 positions 117 us, 85 % of the copy rate; whole prompts of 4096 tokens 925 us, 1026
+// TFLOP/s; 4096 tokens behind 61440 6.9 ms, 1231 TFLOP/s, 65 % of the rate of library
+// products.  What bounds the large ones is a warpgroup's chain: of the 3900 cycles a tile of
+// both takes, 500 go into the maximum, 1900 into the weights, 750 into the wait for P V and
+// the next S; the tensor pipe is active 44 % of the time.  Twice the softmax warps (a row's
+// halves in two threads) took as long or longer; so did every form with more instructions:
+// beside eight other warps' loops it is the instruction cache that the softmax runs out of.
 //
 // Every wait is bounded, as in the decode kernels.
 #include <algorithm>

@@ -26,6 +26,11 @@ namespace pkv {
 // more than the probability of a token of a flat distribution).  Two additions of fp32
 // take a probability apart into them (to_fixed); 2^-60, by shifts of the fraction, took
 // twice the instructions, which are what a pass over registers costs.
+// Measured (a call in a graph): a chain of 5 over 32000 tokens 6.2 us, 64 chains of up to 7
+// 9.0 us, 32 trees of 16 nodes over 128000 tokens 35.5 us, of 4.8 that the bytes of the rows
+// passed over would take: one sequence's passes follow one another, some 3 us each (its
+// eight CTAs' share of two rows, a sum over the cluster), and the most rejected sequence
+// has the last word.  Memory reads 9 % of its rate, 0.4 instructions a cycle.
 // ---------------------------------------------------------------------------
 
 struct VerifyParams {
