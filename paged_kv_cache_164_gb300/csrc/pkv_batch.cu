@@ -15,11 +15,12 @@ namespace pkv {
 // bisection in the sums), so that one sequence's thousand pages take no longer than
 // a thousand sequences' one.  Steps of many tokens write their positions and slots
 // in a second kernel (batch_slots_kernel), which only reads what the first left.
-// Latency is all that it costs (a call in a graph: 6.2 us for 256 sequences of single
-// tokens, 9 us for 200 of which 24 bring some 15000 together, whose positions the second
-// kernel writes): a launch, three rounds of loads that depend on one another and two
-// scans.  Under the profiler, with cold caches, 10.5 us, a third of the stalls on loads,
-// a quarter on instructions that are met for the first time.
+// Latency is all that it costs (a call in a graph: 4.5 us for 256 sequences of single
+// tokens, 7.9 us for 200 of which 24 bring some 15000 together, whose positions the second
+// kernel writes): a launch, three rounds of loads that depend on one another and a scan.
+// What is known to need no sum is not summed (no page given back, everyone served), a
+// batch of one run is read once, and the tokens' bisections run in shared memory: without
+// these 6.3 and 8.9 us.
 // ---------------------------------------------------------------------------
 
 struct BatchPlanParams {
@@ -45,10 +46,12 @@ struct BatchPlanParams {
     int cap;  // tokens of a block table
 };
 
-constexpr int kBatchThreads = 1024;
+// (With 1024 threads 256 single tokens took 0.6 us longer, with 256 24 chunks of 15000
+// tokens 1.2 us.)
+constexpr int kBatchThreads = 512;
 constexpr int kBatchWarps = kBatchThreads / 32;
 // Up to this many token places the first kernel writes them itself.
-constexpr int kBatchOwnTokens = 4 * kBatchThreads;
+constexpr int kBatchOwnTokens = 8 * kBatchThreads;
 
 // A sequence's part of the step, before the free list is asked.
 struct BatchSeq {
@@ -106,7 +109,8 @@ __device__ __forceinline__ Sums block_sums(int64_t a, int64_t b, int64_t (*s_war
     }
     __syncthreads();
     if (warp == 0) {
-        int64_t x = s_warp[lane][0], y = s_warp[lane][1];
+        const bool has = lane < kBatchWarps;
+        int64_t x = has ? s_warp[lane][0] : 0, y = has ? s_warp[lane][1] : 0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t u = __shfl_up_sync(0xffffffffu, x, o),
@@ -116,8 +120,10 @@ __device__ __forceinline__ Sums block_sums(int64_t a, int64_t b, int64_t (*s_war
                 y += v;
             }
         }
-        s_warp[lane][0] = x;
-        s_warp[lane][1] = y;
+        if (has) {
+            s_warp[lane][0] = x;
+            s_warp[lane][1] = y;
+        }
     }
     __syncthreads();
     if (warp > 0) {
@@ -141,15 +147,16 @@ __device__ __forceinline__ int first_above(const I* sums, int n, int64_t x) {
     return lo;
 }
 
-// Position and slot of token place j of the step.
+// Position and slot of token place j of the step, whose row starts and new lengths are
+// `starts` and `lens`.
 __device__ __forceinline__ void batch_token(const BatchPlanParams& p, const int32_t* starts,
-                                            int j) {
+                                            const int32_t* lens, int j) {
     int pos = 0;
     int64_t slot = -1;
     if (j < starts[p.num_seqs]) {
         const int b = first_above(starts + 1, p.num_seqs, j);
         const int first = starts[b], count = starts[b + 1] - first;
-        pos = p.new_context_lens[b] - count + (j - first);
+        pos = lens[b] - count + (j - first);
         const int shift = __ffs(p.block_size) - 1;
         const int blk = p.block_tables[(int64_t)b * p.max_blocks_per_seq + (pos >> shift)];
         if (blk < 0 || blk >= p.num_blocks)
@@ -165,7 +172,9 @@ __global__ void __launch_bounds__(kBatchThreads, 1) batch_plan_kernel(const Batc
     __shared__ int64_t s_warp[kBatchWarps][2];
     __shared__ int64_t s_sum[kBatchThreads];
     __shared__ int s_first[kBatchThreads];
+    __shared__ int32_t s_starts[kBatchThreads + 1], s_lens[kBatchThreads];
     const int tid = threadIdx.x;
+    const bool one_run = p.num_seqs <= kBatchThreads;
     ptx::launch_dependents();
     ptx::grid_dependency_wait();
     int bad = 0;
@@ -174,10 +183,12 @@ __global__ void __launch_bounds__(kBatchThreads, 1) batch_plan_kernel(const Batc
     int64_t top = min(max(count, 0), p.free_capacity);
 
     // the released pages, a run of sequences at a time
+    BatchSeq s = {};
     for (int b0 = 0; b0 < p.num_seqs; b0 += kBatchThreads) {
         const int b = b0 + tid;
-        BatchSeq s = {};
+        s = {};
         if (b < p.num_seqs) s = batch_seq(p, b, bad);
+        if (!__syncthreads_or(s.back)) continue;  // (none, in most decode steps)
         const Sums sum = block_sums(s.back, 0, s_warp);
         s_sum[tid] = sum.a;
         s_first[tid] = s.first;
@@ -203,18 +214,28 @@ __global__ void __launch_bounds__(kBatchThreads, 1) batch_plan_kernel(const Batc
     int given = 0;                  // tokens that they receive
     for (int b0 = 0; b0 < p.num_seqs; b0 += kBatchThreads) {
         const int b = b0 + tid;
-        BatchSeq s = {};
-        int again = 0;
-        if (b < p.num_seqs) s = batch_seq(p, b, again);
+        if (!one_run) {
+            int again = 0;
+            s = {};
+            if (b < p.num_seqs) s = batch_seq(p, b, again);
+        }
         const Sums ask = block_sums(s.need, s.add, s_warp);
         const bool served = pages + ask.a <= top && tokens + ask.b <= p.max_tokens;
         if (!served && s.add > 0) bad |= PKV_EFLAG_POOL;
-        const Sums sum = block_sums(served ? s.need : 0, served ? s.add : 0, s_warp);
+        // (the last one served: all are)
+        const bool all = pages + ask.total_a <= top && tokens + ask.total_b <= p.max_tokens;
+        const Sums sum =
+            all ? ask : block_sums(served ? s.need : 0, served ? s.add : 0, s_warp);
         s_sum[tid] = sum.a;
         s_first[tid] = s.keep == 0 ? 0 : (s.keep - 1) / p.block_size + 1;
         if (b < p.num_seqs) {
-            p.query_starts[b + 1] = given + (int)sum.b;
-            p.new_context_lens[b] = s.keep + (served ? s.add : 0);
+            const int next = given + (int)sum.b, len = s.keep + (served ? s.add : 0);
+            p.query_starts[b + 1] = next;
+            p.new_context_lens[b] = len;
+            if (one_run) {  // (the tokens' bisection reads them from here)
+                s_starts[tid + 1] = next;
+                s_lens[tid] = len;
+            }
         }
         __syncthreads();
         for (int64_t i = tid; i < sum.total_a; i += kBatchThreads) {
@@ -232,19 +253,31 @@ __global__ void __launch_bounds__(kBatchThreads, 1) batch_plan_kernel(const Batc
     }
     if (tid == 0) {
         p.query_starts[0] = 0;
+        s_starts[0] = 0;
         p.new_free_count[0] = (int)(top - taken);
     }
     if (bad) flag_error(p.err_flag, bad);
     if (p.max_tokens > kBatchOwnTokens) return;
     __syncthreads();
-    for (int j = tid; j < p.max_tokens; j += kBatchThreads) batch_token(p, p.query_starts, j);
+    const int32_t* starts = one_run ? s_starts : p.query_starts;
+    const int32_t* lens = one_run ? s_lens : p.new_context_lens;
+    for (int j = tid; j < p.max_tokens; j += kBatchThreads) batch_token(p, starts, lens, j);
 }
 
+// The row starts are read once, not at every step of a bisection.
+constexpr int kSlotsStarts = 2047;
 __global__ void __launch_bounds__(256) batch_slots_kernel(const BatchPlanParams p) {
+    __shared__ int32_t s_starts[kSlotsStarts + 1];
     ptx::launch_dependents();
     ptx::grid_dependency_wait();
+    const bool few = p.num_seqs <= kSlotsStarts;
+    if (few) {
+        for (int i = threadIdx.x; i <= p.num_seqs; i += 256) s_starts[i] = p.query_starts[i];
+        __syncthreads();
+    }
     const int j = blockIdx.x * 256 + threadIdx.x;
-    if (j < p.max_tokens) batch_token(p, p.query_starts, j);
+    if (j < p.max_tokens)
+        batch_token(p, few ? s_starts : p.query_starts, p.new_context_lens, j);
 }
 
 static pkv_status launch_batch(void (*kern)(const BatchPlanParams), const BatchPlanParams& p,
