@@ -1053,19 +1053,19 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                                                                  ptx::rcp_approx(y.y)),
                                                      make_float2(cap2, cap2));
                                 });
-                            } else {
-                                const float k1 = p.scale_log2;
+                            } else if (p.slopes == nullptr) {
+                                const float k = p.scale_log2;
                                 pairs(r, [&](float2 y, int) {
-                                    return ptx::mul2(y, make_float2(k1, k1));
+                                    return ptx::mul2(y, make_float2(k, k));
                                 });
                             }
                             if (p.slopes != nullptr) {
-                                const float away = (float)(at - m);
+                                const float k = p.softcap > 0.f ? 1.f : p.scale_log2;
+                                const float base = slope * (float)(at - m);
                                 pairs(r, [&](float2 y, int i) {
-                                    return ptx::fma2(make_float2(slope, slope),
-                                                     ptx::add2(make_float2(away, away),
-                                                               make_float2((float)i, (float)(i + 1))),
-                                                     y);
+                                    return ptx::fma2(y, make_float2(k, k),
+                                                     make_float2(fmaf(slope, (float)i, base),
+                                                                 fmaf(slope, (float)(i + 1), base)));
                                 });
                             }
                         }
