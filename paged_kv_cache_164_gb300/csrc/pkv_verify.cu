@@ -52,6 +52,8 @@ struct VerifyParams {
     int slice;  // of the vocabulary, a CTA's
 };
 
+// (32 trees over 128000 tokens: 35 us, with 256 threads and four CTAs an SM 45, with 1024
+// and one 39)
 constexpr int kVerifyThreads = 512;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kVerifyCtas = 2;     // an SM
