@@ -637,8 +637,11 @@ pkv_status pkv_batch_plan(int32_t* query_starts, int32_t* positions, int64_t* sl
  *     z_t += slopes[h] (t - m) where slopes are given;  out = sum_t softmax(z)_t V_t
  * A row that sees nothing becomes zero.  What the cache holds at a position that a
  * row does not see never reaches that row, whatever its bits (infinities and NaN
- * included).  Rows of q before query_starts[0] and from query_starts[num_seqs] on
- * are left as they were.
+ * included); an infinity in the V of one that it sees makes that dim infinite or NaN.
+ * Rows of q before query_starts[0] and from query_starts[num_seqs] on are left as they
+ * were.  Scores, softmax sums and accumulators are fp32; a softmax weight meets V as two
+ * terms of the cache's type where a row block has up to 128 rows (new tokens times query
+ * heads of a KV head), rounded to one where it has more.
  *
  *   q, out        [num_tokens][num_q_heads][head_dim], dtype; out may be q itself,
  *                 must not overlap any argument otherwise
