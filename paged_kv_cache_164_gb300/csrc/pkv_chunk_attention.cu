@@ -1018,8 +1018,8 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                     const float scale = MOD ? 1.f : p.scale_log2;
                     // Two small loops over the row's scores, which are read twice, 32 at a
                     // time: unrolled further, the instructions did not stay in their cache
-                    // beside the other warps' (64 tokens of 64 sequences of 2000: 123 us, 142
-                    // with 64 at a time, 188 with the tile in one piece).
+                    // beside the other warps' (single tokens of 64 sequences of 2500: 123
+                    // us, 142 with 64 at a time, 188 with the tile in one piece).
 
                     // f over the pairs of neighbouring scores
                     auto pairs = [](auto& r, auto f) {
